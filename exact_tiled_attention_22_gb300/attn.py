@@ -30,7 +30,9 @@ ERROR_NAMES = {0: "ATTN_OK", -1: "ATTN_ERR_INVALID", -2: "ATTN_ERR_UNSUPPORTED",
 
 # Kernel ids of attn_profile_end.
 KERNEL_NAMES = ["attn_fwd", "attn_bwd_pre", "attn_bwd_main", "attn_dq_post",
-                "attn_decode_split", "attn_decode_merge"]
+                "attn_decode_split", "attn_decode_merge", "attn_pages_extend",
+                "attn_pages_release", "attn_kv8_append", "attn_kv8_split", "attn_kv8_merge",
+                "attn_varlen_plan"]
 
 
 class AttnError(RuntimeError):
@@ -94,6 +96,17 @@ def _load() -> ctypes.CDLL:
     lib.attn_cast_acc.restype = i
     lib.attn_philox4x32_10.argtypes = [vp, vp, i, vp]
     lib.attn_philox4x32_10.restype = i
+    ll = ctypes.c_longlong
+    lib.attn_pages_extend.argtypes = [vp, vp, i, vp, i, vp, vp, i, i, ll, vp, vp, vp, vp, vp, vp]
+    lib.attn_pages_extend.restype = i
+    lib.attn_pages_release.argtypes = [vp, vp, i, vp, i, vp, vp, i, i, vp, vp, vp]
+    lib.attn_pages_release.restype = i
+    lib.attn_kv8_append.argtypes = [vp, vp, ll, ll, vp, ll, i, i, vp, vp, vp, vp, i, i, i, vp]
+    lib.attn_kv8_append.restype = i
+    lib.attn_kv8_decode_workspace_size.argtypes = [i, i, i, i]
+    lib.attn_kv8_decode_workspace_size.restype = sz
+    lib.attn_kv8_decode.argtypes = [vp] * 9 + [i] * 8 + [f, i, i, vp, sz, vp]
+    lib.attn_kv8_decode.restype = i
     return lib
 
 
@@ -260,6 +273,42 @@ def attn_decode(q, k, v, o, lse, B, H, Nq, Nk, d, scale, causal, dtype, workspac
                            int(workspace_bytes), _stream(stream))
 
 
+def attn_pages_extend(lens, add, B, block_table, width, free_pages, free_count, free_cap, page, T,
+                      new_lens, granted, cu_new, slots, free_left, stream=None) -> int:
+    return lib.attn_pages_extend(_ptr(lens), _ptr(add), B, _ptr(block_table), width,
+                                 _ptr(free_pages), _ptr(free_count), free_cap, page, T,
+                                 _ptr(new_lens), _ptr(granted), _ptr(cu_new), _ptr(slots),
+                                 _ptr(free_left), _stream(stream))
+
+
+def attn_pages_release(lens, finished, B, block_table, width, free_pages, free_count, free_cap,
+                       page, new_lens, free_left, stream=None) -> int:
+    return lib.attn_pages_release(_ptr(lens), _ptr(finished), B, _ptr(block_table), width,
+                                  _ptr(free_pages), _ptr(free_count), free_cap, page,
+                                  _ptr(new_lens), _ptr(free_left), _stream(stream))
+
+
+def attn_kv8_append(k, v, k_stride, v_stride, slots, T, H, d, k_cache, v_cache, k_scale, v_scale,
+                    P, page, dtype, stream=None) -> int:
+    return lib.attn_kv8_append(_ptr(k), _ptr(v), k_stride, v_stride, _ptr(slots), T, H, d,
+                               _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), P, page,
+                               dtype_code(dtype), _stream(stream))
+
+
+def attn_kv8_decode_workspace_size(Nq, Hq, H, d) -> int:
+    return int(lib.attn_kv8_decode_workspace_size(Nq, Hq, H, d))
+
+
+def attn_kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o, lse, B, Nq, Hq, H,
+                    d, P, page, width, scale, causal, dtype, workspace, workspace_bytes,
+                    stream=None) -> int:
+    return lib.attn_kv8_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                               _ptr(v_scale), _ptr(block_table), _ptr(lens), _ptr(o), _ptr(lse),
+                               B, Nq, Hq, H, d, P, page, width, float(scale), int(bool(causal)),
+                               dtype_code(dtype), _ptr(workspace), int(workspace_bytes),
+                               _stream(stream))
+
+
 def attn_status(stream=None) -> int:
     return lib.attn_status(_stream(stream))
 
@@ -350,6 +399,155 @@ def decode(q, k, v, scale=None, causal=False, ws=None, stream=None, alibi=None):
                          device=q.device)
     check(attn_decode_alibi(q, k, v, o, lse, B, H, Nq, Nk, d, scale, causal, alibi, q.dtype, ws,
                             ws.numel(), stream))
+    return o, lse
+
+
+# ---- paged key/value cache in 8 bits --------------------------------------
+def _want(t, name, dtypes, shape):
+    """Checks a contiguous CUDA tensor's type and shape (None: any extent)."""
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    if (t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous() or t.dim() != len(shape)
+            or any(w is not None and n != w for n, w in zip(t.shape, shape))):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} of "
+                         f"{' or '.join(str(x) for x in dtypes)}, got {list(t.shape)} {t.dtype}")
+
+
+def _one_device(first, *rest):
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors are on different devices ({first.device}, {t.device})")
+    return first.device
+
+
+class _on:
+    """The tensors' device as the current one (the library acts on it)."""
+
+    def __init__(self, device):
+        self.dev, self.prev = device.index, None
+
+    def __enter__(self):
+        prev = torch.cuda.current_device()
+        if prev != self.dev:
+            torch.cuda.set_device(self.dev)
+            self.prev = prev
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def pages_extend(lens, add, block_table, free_pages, free_count, page, max_new, new_lens=None,
+                 free_left=None, stream=None):
+    """Pages and slots for add[b] new tokens of each request (attn_pages_extend).
+    lens, add: int32 [B]; block_table: int32 [B, width], updated in place;
+    free_pages: int32 [cap], a stack of free page ids, free_count: int32 [1];
+    max_new: length of the slot map.  new_lens may be lens and free_left may
+    be free_count.  Returns (new_lens, granted, cu_new, slots, free_left)."""
+    B = lens.shape[0]
+    _want(lens, "lens", torch.int32, (None,))
+    _want(add, "add", torch.int32, (B,))
+    _want(block_table, "block_table", torch.int32, (B, None))
+    _want(free_pages, "free_pages", torch.int32, (None,))
+    _want(free_count, "free_count", torch.int32, (1,))
+    if new_lens is not None:
+        _want(new_lens, "new_lens", torch.int32, (B,))
+    if free_left is not None:
+        _want(free_left, "free_left", torch.int32, (1,))
+    dev = _one_device(lens, add, block_table, free_pages, free_count, new_lens, free_left)
+    new_lens = torch.empty_like(lens) if new_lens is None else new_lens
+    free_left = torch.empty_like(free_count) if free_left is None else free_left
+    granted = torch.empty_like(lens)
+    cu_new = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    slots = torch.empty(max_new, dtype=torch.int64, device=dev)
+    with _on(dev):
+        check(attn_pages_extend(lens, add, B, block_table, block_table.shape[1], free_pages,
+                                free_count, free_pages.shape[0], page, max_new, new_lens, granted,
+                                cu_new, slots, free_left, stream))
+    return new_lens, granted, cu_new, slots, free_left
+
+
+def pages_release(lens, finished, block_table, free_pages, free_count, page, new_lens=None,
+                  free_left=None, stream=None):
+    """Pages of the requests with finished[b] != 0 (int32 [B]) go back onto the
+    stack free_pages, written in place (attn_pages_release).  Returns (new_lens, free_left)."""
+    B = lens.shape[0]
+    _want(lens, "lens", torch.int32, (None,))
+    _want(finished, "finished", torch.int32, (B,))
+    _want(block_table, "block_table", torch.int32, (B, None))
+    _want(free_pages, "free_pages", torch.int32, (None,))
+    _want(free_count, "free_count", torch.int32, (1,))
+    if new_lens is not None:
+        _want(new_lens, "new_lens", torch.int32, (B,))
+    if free_left is not None:
+        _want(free_left, "free_left", torch.int32, (1,))
+    dev = _one_device(lens, finished, block_table, free_pages, free_count, new_lens, free_left)
+    new_lens = torch.empty_like(lens) if new_lens is None else new_lens
+    free_left = torch.empty_like(free_count) if free_left is None else free_left
+    with _on(dev):
+        check(attn_pages_release(lens, finished, B, block_table, block_table.shape[1], free_pages,
+                                 free_count, free_pages.shape[0], page, new_lens, free_left,
+                                 stream))
+    return new_lens, free_left
+
+
+def _packed(t, name, dtype=None):
+    """A [T, H, d] CUDA tensor with heads d apart; its token stride."""
+    if t.dim() != 3 or not t.is_cuda or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be a CUDA tensor [T, H, d]" + (f" of {dtype}" if dtype else ""))
+    T, H, d = t.shape
+    if t.numel() and (t.stride(2) != 1 and d > 1 or t.stride(1) != d and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return max(t.stride(0), H * d) if T > 1 else H * d
+
+
+def _cache_shape(k_cache, v_cache, k_scale, v_scale):
+    _want(k_cache, "k_cache", _CODES, (None, None, None, None))
+    P, H, page, d = k_cache.shape
+    _want(v_cache, "v_cache", _CODES, (P, H, page, d))
+    _want(k_scale, "k_scale", torch.float32, (P, H))
+    _want(v_scale, "v_scale", torch.float32, (P, H))
+    return P, H, page, d
+
+
+def kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
+    """Rounds new keys and values [T, H, d] into their slots (int64 [T]) of the
+    8-bit cache [P, H, page, d] with scales [P, H], in place (attn_kv8_append).
+    k and v may be slices of a wider projection (any token stride)."""
+    P, H, page, d = _cache_shape(k_cache, v_cache, k_scale, v_scale)
+    T = k.shape[0]
+    ks, vs = _packed(k, "k"), _packed(v, "v", k.dtype)
+    if tuple(k.shape) != (T, H, d) or tuple(v.shape) != (T, H, d):
+        raise ValueError(f"k and v must be [T, {H}, {d}]")
+    _want(slots, "slots", torch.int64, (T,))
+    dev = _one_device(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+    with _on(dev):
+        check(attn_kv8_append(k, v, ks, vs, slots, T, H, d, k_cache, v_cache, k_scale, v_scale, P,
+                              page, k.dtype, stream))
+
+
+def kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=None, causal=True,
+               ws=None, stream=None):
+    """(o, lse) of q [B, Nq, Hq, d], the last Nq tokens of every request, against
+    the 8-bit cache (attn_kv8_decode); lens counts the Nq tokens."""
+    P, H, page, d = _cache_shape(k_cache, v_cache, k_scale, v_scale)
+    B, Nq, Hq, dq = _shape(q)
+    if dq != d:
+        raise ValueError(f"q has d = {dq}, the cache {d}")
+    _want(block_table, "block_table", torch.int32, (B, None))
+    _want(lens, "lens", torch.int32, (B,))
+    dev = _one_device(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, ws)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = torch.empty(attn_kv8_decode_workspace_size(Nq, Hq, H, d), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        check(attn_kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o, lse, B,
+                              Nq, Hq, H, d, P, page, block_table.shape[1], scale, causal, q.dtype,
+                              ws, ws.numel(), stream))
     return o, lse
 
 

@@ -686,6 +686,229 @@ int attn_cast_acc(const float* acc, void* out, size_t n, float mul, attn_dtype_t
   return ATTN_OK;
 }
 
+// ------------------------------------------------------------ paged 8-bit cache
+namespace {
+
+int page_shift_of(int page) {
+  for (int s = 4; s <= 7; ++s)
+    if (page == 1 << s) return s;
+  return -1;
+}
+
+// One page of one head of a code tensor [P, H, page, d] per box.
+int encode_pages(CUtensorMap* m, const void* ptr, long long PH, int page, int d) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)PH};
+  const cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)page * d};
+  const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)page, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return ATTN_OK;
+}
+
+// Outputs must not overlap one another or any input; allowed[i] (an input
+// index or -1) names the input that output i may be.
+int check_overlaps(const Range* outs, int n_out, const Range* ins, int n_in, const int* allowed = nullptr) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = i + 1; j < n_out; ++j)
+      if (overlap(outs[i], outs[j])) return fail(ATTN_ERR_INVALID, "output buffers overlap");
+    for (int j = 0; j < n_in; ++j) {
+      if (allowed && allowed[i] == j && outs[i].lo == ins[j].lo) continue;
+      if (overlap(outs[i], ins[j])) return fail(ATTN_ERR_INVALID, "an output or the workspace overlaps an input");
+    }
+  }
+  return ATTN_OK;
+}
+
+int check_pages(const void* const* ptrs, int n, int B, int width, int free_cap, int page) {
+  for (int i = 0; i < n; ++i) {
+    if (!ptrs[i]) return fail(ATTN_ERR_INVALID, "null pointer argument");
+    if (!aligned4(ptrs[i])) return fail(ATTN_ERR_ALIGN, "pointers must be 4-byte aligned");
+  }
+  if (B < 1 || width < 1 || free_cap < 1)
+    return fail(ATTN_ERR_INVALID, "B, width, free_cap must be >= 1 (got %d, %d, %d)", B, width, free_cap);
+  if (B > attn::kPagesMaxB) return fail(ATTN_ERR_UNSUPPORTED, "at most %d requests (got %d)", attn::kPagesMaxB, B);
+  if (page_shift_of(page) < 0) return fail(ATTN_ERR_UNSUPPORTED, "page must be 16, 32, 64 or 128 (got %d)", page);
+  if ((long long)width * page >= (1ll << 31)) return fail(ATTN_ERR_INVALID, "width * page must be < 2^31");
+  return ATTN_OK;
+}
+
+void wait_ctl(DeviceInfo* dev, attn::WaitCtlHost* w, int* debug_flags) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  *debug_flags = g_debug_flags;
+  w->limit_ns = g_wait_ns;
+  w->status = dev->status;
+}
+
+}  // namespace
+
+int attn_pages_extend(const int32_t* lens, const int32_t* add, int B, int32_t* block_table, int width,
+                      const int32_t* free_pages, const int32_t* free_count, int free_cap, int page, long long T,
+                      int32_t* new_lens, int32_t* granted, int32_t* cu_new, int64_t* slots, int32_t* free_left,
+                      void* stream) {
+  t_err.clear();
+  const void* ptrs[9] = {lens, add, block_table, free_pages, free_count, new_lens, granted, cu_new, free_left};
+  int rc = check_pages(ptrs, 9, B, width, free_cap, page);
+  if (rc) return rc;
+  if (T < 0 || T >= (1ll << 31)) return fail(ATTN_ERR_INVALID, "T must be in [0, 2^31) (got %lld)", T);
+  if (T > 0 && !slots) return fail(ATTN_ERR_INVALID, "null pointer argument");
+  if (reinterpret_cast<uintptr_t>(slots) & 7u) return fail(ATTN_ERR_ALIGN, "slots must be 8-byte aligned");
+  const size_t bb = (size_t)B * 4;
+  const Range outs[6] = {rng(new_lens, bb), rng(free_left, 4), rng(block_table, bb * width), rng(granted, bb),
+                         rng(cu_new, bb + 4), rng(slots, (size_t)T * 8)};
+  const Range ins[4] = {rng(lens, bb), rng(free_count, 4), rng(add, bb), rng(free_pages, (size_t)free_cap * 4)};
+  const int allowed[6] = {0, 1, -1, -1, -1, -1};
+  if ((rc = check_overlaps(outs, 6, ins, 4, allowed))) return rc;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  attn::PagesArgs a = {};
+  a.lens = lens; a.add = add; a.table = block_table; a.free_pages = free_pages; a.free_count = free_count;
+  a.new_lens = new_lens; a.granted = granted; a.cu_new = cu_new;
+  a.slots = reinterpret_cast<long long*>(slots);
+  a.left = free_left;
+  a.B = B; a.width = width; a.free_cap = free_cap; a.page_shift = page_shift_of(page); a.T = T;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = timed(attn::kKPagesExtend, s, [&] { return attn::launch_pages_extend(a, s); });
+  return e != cudaSuccess ? cuda_fail(e, "attn_pages_extend launch") : ATTN_OK;
+}
+
+int attn_pages_release(const int32_t* lens, const int32_t* finished, int B, const int32_t* block_table, int width,
+                       int32_t* free_pages, const int32_t* free_count, int free_cap, int page, int32_t* new_lens,
+                       int32_t* free_left, void* stream) {
+  t_err.clear();
+  const void* ptrs[7] = {lens, finished, block_table, free_pages, free_count, new_lens, free_left};
+  int rc = check_pages(ptrs, 7, B, width, free_cap, page);
+  if (rc) return rc;
+  const size_t bb = (size_t)B * 4;
+  const Range outs[3] = {rng(new_lens, bb), rng(free_left, 4), rng(free_pages, (size_t)free_cap * 4)};
+  const Range ins[4] = {rng(lens, bb), rng(free_count, 4), rng(finished, bb), rng(block_table, bb * width)};
+  const int allowed[3] = {0, 1, -1};
+  if ((rc = check_overlaps(outs, 3, ins, 4, allowed))) return rc;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  attn::PagesArgs a = {};
+  a.lens = lens; a.add = finished; a.table = const_cast<int32_t*>(block_table); a.free_out = free_pages;
+  a.free_count = free_count; a.new_lens = new_lens; a.left = free_left;
+  a.B = B; a.width = width; a.free_cap = free_cap; a.page_shift = page_shift_of(page);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = timed(attn::kKPagesRelease, s, [&] { return attn::launch_pages_release(a, s); });
+  return e != cudaSuccess ? cuda_fail(e, "attn_pages_release launch") : ATTN_OK;
+}
+
+int attn_kv8_append(const void* k, const void* v, long long k_stride, long long v_stride, const int64_t* slots,
+                    long long T, int H, int d, uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale,
+                    int P, int page, attn_dtype_t dtype, void* stream) {
+  t_err.clear();
+  if (T == 0) return ATTN_OK;
+  if (!k || !v || !slots || !k_cache || !v_cache || !k_scale || !v_scale)
+    return fail(ATTN_ERR_INVALID, "null pointer argument");
+  if (T < 0 || H < 1 || P < 1) return fail(ATTN_ERR_INVALID, "T >= 0, H >= 1, P >= 1 needed (got %lld, %d, %d)", T, H, P);
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim d=%d not supported (64 or 128)", d);
+  if (dtype != ATTN_F16 && dtype != ATTN_BF16) return fail(ATTN_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
+  if (page_shift_of(page) < 0) return fail(ATTN_ERR_UNSUPPORTED, "page must be 16, 32, 64 or 128 (got %d)", page);
+  if (T * H >= (1ll << 30) || T >= (1ll << 31)) return fail(ATTN_ERR_INVALID, "T * H must be < 2^30");
+  if ((long long)P * H >= (1ll << 31)) return fail(ATTN_ERR_INVALID, "P * H must be < 2^31");
+  const long long hd = (long long)H * d;
+  if (k_stride < hd || v_stride < hd || k_stride % 8 || v_stride % 8 || k_stride >= (1ll << 32) || v_stride >= (1ll << 32))
+    return fail(ATTN_ERR_INVALID, "token strides must be multiples of 8, at least H * d");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache))
+    return fail(ATTN_ERR_ALIGN, "k, v and the caches must be 16-byte aligned");
+  if (!aligned4(k_scale) || !aligned4(v_scale) || (reinterpret_cast<uintptr_t>(slots) & 7u))
+    return fail(ATTN_ERR_ALIGN, "scales must be 4-byte, slots 8-byte aligned");
+  const size_t cb = (size_t)P * H * page * d, sb = (size_t)P * H * 4;
+  const Range outs[4] = {rng(k_cache, cb), rng(v_cache, cb), rng(k_scale, sb), rng(v_scale, sb)};
+  const Range ins[3] = {rng(k, ((size_t)(T - 1) * k_stride + hd) * 2), rng(v, ((size_t)(T - 1) * v_stride + hd) * 2),
+                        rng(slots, (size_t)T * 8)};
+  int rc = check_overlaps(outs, 4, ins, 3);
+  if (rc) return rc;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  attn::Kv8AppendArgs a = {};
+  a.x[0] = k; a.x[1] = v;
+  a.cache[0] = k_cache; a.cache[1] = v_cache;
+  a.scale[0] = k_scale; a.scale[1] = v_scale;
+  a.slots = reinterpret_cast<const long long*>(slots);
+  a.x_stride[0] = k_stride; a.x_stride[1] = v_stride;
+  a.T = T;
+  a.n_slots = (long long)P * page;
+  a.H = H; a.d = d; a.page = page; a.bf16 = dtype == ATTN_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = timed(attn::kKKv8Append, s, [&] { return attn::launch_kv8_append(a, dev->sms, s); });
+  return e != cudaSuccess ? cuda_fail(e, "attn_kv8_append launch") : ATTN_OK;
+}
+
+size_t attn_kv8_decode_workspace_size(int Nq, int Hq, int H, int d) {
+  if (Nq < 1 || H < 1 || Hq < H || Hq % H || (d != 64 && d != 128)) return 0;
+  const size_t rows = (size_t)attn::kKv8MaxCtas * 2 * attn::kv8_rows(Nq * (Hq / H));
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  return up(rows * d * 4) + up(rows * 2 * 4);
+}
+
+int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
+                    const float* v_scale, const int32_t* block_table, const int32_t* lens, void* o, float* lse, int B,
+                    int Nq, int Hq, int H, int d, int P, int page, int width, float scale, int causal,
+                    attn_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  t_err.clear();
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !lens || !o || !lse)
+    return fail(ATTN_ERR_INVALID, "null pointer argument");
+  if (B < 1 || Nq < 1 || H < 1 || Hq < 1 || P < 1 || width < 1)
+    return fail(ATTN_ERR_INVALID, "B, Nq, Hq, H, P, width must be >= 1");
+  if (Hq % H) return fail(ATTN_ERR_INVALID, "Hq = %d is no multiple of H = %d", Hq, H);
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim d=%d not supported (64 or 128)", d);
+  if (dtype != ATTN_F16 && dtype != ATTN_BF16) return fail(ATTN_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
+  if (Nq > 128) return fail(ATTN_ERR_UNSUPPORTED, "decode takes at most 128 query rows (got %d)", Nq);
+  const int shift = page_shift_of(page);
+  if (shift < 0) return fail(ATTN_ERR_UNSUPPORTED, "page must be 16, 32, 64 or 128 (got %d)", page);
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_INVALID, "scale must be finite and > 0");
+  if ((long long)P * H >= (1ll << 31) || (long long)width * page >= (1ll << 31) || (long long)B * Nq * Hq >= (1ll << 31))
+    return fail(ATTN_ERR_INVALID, "P * H, width * page and B * Nq * Hq must be < 2^31");
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(lse))
+    return fail(ATTN_ERR_ALIGN, "q, o, lse and the caches must be 16-byte aligned");
+  if (!aligned4(k_scale) || !aligned4(v_scale) || !aligned4(block_table) || !aligned4(lens))
+    return fail(ATTN_ERR_ALIGN, "scales, block_table and lens must be 4-byte aligned");
+  const size_t need = attn_kv8_decode_workspace_size(Nq, Hq, H, d);
+  if (!workspace || workspace_bytes < need)
+    return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(ATTN_ERR_ALIGN, "workspace must be 256-byte aligned");
+  const size_t qb = (size_t)B * Nq * Hq * d * 2, cb = (size_t)P * H * page * d, sb = (size_t)P * H * 4;
+  const Range outs[3] = {rng(o, qb), rng(lse, (size_t)B * Nq * Hq * 4), rng(workspace, need)};
+  const Range ins[7] = {rng(q, qb), rng(k_cache, cb), rng(v_cache, cb), rng(k_scale, sb), rng(v_scale, sb),
+                        rng(block_table, (size_t)B * width * 4), rng(lens, (size_t)B * 4)};
+  int rc = check_overlaps(outs, 3, ins, 7);
+  if (rc) return rc;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  attn::Kv8DecArgs a;
+  std::memset(&a, 0, sizeof a);
+  if ((rc = encode_pages(&a.tm_k, k_cache, (long long)P * H, page, d)) ||
+      (rc = encode_pages(&a.tm_v, v_cache, (long long)P * H, page, d)))
+    return rc;
+  a.q = q; a.o = o; a.lse = lse;
+  a.k_scale = k_scale; a.v_scale = v_scale; a.table = block_table; a.lens = lens;
+  a.B = B; a.Nq = Nq; a.Hq = Hq; a.H = H; a.G = Hq / H; a.d = d;
+  a.width = width; a.page_shift = shift; a.P = P;
+  const int R = Nq * a.G;
+  a.rp = attn::kv8_rows(R);
+  a.n_rb = (R + a.rp - 1) / a.rp;
+  a.causal = causal ? 1 : 0;
+  a.bf16 = dtype == ATTN_BF16;
+  a.scale = scale;
+  const long long tiles = ((long long)width * page + 127) / 128;
+  a.grid = attn::kv8_grid(d, a.rp, a.bf16, dev->sms, tiles * B * H * a.n_rb);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.ws_o = reinterpret_cast<float*>(ws);
+  a.ws_ml = reinterpret_cast<float*>(ws + ((size_t)attn::kKv8MaxCtas * 2 * a.rp * d * 4 + 255) / 256 * 256);
+  wait_ctl(dev, &a.wait, &a.debug_flags);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = timed(attn::kKKv8Split, s, [&] { return attn::launch_kv8_split(a, s); });
+  if (e != cudaSuccess) return cuda_fail(e, "attn_kv8_decode launch");
+  e = timed(attn::kKKv8Merge, s, [&] { return attn::launch_kv8_merge(a, s); });
+  return e != cudaSuccess ? cuda_fail(e, "attn_kv8_decode merge launch") : ATTN_OK;
+}
+
 int attn_status(void* stream) {
   t_err.clear();
   DeviceInfo* dev = nullptr;

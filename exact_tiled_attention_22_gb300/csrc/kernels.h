@@ -10,7 +10,9 @@ namespace attn {
 
 // Kernel ids used by the per-kernel timing of attn_profile_*.
 enum KernelId {
-  kKFwd = 0, kKBwdPre = 1, kKBwdMain = 2, kKDqPost = 3, kKDecSplit = 4, kKDecMerge = 5, kKNum = 6
+  kKFwd = 0, kKBwdPre = 1, kKBwdMain = 2, kKDqPost = 3, kKDecSplit = 4, kKDecMerge = 5,
+  kKPagesExtend = 6, kKPagesRelease = 7, kKKv8Append = 8, kKKv8Split = 9, kKKv8Merge = 10, kKVarPlan = 11,
+  kKNum = 12
 };
 
 struct WaitCtlHost {
@@ -138,6 +140,64 @@ int decode_keys_per_split(int Nk, int n_split);
 int decode_smem_bytes(int d);
 cudaError_t launch_decode_split(const DecArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_merge(const DecArgs& a, cudaStream_t stream);
+
+// Paged key/value cache: block tables and slots (attn_pages.cu).
+constexpr int kPagesMaxB = 8192;
+struct PagesArgs {
+  const int* lens;        // [B]
+  const int* add;         // [B] new tokens (extend) / finished flags (release)
+  int* table;             // [B][width]
+  const int* free_pages;  // stack of free page ids, free_cap entries
+  int* free_out;          // the same, written by release
+  const int* free_count;
+  int* new_lens;
+  int* granted;
+  int* cu_new;
+  long long* slots;       // [T]
+  int* left;
+  int B, width, free_cap, page_shift;
+  long long T;
+};
+cudaError_t launch_pages_extend(const PagesArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_release(const PagesArgs& a, cudaStream_t stream);
+
+// Cache in 8 bits (attn_kv8.cu): codes [P][H][page][d] e4m3, scales [P][H].
+struct Kv8AppendArgs {
+  const void* x[2];         // new keys, values: token stride x_stride elements, heads d apart
+  uint8_t* cache[2];
+  float* scale[2];
+  const long long* slots;   // [T]
+  long long x_stride[2];
+  long long T, n_slots;     // n_slots = P * page
+  int H, d, page, bf16;
+};
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int sms, cudaStream_t stream);
+
+constexpr int kKv8MaxCtas = 640;  // workspace bound of the decode grid
+struct Kv8DecArgs {
+  CUtensorMap tm_k, tm_v;  // (d, page, P * H), one page of one head a box
+  const void* q;           // [B, Nq, Hq, d]
+  void* o;
+  float* lse;              // [B, Hq, Nq]
+  const float* k_scale;
+  const float* v_scale;
+  const int* table;        // [B][width]
+  const int* lens;         // [B]
+  float* ws_o;             // [CTA][2][rows][d]
+  float* ws_ml;            // [CTA][2][rows][2]
+  int B, Nq, Hq, H, G, d, width, page_shift, P;
+  int rp, n_rb;            // rows of a row block, row blocks
+  int grid;
+  int causal, bf16;
+  float scale;
+  int debug_flags;
+  WaitCtlHost wait;
+};
+// Rows of one row block for R = Nq * Hq / H query rows of a key head.
+int kv8_rows(int R);
+int kv8_grid(int d, int rp, int bf16, int sms, long long max_units);
+cudaError_t launch_kv8_split(const Kv8DecArgs& a, cudaStream_t stream);
+cudaError_t launch_kv8_merge(const Kv8DecArgs& a, cudaStream_t stream);
 
 // Id of the calling thread's current CUDA context (unique for the life of
 // the process, unlike the CUcontext handle, which a new context may reuse).

@@ -131,6 +131,16 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// 3-D tiled load, as above.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                            int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 // 4-D tiled store shared -> global, tracked by bulk groups (bulk_commit /
 // bulk_wait_*).  c0 is the innermost coordinate (c0 * element size a
 // multiple of 16 bytes); rows outside the tensor are not written.
@@ -275,6 +285,18 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       : "memory");
 }
 
+// D(tmem) (+)= A(smem desc) * B(smem desc) on 8-bit floats (K = 32 a step).
+__device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
 // Instruction descriptor for kind::f16 with fp32 accumulation.
 //   bits 4-5 D type (1 = f32); 7-9 A type, 10-12 B type (0 f16, 1 bf16);
 //   15 / 16: A / B MN-major; 17-22 N >> 3; 24-28 M >> 4.
@@ -283,6 +305,11 @@ __host__ __device__ constexpr uint32_t make_idesc(bool bf16, int M, int N, bool 
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
          ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same for kind::f8f6f4 with e4m3 operands (types 0) and fp32 accumulation.
+__host__ __device__ constexpr uint32_t make_idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
+  return make_idesc(false, M, N, a_mn, b_mn);
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle, version 1.
@@ -296,6 +323,14 @@ __device__ __forceinline__ uint64_t make_sdesc(uint32_t saddr, uint32_t lbo,
   return (uint64_t)((saddr >> 4) & 0x3FFFu) |
          ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// The same with the 64-byte swizzle (layout 4): rows of 64 bytes, 8-row atoms
+// of 512 bytes, 16-byte chunk c of row r at chunk c ^ ((r / 2) % 4).
+__device__ __forceinline__ uint64_t make_sdesc64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) |
+         ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (4ull << 61);
 }
 
 // ---- TMEM loads / stores: 32 lanes x 32-bit, one lane (row) per thread.
@@ -418,6 +453,27 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   } else {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   }
+  return r;
+}
+
+// Two fp32 values to e4m3 (RNE, saturating at +-448, NaN stays NaN): `lo` in
+// bits 0-7, `hi` in bits 8-15.
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The two e4m3 values in the low 16 bits of w (exact).
+__device__ __forceinline__ float2 unpack_e4m3(uint32_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+// Maximum of v over the warp's lanes (NaN ignored unless every lane has one).
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
 

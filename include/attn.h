@@ -336,6 +336,94 @@ int attn_decode(const void* q, const void* k, const void* v, void* o, float* lse
                 void* stream);
 
 /*
+ * A paged key/value cache in 8 bits, for requests of different lengths.
+ *
+ * The cache of one layer is k_cache, v_cache : [P, H, page, d] e4m3 codes (one
+ * byte each; P pages of `page` tokens, H key heads) and k_scale, v_scale : fp32
+ * [P, H], one scale per page and head: a cached key is k_scale * code.  A
+ * request b of length len_b holds its token i at page block_table[b][i / page],
+ * place i % page; block_table is int32 [B, width].  A slot is the int64
+ * page id * page + place.  page is 16, 32, 64 or 128.  All of it lives on the
+ * device, lengths included, so a whole decoding step can be captured into a
+ * graph and replayed while the requests grow.  The pages are those that page
+ * "突破单卡显存极限：FlashAttention-2技术解析与实战指南", section 3.2, names by way of
+ * vLLM inference; the page gives no layout.
+ *
+ * attn_pages_extend -- pages and slots for add[b] >= 0 new tokens of each
+ * request.  The free pages are a stack: free_pages[0 .. *free_count), int32, of
+ * an array of free_cap entries.  Request b needs ceil((lens[b] + add[b]) / page)
+ * - ceil(lens[b] / page) new pages; it is served if it needs none, or if its
+ * pages and those of all requests before it are no more than there are (and it
+ * fits `width` pages, and neither number is negative).  Served requests take
+ * pages from the top of the stack in order.
+ *   block_table : [B, width], the new pages' entries are written
+ *   new_lens    : [B] lens + granted (may be lens itself)
+ *   granted     : [B] add[b] if served, else 0
+ *   cu_new      : [B + 1] exclusive prefix sums of max(add, 0)
+ *   slots       : int64 [T]; new token t (token t - cu_new[b] of request b) has
+ *                 slots[t]; -1 for tokens of requests that were not served and
+ *                 for t >= cu_new[B] (tokens past T get no entry)
+ *   free_left   : [1] pages left on the stack (may be free_count itself)
+ * free_pages itself is not written.  1 <= B <= 8192, 0 <= T < 2^31.
+ *
+ * attn_pages_release -- the pages of the requests with finished[b] != 0 go back
+ * onto the stack (free_pages is written, in the order of requests and pages),
+ * their lengths become 0: new_lens (may be lens), free_left (may be
+ * free_count).  Pages past free_cap entries are dropped.
+ *
+ * attn_kv8_append -- rounds T new keys and values into their slots.
+ *   k, v  : [T, H, d] of dtype, token t at t * k_stride (v_stride) elements
+ *           (strides multiples of 8, at least H * d), heads d apart
+ *   slots : int64 [T], -1 (or anything outside the cache): the token is skipped
+ * Tokens of one page are consecutive in the list, with ascending consecutive
+ * slots, and no page stands for two requests (as attn_pages_extend makes them);
+ * contents of pages for which that does not hold are unspecified.  For the
+ * tokens of the call that go to one page and head, s = the smallest power of two
+ * with max |x| <= 448 s, clamped to [2^-64, 2^60]; codes are x / s rounded to
+ * nearest even (saturating at 448; a NaN stays one).  If they begin at the
+ * page's place 0, s becomes the page's scale and what the page held before does
+ * not matter.  If they begin further back, the scale becomes max(s, old scale)
+ * and the places before them are rounded again when it grew.  Places behind
+ * them are left as they are.
+ *
+ * attn_kv8_decode -- attention of the last Nq tokens of every request to all of
+ * its cached tokens, theirs among them (lens counts them, as attn_decode's Nk).
+ *   q, o : [B, Nq, Hq, d] of dtype, Hq a multiple of H (head h reads key head
+ *          h / (Hq / H))
+ *   lse  : fp32 [B, Hq, Nq]
+ * With causal, query i sees tokens j <= len - Nq + i; a query that sees none
+ * gets O = 0 and LSE = -inf.  Scales must be positive and finite, and those of
+ * one request's values within a factor of 2^100 of one another (append's are
+ * not further apart than 2^124, and that far only for values beyond 2^46).
+ * Lengths are clamped to [0, width * page]; codes behind a request's last token
+ * and entries of block_table behind its last page are not used; a page id
+ * outside [0, P) reads as zeros.  Query and key products carry fp16 / bf16
+ * queries exactly up to 2^-21 of a row's largest element; probabilities are
+ * rounded to 2^-13 (fp16) or 2^-9 (bf16) of their value.
+ * workspace: as attn_decode's, size from attn_kv8_decode_workspace_size.
+ */
+int attn_pages_extend(const int32_t* lens, const int32_t* add, int B, int32_t* block_table,
+                      int width, const int32_t* free_pages, const int32_t* free_count,
+                      int free_cap, int page, long long T, int32_t* new_lens,
+                      int32_t* granted, int32_t* cu_new, int64_t* slots,
+                      int32_t* free_left, void* stream);
+int attn_pages_release(const int32_t* lens, const int32_t* finished, int B,
+                       const int32_t* block_table, int width, int32_t* free_pages,
+                       const int32_t* free_count, int free_cap, int page,
+                       int32_t* new_lens, int32_t* free_left, void* stream);
+int attn_kv8_append(const void* k, const void* v, long long k_stride, long long v_stride,
+                    const int64_t* slots, long long T, int H, int d, uint8_t* k_cache,
+                    uint8_t* v_cache, float* k_scale, float* v_scale, int P, int page,
+                    attn_dtype_t dtype, void* stream);
+size_t attn_kv8_decode_workspace_size(int Nq, int Hq, int H, int d);
+int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                    const float* k_scale, const float* v_scale,
+                    const int32_t* block_table, const int32_t* lens, void* o,
+                    float* lse, int B, int Nq, int Hq, int H, int d, int P, int page,
+                    int width, float scale, int causal, attn_dtype_t dtype,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * attn_philox4x32_10 -- diagnostic: the dropout decisions' generator itself.
  * Runs the kernels' Philox4x32-10 (Salmon et al., SC 2011, section 3.2; the
  * generator named under attn_fwd_ex) on n caller-given inputs, one GPU thread
@@ -370,7 +458,7 @@ const char* attn_last_error_string(void);
  * hold back its copies, so that its consumers' waits run out (used to test
  * the timeout path without faulting the GPU): bit 0 the forward (no loads),
  * bit 1 the backward main kernel (K and V, but no query steps), bit 2 the
- * decoding chunk kernel (no loads).  Bit 3 changes no result: the
+ * decoding chunk kernel (no loads), bit 4 attn_kv8_decode (no loads).  Bit 3 changes no result: the
  * backward's preprocess and dQ conversion kernels split row indices with
  * 64-bit arithmetic, the form they take by themselves only when
  * B * H * N (N rounded up to 128) reaches 2^31.  Process-wide.
@@ -383,7 +471,8 @@ int attn_set_wait_limit(unsigned long long limit_ns, int debug_flags);
  * library is bracketed by CUDA events on its stream.  attn_profile_end()
  * synchronises those events and fills, for kernel ids 0..n-1
  * (0 forward, 1 backward preprocess, 2 backward main, 3 dQ conversion,
- * 4 decode chunks, 5 decode merge),
+ * 4 decode chunks, 5 decode merge, 6 pages extend, 7 pages release, 8 8-bit
+ * append, 9 8-bit decode, 10 its merge, 11 packed-batch plan),
  * the number of launches and their summed device time in milliseconds.
  * Returns the number of kernel ids filled, or a negative ATTN_ERR_* code.
  */
