@@ -31,8 +31,7 @@ ERROR_NAMES = {0: "ATTN_OK", -1: "ATTN_ERR_INVALID", -2: "ATTN_ERR_UNSUPPORTED",
 # Kernel ids of attn_profile_end.
 KERNEL_NAMES = ["attn_fwd", "attn_bwd_pre", "attn_bwd_main", "attn_dq_post",
                 "attn_decode_split", "attn_decode_merge", "attn_pages_extend",
-                "attn_pages_release", "attn_kv8_append", "attn_kv8_split", "attn_kv8_merge",
-                "attn_varlen_plan"]
+                "attn_pages_release", "attn_kv8_append", "attn_kv8_split", "attn_kv8_merge"]
 
 
 class AttnError(RuntimeError):
@@ -107,6 +106,12 @@ def _load() -> ctypes.CDLL:
     lib.attn_kv8_decode_workspace_size.restype = sz
     lib.attn_kv8_decode.argtypes = [vp] * 9 + [i] * 8 + [f, i, i, vp, sz, vp]
     lib.attn_kv8_decode.restype = i
+    lib.attn_varlen_fwd.argtypes = [vp] * 7 + [i, ll, ll, i, i, i, ll, ll, ll, f, i, i, vp]
+    lib.attn_varlen_fwd.restype = i
+    lib.attn_varlen_bwd_workspace_size.argtypes = [i, ll, i, i]
+    lib.attn_varlen_bwd_workspace_size.restype = sz
+    lib.attn_varlen_bwd.argtypes = [vp] * 11 + [i, ll, ll, i, i, i, ll, ll, ll, f, i, i, vp, sz, vp]
+    lib.attn_varlen_bwd.restype = i
     return lib
 
 
@@ -309,6 +314,28 @@ def attn_kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o,
                                _stream(stream))
 
 
+def attn_varlen_fwd(q, k, v, o, lse, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, d, q_stride, k_stride,
+                    v_stride, scale, causal, dtype, stream=None) -> int:
+    return lib.attn_varlen_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_q),
+                               _ptr(cu_k), B, Tq, Tk, Hq, Hkv, d, q_stride, k_stride, v_stride,
+                               float(scale), int(bool(causal)), dtype_code(dtype),
+                               _stream(stream))
+
+
+def attn_varlen_bwd_workspace_size(B, Tq, Hq, d) -> int:
+    return int(lib.attn_varlen_bwd_workspace_size(B, Tq, Hq, d))
+
+
+def attn_varlen_bwd(q, k, v, o, lse, dO, dq, dk, dv, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, d, q_stride,
+                    k_stride, v_stride, scale, causal, dtype, workspace, workspace_bytes,
+                    stream=None) -> int:
+    return lib.attn_varlen_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq),
+                               _ptr(dk), _ptr(dv), _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, Hq, Hkv, d,
+                               q_stride, k_stride, v_stride, float(scale), int(bool(causal)),
+                               dtype_code(dtype), _ptr(workspace), int(workspace_bytes),
+                               _stream(stream))
+
+
 def attn_status(stream=None) -> int:
     return lib.attn_status(_stream(stream))
 
@@ -498,9 +525,9 @@ def _packed(t, name, dtype=None):
     if t.dim() != 3 or not t.is_cuda or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{name} must be a CUDA tensor [T, H, d]" + (f" of {dtype}" if dtype else ""))
     T, H, d = t.shape
-    if t.numel() and (t.stride(2) != 1 and d > 1 or t.stride(1) != d and H > 1):
+    if t.numel() and (t.stride(2) != 1 or t.stride(1) != d and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return max(t.stride(0), H * d) if T > 1 else H * d
+    return t.stride(0) if T > 1 else H * d
 
 
 def _cache_shape(k_cache, v_cache, k_scale, v_scale):
@@ -551,6 +578,67 @@ def kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=N
     return o, lse
 
 
+# ---- packed batches ---------------------------------------------------------
+def _packed_args(q, k, v, cu_q, cu_k):
+    qs, ks, vs = _packed(q, "q"), _packed(k, "k", q.dtype), _packed(v, "v", q.dtype)
+    Tq, Hq, d = q.shape
+    Tk, Hkv, dk = k.shape
+    if dk != d or v.shape != k.shape:
+        raise ValueError(f"k and v must be [Tk, Hkv, {d}], got {list(k.shape)} and {list(v.shape)}")
+    _want(cu_q, "cu_q", torch.int32, (None,))
+    _want(cu_k, "cu_k", torch.int32, (cu_q.shape[0],))
+    dev = _one_device(q, k, v, cu_q, cu_k)
+    return dev, (cu_q.shape[0] - 1, Tq, Tk, Hq, Hkv, d, qs, ks, vs)
+
+
+def varlen_fwd(q, k, v, cu_q, cu_k, scale=None, causal=False, o=None, stream=None):
+    """(o, lse [Hq, Tq]) of packed sequences: q [Tq, Hq, d], k, v [Tk, Hkv, d]
+    fp16/bf16 CUDA tensors (any token stride that is a multiple of d), cu_q, cu_k
+    int32 [B + 1] row offsets on the device (attn_varlen_fwd).  o: an output to
+    write into; rows of no sequence are left as they are there."""
+    dev, sizes = _packed_args(q, k, v, cu_q, cu_k)
+    Tq, Hq, d = q.shape
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if o is None:
+        o = torch.empty((Tq, Hq, d), dtype=q.dtype, device=dev)
+    else:
+        _want(o, "o", q.dtype, (Tq, Hq, d))
+        _one_device(q, o)
+    lse = torch.empty((Hq, Tq), dtype=torch.float32, device=dev)
+    with _on(dev):
+        check(attn_varlen_fwd(q, k, v, o, lse, cu_q, cu_k, *sizes, scale, causal, q.dtype, stream))
+    return o, lse
+
+
+def varlen_bwd(q, k, v, o, lse, do, cu_q, cu_k, scale=None, causal=False, ws=None, grads=None,
+               stream=None):
+    """(dq, dk, dv) for the varlen_fwd that produced (o, lse).  grads: three
+    contiguous tensors to write into (rows of no sequence are left as they are)."""
+    dev, sizes = _packed_args(q, k, v, cu_q, cu_k)
+    Tq, Hq, d = q.shape
+    _want(o, "o", q.dtype, (Tq, Hq, d))
+    _want(do, "do", q.dtype, (Tq, Hq, d))
+    _want(lse, "lse", torch.float32, (Hq, Tq))
+    _one_device(q, o, do, lse, ws)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if grads is None:
+        dq = torch.empty((Tq, Hq, d), dtype=q.dtype, device=dev)
+        dk, dv = (torch.empty(k.shape, dtype=q.dtype, device=dev) for _ in range(2))
+    else:
+        dq, dk, dv = grads
+        _want(dq, "dq", q.dtype, (Tq, Hq, d))
+        _want(dk, "dk", q.dtype, k.shape)
+        _want(dv, "dv", q.dtype, k.shape)
+        _one_device(q, dq, dk, dv)
+    if ws is None:
+        ws = torch.empty(attn_varlen_bwd_workspace_size(sizes[0], Tq, Hq, d), dtype=torch.uint8,
+                         device=dev)
+    with _on(dev):
+        check(attn_varlen_bwd(q, k, v, o, lse, do, dq, dk, dv, cu_q, cu_k, *sizes, scale, causal,
+                              q.dtype, ws, ws.numel(), stream))
+    return dq, dk, dv
+
+
 # ---- autograd -------------------------------------------------------------
 class AttentionFunction(torch.autograd.Function):
     """O = attention(q, k, v) with the backward of the library (attn_bwd_ex):
@@ -579,3 +667,30 @@ def attention(q, k, v, scale=None, causal=False, alibi=None, block_mask=None, dr
     tensors (forward and backward in the library's kernels)."""
     return AttentionFunction.apply(q, k, v, scale, causal, alibi, block_mask, dropout_p, seed,
                                    offset)
+
+
+class VarlenAttentionFunction(torch.autograd.Function):
+    """Packed attention with the backward of the library (attn_varlen_bwd).
+    Rows of no sequence (padding behind the last one) have zero output and zero
+    gradients here, so that they add nothing to the parameters' gradients."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, cu_q, cu_k, scale, causal):
+        o, lse = varlen_fwd(q, k, v, cu_q, cu_k, scale, causal,
+                            o=torch.zeros(q.shape, dtype=q.dtype, device=q.device))
+        ctx.save_for_backward(q, k, v, o, lse, cu_q, cu_k)
+        ctx.opts = (scale, causal)
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
+        grads = [torch.zeros(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v)]
+        dq, dk, dv = varlen_bwd(q, k, v, o, lse, do.contiguous(), cu_q, cu_k, *ctx.opts,
+                                grads=grads)
+        return dq, dk, dv, None, None, None, None
+
+
+def attention_varlen(q, k, v, cu_q, cu_k, scale=None, causal=False):
+    """Differentiable attention on packed sequences (see varlen_fwd)."""
+    return VarlenAttentionFunction.apply(q, k, v, cu_q, cu_k, scale, causal)

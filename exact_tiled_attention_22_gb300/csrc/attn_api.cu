@@ -909,6 +909,184 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   return e != cudaSuccess ? cuda_fail(e, "attn_kv8_decode merge launch") : ATTN_OK;
 }
 
+// ------------------------------------------------------------ packed batches
+namespace {
+
+// A packed [T, H, d] 16-bit tensor, `stride` elements from token to token, as
+// (d, head, row window, place): the last two dimensions both step by a token,
+// so that a box may begin up to `rows` tokens before its place and reads zeros
+// there (see attn_fwd.cu).
+int encode_packed(CUtensorMap* m, const void* ptr, long long T, int H, int d, long long stride, int rows, bool bf16) {
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, 128, (cuuint64_t)T};
+  const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                        const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return ATTN_OK;
+}
+
+int check_packed(const int32_t* cu_q, const int32_t* cu_k, int B, long long Tq, long long Tk, int Hq, int Hkv, int d,
+                 long long q_stride, long long k_stride, long long v_stride, float scale, attn_dtype_t dtype) {
+  if (!cu_q || !cu_k) return fail(ATTN_ERR_INVALID, "null pointer argument");
+  if (!aligned4(cu_q) || !aligned4(cu_k)) return fail(ATTN_ERR_ALIGN, "cu_q, cu_k must be 4-byte aligned");
+  if (B < 1 || Hq < 1 || Hkv < 1) return fail(ATTN_ERR_INVALID, "B, Hq, Hkv must be >= 1 (got %d, %d, %d)", B, Hq, Hkv);
+  if (B > attn::kVarMaxB) return fail(ATTN_ERR_UNSUPPORTED, "at most %d sequences (got %d)", attn::kVarMaxB, B);
+  if (Hq % Hkv || Hq / Hkv > 1024)
+    return fail(ATTN_ERR_INVALID, "Hq = %d must be a multiple of Hkv = %d, at most 1024 times it", Hq, Hkv);
+  if (Tq < 0 || Tk < 0 || Tq >= (1ll << 26) || Tk >= (1ll << 26))
+    return fail(ATTN_ERR_INVALID, "Tq, Tk must be in [0, 2^26) (got %lld, %lld)", Tq, Tk);
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim d=%d not supported (64 or 128)", d);
+  if (dtype != ATTN_F16 && dtype != ATTN_BF16) return fail(ATTN_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_INVALID, "scale must be finite and > 0");
+  const long long hq = (long long)Hq * d, hk = (long long)Hkv * d;
+  if (q_stride < hq || k_stride < hk || v_stride < hk || q_stride % d || k_stride % d || v_stride % d ||
+      q_stride >= (1ll << 30) || k_stride >= (1ll << 30) || v_stride >= (1ll << 30))
+    return fail(ATTN_ERR_INVALID, "token strides must be multiples of d, at least heads * d");
+  if ((Tq / 128 + B) * Hq >= (1ll << 31) || (Tk / 128 + B) * Hkv >= (1ll << 31) || Tq * hq >= (1ll << 40) ||
+      Tk * hk >= (1ll << 40))
+    return fail(ATTN_ERR_INVALID, "too many tiles or elements");
+  return ATTN_OK;
+}
+
+long long varlen_padded(int B, long long Tq) { return (Tq / 64 + B) * 64; }
+
+size_t packed_bytes(long long T, long long stride, long long row) {
+  return T > 0 ? ((size_t)(T - 1) * stride + row) * 2 : 0;
+}
+
+}  // namespace
+
+int attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_q,
+                    const int32_t* cu_k, int B, long long Tq, long long Tk, int Hq, int Hkv, int d, long long q_stride,
+                    long long k_stride, long long v_stride, float scale, int causal, attn_dtype_t dtype, void* stream) {
+  t_err.clear();
+  int rc = check_packed(cu_q, cu_k, B, Tq, Tk, Hq, Hkv, d, q_stride, k_stride, v_stride, scale, dtype);
+  if (rc) return rc;
+  if (Tq == 0) return ATTN_OK;
+  if (!q || !o || !lse || (Tk > 0 && (!k || !v))) return fail(ATTN_ERR_INVALID, "null pointer argument");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
+    return fail(ATTN_ERR_ALIGN, "q, k, v, o and lse must be 16-byte aligned");
+  const long long hq = (long long)Hq * d, hk = (long long)Hkv * d;
+  const size_t cb = ((size_t)B + 1) * 4;
+  const Range outs[2] = {rng(o, packed_bytes(Tq, hq, hq)), rng(lse, (size_t)Tq * Hq * 4)};
+  const Range ins[5] = {rng(q, packed_bytes(Tq, q_stride, hq)), rng(k, packed_bytes(Tk, k_stride, hk)),
+                        rng(v, packed_bytes(Tk, v_stride, hk)), rng(cu_q, cb), rng(cu_k, cb)};
+  if ((rc = check_overlaps(outs, 2, ins, 5))) return rc;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  attn::FwdArgs a;
+  std::memset(&a, 0, sizeof a);
+  const bool bf16 = dtype == ATTN_BF16;
+  // (without keys no K or V tile is loaded; their maps still need an address)
+  if ((rc = encode_packed(&a.tm_q, q, Tq, Hq, d, q_stride, 128, bf16)) ||
+      (rc = encode_packed(&a.tm_k, Tk ? k : q, Tk ? Tk : 1, Hkv, d, Tk ? k_stride : hk, 128, bf16)) ||
+      (rc = encode_packed(&a.tm_v, Tk ? v : q, Tk ? Tk : 1, Hkv, d, Tk ? v_stride : hk, 128, bf16)) ||
+      (rc = encode_packed(&a.tm_o, o, Tq, Hq, d, hq, 128, bf16)))
+    return rc;
+  a.o = o;
+  a.lse = lse;
+  if ((rc = make_dropout(0.f, 0, 0, &a.drop))) return rc;
+  a.B = B; a.H = Hq; a.N = (int)Tq; a.d = d;
+  a.cu_q = cu_q; a.cu_k = cu_k;
+  a.Nk = (int)Tk; a.G = Hq / Hkv;
+  a.head_pairs = a.G % 2 == 0;
+  a.causal = causal ? 1 : 0;
+  a.scale = scale;
+  a.bf16 = bf16;
+  wait_ctl(dev, &a.wait, &a.debug_flags);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = timed(attn::kKFwd, s, [&] { return attn::launch_fwd_varlen(a, s); });
+  return e != cudaSuccess ? cuda_fail(e, "attn_varlen_fwd launch") : ATTN_OK;
+}
+
+size_t attn_varlen_bwd_workspace_size(int B, long long Tq, int Hq, int d) {
+  if (B < 1 || B > attn::kVarMaxB || Tq < 0 || Tq >= (1ll << 26) || Hq < 1 || (d != 64 && d != 128)) return 0;
+  const size_t rows = (size_t)varlen_padded(B, Tq) * Hq;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  return up(rows * 4) * 2 + up(rows * d * 4) + 256 + up((size_t)B * sizeof(attn::VarBwdSeq)) + up(((size_t)B + 1) * 4);
+}
+
+int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                    void* dq, void* dk, void* dv, const int32_t* cu_q, const int32_t* cu_k, int B, long long Tq,
+                    long long Tk, int Hq, int Hkv, int d, long long q_stride, long long k_stride, long long v_stride,
+                    float scale, int causal, attn_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  t_err.clear();
+  int rc = check_packed(cu_q, cu_k, B, Tq, Tk, Hq, Hkv, d, q_stride, k_stride, v_stride, scale, dtype);
+  if (rc) return rc;
+  if (Tq == 0 && Tk == 0) return ATTN_OK;
+  if ((Tq > 0 && (!q || !o || !lse || !dO || !dq)) || (Tk > 0 && (!k || !v || !dk || !dv)))
+    return fail(ATTN_ERR_INVALID, "null pointer argument");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(dO) ||
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return fail(ATTN_ERR_ALIGN, "all pointers must be 16-byte aligned");
+  const size_t need = attn_varlen_bwd_workspace_size(B, Tq, Hq, d);
+  if (!workspace || workspace_bytes < need)
+    return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(ATTN_ERR_ALIGN, "workspace must be 256-byte aligned");
+  const long long hq = (long long)Hq * d, hk = (long long)Hkv * d;
+  const size_t cb = ((size_t)B + 1) * 4, qb = packed_bytes(Tq, hq, hq), kb = packed_bytes(Tk, hk, hk);
+  const Range outs[4] = {rng(dq, qb), rng(dk, kb), rng(dv, kb), rng(workspace, need)};
+  const Range ins[8] = {rng(q, packed_bytes(Tq, q_stride, hq)), rng(k, packed_bytes(Tk, k_stride, hk)),
+                        rng(v, packed_bytes(Tk, v_stride, hk)), rng(o, qb), rng(lse, (size_t)Tq * Hq * 4),
+                        rng(dO, qb), rng(cu_q, cb), rng(cu_k, cb)};
+  if ((rc = check_overlaps(outs, 4, ins, 8))) return rc;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  attn::BwdArgs a;
+  std::memset(&a, 0, sizeof a);
+  const bool bf16 = dtype == ATTN_BF16;
+  const long long npad = varlen_padded(B, Tq);
+  const size_t rows = (size_t)npad * Hq;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.o = o;
+  a.dO = dO;
+  a.lse = lse;
+  if ((rc = make_dropout(0.f, 0, 0, &a.drop))) return rc;
+  a.lse2 = reinterpret_cast<float*>(ws);
+  a.dvec = reinterpret_cast<float*>(ws + up(rows * 4));
+  a.dqacc = reinterpret_cast<float*>(ws + 2 * up(rows * 4));
+  ws += 2 * up(rows * 4) + up(rows * (size_t)d * 4);
+  a.sched = reinterpret_cast<unsigned*>(ws);
+  a.var_seq = reinterpret_cast<attn::VarBwdSeq*>(ws + 256);
+  a.var_items = reinterpret_cast<int*>(ws + 256 + up((size_t)B * sizeof(attn::VarBwdSeq)));
+  a.dq = dq; a.dk = dk; a.dv = dv;
+  a.B = B; a.H = Hq; a.N = (int)Tq; a.Npad = (int)npad; a.d = d;
+  a.cu_q = cu_q; a.cu_k = cu_k;
+  a.Nk = (int)Tk; a.G = Hq / Hkv; a.Hkv = Hkv;
+  a.sms = dev->sms;
+  a.causal = causal ? 1 : 0;
+  a.scale = scale;
+  a.bf16 = bf16;
+  wait_ctl(dev, &a.wait, &a.debug_flags);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = timed(attn::kKBwdPre, s, [&] { return attn::launch_var_pre(a, s); });
+  if (e != cudaSuccess) return cuda_fail(e, "attn_varlen_bwd preprocess launch");
+  if (Tq > 0 && Tk > 0) {
+    const int qrows = attn::bwd_q_rows(d);
+    if ((rc = encode_packed(&a.tm_q, q, Tq, Hq, d, q_stride, qrows, bf16)) ||
+        (rc = encode_packed(&a.tm_k, k, Tk, Hkv, d, k_stride, 128, bf16)) ||
+        (rc = encode_packed(&a.tm_v, v, Tk, Hkv, d, v_stride, 128, bf16)) ||
+        (rc = encode_packed(&a.tm_do, dO, Tq, Hq, d, hq, qrows, bf16)) ||
+        (rc = encode_packed(&a.tm_dk, dk, Tk, Hkv, d, hk, 128, bf16)) ||
+        (rc = encode_packed(&a.tm_dv, dv, Tk, Hkv, d, hk, 128, bf16)))
+      return rc;
+    e = timed(attn::kKBwdMain, s, [&] { return attn::launch_bwd_main_varlen(a, s); });
+    if (e != cudaSuccess) return cuda_fail(e, "attn_varlen_bwd main launch");
+  }
+  if (Tq > 0) {
+    e = timed(attn::kKDqPost, s, [&] { return attn::launch_var_post(a, s); });
+    if (e != cudaSuccess) return cuda_fail(e, "attn_varlen_bwd dQ conversion launch");
+  }
+  return ATTN_OK;
+}
+
 int attn_status(void* stream) {
   t_err.clear();
   DeviceInfo* dev = nullptr;

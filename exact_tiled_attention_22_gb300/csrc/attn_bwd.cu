@@ -40,6 +40,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
+
 #include "dropout.cuh"
 #include "kernels.h"
 #include "sm103_ptx.cuh"
@@ -270,10 +272,23 @@ __host__ __device__ inline int bwd_head_group(int N, int d, int BH) {
 // completed (they read K and V in shared memory), and the next item's first
 // dV and dK MMAs (which start their accumulators) wait until the dV and dK
 // stores of the item have read those TMEM columns.
-template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false>
+//
+// VARLEN (with none of the above): packed sequences of different lengths with
+// G query heads to a key head.  An item is a 128-key tile of one sequence and
+// KEY head, and its steps run over the rows of all G query heads of the group:
+// dK and dV of a shared head are summed in the same TMEM accumulators, in a
+// fixed order, and K and V are loaded once for the group.  Tiles and steps
+// count from the end of their sequence (see attn_fwd.cu): key tile tk sees the
+// 64-row steps u <= 2 tk + 1, the ragged ones are the first and TMA fills their
+// missing rows with zeros.  -LSE, D and the dQ accumulator are kept in a padded
+// layout [head][row], every sequence padded in front to whole steps.  The
+// producer finds an item's sequence and publishes its description with it
+// (sequences without queries have no items).
+template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false, bool VARLEN = false>
 __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
     attn_bwd_main_kernel(const __grid_constant__ BwdArgs p) {
   static_assert(!ACC || !(ALIBI || SPARSE || DROPOUT), "the accumulating variant is plain only");
+  static_assert(!VARLEN || !(ALIBI || SPARSE || DROPOUT || ACC), "the packed variant is plain only");
   constexpr int NWG = BwdNwg<DROPOUT>::value;
   using R = BwdRoles<NWG>;
   constexpr int kWarpDrain0 = R::kDrain0, kWarpProducer = R::kProducer;
@@ -291,17 +306,20 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
   griddep_wait();  // (programmatic serialization: see griddep_wait)
   const int BH = p.B * p.H;
   const int nkb = (p.N + 127) / 128;
-  const int n_items = nkb * BH;
-  const int G = bwd_head_group(p.N, D, BH);
+  const int n_items = VARLEN ? p.var_items[p.B] : nkb * BH;
+  const int G = VARLEN ? 1 : bwd_head_group(p.N, D, BH);
   const int nq = (p.N + BQ - 1) / BQ;
   const WaitCtl wc{p.wait.status, p.wait.limit_ns};
 
   // The work item with index `item`.
+  // (VARLEN: h is the key head, k0 the first key's position in its sequence,
+  // n_steps the steps of one query head, n_it those of the group.)
   struct Item {
     int jblk, bh, b, h, k0, i_begin, n_it;
+    int kbase, qbase, lq, diag, pbase, n_steps;
   };
   auto decode = [&](int item) -> Item {
-    Item it;
+    Item it{};
     const int grp = item / (G * nkb), r_in = item % (G * nkb);
     const int gsize = min(G, BH - grp * G);  // the last group may be smaller
     it.jblk = r_in / gsize;
@@ -319,6 +337,54 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
   auto do_addr = [&](int st) -> uint32_t { return q_addr(st) + L::kQT; };
   volatile int* item_slot = reinterpret_cast<volatile int*>(sbase + L::kItemSlot);
 
+  // (VARLEN) The item `item` described for its slot: the sequence by bisection
+  // of the item counts, then, as in decode, groups of key heads whose dQ
+  // accumulators fit the L2, the key tiles with the most steps (the first ones)
+  // first.  Slot words: tile, key head, first query row, queries, first key row,
+  // keys, padded row of query 0.
+  volatile int* var_slot = reinterpret_cast<volatile int*>(sbase + L::kQBits);
+  auto var_publish = [&](int slot, int item) {
+    int lo = 0, hi = p.B - 1;  // last sequence with var_items <= item
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.var_items[mid] <= item) lo = mid; else hi = mid - 1;
+    }
+    const VarBwdSeq q = p.var_seq[lo];
+    const int r = item - p.var_items[lo], nkt = (q.lk + 127) >> 7;
+    const int gh = bwd_head_group(q.lq, D * p.G, p.Hkv);
+    const int grp = r / (gh * nkt), r_in = r - grp * gh * nkt;
+    const int gsize = min(gh, p.Hkv - grp * gh);
+    volatile int* v = var_slot + 8 * slot;
+    v[0] = nkt - 1 - r_in / gsize;
+    v[1] = grp * gh + r_in % gsize;
+    v[2] = q.q0;
+    v[3] = q.lq;
+    v[4] = q.k0;
+    v[5] = q.lk;
+    v[6] = q.pbase;
+  };
+  auto var_item = [&](int slot) -> Item {
+    const volatile int* v = var_slot + 8 * slot;
+    Item it{};
+    const int tk = v[0], lk = v[5];
+    it.h = v[1];
+    it.qbase = v[2];
+    it.lq = v[3];
+    it.kbase = v[4];
+    it.pbase = v[6];
+    it.k0 = lk - 128 * (tk + 1);
+    it.diag = lk - it.lq;
+    const int nqs = (it.lq + BQ - 1) / BQ;
+    it.n_steps = p.causal ? min(nqs, 2 * tk + 2) : nqs;
+    it.n_it = it.n_steps * p.G;
+    return it;
+  };
+  // (VARLEN) a step is (query head of the group) << 20 | step of that head;
+  // first query row of a step: ascending, the last step ends the sequence
+  auto step_q0 = [&](const Item& I, int step) -> int {
+    return VARLEN ? I.lq - BQ * (I.n_steps - (step & 0xFFFFF)) : (I.i_begin + step) * BQ;
+  };
+
   uint32_t* qbits = reinterpret_cast<uint32_t*>(sbase + L::kQBits);
   int* npos_s = reinterpret_cast<int*>(sbase + L::kNPos);
   // (SPARSE: one item per CTA) step `it` of the item (query rows
@@ -329,6 +395,7 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
     return ((qbits[qb >> 5] >> (qb & 31)) & 1u) != 0;
   };
   auto next_step = [&](const Item& I, int it) -> int {  // the next visited step after `it` (n_it: none)
+    if constexpr (VARLEN) return it >= 0 && (it & 0xFFFFF) + 1 == I.n_steps ? ((it >> 20) + 1) << 20 : it + 1;
     ++it;
     if constexpr (SPARSE) {
       while (it < I.n_it && !step_ok(I, it)) ++it;
@@ -342,22 +409,26 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
   // kStages, across items).
   auto load_stage = [&](const Item& I, int g, int it) {
     const int st = g % L::kStages;
-    const int q0 = (I.i_begin + it) * BQ;
+    const int q0 = step_q0(I, it);
     const uint32_t fb = bar(L::kBarQFull + st);
     mbar_expect_tx(fb, 2 * L::kQT + 2 * BQ * 4);
+    // head, row window and place (VARLEN), or head, row and batch
+    const int hq = VARLEN ? I.h * p.G + (it >> 20) : I.h;
+    const int c2 = VARLEN ? min(q0, 0) : q0, c3 = VARLEN ? I.qbase + max(q0, 0) : I.b;
     for (int s = 0; s < L::kNSub; ++s) {
-      tma_load_4d(q_addr(st) + s * L::kSubQ, &p.tm_q, fb, s * 64, I.h, q0, I.b);
-      tma_load_4d(do_addr(st) + s * L::kSubQ, &p.tm_do, fb, s * 64, I.h, q0, I.b);
+      tma_load_4d(q_addr(st) + s * L::kSubQ, &p.tm_q, fb, s * 64, hq, c2, c3);
+      tma_load_4d(do_addr(st) + s * L::kSubQ, &p.tm_do, fb, s * 64, hq, c2, c3);
     }
-    const size_t row0 = (size_t)I.bh * p.Npad + q0;
+    const size_t row0 = VARLEN ? (size_t)hq * p.Npad + (I.pbase + q0) : (size_t)I.bh * p.Npad + q0;
     bulk_load(base + L::kLse + st * BQ * 4, p.lse2 + row0, BQ * 4, fb);
     bulk_load(base + L::kDv + st * BQ * 4, p.dvec + row0, BQ * 4, fb);
   };
   auto load_kv = [&](const Item& I) {
     mbar_expect_tx(bar(L::kBarKV), 2 * L::kKV);
+    const int c2 = VARLEN ? min(I.k0, 0) : I.k0, c3 = VARLEN ? I.kbase + max(I.k0, 0) : I.b;
     for (int s = 0; s < L::kNSub; ++s) {
-      tma_load_4d(base + L::kK + s * L::kSubKV, &p.tm_k, bar(L::kBarKV), s * 64, I.h, I.k0, I.b);
-      tma_load_4d(base + L::kV + s * L::kSubKV, &p.tm_v, bar(L::kBarKV), s * 64, I.h, I.k0, I.b);
+      tma_load_4d(base + L::kK + s * L::kSubKV, &p.tm_k, bar(L::kBarKV), s * 64, I.h, c2, c3);
+      tma_load_4d(base + L::kV + s * L::kSubKV, &p.tm_v, bar(L::kBarKV), s * 64, I.h, c2, c3);
     }
   };
 
@@ -428,10 +499,12 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
   // Consumers: the item of position n in the CTA's sequence (-1: no more),
   // or -2 if the wait gave up.  Every lane of the calling warp waits; lane
   // 0 then frees the slot for the producer.
+  Item V_item{};  // (VARLEN) the item take_item read last
   auto take_item = [&](int n) -> int {
     const bool ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarItemFull + (n & 1)), (n >> 1) & 1, wc));
     int item = -2;
     if (ok) item = item_slot[n & 1];
+    if (VARLEN && item >= 0) V_item = var_item(n & 1);
     __syncwarp();
     if (ok && lane == 0) mbar_arrive(bar(L::kBarItemEmpty + (n & 1)));
     return item;
@@ -460,9 +533,10 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
           break;
         }
         item_slot[n & 1] = item;
+        if (VARLEN && item >= 0) var_publish(n & 1, item);
         mbar_arrive(bar(L::kBarItemFull + (n & 1)));  // release: the slot is visible to the waiters
         if (item < 0) break;
-        const Item I = decode(item);
+        const Item I = VARLEN ? var_item(n & 1) : decode(item);
         const int n_pos = n_pos_of(I);
         if (n_pos == 0) continue;  // (SPARSE) a key block with no visited step loads nothing
         if (p.debug_flags & 2) {   // (timeout test: K and V, but no query step)
@@ -523,7 +597,7 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
         named_bar_and(kHandoffBar, 64, true);
         break;
       }
-      const Item I = decode(item);
+      const Item I = VARLEN ? V_item : decode(item);
       const int n_pos = n_pos_of(I);
       if (n_pos == 0) {  // (SPARSE) nothing to issue; the issuer still takes H0
         ok = named_bar_and(kHandoffBar, 64, true);
@@ -641,10 +715,11 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
       ok = named_bar_and(kHandoffBar, 64, true);  // H0
       if (!ok) break;
       const int item = item_slot[n & 1];
+      if (VARLEN && item >= 0) V_item = var_item(n & 1);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kBarItemEmpty + (n & 1)));
       if (item < 0) break;
-      const Item I = decode(item);
+      const Item I = VARLEN ? V_item : decode(item);
       const int n_pos = n_pos_of(I);
       if (n_pos == 0) continue;
       int st = g % L::kStages;  // stage of step g (advanced incrementally)
@@ -708,10 +783,10 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
         break;
       }
       if (item < 0) break;  // (-1: no more items, read alike by every warp from the slot)
-      const Item I = decode(item);
+      const Item I = VARLEN ? V_item : decode(item);
       const int n_pos = n_pos_of(I);
       const int key = I.k0 + kl;
-      const bool key_ok = key < p.N;
+      const bool key_ok = VARLEN ? key >= 0 : key < p.N;
       const float slope2 = ALIBI ? p.alibi[I.h] * kLog2e : 0.f;  // ALiBi slope, log2 units
       if (hf == 0 && n_pos > 0) {
         // K row kl -> TMEM lane kl as the 16-bit A operand of S^T = K Q^T:
@@ -743,7 +818,7 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
       // CTA's step counter (stages, buffers and barrier parities).
       for (int it = 0, step = next_step(I, -1); ok && it < n_pos; ++it, step = next_step(I, step), ++g) {
         const int st = g % L::kStages;
-        const int q0 = (I.i_begin + step) * BQ;
+        const int q0 = step_q0(I, step);
         // dropout: bit i keeps score (query q0 + cbase + i, this key)
         uint32_t keepw = 0xffffffffu;
         if constexpr (DROPOUT) {
@@ -791,7 +866,7 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
         const float4* dvec = reinterpret_cast<const float4*>(sbase + L::kDv + st * BQ * 4 + cbase * 4);
         // visible(q) = key < N && (!causal || key <= q): column i of this
         // warpgroup is visible iff i >= vis_from (vis_from > CW: none).
-        const int vis_from = !key_ok ? CW + 1 : (p.causal ? max(0, key - (q0 + cbase)) : 0);
+        const int vis_from = !key_ok ? CW + 1 : (p.causal ? max(0, key - (VARLEN ? I.diag : 0) - (q0 + cbase)) : 0);
         const bool warp_all_vis = __all_sync(0xffffffffu, vis_from == 0);
         float pr[CW];
 #pragma unroll
@@ -888,7 +963,8 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
       ok = named_bar_and(kPdsBar, kPdsThreads, ok);  // (a warp that gave up in the steps)
       if (!ok) break;
       uint8_t* dst = reinterpret_cast<uint8_t*>(p.dv) +
-                     ((((size_t)I.b * p.N + (key_ok ? key : 0)) * p.H + I.h) * D) * 2;
+                     ((VARLEN ? ((size_t)I.kbase + (key_ok ? key : 0)) * p.Hkv + I.h
+                              : ((size_t)I.b * p.N + (key_ok ? key : 0)) * p.H + I.h) * D) * 2;
       if (n_pos > 0) {
         // (every P/dS warp takes the same branch: the TMA store below meets
         // at a named barrier)
@@ -902,6 +978,11 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
                                      p.dv_acc + (((size_t)I.b * p.N + (key_ok ? key : 0)) * p.H + I.h) * D);
           tc_fence_before();
           mbar_arrive(bar(L::kBarDVEmpty));  // the next item's first dV may overwrite the columns
+        } else if (VARLEN && I.k0 < 0) {
+          // the ragged tile: the rows before the sequence are its neighbour's
+          store_row_from_tmem<D / NWG, BF16>(tmem + lane_off + L::kColDV, hf * (D / NWG), 1.f, key_ok, dst);
+          tc_fence_before();
+          mbar_arrive(bar(L::kBarDVEmpty));
         } else {
           // Through shared memory and one TMA store per 64-column box (the
           // dS buffers are free: the item's last dQ MMA has completed); rows
@@ -914,7 +995,8 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
           named_bar_sync(kPdsBar, kPdsThreads);
           if (warp == 0 && lane == 0) {
             for (int bx = 0; bx < D / 64; ++bx)
-              tma_store_4d(&p.tm_dv, base + L::kDS + bx * 16384, bx * 64, I.h, I.k0, I.b);
+              tma_store_4d(&p.tm_dv, base + L::kDS + bx * 16384, bx * 64, I.h, VARLEN ? 0 : I.k0,
+                           VARLEN ? I.kbase + I.k0 : I.b);
             bulk_commit();
             bulk_wait_read_all();  // the buffers are written again by the next item's dS
           }
@@ -944,10 +1026,10 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
         break;
       }
       if (item < 0) break;
-      const Item I = decode(item);
+      const Item I = VARLEN ? V_item : decode(item);
       const int n_pos = n_pos_of(I);
       for (int it = 0, step = next_step(I, -1); ok && it < n_pos; ++it, step = next_step(I, step), ++g) {
-        const int q0 = (I.i_begin + step) * BQ;
+        const int q0 = step_q0(I, step);
         // The four warps meet at named barriers below: the give-up flag of a
         // bounded wait travels through the first one so they branch together.
         ok = named_bar_and(kDrainBar, 128,
@@ -976,7 +1058,9 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
           fence_proxy_async_smem();
           named_bar_sync(kDrainBar, 128);
           if (leader) {
-            bulk_reduce_add_f32(p.dqacc + ((size_t)I.bh * p.Npad + q0 + hh * (BQ / 2)) * D,
+            const size_t row0 = VARLEN ? (size_t)(I.h * p.G + (step >> 20)) * p.Npad + (I.pbase + q0)
+                                       : (size_t)I.bh * p.Npad + q0;
+            bulk_reduce_add_f32(p.dqacc + (row0 + hh * (BQ / 2)) * D,
                                 base + L::kDQ + hh * (L::kDQBytes / 2), L::kDQBytes / 2);
             bulk_commit();
           }
@@ -984,9 +1068,10 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
       }
       if (!ok) break;
       const int key = I.k0 + ln;
-      const bool key_ok = key < p.N;
+      const bool key_ok = VARLEN ? key >= 0 : key < p.N;
       uint8_t* dst = reinterpret_cast<uint8_t*>(p.dk) +
-                     ((((size_t)I.b * p.N + (key_ok ? key : 0)) * p.H + I.h) * D) * 2;
+                     ((VARLEN ? ((size_t)I.kbase + (key_ok ? key : 0)) * p.Hkv + I.h
+                              : ((size_t)I.b * p.N + (key_ok ? key : 0)) * p.H + I.h) * D) * 2;
       if (n_pos > 0) {
         // (the four drain warps take the same branch: they meet at named
         // barriers below)
@@ -998,6 +1083,10 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
                                p.dk_acc + (((size_t)I.b * p.N + (key_ok ? key : 0)) * p.H + I.h) * D);
           tc_fence_before();
           mbar_arrive(bar(L::kBarDKEmpty));  // the next item's first dK may overwrite the columns
+        } else if (VARLEN && I.k0 < 0) {  // the ragged tile, as dV's
+          store_row_from_tmem<D, BF16>(tmem + lane_off + L::kColDK, 0, p.scale, key_ok, dst);
+          tc_fence_before();
+          mbar_arrive(bar(L::kBarDKEmpty));
         } else {
           // Through the dQ staging tile (once the last dQ reduce has read it)
           // and one TMA store per 64-column box.
@@ -1010,7 +1099,8 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
           named_bar_sync(kDrainBar, 128);
           if (leader) {
             for (int bx = 0; bx < D / 64; ++bx)
-              tma_store_4d(&p.tm_dk, base + L::kDQ + bx * 16384, bx * 64, I.h, I.k0, I.b);
+              tma_store_4d(&p.tm_dk, base + L::kDQ + bx * 16384, bx * 64, I.h, VARLEN ? 0 : I.k0,
+                           VARLEN ? I.kbase + I.k0 : I.b);
             bulk_commit();
             bulk_wait_read_all();  // the next item's dQ is staged here
           }
@@ -1039,6 +1129,7 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
 // in flight per SM.
 constexpr int kAuxThreads = 256;
 constexpr int kAuxBlocksPerSm = 4;
+static_assert(kAuxThreads / 32 == 8, "var_scan's warp sums");
 
 // (1) D_r = sum_c dO[r][c] O[r][c] for every row r = (b, n, h) of the
 //     [B, N, H, d] tensors, in their memory order: one row is 16 lanes
@@ -1161,20 +1252,264 @@ __global__ void __launch_bounds__(kAuxThreads, kAuxBlocksPerSm) attn_dq_post_ker
   griddep_launch_dependents();  // (see launch_pdl)
 }
 
-template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false>
+template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false, bool VARLEN = false>
 cudaError_t launch_main_t(const BwdArgs& a, cudaStream_t stream) {
   using L = BwdLayout<D, BwdNwg<DROPOUT>::value>;
-  auto* k = attn_bwd_main_kernel<D, BF16, ALIBI, SPARSE, DROPOUT, ACC>;
+  auto* k = attn_bwd_main_kernel<D, BF16, ALIBI, SPARSE, DROPOUT, ACC, VARLEN>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   // one CTA per item (block-sparse), else a persistent grid of one CTA per SM
-  const long long items = (long long)((a.N + 127) / 128) * a.B * a.H;
+  // (VARLEN: no more items than the worst split of the keys into sequences has)
+  const long long items = VARLEN ? ((long long)a.Nk / 128 + a.B) * a.Hkv : (long long)((a.N + 127) / 128) * a.B * a.H;
   const unsigned grid = (unsigned)(SPARSE ? items : (items < a.sms ? items : a.sms));
   e = launch_pdl(k, grid, BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, L::kSmem, stream, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// ------------------------------------------------------------ packed pre / post
+// Every CTA of these two kernels computes the sequences' descriptions for
+// itself (B offsets from L2, one block-wide scan per 256 of them): first query
+// rows and padded starts go to shared memory, where a token's sequence is found
+// by bisection.
+struct VarScan {
+  int* q0;     // [B] first query row
+  int* lq;     // [B]
+  int* pbase;  // [B] padded row of query 0
+};
+
+// Also leaves, from CTA 0, what the main kernel reads: p.var_seq, p.var_items.
+__device__ __forceinline__ VarScan var_scan(const BwdArgs& p, uint8_t* smem, bool publish) {
+  __shared__ long long wsum[8];
+  VarScan v;
+  v.q0 = reinterpret_cast<int*>(smem);
+  v.lq = v.q0 + p.B;
+  v.pbase = v.lq + p.B;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // Exclusive sum of x over the block's threads plus the carry, which grows by
+  // the block's total.
+  auto scan = [&](long long x, long long& carry) -> long long {
+    long long inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    long long before = carry;
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) before += wsum[w];
+      carry += wsum[w];
+    }
+    __syncthreads();
+    return before + inc - x;
+  };
+  long long c_pad = 0, c_item = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kAuxThreads) {
+    const int b = b0 + threadIdx.x;
+    int q0 = 0, lq = 0, k0 = 0, lk = 0;
+    if (b < p.B) {
+      q0 = min(max(p.cu_q[b], 0), p.N);
+      lq = min(max(p.cu_q[b + 1], q0), p.N) - q0;
+      k0 = min(max(p.cu_k[b], 0), p.Nk);
+      lk = min(max(p.cu_k[b + 1], k0), p.Nk) - k0;
+    }
+    const int pad = (lq + 63) / 64 * 64;
+    const long long ps = scan(pad, c_pad);
+    // (offsets that do not ascend could ask for more rows than there are: such
+    // a sequence has no queries, so that nothing leaves the workspace)
+    if (ps > p.Npad - pad) lq = 0;
+    const int items = lq > 0 ? (lk + 127) / 128 * p.Hkv : 0;
+    const long long is = scan(items, c_item);
+    if (b < p.B) {
+      const int pbase = lq > 0 ? (int)ps + pad - lq : 0;
+      v.q0[b] = q0;
+      v.lq[b] = lq;
+      v.pbase[b] = pbase;
+      if (publish) {
+        p.var_seq[b] = VarBwdSeq{q0, lq, k0, lk, pbase, {0, 0, 0}};
+        p.var_items[b] = (int)min(is, (long long)INT_MAX);
+      }
+    }
+  }
+  __syncthreads();
+  if (publish && threadIdx.x == 0) p.var_items[p.B] = (int)min(c_item, (long long)INT_MAX);
+  return v;
+}
+
+// Padded row of packed query t, or -1 if no sequence has it.
+__device__ __forceinline__ int var_row(const VarScan& v, int B, int t) {
+  int lo = 0, hi = B - 1;  // last sequence with q0 <= t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (v.q0[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  const int i = t - v.q0[lo];
+  return i >= 0 && i < v.lq[lo] ? v.pbase[lo] + i : -1;
+}
+
+// As attn_bwd_pre_kernel, on packed rows: D and -LSE log2 e into the padded
+// layout [H][Npad], the padding rows, the cleared accumulator, the counter; and
+// zeros for the gradients of keys whose sequence has no query.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kAuxThreads, kAuxBlocksPerSm) attn_var_pre_kernel(const __grid_constant__ BwdArgs p) {
+  extern __shared__ __align__(16) uint8_t var_smem[];
+  griddep_wait();
+  constexpr int kLanesPerRow = D * 2 / 16;
+  constexpr int kRowsPerWarp = 32 / kLanesPerRow;
+  constexpr int kU = 4;
+  const int lane = threadIdx.x & 31;
+  const long long nthreads = (long long)gridDim.x * blockDim.x;
+  const long long tid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long nwarps = nthreads >> 5, gw = tid >> 5;
+  float4* z = reinterpret_cast<float4*>(p.dqacc);
+  const long long nz = (long long)p.H * p.Npad * D / 4;
+  for (long long i = tid; i < nz; i += nthreads) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const VarScan v = var_scan(p, var_smem, blockIdx.x == 0);
+
+  const long long rows = (long long)p.N * p.H;
+  const long long groups = (rows + kRowsPerWarp - 1) / kRowsPerWarp;
+  const int sub = lane / kLanesPerRow, part = lane % kLanesPerRow;
+  for (long long g0 = gw * kU; g0 < groups; g0 += nwarps * kU) {
+    uint4 ov[kU], gv[kU];
+#pragma unroll
+    for (int j = 0; j < kU; ++j) {
+      const long long r = (g0 + j) * kRowsPerWarp + sub;
+      if (r < rows) {
+        ov[j] = reinterpret_cast<const uint4*>(p.o)[r * kLanesPerRow + part];
+        gv[j] = reinterpret_cast<const uint4*>(p.dO)[r * kLanesPerRow + part];
+      } else {
+        ov[j] = make_uint4(0, 0, 0, 0);
+        gv[j] = ov[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kU; ++j) {
+      const uint32_t* ow = &ov[j].x;
+      const uint32_t* gwv = &gv[j].x;
+      float acc = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 x = unpack2<BF16>(ow[w]), y = unpack2<BF16>(gwv[w]);
+        acc = fmaf(x.x, y.x, acc);
+        acc = fmaf(x.y, y.y, acc);
+      }
+#pragma unroll
+      for (int off = kLanesPerRow / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+      const long long r = (g0 + j) * kRowsPerWarp + sub;
+      if (part == 0 && r < rows) {
+        const int t = (int)(r / p.H), h = (int)(r - (long long)t * p.H);
+        const int row = var_row(v, p.B, t);
+        if (row >= 0) {
+          const size_t at = (size_t)h * p.Npad + row;
+          const float l = p.lse[(size_t)h * p.N + t];
+          const bool none = l == -INFINITY;  // a query that sees no key: its P is 0
+          p.dvec[at] = none ? 0.f : acc;
+          p.lse2[at] = none ? -INFINITY : -l * kLog2e;
+        }
+      }
+    }
+  }
+  // padding rows (fewer than 64 to a sequence and head), keys without queries
+  for (long long i = gw; i < (long long)p.B * p.H; i += nwarps) {
+    const int b = (int)(i / p.H), h = (int)(i - (long long)b * p.H);
+    const int n = (64 - (v.lq[b] & 63)) & 63;
+    for (int j = lane; j < n; j += 32) {
+      const size_t at = (size_t)h * p.Npad + (v.pbase[b] - n + j);
+      p.lse2[at] = -INFINITY;
+      p.dvec[at] = 0.f;
+    }
+  }
+  for (int b = 0; b < p.B; ++b) {
+    if (v.lq[b] > 0) continue;
+    const int k0 = min(max(p.cu_k[b], 0), p.Nk), lk = min(max(p.cu_k[b + 1], k0), p.Nk) - k0;
+    const long long n = (long long)lk * p.Hkv * D / 8, at = (long long)k0 * p.Hkv * D / 8;
+    for (long long i = tid; i < n; i += nthreads) {
+      reinterpret_cast<uint4*>(p.dk)[at + i] = make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4*>(p.dv)[at + i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  if (tid == 0) {
+    p.sched[0] = 0u;
+    p.sched[1] = 0u;
+  }
+  griddep_launch_dependents();
+}
+
+// dQ = scale * accumulator, to 16-bit, packed rows (rows of no sequence are
+// left as they are).
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kAuxThreads, kAuxBlocksPerSm) attn_var_post_kernel(const __grid_constant__ BwdArgs p) {
+  extern __shared__ __align__(16) uint8_t var_smem[];
+  griddep_wait();
+  const VarScan v = var_scan(p, var_smem, false);
+  constexpr int kU = 4;
+  const long long nthreads = (long long)gridDim.x * blockDim.x;
+  const long long total = (long long)p.N * p.H * D / 8;
+  const float s = p.scale;
+  for (long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x; i0 < total; i0 += kU * nthreads) {
+    float4 x[kU], y[kU];
+    bool in[kU];
+#pragma unroll
+    for (int j = 0; j < kU; ++j) {
+      const long long idx = i0 + j * nthreads;
+      in[j] = false;
+      if (idx < total) {
+        const int c = (int)(idx % (D / 8)) * 8;
+        const long long r = idx / (D / 8);
+        const int t = (int)(r / p.H), h = (int)(r - (long long)t * p.H);
+        const int row = var_row(v, p.B, t);
+        in[j] = row >= 0;
+        if (in[j]) {
+          const float4* src = reinterpret_cast<const float4*>(p.dqacc + ((size_t)h * p.Npad + row) * D + c);
+          x[j] = src[0];
+          y[j] = src[1];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kU; ++j)
+      if (in[j])
+        reinterpret_cast<uint4*>(p.dq)[i0 + j * nthreads] =
+            make_uint4(pack2<BF16>(x[j].x * s, x[j].y * s), pack2<BF16>(x[j].z * s, x[j].w * s),
+                       pack2<BF16>(y[j].x * s, y[j].y * s), pack2<BF16>(y[j].z * s, y[j].w * s));
+  }
+  griddep_launch_dependents();
+}
+
+template <typename K>
+cudaError_t launch_var_aux(K k, const BwdArgs& a, cudaStream_t stream) {
+  const size_t smem = (size_t)a.B * 12;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kVarMaxB * 12);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, (unsigned)(a.sms * kAuxBlocksPerSm), kAuxThreads, smem, stream, a);
+}
+
 }  // namespace
+
+cudaError_t launch_var_pre(const BwdArgs& a, cudaStream_t stream) {
+  if (a.d == 128)
+    return a.bf16 ? launch_var_aux(attn_var_pre_kernel<128, true>, a, stream)
+                  : launch_var_aux(attn_var_pre_kernel<128, false>, a, stream);
+  return a.bf16 ? launch_var_aux(attn_var_pre_kernel<64, true>, a, stream)
+                : launch_var_aux(attn_var_pre_kernel<64, false>, a, stream);
+}
+
+cudaError_t launch_var_post(const BwdArgs& a, cudaStream_t stream) {
+  if (a.d == 128)
+    return a.bf16 ? launch_var_aux(attn_var_post_kernel<128, true>, a, stream)
+                  : launch_var_aux(attn_var_post_kernel<128, false>, a, stream);
+  return a.bf16 ? launch_var_aux(attn_var_post_kernel<64, true>, a, stream)
+                : launch_var_aux(attn_var_post_kernel<64, false>, a, stream);
+}
+
+cudaError_t launch_bwd_main_varlen(const BwdArgs& a, cudaStream_t stream) {
+  if (a.d == 128)
+    return a.bf16 ? launch_main_t<128, true, false, false, false, false, true>(a, stream)
+                  : launch_main_t<128, false, false, false, false, false, true>(a, stream);
+  return a.bf16 ? launch_main_t<64, true, false, false, false, false, true>(a, stream)
+                : launch_main_t<64, false, false, false, false, false, true>(a, stream);
+}
 
 int bwd_q_rows(int d) { return d == 128 ? BwdLayout<128>::BQ : BwdLayout<64>::BQ; }
 int bwd_smem_bytes(int d) { return d == 128 ? BwdLayout<128>::kSmem : BwdLayout<64>::kSmem; }

@@ -89,6 +89,49 @@ struct FwdLayout {
   static constexpr int kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
 };
 
+// A sequence of a packed batch: first rows and lengths of its queries and keys.
+struct VarSeq {
+  int q0, lq, k0, lk;
+};
+
+// The sequence that holds work unit `unit` when a sequence of lq queries has
+// ceil(lq / tile_rows) of them; `unit` becomes its index there.  Every warp
+// searches by itself, 32 sequences at a time (no shared memory, no barrier).
+// Offsets are clamped to the tensors, so that wrong ones read and write
+// nothing outside them.
+__device__ __forceinline__ bool var_find(const FwdArgs& p, int& unit, int tile_rows, VarSeq& vs) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int q0 = 0, lq = 0;
+    if (b < p.B) {
+      q0 = min(max(p.cu_q[b], 0), p.N);
+      lq = min(max(p.cu_q[b + 1], q0), p.N) - q0;
+    }
+    const int n = (lq + tile_rows - 1) / tile_rows;
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += a;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, unit < carry + inc);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int bs = b0 + src;
+      unit -= carry + __shfl_sync(0xffffffffu, inc - n, src);
+      vs.q0 = __shfl_sync(0xffffffffu, q0, src);
+      vs.lq = __shfl_sync(0xffffffffu, lq, src);
+      vs.k0 = min(max(p.cu_k[bs], 0), p.Nk);
+      vs.lk = min(max(p.cu_k[bs + 1], vs.k0), p.Nk) - vs.k0;
+      return true;
+    }
+    carry += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return false;
+}
+
 // ALIBI: add the linear bias -m_h |i - j| (m_h = p.alibi[h]) to the scaled
 // scores, the ALiBi of page "FlashAttention技术解析：如何让GPT训练速度提升5-9倍",
 // section 4.1.
@@ -111,10 +154,25 @@ struct FwdLayout {
 // O is a softmax-weighted mean over its own keys (the block recurrence of
 // page "突破单卡显存极限", section 2.1, applied to whole key ranges).  On the
 // last partial the merged O is written as 16-bit to p.o.
-template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false>
+//
+// VARLEN (with none of the above): packed sequences of different lengths, with
+// Hq / Hkv query heads to a key head (p.cu_q, p.cu_k; VarSeq below).  Query and
+// key tiles are counted from the END of their sequence, so that the ragged tile
+// is the first one and the causal diagonal, aligned at the ends, always runs
+// through tile corners whatever the two lengths are.  The ragged tile's rows
+// before the sequence would be its neighbour's: the tensor maps have the row
+// stride twice, as a 128-row window (r) and as its place (s), and a tile that
+// begins at row -m of its sequence is loaded at (r = -m, s = first row), where
+// TMA fills the m rows with zeros.  So nothing of another sequence, not even an
+// infinity times a zero, enters a product.  The two query tiles of a CTA are
+// the same rows of two heads of one group where the group is even (they share
+// every K/V tile, and a short prompt fills both), else neighbouring rows of
+// one head.
+template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false, bool VARLEN = false>
 __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ FwdArgs p) {
   static_assert(!ACC || !(ALIBI || SPARSE || DROPOUT), "the accumulating variant is plain only");
+  static_assert(!VARLEN || !(ALIBI || SPARSE || DROPOUT || ACC), "the packed variant is plain only");
   constexpr int kWarpProducer = FwdRoles<DROPOUT>::kProducer;
   constexpr int kWarpMma = FwdRoles<DROPOUT>::kMma;
   constexpr int kWarpWaiter = FwdRoles<DROPOUT>::kWaiter;
@@ -135,8 +193,30 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
   const int b = bh / p.H, h = bh % p.H;
   const int q0 = pair * 256;
   const int n_kv_all = (p.N + 127) / 128;
-  const int n0 = p.causal ? min(2 * pair + 1, n_kv_all) : n_kv_all;
-  const int n1 = p.causal ? min(2 * pair + 2, n_kv_all) : n_kv_all;
+  int n0 = p.causal ? min(2 * pair + 1, n_kv_all) : n_kv_all;
+  int n1 = p.causal ? min(2 * pair + 2, n_kv_all) : n_kv_all;
+  // (VARLEN) the sequence, its key tiles, and per query tile its head and the
+  // position of its first row in the sequence (negative: the ragged tile)
+  VarSeq vs{};
+  int v_nk = 0, v_head[2] = {0, 0}, v_row[2] = {0, 0};
+  if constexpr (VARLEN) {
+    const int n_hb = p.head_pairs ? p.H / 2 : p.H;
+    const int hb = blockIdx.x % n_hb;
+    const int tile_rows = p.head_pairs ? 128 : 256;
+    int unit = (int)(blockIdx.x / n_hb);
+    if (!var_find(p, unit, tile_rows, vs)) {  // (the grid is sized for the worst split into sequences)
+      if (threadIdx.x == 0) griddep_launch_dependents();
+      return;
+    }
+    v_nk = (vs.lk + 127) / 128;
+    const int tq0 = p.head_pairs ? unit : 2 * unit + 1, tq1 = p.head_pairs ? unit : 2 * unit;
+    v_head[0] = p.head_pairs ? 2 * hb : hb;
+    v_head[1] = p.head_pairs ? 2 * hb + 1 : hb;
+    v_row[0] = vs.lq - 128 * (tq0 + 1);
+    v_row[1] = vs.lq - 128 * (tq1 + 1);
+    n1 = p.causal ? max(0, v_nk - tq1) : v_nk;
+    n0 = v_row[0] <= -128 ? 0 : (p.causal ? max(0, v_nk - tq0) : v_nk);
+  }
   const WaitCtl wc{p.wait.status, p.wait.limit_ns};
 
   auto bar = [&](int i) -> uint32_t { return base + L::kBar + 8u * i; };
@@ -167,6 +247,24 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
     if constexpr (SPARSE) return ((list_flag[j] >> t) & 1) != 0;
     if constexpr (ALIBI) return t == 1 || alibi_tile(j) < n0;
     return true;
+  };
+
+  // Load s of the 64-column boxes of query tile t, and of the K (V) tile at
+  // position j.
+  auto load_q = [&](int t, int s) {
+    const uint32_t dst = base + L::kQ0 + t * L::kTile + s * L::kSub;
+    if constexpr (VARLEN)
+      tma_load_4d(dst, &p.tm_q, bar(L::kBarQ), s * 64, v_head[t], min(v_row[t], 0), vs.q0 + max(v_row[t], 0));
+    else
+      tma_load_4d(dst, &p.tm_q, bar(L::kBarQ), s * 64, h, q0 + t * 128, b);
+  };
+  auto load_kv = [&](uint32_t dst, const CUtensorMap* m, uint32_t fb, int s, int j) {
+    if constexpr (VARLEN) {
+      const int k0 = vs.lk - 128 * (v_nk - j);
+      tma_load_4d(dst, m, fb, s * 64, v_head[0] / p.G, min(k0, 0), vs.k0 + max(k0, 0));
+    } else {
+      tma_load_4d(dst, m, fb, s * 64, h, kv_tile(j) * 128, b);
+    }
   };
 
   // The producer's lane initialises the barriers and issues the Q tiles and
@@ -236,14 +334,11 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
       tma_prefetch(&p.tm_v);
       mbar_expect_tx(bar(L::kBarQ), 2 * L::kTile);
       for (int t = 0; t < 2; ++t)
-        for (int s = 0; s < L::kNSub; ++s)
-          tma_load_4d(base + L::kQ0 + t * L::kTile + s * L::kSub, &p.tm_q, bar(L::kBarQ),
-                      s * 64, h, q0 + t * 128, b);
+        for (int s = 0; s < L::kNSub; ++s) load_q(t, s);
       for (int i = 0; i < n_early; ++i) {  // every slot starts empty
         mbar_expect_tx(bar(L::kBarKVFull + i), L::kTile);
         for (int s = 0; s < L::kNSub; ++s)
-          tma_load_4d(slot_addr(i) + s * L::kSub, (i & 1) ? &p.tm_v : &p.tm_k,
-                      bar(L::kBarKVFull + i), s * 64, h, kv_tile(i >> 1) * 128, b);
+          load_kv(slot_addr(i) + s * L::kSub, (i & 1) ? &p.tm_v : &p.tm_k, bar(L::kBarKVFull + i), s, i >> 1);
       }
     }
   }
@@ -277,8 +372,7 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
           mbar_expect_tx(bar(L::kBarKVFull + slot), L::kTile);
           const CUtensorMap* m = kind ? &p.tm_v : &p.tm_k;
           for (int s = 0; s < L::kNSub; ++s)
-            tma_load_4d(slot_addr(slot) + s * L::kSub, m, bar(L::kBarKVFull + slot), s * 64, h,
-                        kv_tile(j) * 128, b);
+            load_kv(slot_addr(slot) + s * L::kSub, m, bar(L::kBarKVFull + slot), s, j);
           ++issued;
         }
       }
@@ -640,14 +734,18 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
   } else {
     // ------------------------------------------------------------ softmax
     const int t = warp >> 2, qd = warp & 3;
-    const int row_lo = q0 + t * 128;
+    // (VARLEN: rows count from the sequence's first one; keys too, and row i is
+    // aligned with key i + diag)
+    const int row_lo = VARLEN ? (t ? v_row[1] : v_row[0]) : q0 + t * 128;
     const int row = row_lo + qd * 32 + lane;
+    const int diag = VARLEN ? vs.lk - vs.lq : 0;
     const int n_t = t ? len : cnt0;  // positions this query tile takes
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     const uint32_t tS = tmem + lane_off + (t ? L::kColS1 : L::kColS0);
     const uint32_t tO = tmem + lane_off + (t ? L::kColO1 : L::kColO0);
     const float c = p.scale * kLog2e;
-    const int lim = p.causal ? min(row + 1, p.N) : p.N;  // keys < lim are visible
+    const int lim = VARLEN ? (p.causal ? row + diag + 1 : vs.lk)
+                           : (p.causal ? min(row + 1, p.N) : p.N);  // keys < lim are visible
     const float slope2 = ALIBI ? p.alibi[h] * kLog2e : 0.f;  // ALiBi slope, log2 units
     float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
@@ -683,16 +781,17 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
       tmem_ld32(tS + 96, s + 96);
       tmem_ld_wait();
       reg_fence<128>(s);
-      const int kv0 = kv_tile(j) * 128;
+      const int kv0 = VARLEN ? vs.lk - 128 * (v_nk - j) : kv_tile(j) * 128;
       if ((SPARSE || ALIBI) && !tile_kept(j, t)) {
 #pragma unroll
         for (int i = 0; i < 128; ++i) s[i] = __float_as_uint(-INFINITY);  // block removed
       }
-      const bool need_mask = (kv0 + 128 > p.N) || (p.causal && kv0 + 127 > row_lo);
+      const bool need_mask = VARLEN ? (kv0 < 0 || (p.causal && kv0 + 127 > row_lo + diag))
+                                    : ((kv0 + 128 > p.N) || (p.causal && kv0 + 127 > row_lo));
       if (need_mask) {
 #pragma unroll
         for (int i = 0; i < 128; ++i)
-          if (kv0 + i >= lim) s[i] = __float_as_uint(-INFINITY);
+          if (kv0 + i >= lim || (VARLEN && kv0 + i < 0)) s[i] = __float_as_uint(-INFINITY);
       }
       if constexpr (ALIBI) {
         // s <- s * scale * log2(e) - m |row - key| (log2 units).  On a tile
@@ -800,9 +899,10 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
       // a row that saw no key (possible only under a block-sparse mask) has
       // O = 0 and LSE = -inf
       const float inv_l = l > 0.f ? (DROPOUT ? p.drop.scale : 1.f) / l : 0.f;
-      const bool valid = row < p.N;
-      uint8_t* orow = reinterpret_cast<uint8_t*>(p.o) +
-                      ((((size_t)b * p.N + (valid ? row : 0)) * p.H + h) * D) * 2;
+      const bool valid = VARLEN ? row >= 0 : row < p.N;
+      const int hq = VARLEN ? (t ? v_head[1] : v_head[0]) : h;
+      const size_t o_row = VARLEN ? (size_t)vs.q0 + (valid ? row : 0) : (size_t)b * p.N + (valid ? row : 0);
+      uint8_t* orow = reinterpret_cast<uint8_t*>(p.o) + ((o_row * p.H + hq) * D) * 2;
       if constexpr (ACC) {
         // Merge with the accumulated (O, LSE) of earlier calls, in log2 units.
         const bool first = (p.acc_flags & kAccFirst) != 0, last = (p.acc_flags & kAccLast) != 0;
@@ -853,6 +953,31 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
           }
         }
         if (valid) p.lse[lrow] = lse_out;
+      } else if (VARLEN && row_lo < 0) {
+        // The ragged tile: rows before the sequence belong to its neighbour, so
+        // every thread stores its own row.
+#pragma unroll 1
+        for (int cc = 0; cc < D; cc += 32) {
+          uint32_t o[32];
+          if (n_t > 0) {
+            tmem_ld32(tO + cc, o);
+            tmem_ld_wait();
+            reg_fence<32>(o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            w[i] = pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
+          if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(orow + cc * 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        }
+        if (valid) p.lse[(size_t)hq * p.N + o_row] = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
       } else {
       // O/l rounded to 16-bit into this tile's Q buffer (no S of the tile
       // reads Q any more: its last S completed before its last P), laid out
@@ -882,16 +1007,23 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
                             pack2<BF16>(__uint_as_float(o[8 * i + 6]) * inv_l, __uint_as_float(o[8 * i + 7]) * inv_l));
         }
       }
-      if (valid) p.lse[(size_t)bh * p.N + row] = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
+      if (valid)
+        p.lse[VARLEN ? (size_t)hq * p.N + o_row : (size_t)bh * p.N + row] =
+            l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
       fence_proxy_async_smem();
       }
     }
     if constexpr (!ACC) {
       // The tile's four warps meet (agreeing on whether all of them got
       // here without giving up), then one thread stores the staged O.
-      if (named_bar_and(kTileBar0 + t, 128, ok) && qd == 0 && lane == 0) {
-        for (int bx = 0; bx < L::kNSub; ++bx)
-          tma_store_4d(&p.tm_o, base + L::kQ0 + t * L::kTile + bx * L::kSub, bx * 64, h, row_lo, b);
+      if (named_bar_and(kTileBar0 + t, 128, ok) && qd == 0 && lane == 0 && !(VARLEN && row_lo < 0)) {
+        for (int bx = 0; bx < L::kNSub; ++bx) {
+          const uint32_t src = base + L::kQ0 + t * L::kTile + bx * L::kSub;
+          if constexpr (VARLEN)
+            tma_store_4d(&p.tm_o, src, bx * 64, t ? v_head[1] : v_head[0], 0, vs.q0 + row_lo);
+          else
+            tma_store_4d(&p.tm_o, src, bx * 64, h, row_lo, b);
+        }
         bulk_commit();
         bulk_wait_all();  // shared memory stays until the store has read it
       }
@@ -907,18 +1039,28 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
   }
 }
 
-template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false>
+template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false, bool VARLEN = false>
 cudaError_t launch_fwd_t(const FwdArgs& a, cudaStream_t stream) {
   using L = FwdLayout<D>;
-  auto* k = attn_fwd_kernel<D, BF16, ALIBI, SPARSE, DROPOUT, ACC>;
+  auto* k = attn_fwd_kernel<D, BF16, ALIBI, SPARSE, DROPOUT, ACC, VARLEN>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)(((a.N + 255) / 256) * a.B * a.H);
+  const unsigned grid = VARLEN ? (unsigned)fwd_varlen_grid(a.N, a.B, a.H, a.head_pairs)
+                               : (unsigned)(((a.N + 255) / 256) * a.B * a.H);
   e = launch_pdl(k, grid, FwdRoles<DROPOUT>::kThreads, L::kSmem, stream, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
+
+// Blocks for N packed queries in B sequences, whatever the lengths: a sequence
+// has at most one ragged tile, and no tile is empty.
+long long fwd_varlen_grid(long long N, int B, int H, int head_pairs) {
+  const long long rows = head_pairs ? 128 : 256;
+  long long units = N / rows + B;
+  if (units > N) units = N;
+  return units * (head_pairs ? H / 2 : H);
+}
 
 int fwd_smem_bytes(int d) {
   return d == 128 ? FwdLayout<128>::kSmem : FwdLayout<64>::kSmem;
@@ -942,6 +1084,14 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t stream) {
   return a.drop.t < 256 ? launch_fwd_d<true>(a, stream) : launch_fwd_d<false>(a, stream);
+}
+
+cudaError_t launch_fwd_varlen(const FwdArgs& a, cudaStream_t stream) {
+  if (a.d == 128)
+    return a.bf16 ? launch_fwd_t<128, true, false, false, false, false, true>(a, stream)
+                  : launch_fwd_t<128, false, false, false, false, false, true>(a, stream);
+  return a.bf16 ? launch_fwd_t<64, true, false, false, false, false, true>(a, stream)
+                : launch_fwd_t<64, false, false, false, false, false, true>(a, stream);
 }
 
 cudaError_t launch_fwd_acc(const FwdArgs& a, cudaStream_t stream) {

@@ -11,8 +11,7 @@ namespace attn {
 // Kernel ids used by the per-kernel timing of attn_profile_*.
 enum KernelId {
   kKFwd = 0, kKBwdPre = 1, kKBwdMain = 2, kKDqPost = 3, kKDecSplit = 4, kKDecMerge = 5,
-  kKPagesExtend = 6, kKPagesRelease = 7, kKKv8Append = 8, kKKv8Split = 9, kKKv8Merge = 10, kKVarPlan = 11,
-  kKNum = 12
+  kKPagesExtend = 6, kKPagesRelease = 7, kKKv8Append = 8, kKKv8Split = 9, kKKv8Merge = 10, kKNum = 11
 };
 
 struct WaitCtlHost {
@@ -63,9 +62,17 @@ struct FwdArgs {
   int bf16;
   int debug_flags;
   WaitCtlHost wait;
+  // Packed variant (attn_varlen_fwd): B sequences of N queries and Nk keys in
+  // all, H query heads, G to a key head; the maps are (d, head, row, place).
+  const int* cu_q;
+  const int* cu_k;
+  int Nk, G;
+  int head_pairs;  // the two query tiles of a CTA are two heads (G even)
 };
 int fwd_smem_bytes(int d);
+long long fwd_varlen_grid(long long N, int B, int H, int head_pairs);
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t stream);
+cudaError_t launch_fwd_varlen(const FwdArgs& a, cudaStream_t stream);
 
 // Largest N / 128 the block-sparse variants take.
 constexpr int kMaxSparseTiles = 512;
@@ -73,6 +80,14 @@ constexpr int kMaxSparseTiles = 512;
 // Backward.  Workspace regions (fp32): lse2 [BH][Npad] (-LSE * log2 e),
 // dvec [BH][Npad] (D = rowsum(dO * O)), dqacc [BH][Npad][d], Npad = N
 // rounded up to 128; then 256 bytes holding the main kernel's work counter.
+// One sequence of a packed batch, as the backward keeps it in the workspace.
+struct VarBwdSeq {
+  int q0, lq, k0, lk;  // first rows and lengths
+  int pbase;           // padded row of query 0 (a multiple of 64 rows before its last step's end)
+  int pad[3];
+};
+constexpr int kVarMaxB = 8192;
+
 struct BwdArgs {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;  // q/do boxes of bwd_q_rows(d) rows, k/v 128 rows
   CUtensorMap tm_dk, tm_dv;             // stores of dK, dV: boxes of 64 columns x 128 rows
@@ -103,7 +118,17 @@ struct BwdArgs {
   int debug_flags;  // bit 1: the main kernel loads K and V but no query steps (timeout tests);
                    // bit 3: 64-bit row splits in the pre / post kernels
   WaitCtlHost wait;
+  // Packed variant (attn_varlen_bwd): B sequences, N queries and Nk keys in
+  // all, H query heads, G to each of Hkv key heads; Npad padded rows a head.
+  const int* cu_q;
+  const int* cu_k;
+  int Nk, G, Hkv;
+  VarBwdSeq* var_seq;  // [B]
+  int* var_items;      // [B + 1] items before each sequence
 };
+cudaError_t launch_var_pre(const BwdArgs& a, cudaStream_t stream);
+cudaError_t launch_var_post(const BwdArgs& a, cudaStream_t stream);
+cudaError_t launch_bwd_main_varlen(const BwdArgs& a, cudaStream_t stream);
 int bwd_q_rows(int d);
 int bwd_smem_bytes(int d);
 cudaError_t launch_bwd_pre(const BwdArgs& a, cudaStream_t stream);

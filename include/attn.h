@@ -336,6 +336,45 @@ int attn_decode(const void* q, const void* k, const void* v, void* o, float* lse
                 void* stream);
 
 /*
+ * Packed batches: B sequences of different lengths laid one after the other
+ * without padding, and grouped heads.
+ *   q, o, dO, dq   : [Tq, Hq, d];  k, v, dk, dv : [Tk, Hkv, d];  Hq a multiple
+ *                    of Hkv (query head h reads key head h / (Hq / Hkv))
+ *   cu_q, cu_k     : device int32 [B + 1], ascending: sequence b has query rows
+ *                    cu_q[b] .. cu_q[b + 1] - 1 and key rows cu_k[b] .. ; either
+ *                    may be empty.  cu_k may be cu_q
+ *   lse            : fp32 [Hq, Tq]
+ *   q_stride, k_stride, v_stride : elements from one token to the next (multiples
+ *                    of d, at least heads * d; heads lie d apart), so that q, k
+ *                    and v may be slices of one projection.  o, dO, dq, dk, dv are
+ *                    contiguous
+ * With lq queries and lk keys in a sequence, query i sees all keys of its
+ * sequence, or with `causal` the keys j <= lk - lq + i: the queries are the last
+ * lq positions (lk > lq: a prompt that goes on after cached keys).  A query that
+ * sees no key gets O = 0, LSE = -inf, dQ = 0; a key that no query sees gets
+ * dK = dV = 0.  Rows of no sequence (before cu[0], behind cu[B]) are neither read
+ * nor written.  dK and dV of a key head sum over its group in a fixed order;
+ * dQ as in attn_bwd.  o and lse are the forward's.  Offsets are clamped to the
+ * tensors; if they do not ascend, outputs are unspecified.
+ * 1 <= B <= 8192, 0 <= Tq, Tk < 2^26, Hq / Hkv <= 1024.
+ * The pages name batches of sequences only as [B, N, H, d]; the packed layout
+ * and the grouped heads are an addition of this library.
+ */
+int attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
+                    const int32_t* cu_q, const int32_t* cu_k, int B, long long Tq,
+                    long long Tk, int Hq, int Hkv, int d, long long q_stride,
+                    long long k_stride, long long v_stride, float scale, int causal,
+                    attn_dtype_t dtype, void* stream);
+size_t attn_varlen_bwd_workspace_size(int B, long long Tq, int Hq, int d);
+int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o,
+                    const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                    const int32_t* cu_q, const int32_t* cu_k, int B, long long Tq,
+                    long long Tk, int Hq, int Hkv, int d, long long q_stride,
+                    long long k_stride, long long v_stride, float scale, int causal,
+                    attn_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/*
  * A paged key/value cache in 8 bits, for requests of different lengths.
  *
  * The cache of one layer is k_cache, v_cache : [P, H, page, d] e4m3 codes (one
@@ -472,7 +511,7 @@ int attn_set_wait_limit(unsigned long long limit_ns, int debug_flags);
  * synchronises those events and fills, for kernel ids 0..n-1
  * (0 forward, 1 backward preprocess, 2 backward main, 3 dQ conversion,
  * 4 decode chunks, 5 decode merge, 6 pages extend, 7 pages release, 8 8-bit
- * append, 9 8-bit decode, 10 its merge, 11 packed-batch plan),
+ * append, 9 8-bit decode, 10 its merge),
  * the number of launches and their summed device time in milliseconds.
  * Returns the number of kernel ids filled, or a negative ATTN_ERR_* code.
  */
