@@ -18,7 +18,7 @@
 //   q 2^-e = q1 + q2 / 16 [+ q3 / 256],   p = p1 + p2 / 16 [+ p3 / 256],
 // each term the rounding of what the ones before it leave: four significant
 // bits a term.  Two terms hold a bf16 q exactly (8 bits) and p to 2^-9 of its
-// binade; three hold an fp16 q exactly (11 bits) and p to 2^-13.  (Elements
+// value; three hold an fp16 q exactly (11 bits) and p to 2^-14.  (Elements
 // below 2^-13 of their row's largest lose bits, none more than 2^-21 of that
 // largest.)  The terms are rows of one operand, so they cost columns of an
 // MMA that is nearly empty anyway:
@@ -218,6 +218,8 @@ struct Kv8Layout {
   static_assert(kBar % 8 == 0 && kStart % 8 == 0 && kScan % 8 == 0, "alignment");
 };
 
+// The tiles are dealt to min(grid, units) CTAs, so that none of those has an
+// empty range (the merge kernel reads a part from each CTA of a segment).
 __host__ __device__ inline long long range_start(long long c, long long units, long long grid) { return c * units / grid; }
 // The CTA whose range holds unit u.
 __device__ __forceinline__ long long range_owner(long long u, long long units, long long grid) {
@@ -292,7 +294,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
       total += wsum[w];
     }
     const long long units = total * Hr;
-    const long long u0 = range_start(blockIdx.x, units, p.grid), u1 = range_start(blockIdx.x + 1ll, units, p.grid);
+    const long long n_cta = min((long long)p.grid, units);
+    const bool has = blockIdx.x < n_cta;
+    const long long u0 = has ? range_start(blockIdx.x, units, n_cta) : 0;
+    const long long u1 = has ? range_start(blockIdx.x + 1ll, units, n_cta) : 0;
     long long* st = reinterpret_cast<long long*>(sbase + L::kStart);
     if (threadIdx.x == 0) {
       st[0] = u0;
@@ -765,10 +770,11 @@ __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_consta
   const int nt = (kv8_len(p, b) + 127) >> 7;
   const int R = p.Nq * p.G, rows = min(p.rp, R - rb * p.rp);
   const long long units = total * Hr, u0 = before * Hr + (long long)hr * nt;
-  const int c0 = nt ? (int)range_owner(u0, units, p.grid) : 0;
-  const int c1 = nt ? (int)range_owner(u0 + nt - 1, units, p.grid) : 0;
+  const long long n_cta = min((long long)p.grid, units);
+  const int c0 = nt ? (int)range_owner(u0, units, n_cta) : 0;
+  const int c1 = nt ? (int)range_owner(u0 + nt - 1, units, n_cta) : 0;
   if (nt == 0 || c0 != c1) {
-    const int s0 = nt && range_start(c0, units, p.grid) < u0 ? 1 : 0;  // slot of the first part (later ones: 0)
+    const int s0 = nt && range_start(c0, units, n_cta) < u0 ? 1 : 0;  // slot of the first part (later ones: 0)
     constexpr int kPer = D / 32;
     for (int r = warp; r < rows; r += 4) {
       const int idx = rb * p.rp + r, i = idx / p.G, hq = h * p.G + idx % p.G;

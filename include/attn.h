@@ -438,7 +438,7 @@ int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o,
  * and entries of block_table behind its last page are not used; a page id
  * outside [0, P) reads as zeros.  Query and key products carry fp16 / bf16
  * queries exactly up to 2^-21 of a row's largest element; probabilities are
- * rounded to 2^-13 (fp16) or 2^-9 (bf16) of their value.
+ * rounded to 2^-14 (fp16) or 2^-9 (bf16) of their value.
  * workspace: as attn_decode's, size from attn_kv8_decode_workspace_size.
  */
 int attn_pages_extend(const int32_t* lens, const int32_t* add, int B, int32_t* block_table,

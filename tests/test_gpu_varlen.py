@@ -1,0 +1,265 @@
+"""Packed sequences (attn_varlen_fwd, attn_varlen_bwd) against attention written
+out in 64 bits, element by element within derived bounds (plain64.py): lengths
+around the tile sizes, empty sequences, queries without keys and keys without
+queries, grouped heads, strided inputs, neighbours full of NaN."""
+import math
+
+import pytest
+import torch
+
+import plain64
+from plain64 import DT
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from exact_tiled_attention_22_gb300 import build
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    from exact_tiled_attention_22_gb300 import attn
+    attn.attn_set_wait_limit(0, 0)
+    yield
+    assert attn.attn_status() == 0
+
+
+def cu(lens):
+    return [0] + torch.tensor(lens).cumsum(0).tolist()
+
+
+def draw(lens_q, lens_k, Hq, H, d, dtype, seed, extra=0):
+    g = torch.Generator().manual_seed(seed)
+    Tq, Tk = sum(lens_q) + extra, sum(lens_k) + extra
+    mk = lambda t, h: torch.randn((t, h, d), generator=g).to(DT[dtype])  # noqa: E731
+    return mk(Tq, Hq), mk(Tk, H), mk(Tk, H), mk(Tq, Hq)
+
+
+def dev(x):
+    return x.cuda()
+
+
+def offsets(lens):
+    return torch.tensor(cu(lens), dtype=torch.int32).cuda()
+
+
+CASES = [
+    # (lens_q, lens_k, Hq, Hkv, d, dtype, causal)
+    ([1], [1], 1, 1, 64, "fp16", True),
+    ([1, 1, 1], [1, 5, 129], 2, 1, 128, "bf16", True),
+    ([127, 128, 129], [127, 128, 129], 2, 2, 64, "bf16", True),
+    ([255, 1, 257, 0, 63], [255, 1, 257, 0, 63], 4, 1, 128, "fp16", True),
+    ([300, 0, 5, 64], [300, 17, 0, 200], 3, 1, 64, "fp16", True),
+    ([300, 0, 5, 64], [300, 17, 0, 200], 3, 3, 128, "bf16", False),
+    ([130, 7], [20, 500], 4, 2, 64, "bf16", True),      # more queries than keys; a prefix
+    ([640], [640], 16, 2, 128, "bf16", True),
+    ([513, 70], [1025, 1000], 5, 5, 64, "fp16", True),
+    ([200, 385], [129, 640], 6, 2, 128, "fp16", False),
+    ([65], [300], 7, 1, 64, "bf16", True),
+]
+IDS = [f"{i}-{c[2]}x{c[3]}d{c[4]}{c[5]}{'c' if c[6] else ''}" for i, c in enumerate(CASES)]
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_forward_and_gradients(case):
+    from exact_tiled_attention_22_gb300 import attn
+    lens_q, lens_k, Hq, H, d, dtype, causal = case
+    q, k, v, do = draw(lens_q, lens_k, Hq, H, d, dtype, seed=sum(lens_q))
+    scale = d ** -0.5
+    cq, ck = offsets(lens_q), offsets(lens_k)
+    o, lse = attn.varlen_fwd(dev(q), dev(k), dev(v), cq, ck, scale, causal)
+    grads = attn.varlen_bwd(dev(q), dev(k), dev(v), o, lse, dev(do), cq, ck, scale, causal)
+    attn.check(attn.attn_status())
+    ref = plain64.packed(q.double(), k.double(), v.double(), cu(lens_q), cu(lens_k), scale, causal, dtype, do.double())
+    for name, got in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+        plain64.check(got, *ref[name], name)
+
+
+def test_many_short_sequences():
+    """More sequences than a warp and than a block of the scans, zeros among them."""
+    from exact_tiled_attention_22_gb300 import attn
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 7, (700,), generator=g).tolist()
+    q, k, v, do = draw(lens, lens, 2, 1, 64, "fp16", seed=4)
+    c = offsets(lens)
+    o, lse = attn.varlen_fwd(dev(q), dev(k), dev(v), c, c, 0.125, True)
+    grads = attn.varlen_bwd(dev(q), dev(k), dev(v), o, lse, dev(do), c, c, 0.125, True)
+    ref = plain64.packed(q.double(), k.double(), v.double(), cu(lens), cu(lens), 0.125, True, "fp16", do.double())
+    for name, got in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+        plain64.check(got, *ref[name], name)
+
+
+@pytest.mark.parametrize("d,group", [(64, 2), (128, 3)])
+def test_neighbours_and_padding_do_not_leak(d, group):
+    """Sequences between others full of NaN and infinities, rows behind the last
+    sequence left as they were."""
+    from exact_tiled_attention_22_gb300 import attn
+    lens = [70, 129, 200, 33]
+    extra = 50
+    q, k, v, do = draw(lens, lens, group, 1, d, "bf16", seed=11, extra=extra)
+    c = cu(lens)
+    for i, bad in ((0, math.nan), (2, math.inf)):
+        for x in (q, k, v, do):
+            x[c[i]:c[i + 1]] = bad
+    for x in (q, k, v, do):
+        x[c[-1]:] = math.nan
+    cg = offsets(lens)
+    marks = [torch.full(x.shape, 7.0, dtype=q.dtype, device="cuda") for x in (q, q, k, v)]
+    o, lse = attn.varlen_fwd(dev(q), dev(k), dev(v), cg, cg, d ** -0.5, True, o=marks[0])
+    # (lse comes from an uninitialised buffer: rows of no sequence are not read)
+    grads = attn.varlen_bwd(dev(q), dev(k), dev(v), o, lse, dev(do), cg, cg, d ** -0.5, True, grads=marks[1:])
+    attn.check(attn.attn_status())
+    for x in (o, *grads):
+        assert (x[c[-1]:] == 7.0).all()
+    zero = lambda x: torch.nan_to_num(x.double(), 0.0, 0.0, 0.0)  # noqa: E731
+    ref = plain64.packed(zero(q), zero(k), zero(v), c, c, d ** -0.5, True, "bf16", zero(do))
+    for name, got in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+        for i in (1, 3):
+            s = slice(c[i], c[i + 1])
+            val, bound = ref[name]
+            if name == "lse":
+                plain64.check(got[:, s], val[:, s], bound[:, s], f"{name} of sequence {i}")
+            else:
+                plain64.check(got[s], val[s], bound[s], f"{name} of sequence {i}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_slices_of_one_projection(d):
+    """q, k, v as slices of one [T, Hq + 2 Hkv, d] tensor: bit-equal to copies."""
+    from exact_tiled_attention_22_gb300 import attn
+    lens = [100, 300, 1]
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn((sum(lens), 6 + 4, d), generator=g).half().cuda()
+    q, k, v = x[:, :6], x[:, 6:8], x[:, 8:]
+    do = torch.randn((sum(lens), 6, d), generator=g).half().cuda()
+    c = offsets(lens)
+    o, lse = attn.varlen_fwd(q, k, v, c, c, None, True)
+    o2, lse2 = attn.varlen_fwd(q.contiguous(), k.contiguous(), v.contiguous(), c, c, None, True)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    _, dk, dv = attn.varlen_bwd(q, k, v, o, lse, do, c, c, None, True)
+    _, dk2, dv2 = attn.varlen_bwd(q.contiguous(), k.contiguous(), v.contiguous(), o, lse, do, c, c, None, True)
+    assert torch.equal(dk, dk2) and torch.equal(dv, dv2)
+
+
+def test_equals_the_batched_forward():
+    """Sequences of one length are the [B, N, H, d] call's batch (both within
+    their own rounding)."""
+    from exact_tiled_attention_22_gb300 import attn
+    B, N, H, d = 3, 384, 4, 128
+    g = torch.Generator().manual_seed(6)
+    q, k, v = (torch.randn((B, N, H, d), generator=g).bfloat16().cuda() for _ in range(3))
+    o, lse = attn.fwd(q, k, v, None, True)
+    c = offsets([N] * B)
+    o2, lse2 = attn.varlen_fwd(q.view(-1, H, d), k.view(-1, H, d), v.view(-1, H, d), c, c, None, True)
+    assert (lse2.view(H, B, N).transpose(0, 1) - lse).abs().max() <= 2.0 ** -16 * (1 + lse.abs().max())
+    top = v.float().abs().max()
+    assert (o2.view(B, N, H, d).float() - o.float()).abs().max() <= 2 * 2 * 2.0 ** -8 * top
+
+
+def test_autograd_and_differences():
+    """attention_varlen's gradients against directional differences of the
+    64-bit formula, and zeros for rows of no sequence."""
+    from exact_tiled_attention_22_gb300 import attn
+    lens_q, lens_k, Hq, H, d = [60, 131], [75, 131], 4, 2, 64
+    q, k, v, w = draw(lens_q, lens_k, Hq, H, d, "fp16", seed=21, extra=9)
+    cq, ck = cu(lens_q), cu(lens_k)
+    scale = 0.125
+    a = [dev(x).requires_grad_() for x in (q, k, v)]
+    o = attn.attention_varlen(*a, offsets(lens_q), offsets(lens_k), scale, True)
+    o.backward(dev(w))
+    for x, n in zip(a, (cq[-1], ck[-1], ck[-1])):
+        assert (x.grad[n:] == 0).all()
+    assert (o[cq[-1]:] == 0).all()
+
+    def loss(q, k, v):
+        r = plain64.packed(q, k, v, cq, ck, scale, True, "fp16")["o"][0]
+        return (r[:cq[-1]] * w.double()[:cq[-1]]).sum().item()
+
+    ref = plain64.packed(q.double(), k.double(), v.double(), cq, ck, scale, True, "fp16", w.double())
+    g = torch.Generator().manual_seed(8)
+    for i, name in enumerate(("dq", "dk", "dv")):
+        base = [x.double() for x in (q, k, v)]
+        step = torch.randn(base[i].shape, generator=g, dtype=torch.float64)
+        step[(cq if i == 0 else ck)[-1]:] = 0
+        h = 1e-4
+        lo, hi = list(base), list(base)
+        lo[i], hi[i] = base[i] - h * step, base[i] + h * step
+        slope = (loss(*hi) - loss(*lo)) / (2 * h)
+        got = (a[i].grad.double().cpu() * step).sum().item()
+        # the gradient's own bound along the step, and the difference's h^2 term
+        tol = (torch.nan_to_num(ref[name][1]) * step.abs()).sum().item() + 1e-3
+        assert abs(got - slope) <= tol, (name, got, slope, tol)
+
+
+def test_captured_and_on_another_stream():
+    """Forward and backward captured into a graph on a side stream, replayed on
+    other values AND other lengths (both live on the device)."""
+    from exact_tiled_attention_22_gb300 import attn
+    T, Hq, H, d = 500, 4, 2, 64
+    lens = [[100, 150, 250], [3, 497, 0]]
+    xs = [draw(l, l, Hq, H, d, "bf16", seed=30 + i) for i, l in enumerate(lens)]
+    q, k, v, do = (x.cuda() for x in xs[0])
+    c = offsets(lens[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ws = torch.empty(attn.attn_varlen_bwd_workspace_size(3, T, Hq, d), dtype=torch.uint8, device="cuda")
+
+    def step():
+        o, lse = attn.varlen_fwd(q, k, v, c, c, 0.125, True)
+        return (o, lse, *attn.varlen_bwd(q, k, v, o, lse, do, c, c, 0.125, True, ws=ws))
+
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = step()
+    for i in (1, 0):
+        for t, x in zip((q, k, v, do), xs[i]):
+            t.copy_(x.cuda())
+        c.copy_(offsets(lens[i]))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = plain64.packed(*(x.double() for x in xs[i][:3]), cu(lens[i]), cu(lens[i]), 0.125, True, "bf16",
+                             xs[i][3].double())
+        for name, got in zip(("o", "lse", "dq", "dk", "dv"), out):
+            plain64.check(got, *ref[name], name)
+    assert attn.attn_status() == 0
+
+
+def test_repeats_are_equal():
+    """O, LSE, dK, dV do not depend on the order in which blocks finish."""
+    from exact_tiled_attention_22_gb300 import attn
+    lens = [900, 40, 333]
+    q, k, v, do = (x.cuda() for x in draw(lens, lens, 8, 2, 128, "bf16", seed=40))
+    c = offsets(lens)
+    first = None
+    for _ in range(3):
+        o, lse = attn.varlen_fwd(q, k, v, c, c, None, True)
+        _, dk, dv = attn.varlen_bwd(q, k, v, o, lse, do, c, c, None, True)
+        now = (o, lse, dk, dv)
+        assert first is None or all(torch.equal(a, b) for a, b in zip(first, now))
+        first = now
+
+
+def test_wait_limit_reports_a_timeout():
+    """A load warp that holds back its copies: the waits run out, the call
+    returns, attn_status says so, and the next call is right again."""
+    from exact_tiled_attention_22_gb300 import attn
+    lens = [200]
+    q, k, v, do = (x.cuda() for x in draw(lens, lens, 2, 1, 64, "fp16", seed=50))
+    c = offsets(lens)
+    o, lse = attn.varlen_fwd(q, k, v, c, c, None, True)
+    attn.check(attn.attn_status())
+    try:
+        attn.attn_set_wait_limit(50_000_000, 1)
+        attn.varlen_fwd(q, k, v, c, c, None, True)
+        assert attn.attn_status() == attn.ATTN_ERR_TIMEOUT
+        attn.attn_set_wait_limit(50_000_000, 2)
+        attn.varlen_bwd(q, k, v, o, lse, do, c, c, None, True)
+        assert attn.attn_status() == attn.ATTN_ERR_TIMEOUT
+    finally:
+        attn.attn_set_wait_limit(0, 0)
+    o2, lse2 = attn.varlen_fwd(q, k, v, c, c, None, True)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
