@@ -9,6 +9,7 @@ implementation to fall back to.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -126,8 +127,15 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
+# The current stream's handle without building a torch.cuda.Stream (0.1 against
+# 3.8 us on the GPU's Grace host, a third of a small call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, int):
         return stream
@@ -430,40 +438,30 @@ def decode(q, k, v, scale=None, causal=False, ws=None, stream=None, alibi=None):
 
 
 # ---- paged key/value cache in 8 bits --------------------------------------
-def _want(t, name, dtypes, shape):
-    """Checks a contiguous CUDA tensor's type and shape (None: any extent)."""
-    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
-    if (t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous() or t.dim() != len(shape)
-            or any(w is not None and n != w for n, w in zip(t.shape, shape))):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} of "
-                         f"{' or '.join(str(x) for x in dtypes)}, got {list(t.shape)} {t.dtype}")
+# A decoding step's calls are short (the kernels take a few microseconds, the
+# host's part several times that), so these wrappers look at each tensor once,
+# with the cheapest tests there are, and make few torch calls: on the GPU's Grace
+# host each allocation or view costs 2-4 us among others, each test 0.1.
+def _want(t, name, dtype, shape, index):
+    """t is a contiguous tensor of this type and shape on CUDA device `index`."""
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != index or index < 0
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on one CUDA "
+                         f"device with the others, got {list(t.shape)} {t.dtype} on {t.device}")
 
 
-def _one_device(first, *rest):
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors are on different devices ({first.device}, {t.device})")
-    return first.device
-
-
-class _on:
-    """The tensors' device as the current one (the library acts on it)."""
-
-    def __init__(self, device):
-        self.dev, self.prev = device.index, None
-
-    def __enter__(self):
-        prev = torch.cuda.current_device()
-        if prev != self.dev:
-            torch.cuda.set_device(self.dev)
-            self.prev = prev
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
-
-
-_CODES = (torch.float8_e4m3fn, torch.uint8)
+def _run(index, stream, fn, *args):
+    """fn(*args, stream) with CUDA device `index` current (the library acts on the
+    current device; a None stream is that device's current one)."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _run(index, stream, fn, *args)
+    if stream is None and _raw_stream is not None:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        rc = fn(*args, _stream(stream))
+    if rc:
+        check(rc)
 
 
 def pages_extend(lens, add, block_table, free_pages, free_count, page, max_new, new_lens=None,
@@ -473,26 +471,27 @@ def pages_extend(lens, add, block_table, free_pages, free_count, page, max_new, 
     free_pages: int32 [cap], a stack of free page ids, free_count: int32 [1];
     max_new: length of the slot map.  new_lens may be lens and free_left may
     be free_count.  Returns (new_lens, granted, cu_new, slots, free_left)."""
-    B = lens.shape[0]
-    _want(lens, "lens", torch.int32, (None,))
-    _want(add, "add", torch.int32, (B,))
-    _want(block_table, "block_table", torch.int32, (B, None))
-    _want(free_pages, "free_pages", torch.int32, (None,))
-    _want(free_count, "free_count", torch.int32, (1,))
+    (B, width), (cap,) = block_table.shape, free_pages.shape
+    i32, dev = torch.int32, lens.get_device()
+    _want(lens, "lens", i32, (B,), dev)
+    _want(add, "add", i32, (B,), dev)
+    _want(block_table, "block_table", i32, (B, width), dev)
+    _want(free_pages, "free_pages", i32, (cap,), dev)
+    _want(free_count, "free_count", i32, (1,), dev)
     if new_lens is not None:
-        _want(new_lens, "new_lens", torch.int32, (B,))
+        _want(new_lens, "new_lens", i32, (B,), dev)
     if free_left is not None:
-        _want(free_left, "free_left", torch.int32, (1,))
-    dev = _one_device(lens, add, block_table, free_pages, free_count, new_lens, free_left)
-    new_lens = torch.empty_like(lens) if new_lens is None else new_lens
-    free_left = torch.empty_like(free_count) if free_left is None else free_left
-    granted = torch.empty_like(lens)
-    cu_new = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    slots = torch.empty(max_new, dtype=torch.int64, device=dev)
-    with _on(dev):
-        check(attn_pages_extend(lens, add, B, block_table, block_table.shape[1], free_pages,
-                                free_count, free_pages.shape[0], page, max_new, new_lens, granted,
-                                cu_new, slots, free_left, stream))
+        _want(free_left, "free_left", i32, (1,), dev)
+    # one allocation for the four small outputs (views of it that no gradient sees)
+    new, granted, cu_new, left = torch.empty(3 * B + 2, dtype=i32, device=lens.device) \
+        .unsafe_split_with_sizes((B, B, B + 1, 1))
+    new_lens = new if new_lens is None else new_lens
+    free_left = left if free_left is None else free_left
+    slots = torch.empty(max_new, dtype=torch.int64, device=lens.device)
+    _run(dev, stream, lib.attn_pages_extend, lens.data_ptr(), add.data_ptr(), B,
+         block_table.data_ptr(), width, free_pages.data_ptr(), free_count.data_ptr(), cap, page,
+         max_new, new_lens.data_ptr(), granted.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
+         free_left.data_ptr())
     return new_lens, granted, cu_new, slots, free_left
 
 
@@ -500,95 +499,102 @@ def pages_release(lens, finished, block_table, free_pages, free_count, page, new
                   free_left=None, stream=None):
     """Pages of the requests with finished[b] != 0 (int32 [B]) go back onto the
     stack free_pages, written in place (attn_pages_release).  Returns (new_lens, free_left)."""
-    B = lens.shape[0]
-    _want(lens, "lens", torch.int32, (None,))
-    _want(finished, "finished", torch.int32, (B,))
-    _want(block_table, "block_table", torch.int32, (B, None))
-    _want(free_pages, "free_pages", torch.int32, (None,))
-    _want(free_count, "free_count", torch.int32, (1,))
-    if new_lens is not None:
-        _want(new_lens, "new_lens", torch.int32, (B,))
-    if free_left is not None:
-        _want(free_left, "free_left", torch.int32, (1,))
-    dev = _one_device(lens, finished, block_table, free_pages, free_count, new_lens, free_left)
+    (B, width), (cap,) = block_table.shape, free_pages.shape
+    i32, dev = torch.int32, lens.get_device()
+    _want(lens, "lens", i32, (B,), dev)
+    _want(finished, "finished", i32, (B,), dev)
+    _want(block_table, "block_table", i32, (B, width), dev)
+    _want(free_pages, "free_pages", i32, (cap,), dev)
+    _want(free_count, "free_count", i32, (1,), dev)
     new_lens = torch.empty_like(lens) if new_lens is None else new_lens
     free_left = torch.empty_like(free_count) if free_left is None else free_left
-    with _on(dev):
-        check(attn_pages_release(lens, finished, B, block_table, block_table.shape[1], free_pages,
-                                 free_count, free_pages.shape[0], page, new_lens, free_left,
-                                 stream))
+    _want(new_lens, "new_lens", i32, (B,), dev)
+    _want(free_left, "free_left", i32, (1,), dev)
+    _run(dev, stream, lib.attn_pages_release, lens.data_ptr(), finished.data_ptr(), B,
+         block_table.data_ptr(), width, free_pages.data_ptr(), free_count.data_ptr(), cap, page,
+         new_lens.data_ptr(), free_left.data_ptr())
     return new_lens, free_left
 
 
-def _packed(t, name, dtype=None):
-    """A [T, H, d] CUDA tensor with heads d apart; its token stride."""
-    if t.dim() != 3 or not t.is_cuda or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be a CUDA tensor [T, H, d]" + (f" of {dtype}" if dtype else ""))
-    T, H, d = t.shape
-    if t.numel() and (t.stride(2) != 1 or t.stride(1) != d and H > 1):
+def _packed(t, name, dtype, shape, index):
+    """t is [T, H, d] on CUDA device `index`, heads d apart; its token stride."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} on one CUDA device with "
+                         f"the others, got {list(t.shape)} {t.dtype} on {t.device}")
+    T, H, d = shape
+    if t.is_contiguous():
+        return H * d
+    if t.stride(2) != 1 or t.stride(1) != d and H > 1:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return t.stride(0) if T > 1 else H * d
 
 
-def _cache_shape(k_cache, v_cache, k_scale, v_scale):
-    _want(k_cache, "k_cache", _CODES, (None, None, None, None))
-    P, H, page, d = k_cache.shape
-    _want(v_cache, "v_cache", _CODES, (P, H, page, d))
-    _want(k_scale, "k_scale", torch.float32, (P, H))
-    _want(v_scale, "v_scale", torch.float32, (P, H))
-    return P, H, page, d
+def _cache(k_cache, v_cache, k_scale, v_scale, dev):
+    P, H, page, d = shape = k_cache.shape
+    code = k_cache.dtype
+    if code is not torch.float8_e4m3fn and code is not torch.uint8:
+        raise ValueError(f"the caches hold float8_e4m3fn or uint8 codes, got {code}")
+    _want(k_cache, "k_cache", code, shape, dev)
+    _want(v_cache, "v_cache", code, shape, dev)
+    _want(k_scale, "k_scale", torch.float32, (P, H), dev)
+    _want(v_scale, "v_scale", torch.float32, (P, H), dev)
+    return shape
 
 
 def kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
     """Rounds new keys and values [T, H, d] into their slots (int64 [T]) of the
     8-bit cache [P, H, page, d] with scales [P, H], in place (attn_kv8_append).
     k and v may be slices of a wider projection (any token stride)."""
-    P, H, page, d = _cache_shape(k_cache, v_cache, k_scale, v_scale)
+    dev = k.get_device()
+    P, H, page, d = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     T = k.shape[0]
-    ks, vs = _packed(k, "k"), _packed(v, "v", k.dtype)
-    if tuple(k.shape) != (T, H, d) or tuple(v.shape) != (T, H, d):
-        raise ValueError(f"k and v must be [T, {H}, {d}]")
-    _want(slots, "slots", torch.int64, (T,))
-    dev = _one_device(k, v, slots, k_cache, v_cache, k_scale, v_scale)
-    with _on(dev):
-        check(attn_kv8_append(k, v, ks, vs, slots, T, H, d, k_cache, v_cache, k_scale, v_scale, P,
-                              page, k.dtype, stream))
+    ks, vs = _packed(k, "k", k.dtype, (T, H, d), dev), _packed(v, "v", k.dtype, (T, H, d), dev)
+    _want(slots, "slots", torch.int64, (T,), dev)
+    _run(dev, stream, lib.attn_kv8_append, k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T,
+         H, d, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P,
+         page, dtype_code(k.dtype))
+
+
+@functools.lru_cache(maxsize=256)
+def _kv8_workspace_size(Nq, Hq, H, d):
+    return attn_kv8_decode_workspace_size(Nq, Hq, H, d)
 
 
 def kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=None, causal=True,
                ws=None, stream=None):
     """(o, lse) of q [B, Nq, Hq, d], the last Nq tokens of every request, against
     the 8-bit cache (attn_kv8_decode); lens counts the Nq tokens."""
-    P, H, page, d = _cache_shape(k_cache, v_cache, k_scale, v_scale)
-    B, Nq, Hq, dq = _shape(q)
-    if dq != d:
-        raise ValueError(f"q has d = {dq}, the cache {d}")
-    _want(block_table, "block_table", torch.int32, (B, None))
-    _want(lens, "lens", torch.int32, (B,))
-    dev = _one_device(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, ws)
+    dev = q.get_device()
+    P, H, page, d = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    (B, Nq, Hq, _), (_, width) = q.shape, block_table.shape
+    code = dtype_code(q.dtype)
+    _want(q, "q", q.dtype, (B, Nq, Hq, d), dev)
+    _want(block_table, "block_table", torch.int32, (B, width), dev)
+    _want(lens, "lens", torch.int32, (B,), dev)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     o = torch.empty_like(q)
-    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
     if ws is None:
-        ws = torch.empty(attn_kv8_decode_workspace_size(Nq, Hq, H, d), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        check(attn_kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o, lse, B,
-                              Nq, Hq, H, d, P, page, block_table.shape[1], scale, causal, q.dtype,
-                              ws, ws.numel(), stream))
+        ws = torch.empty(_kv8_workspace_size(Nq, Hq, H, d), dtype=torch.uint8, device=q.device)
+    elif ws.get_device() != dev:
+        raise ValueError(f"ws is on {ws.device}")
+    _run(dev, stream, lib.attn_kv8_decode, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+         k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+         o.data_ptr(), lse.data_ptr(), B, Nq, Hq, H, d, P, page, width, scale, 1 if causal else 0,
+         code, ws.data_ptr(), ws.numel() * ws.element_size())
     return o, lse
 
 
 # ---- packed batches ---------------------------------------------------------
 def _packed_args(q, k, v, cu_q, cu_k):
-    qs, ks, vs = _packed(q, "q"), _packed(k, "k", q.dtype), _packed(v, "v", q.dtype)
-    Tq, Hq, d = q.shape
-    Tk, Hkv, dk = k.shape
-    if dk != d or v.shape != k.shape:
-        raise ValueError(f"k and v must be [Tk, Hkv, {d}], got {list(k.shape)} and {list(v.shape)}")
-    _want(cu_q, "cu_q", torch.int32, (None,))
-    _want(cu_k, "cu_k", torch.int32, (cu_q.shape[0],))
-    dev = _one_device(q, k, v, cu_q, cu_k)
-    return dev, (cu_q.shape[0] - 1, Tq, Tk, Hq, Hkv, d, qs, ks, vs)
+    """The device index and the sizes the calls take from B to the strides."""
+    (Tq, Hq, d), (Tk, Hkv, _), (n,) = sq, _, _ = q.shape, k.shape, cu_q.shape
+    dev, dt, sk = q.get_device(), q.dtype, (Tk, Hkv, d)
+    qs, ks, vs = (_packed(q, "q", dt, sq, dev), _packed(k, "k", dt, sk, dev),
+                  _packed(v, "v", dt, sk, dev))
+    _want(cu_q, "cu_q", torch.int32, (n,), dev)
+    _want(cu_k, "cu_k", torch.int32, (n,), dev)
+    return dev, (n - 1, Tq, Tk, Hq, Hkv, d, qs, ks, vs)
 
 
 def varlen_fwd(q, k, v, cu_q, cu_k, scale=None, causal=False, o=None, stream=None):
@@ -598,15 +604,15 @@ def varlen_fwd(q, k, v, cu_q, cu_k, scale=None, causal=False, o=None, stream=Non
     write into; rows of no sequence are left as they are there."""
     dev, sizes = _packed_args(q, k, v, cu_q, cu_k)
     Tq, Hq, d = q.shape
+    code = dtype_code(q.dtype)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     if o is None:
-        o = torch.empty((Tq, Hq, d), dtype=q.dtype, device=dev)
+        o = torch.empty((Tq, Hq, d), dtype=q.dtype, device=q.device)
     else:
-        _want(o, "o", q.dtype, (Tq, Hq, d))
-        _one_device(q, o)
-    lse = torch.empty((Hq, Tq), dtype=torch.float32, device=dev)
-    with _on(dev):
-        check(attn_varlen_fwd(q, k, v, o, lse, cu_q, cu_k, *sizes, scale, causal, q.dtype, stream))
+        _want(o, "o", q.dtype, (Tq, Hq, d), dev)
+    lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
+    _run(dev, stream, lib.attn_varlen_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+         lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), *sizes, scale, 1 if causal else 0, code)
     return o, lse
 
 
@@ -616,26 +622,29 @@ def varlen_bwd(q, k, v, o, lse, do, cu_q, cu_k, scale=None, causal=False, ws=Non
     contiguous tensors to write into (rows of no sequence are left as they are)."""
     dev, sizes = _packed_args(q, k, v, cu_q, cu_k)
     Tq, Hq, d = q.shape
-    _want(o, "o", q.dtype, (Tq, Hq, d))
-    _want(do, "do", q.dtype, (Tq, Hq, d))
-    _want(lse, "lse", torch.float32, (Hq, Tq))
-    _one_device(q, o, do, lse, ws)
+    dt, sq, sk = q.dtype, (Tq, Hq, d), tuple(k.shape)
+    code = dtype_code(dt)
+    _want(o, "o", dt, sq, dev)
+    _want(do, "do", dt, sq, dev)
+    _want(lse, "lse", torch.float32, (Hq, Tq), dev)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     if grads is None:
-        dq = torch.empty((Tq, Hq, d), dtype=q.dtype, device=dev)
-        dk, dv = (torch.empty(k.shape, dtype=q.dtype, device=dev) for _ in range(2))
+        dq = torch.empty(sq, dtype=dt, device=q.device)
+        dk, dv = (torch.empty(sk, dtype=dt, device=q.device) for _ in range(2))
     else:
         dq, dk, dv = grads
-        _want(dq, "dq", q.dtype, (Tq, Hq, d))
-        _want(dk, "dk", q.dtype, k.shape)
-        _want(dv, "dv", q.dtype, k.shape)
-        _one_device(q, dq, dk, dv)
+        _want(dq, "dq", dt, sq, dev)
+        _want(dk, "dk", dt, sk, dev)
+        _want(dv, "dv", dt, sk, dev)
     if ws is None:
         ws = torch.empty(attn_varlen_bwd_workspace_size(sizes[0], Tq, Hq, d), dtype=torch.uint8,
-                         device=dev)
-    with _on(dev):
-        check(attn_varlen_bwd(q, k, v, o, lse, do, dq, dk, dv, cu_q, cu_k, *sizes, scale, causal,
-                              q.dtype, ws, ws.numel(), stream))
+                         device=q.device)
+    elif ws.get_device() != dev:
+        raise ValueError(f"ws is on {ws.device}")
+    _run(dev, stream, lib.attn_varlen_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+         lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+         cu_q.data_ptr(), cu_k.data_ptr(), *sizes, scale, 1 if causal else 0, code, ws.data_ptr(),
+         ws.numel() * ws.element_size())
     return dq, dk, dv
 
 

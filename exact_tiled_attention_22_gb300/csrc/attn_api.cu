@@ -897,7 +897,7 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   a.bf16 = dtype == ATTN_BF16;
   a.scale = scale;
   const long long tiles = ((long long)width * page + 127) / 128;
-  a.grid = attn::kv8_grid(d, a.rp, a.bf16, dev->sms, tiles * B * H * a.n_rb);
+  a.grid = attn::kv8_grid(a.rp, dev->sms, tiles * B * H * a.n_rb);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.ws_o = reinterpret_cast<float*>(ws);
   a.ws_ml = reinterpret_cast<float*>(ws + ((size_t)attn::kKv8MaxCtas * 2 * a.rp * d * 4 + 255) / 256 * 256);

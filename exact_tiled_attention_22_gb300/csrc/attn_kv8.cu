@@ -188,7 +188,8 @@ template <int D, int RP, int NP>
 struct Kv8Layout {
   static constexpr int N = (RP * NP + 15) / 16 * 16;  // MMA columns (M = 128 needs a multiple of 16)
   static constexpr int kTile = 128 * D;
-  static constexpr int kStages = D == 128 ? 3 : 6;    // two CTAs to an SM
+  static constexpr int kCtas = RP <= 8 ? 3 : 2;       // CTAs to an SM
+  static constexpr int kStages = (D == 128 ? 1 : 2) * (kCtas == 3 ? 2 : 3);
   static constexpr int kQ = 0;
   static constexpr int kP = kQ + up1024(N * D);
   static constexpr int kKV = kP + up1024(N * 128);    // stage s: K at + s * 2 kTile, V behind it
@@ -212,13 +213,22 @@ struct Kv8Layout {
   static constexpr int kScan = kStart + 32;           // [6] warp sums
   static constexpr int kBytes = kScan + 8 * 8;
   static constexpr int kSmem = kBytes + 1024;
-  static constexpr int kCols = 4 * N <= 128 ? 128 : 256;  // S x 2, O (and padding to a power of two)
+  static constexpr int kCols = 4 * N <= 64 ? 64 : (4 * N <= 128 ? 128 : 256);  // S x 2, O x 2, a power of two
   static constexpr int kColS = 0, kColO = 2 * N;
-  static_assert(3 * N <= kCols, "TMEM budget");
+  static_assert(4 * N <= kCols && kCols * kCtas <= 512, "TMEM budget");
+  static_assert((kSmem + 1024) * kCtas <= 228 * 1024, "shared memory budget");
   static_assert(kBar % 8 == 0 && kStart % 8 == 0 && kScan % 8 == 0, "alignment");
 };
 
-// The tiles are dealt to min(grid, units) CTAs, so that none of those has an
+// What a segment (a request's tiles of one head group) costs besides its tiles,
+// in tiles: its query terms, the first S and the last O^T, during which nothing
+// else of the CTA runs.  Units are counted with it, tile t of a segment being
+// unit kSegCost + t, so that a CTA with many short requests gets fewer tiles.
+constexpr int kSegCost = 2;
+
+__device__ __forceinline__ int seg_units(int nt) { return nt > 0 ? nt + kSegCost : 0; }
+
+// The units are dealt to min(grid, units) CTAs, so that none of those has an
 // empty range (the merge kernel reads a part from each CTA of a segment).
 __host__ __device__ inline long long range_start(long long c, long long units, long long grid) { return c * units / grid; }
 // The CTA whose range holds unit u.
@@ -231,14 +241,45 @@ __device__ __forceinline__ int kv8_len(const Kv8DecArgs& p, int b) {
   return (int)min(max((long long)p.lens[b], 0ll), cap);
 }
 
-// Walks the (request, head, row block) segments of a CTA's range.
+// Walks the (request, head, row block) segments of a CTA's range: `left` units
+// from unit v of segment (b, hr) on.
 struct Walk {
-  int b, hr, t;
+  int b, hr, v;
   long long left;
 };
+// The next segment of which the range holds tiles [t0, t1); false at the end.
+struct Seg {
+  int b, hr, len, nt, t0, t1;
+};
+__device__ __forceinline__ bool next_seg(const Kv8DecArgs& p, int Hr, Walk& w, Seg& s) {
+  while (w.left > 0) {
+    s.len = kv8_len(p, w.b);
+    s.nt = (s.len + 127) >> 7;
+    const int n = seg_units(s.nt);
+    if (n == 0) {  // (a request without tokens has no units)
+      ++w.b;
+      w.hr = 0;
+      w.v = 0;
+      continue;
+    }
+    const int end = (int)min((long long)n, w.v + w.left);
+    s.b = w.b;
+    s.hr = w.hr;
+    s.t0 = max(0, w.v - kSegCost);
+    s.t1 = max(0, end - kSegCost);
+    w.left -= end - w.v;
+    w.v = 0;
+    if (++w.hr == Hr) {
+      w.hr = 0;
+      ++w.b;
+    }
+    if (s.t0 < s.t1) return true;
+  }
+  return false;
+}
 
 template <int D, int RP, int NP>
-__global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __grid_constant__ Kv8DecArgs p) {
+__global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn_kv8_split_kernel(const __grid_constant__ Kv8DecArgs p) {
   using L = Kv8Layout<D, RP, NP>;
   constexpr bool BF16 = NP == 2;
   constexpr int N = L::N;
@@ -279,7 +320,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
     const int per = (p.B + kDecThreads - 1) / kDecThreads;
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += (kv8_len(p, b) + 127) >> 7;
+    for (int b = b0; b < b1; ++b) mine += seg_units((kv8_len(p, b) + 127) >> 7);
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -306,16 +347,16 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
     if (u0 < u1 && before * Hr <= u0 && u0 < (before + mine) * Hr) {
       long long at = before;
       for (int b = b0; b < b1; ++b) {
-        const int nt = (kv8_len(p, b) + 127) >> 7;
-        if (u0 < (at + nt) * Hr) {
+        const int n = seg_units((kv8_len(p, b) + 127) >> 7);
+        if (u0 < (at + n) * Hr) {
           const long long in = u0 - at * Hr;
           int* w = reinterpret_cast<int*>(st + 2);
           w[0] = b;
-          w[1] = (int)(in / nt);
-          w[2] = (int)(in % nt);
+          w[1] = (int)(in / n);
+          w[2] = (int)(in % n);
           break;
         }
-        at += nt;
+        at += n;
       }
     }
   }
@@ -330,7 +371,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
     w0.left = st[1] - st[0];
     w0.b = w[0];
     w0.hr = w[1];
-    w0.t = w[2];
+    w0.v = w[2];
   }
   const int page_rows = 1 << p.page_shift;
   const int tile_pages = 128 >> p.page_shift;
@@ -343,27 +384,21 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
       int g = 0;
       bool ok = true;
       Walk w = w0;
-      while (ok && w.left > 0) {
-        const int len = kv8_len(p, w.b), nt = (len + 127) >> 7;
-        if (w.t >= nt) {
-          ++w.b;
-          w.hr = 0;
-          w.t = 0;
-          continue;
-        }
-        const int cnt = (int)min((long long)(nt - w.t), w.left);
-        const int h = w.hr / p.n_rb;
+      Seg sg;
+      while (ok && next_seg(p, Hr, w, sg)) {
+        const int len = sg.len;
+        const int h = sg.hr / p.n_rb;
         const int pages = (len + page_rows - 1) >> p.page_shift;
-        const int* row = p.table + (size_t)w.b * p.width;
+        const int* row = p.table + (size_t)sg.b * p.width;
         auto page_id = [&](int t) -> int {
           const int j = t * tile_pages + lane;
           return lane < tile_pages && j < pages ? row[j] : -1;
         };
-        int id = page_id(w.t);
-        for (int t = w.t; t < w.t + cnt; ++t, ++g) {
+        int id = page_id(sg.t0);
+        for (int t = sg.t0; t < sg.t1; ++t, ++g) {
           const int here = id;
           const int n_here = min(tile_pages, pages - t * tile_pages);
-          if (t + 1 < w.t + cnt) id = page_id(t + 1);
+          if (t + 1 < sg.t1) id = page_id(t + 1);
           const int s = g % L::kStages;
           const uint32_t ph = (g / L::kStages) & 1;
           ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarEmpty + s), ph ^ 1, wc));
@@ -387,12 +422,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
             tma_load_3d(k + L::kTile, &p.tm_v, bar(L::kBarVFull + s), 0, 0, c2);
           }
           asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar(L::kBarKFull + s)) : "memory");
-        }
-        w.left -= cnt;
-        w.t = 0;
-        if (++w.hr == Hr) {
-          w.hr = 0;
-          ++w.b;
         }
       }
       if (!ok) {
@@ -426,7 +455,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
         // V is MN-major: 32 keys are four 8-key groups of 8 D bytes; for
         // d = 64 a zero block offset makes rows 64-127 of V^T repeat 0-63
         const uint64_t a = D == 128 ? make_sdesc(v + ks * 32 * D, 16, 1024) : make_sdesc64(v + ks * 32 * D, 0, 512);
-        mma_ss_f8(tmem + L::kColO, a, make_sdesc(base + L::kP + ks * 32, 16, 1024), idesc_o, ks > 0);
+        mma_ss_f8(tmem + L::kColO + (g & 1) * N, a, make_sdesc(base + L::kP + ks * 32, 16, 1024), idesc_o, ks > 0);
       }
       tc_commit(bar(L::kBarEmpty + g % L::kStages));
       tc_commit(bar(L::kBarOFull));
@@ -434,15 +463,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
     bool ok = true;
     int g = 0, seg = 0;
     Walk w = w0;
-    while (ok && w.left > 0) {
-      const int nt = (kv8_len(p, w.b) + 127) >> 7;
-      if (w.t >= nt) {
-        ++w.b;
-        w.hr = 0;
-        w.t = 0;
-        continue;
-      }
-      const int cnt = (int)min((long long)(nt - w.t), w.left);
+    Seg sg;
+    while (ok && next_seg(p, Hr, w, sg)) {
+      const int cnt = sg.t1 - sg.t0;
       ok = wt(L::kBarQFull, seg & 1) && wt(L::kBarKFull + g % L::kStages, (g / L::kStages) & 1);
       if (!ok) break;
       tc_fence_after();
@@ -460,12 +483,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
         issue_o(g);
       }
       ++seg;
-      w.left -= cnt;
-      w.t = 0;
-      if (++w.hr == Hr) {
-        w.hr = 0;
-        ++w.b;
-      }
     }
     tc_commit(bar(L::kBarDrain));
     mbar_wait_drain(bar(L::kBarDrain), 0, wc.limit_ns);
@@ -479,22 +496,15 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
     float* qs_s = reinterpret_cast<float*>(sbase + L::kQs);
     int* qi_s = reinterpret_cast<int*>(sbase + L::kQi);
     const int R = p.Nq * p.G;
-    // byte of this key in row n of the P tile: row n at 128 n, chunk XOR n % 8
     uint8_t* prow = sbase + L::kP;
     const uint32_t pcol = (uint32_t)kl;
     bool ok = true;
     int g = 0, seg = 0;
     Walk w = w0;
-    while (ok && w.left > 0) {
-      const int len = kv8_len(p, w.b), nt = (len + 127) >> 7;
-      if (w.t >= nt) {
-        ++w.b;
-        w.hr = 0;
-        w.t = 0;
-        continue;
-      }
-      const int cnt = (int)min((long long)(nt - w.t), w.left);
-      const int h = w.hr / p.n_rb, rb = w.hr % p.n_rb;
+    Seg sg;
+    while (ok && next_seg(p, Hr, w, sg)) {
+      const int len = sg.len;
+      const int h = sg.hr / p.n_rb, rb = sg.hr % p.n_rb;
       // ---- the q terms of the row block: eight lanes to a row
       if (kl < RP * 8) {
         constexpr int E = D / 8;  // elements per lane
@@ -503,7 +513,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
         float f[E];
         if (idx < R) {
           const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) +
-                                                            ((((size_t)w.b * p.Nq + i) * p.Hq + hq) * D + c * E) * 2);
+                                                            ((((size_t)sg.b * p.Nq + i) * p.Hq + hq) * D + c * E) * 2);
 #pragma unroll
           for (int j = 0; j < E / 8; ++j) {
             const uint4 v = src[j];
@@ -562,17 +572,37 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
       mbar_arrive(bar(L::kBarQFull));
       ok = named_bar_and(kWgBar, 128, ok);
       if (!ok) break;
-      float qs[RP], m[RP], l[RP], acc[RP];
+      float m[RP], l[RP], acc[RP];
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
-        qs[r] = qs_s[r];
         m[r] = -INFINITY;
         l[r] = 0.f;
         acc[r] = 0.f;
       }
       const int lim0 = p.causal ? len - p.Nq : len - 1;  // keys <= lim0 are seen by every row
-      for (int t = w.t; t < w.t + cnt; ++t, ++g) {
+      // O^T of a tile is added a tile later, while the tensor core works on the
+      // next one: be is the factor of the tile whose O^T is outstanding (acc is
+      // already on that tile's scale).
+      float be[RP];
+      auto add_o = [&](int go) {
+        tc_fence_after();
+        uint32_t r_[N];
+#pragma unroll
+        for (int c = 0; c < N; c += 16) tmem_ld16(tO + (go & 1) * N + c, r_ + c);
+        tmem_ld_wait();
+        reg_fence<N>(r_);
+        tc_fence_before();
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          float o = __uint_as_float(r_[r]), c = __uint_as_float(r_[RP + r]);
+          if constexpr (NP == 3) c = fmaf(__uint_as_float(r_[2 * RP + r]), 0.0625f, c);
+          o = fmaf(c, 0.0625f, o);
+          acc[r] = fmaf(o, be[r], acc[r]);
+        }
+      };
+      for (int t = sg.t0; t < sg.t1; ++t, ++g) {
         const int st = g % L::kStages, kv0 = t * 128;
+        const bool later = t > sg.t0;  // the tile before is of this segment, its O^T outstanding
         ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarSFull + (g & 1)), (g >> 1) & 1, wc) &&
                                          mbar_wait(bar(L::kBarKFull + st), (g / L::kStages) & 1, wc));
         float x[RP];
@@ -590,12 +620,18 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
           tmem_ld_wait();
           reg_fence<N>(r_);
 #pragma unroll
-          for (int r = 0; r < RP; ++r) {
-            float s = __uint_as_float(r_[r]);
-            float c = __uint_as_float(r_[RP + r]);
-            if constexpr (NP == 3) c = fmaf(__uint_as_float(r_[2 * RP + r]), 0.0625f, c);
-            s = fmaf(c, 0.0625f, s);
-            x[r] = fmaf(s, ks * qs[r], lv);  // w = s + log2 vs
+          for (int r0 = 0; r0 < RP; r0 += 4) {
+            const float4 q4 = *reinterpret_cast<const float4*>(qs_s + r0);
+            const float qs[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int r = r0 + j;
+              float s = __uint_as_float(r_[r]);
+              float c = __uint_as_float(r_[RP + r]);
+              if constexpr (NP == 3) c = fmaf(__uint_as_float(r_[2 * RP + r]), 0.0625f, c);
+              s = fmaf(c, 0.0625f, s);
+              x[r] = fmaf(s, ks * qs[j], lv);  // w = s + log2 vs
+            }
           }
           if (kv0 + 127 > lim0) {
 #pragma unroll
@@ -620,9 +656,12 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
             for (int j = 0; j < D / 16; ++j) z[j] = make_uint4(0, 0, 0, 0);
           }
         }
+        // (the O^T outstanding is complete: its MMA has read P, which is
+        // written again below)
+        if (ok && later) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarOFull), (g - 1) & 1, wc));
         ok = named_bar_and(kWgBar, 128, ok);
         if (!ok) break;
-        float al[RP], be[RP];
+        float al_t[RP], be_t[RP];
 #pragma unroll
         for (int r0 = 0; r0 < RP; r0 += 4) {
           float4 v[4];
@@ -639,11 +678,11 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
             const float mt = mt4[j];
             // running maximum: one of the factors of the old and the new part is 1
             const float e = ex2(mt > m[r] ? m[r] - mt : mt - m[r]);
-            al[r] = mt > m[r] ? e : 1.f;
-            be[r] = (mt < m[r] ? e : 1.f) * 0.00390625f;  // p below carries 2^8
+            al_t[r] = mt > m[r] ? e : 1.f;
+            be_t[r] = (mt < m[r] ? e : 1.f) * 0.00390625f;  // p below carries 2^8
             m[r] = fmaxf(m[r], mt);
             x[r] = ex2(x[r] - (mt == -INFINITY ? 0.f : mt - 8.f));  // p 2^8
-            l[r] = fmaf(x[r], be[r] * inv_vs, l[r] * al[r]);
+            l[r] = fmaf(x[r], be_t[r] * inv_vs, l[r] * al_t[r]);
           }
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -658,35 +697,27 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
               }
             }
           }
+          // byte of this key in row n of the P tile: 128 n, 16-byte chunk XOR n % 8
 #pragma unroll
           for (int t2 = 0; t2 < NP; ++t2)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int r = r0 + j;
-              prow[(t2 * RP + r) * 128 + (pcol ^ ((r & 7) << 4))] = (uint8_t)(code[t2][j >> 1] >> (8 * (j & 1)));
+              const int n = t2 * RP + r0 + j;
+              prow[n * 128 + (pcol ^ ((n & 7) << 4))] = (uint8_t)(code[t2][j >> 1] >> (8 * (j & 1)));
             }
         }
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(bar(L::kBarPFull));
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarOFull), g & 1, wc));
-        if (ok) {
-          tc_fence_after();
-          uint32_t r_[N];
+        if (later) add_o(g - 1);
 #pragma unroll
-          for (int c = 0; c < N; c += 16) tmem_ld16(tO + c, r_ + c);
-          tmem_ld_wait();
-          reg_fence<N>(r_);
-          tc_fence_before();
-#pragma unroll
-          for (int r = 0; r < RP; ++r) {
-            float o = __uint_as_float(r_[r]), c = __uint_as_float(r_[RP + r]);
-            if constexpr (NP == 3) c = fmaf(__uint_as_float(r_[2 * RP + r]), 0.0625f, c);
-            o = fmaf(c, 0.0625f, o);
-            acc[r] = fmaf(o, be[r], acc[r] * al[r]);
-          }
+        for (int r = 0; r < RP; ++r) {
+          acc[r] *= al_t[r];
+          be[r] = be_t[r];
         }
       }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarOFull), (g - 1) & 1, wc));
+      if (ok) add_o(g - 1);
       // ---- end of the segment: row sums over the 128 keys, then O
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
@@ -696,7 +727,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
       }
       ok = named_bar_and(kWgBar, 128, ok);
       if (!ok) break;
-      const bool whole = cnt == nt;
+      const bool whole = sg.t1 - sg.t0 == sg.nt;
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
         const int idx = rb * RP + r;
@@ -707,10 +738,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
           const float v = lt != 0.f ? acc[r] / lt : 0.f;
           if (kl < D) {
             const uint32_t c = pack2<BF16>(v, 0.f);
-            reinterpret_cast<uint16_t*>(p.o)[(((size_t)w.b * p.Nq + i) * p.Hq + hq) * D + kl] = (uint16_t)c;
+            reinterpret_cast<uint16_t*>(p.o)[(((size_t)sg.b * p.Nq + i) * p.Hq + hq) * D + kl] = (uint16_t)c;
           }
           if (kl == 0)
-            p.lse[((size_t)w.b * p.Hq + hq) * p.Nq + i] = lt != 0.f ? (m[r] + __log2f(lt)) * kLn2 : -INFINITY;
+            p.lse[((size_t)sg.b * p.Hq + hq) * p.Nq + i] = lt != 0.f ? (m[r] + __log2f(lt)) * kLn2 : -INFINITY;
         } else {
           const size_t part = ((size_t)blockIdx.x * 2 + (seg > 0 ? 1 : 0)) * RP + r;
           if (kl < D) p.ws_o[part * D + kl] = acc[r];
@@ -721,12 +752,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
         }
       }
       ++seg;
-      w.left -= cnt;
-      w.t = 0;
-      if (++w.hr == Hr) {
-        w.hr = 0;
-        ++w.b;
-      }
     }
   }
   if (threadIdx.x == 0) griddep_launch_dependents();
@@ -738,22 +763,27 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_kv8_split_kernel(const __
   }
 }
 
-// One CTA per (request, key head, row block): joins the parts of a segment
-// that several CTAs share, in the order of the CTAs; requests without keys get
-// O = 0, LSE = -inf.  A warp takes a row at a time.
+// One CTA per (request, query row and head): joins the parts of a segment that
+// several CTAs share; requests without keys get O = 0, LSE = -inf.  The parts
+// are dealt to the four warps, a lane holding D / 32 columns, eight parts'
+// loads in flight, and the warps' sums meet in shared memory: always in the
+// same order.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_constant__ Kv8DecArgs p) {
   __shared__ long long sums[4][2];
+  __shared__ float xo[4][D];
+  __shared__ float xml[4][2];
   griddep_wait();
+  constexpr int kPer = D / 32, kU = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int Hr = p.H * p.n_rb;
-  const int b = blockIdx.x / Hr, hr = blockIdx.x % Hr;
-  const int h = hr / p.n_rb, rb = hr % p.n_rb;
+  const int Hr = p.H * p.n_rb, R = p.Nq * p.G;
+  const int b = blockIdx.x / (p.H * R), hi = blockIdx.x % (p.H * R);
+  const int h = hi / R, idx = hi % R, rb = idx / p.rp, r = idx % p.rp;
   long long before = 0, total = 0;
   for (int i = threadIdx.x; i < p.B; i += 128) {
-    const int nt = (kv8_len(p, i) + 127) >> 7;
-    total += nt;
-    if (i < b) before += nt;
+    const int n = seg_units((kv8_len(p, i) + 127) >> 7);
+    total += n;
+    if (i < b) before += n;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -768,62 +798,78 @@ __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_consta
   before = sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0];
   total = sums[0][1] + sums[1][1] + sums[2][1] + sums[3][1];
   const int nt = (kv8_len(p, b) + 127) >> 7;
-  const int R = p.Nq * p.G, rows = min(p.rp, R - rb * p.rp);
-  const long long units = total * Hr, u0 = before * Hr + (long long)hr * nt;
-  const long long n_cta = min((long long)p.grid, units);
-  const int c0 = nt ? (int)range_owner(u0, units, n_cta) : 0;
-  const int c1 = nt ? (int)range_owner(u0 + nt - 1, units, n_cta) : 0;
+  const long long units = total * Hr, n_cta = min((long long)p.grid, units);
+  const long long u0 = before * Hr + (long long)(h * p.n_rb + rb) * seg_units(nt);
+  const int c0 = nt ? (int)range_owner(u0 + kSegCost, units, n_cta) : 0;
+  const int c1 = nt ? (int)range_owner(u0 + kSegCost + nt - 1, units, n_cta) : 0;
   if (nt == 0 || c0 != c1) {
-    const int s0 = nt && range_start(c0, units, n_cta) < u0 ? 1 : 0;  // slot of the first part (later ones: 0)
-    constexpr int kPer = D / 32;
-    for (int r = warp; r < rows; r += 4) {
-      const int idx = rb * p.rp + r, i = idx / p.G, hq = h * p.G + idx % p.G;
-      float acc[kPer];
+    // the first CTA's part is in its second slot if its range began earlier
+    const int s0 = nt && range_start(c0, units, n_cta) < u0 ? 1 : 0;
+    auto part = [&](int c) -> size_t { return ((size_t)c * 2 + (c == c0 ? s0 : 0)) * p.rp + r; };
+    float acc[kPer];
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-      float M = -INFINITY, Ls = 0.f;
-      if (nt) {
-        auto part = [&](int c) -> size_t { return ((size_t)c * 2 + (c == c0 ? s0 : 0)) * p.rp + r; };
-        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.ws_ml[part(c) * 2]);
-        M = warp_max(M);
-        for (int cb = c0; cb <= c1; cb += 32) {
-          const int c = cb + lane;
-          float wgt = 0.f;
-          if (c <= c1) {
-            const float mc = p.ws_ml[part(c) * 2], lc = p.ws_ml[part(c) * 2 + 1];
-            wgt = mc == -INFINITY ? 0.f : ex2(mc - M);
-            // (a part whose every score is NaN has m = -inf and a NaN sum)
-            Ls += lc != lc ? lc : wgt * lc;
-          }
-          const int n = min(32, c1 - cb + 1);
-          for (int k = 0; k < n; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, wgt, k);
+    for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+    float M = -INFINITY, Ls = 0.f;
+    if (nt) {
+      for (int c = c0 + (int)threadIdx.x; c <= c1; c += 128) M = fmaxf(M, p.ws_ml[part(c) * 2]);
+      M = warp_max(M);
+      if (lane == 0) xml[warp][0] = M;
+      __syncthreads();
+      M = fmaxf(fmaxf(xml[0][0], xml[1][0]), fmaxf(xml[2][0], xml[3][0]));
+      for (int cb = c0 + warp * kU; cb <= c1; cb += 4 * kU) {
+        float wgt = 0.f;
+        if (lane < kU && cb + lane <= c1) {
+          const size_t at = part(cb + lane) * 2;
+          const float mc = p.ws_ml[at], lc = p.ws_ml[at + 1];
+          wgt = mc == -INFINITY ? 0.f : ex2(mc - M);
+          // (a part whose every score is NaN has m = -inf and a NaN sum)
+          Ls += lc != lc ? lc : wgt * lc;
+        }
+        float4 v[kU];
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (cb + k <= c1) {
             const float* o = p.ws_o + part(cb + k) * D + lane * kPer;
             if constexpr (kPer == 4) {
-              const float4 v = *reinterpret_cast<const float4*>(o);
-              acc[0] = fmaf(wk, v.x, acc[0]);
-              acc[1] = fmaf(wk, v.y, acc[1]);
-              acc[2] = fmaf(wk, v.z, acc[2]);
-              acc[3] = fmaf(wk, v.w, acc[3]);
+              v[k] = *reinterpret_cast<const float4*>(o);
             } else {
-              const float2 v = *reinterpret_cast<const float2*>(o);
-              acc[0] = fmaf(wk, v.x, acc[0]);
-              acc[1] = fmaf(wk, v.y, acc[1]);
+              const float2 v2 = *reinterpret_cast<const float2*>(o);
+              v[k].x = v2.x;
+              v[k].y = v2.y;
             }
           }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+        for (int k = 0; k < kU; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, wgt, k);
+          acc[0] = fmaf(wk, v[k].x, acc[0]);
+          acc[1] = fmaf(wk, v[k].y, acc[1]);
+          if constexpr (kPer == 4) {
+            acc[2] = fmaf(wk, v[k].z, acc[2]);
+            acc[3] = fmaf(wk, v[k].w, acc[3]);
+          }
+        }
       }
-      const float inv = Ls != 0.f ? 1.f / Ls : 0.f;
-      uint32_t wv[kPer / 2];
 #pragma unroll
-      for (int k = 0; k < kPer / 2; ++k) wv[k] = pack2<BF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-      uint8_t* dst = static_cast<uint8_t*>(p.o) + ((((size_t)b * p.Nq + i) * p.Hq + hq) * D + lane * kPer) * 2;
-      if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(wv[0], wv[1]);
-      else *reinterpret_cast<uint32_t*>(dst) = wv[0];
-      if (lane == 0) p.lse[((size_t)b * p.Hq + hq) * p.Nq + i] = Ls != 0.f ? (M + __log2f(Ls)) * kLn2 : -INFINITY;
+      for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+      if (lane == 0) xml[warp][1] = Ls;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) xo[warp][lane * kPer + k] = acc[k];
+      __syncthreads();
+      Ls = (xml[0][1] + xml[1][1]) + (xml[2][1] + xml[3][1]);
     }
+    const int i = idx / p.G, hq = h * p.G + idx % p.G;
+    if (threadIdx.x < D / 2) {
+      const int c = 2 * threadIdx.x;
+      const float inv = Ls != 0.f ? 1.f / Ls : 0.f;
+      float a[2] = {0.f, 0.f};
+      if (nt)
+        for (int k = 0; k < 2; ++k) a[k] = ((xo[0][c + k] + xo[1][c + k]) + (xo[2][c + k] + xo[3][c + k])) * inv;
+      reinterpret_cast<uint32_t*>(p.o)[((((size_t)b * p.Nq + i) * p.Hq + hq) * D + c) / 2] = pack2<BF16>(a[0], a[1]);
+    }
+    if (threadIdx.x == 0)
+      p.lse[((size_t)b * p.Hq + hq) * p.Nq + i] = Ls != 0.f ? (M + __log2f(Ls)) * kLn2 : -INFINITY;
   }
   griddep_launch_dependents();
 }
@@ -844,26 +890,27 @@ cudaError_t launch_split_n(const Kv8DecArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// Row blocks of 8 or 16 rows: the S and O columns, and the work per tile, grow
-// with the rows.
-int kv8_rows(int R) { return R <= 8 ? 8 : 16; }
+// Row blocks of 4, 8 or 16 rows: the work per tile grows with the rows.
+int kv8_rows(int R) { return R <= 4 ? 4 : (R <= 8 ? 8 : 16); }
 
-// Two CTAs to an SM, no more than there can be tiles.
-int kv8_grid(int d, int rp, int bf16, int sms, long long max_units) {
-  (void)d; (void)rp; (void)bf16;
-  long long g = 2ll * sms;
+// All CTAs resident at once, no more than there can be tiles.
+int kv8_grid(int rp, int sms, long long max_units) {
+  long long g = (rp <= 8 ? 3ll : 2ll) * sms;
   if (g > kKv8MaxCtas) g = kKv8MaxCtas;
   if (g > max_units) g = max_units;
   return (int)(g < 1 ? 1 : g);
 }
 
 cudaError_t launch_kv8_split(const Kv8DecArgs& a, cudaStream_t stream) {
-  if (a.d == 128) return a.rp == 8 ? launch_split_n<128, 8>(a, stream) : launch_split_n<128, 16>(a, stream);
-  return a.rp == 8 ? launch_split_n<64, 8>(a, stream) : launch_split_n<64, 16>(a, stream);
+  if (a.d == 128)
+    return a.rp == 4 ? launch_split_n<128, 4>(a, stream)
+                     : (a.rp == 8 ? launch_split_n<128, 8>(a, stream) : launch_split_n<128, 16>(a, stream));
+  return a.rp == 4 ? launch_split_n<64, 4>(a, stream)
+                   : (a.rp == 8 ? launch_split_n<64, 8>(a, stream) : launch_split_n<64, 16>(a, stream));
 }
 
 cudaError_t launch_kv8_merge(const Kv8DecArgs& a, cudaStream_t stream) {
-  const unsigned grid = (unsigned)((long long)a.B * a.H * a.n_rb);
+  const unsigned grid = (unsigned)((long long)a.B * a.Hq * a.Nq);
   if (a.d == 128)
     return a.bf16 ? launch_pdl(attn_kv8_merge_kernel<128, true>, grid, 128, 0, stream, a)
                   : launch_pdl(attn_kv8_merge_kernel<128, false>, grid, 128, 0, stream, a);

@@ -220,7 +220,7 @@ struct Kv8DecArgs {
 };
 // Rows of one row block for R = Nq * Hq / H query rows of a key head.
 int kv8_rows(int R);
-int kv8_grid(int d, int rp, int bf16, int sms, long long max_units);
+int kv8_grid(int rp, int sms, long long max_units);
 cudaError_t launch_kv8_split(const Kv8DecArgs& a, cudaStream_t stream);
 cudaError_t launch_kv8_merge(const Kv8DecArgs& a, cudaStream_t stream);
 
