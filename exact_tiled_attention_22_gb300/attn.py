@@ -109,7 +109,7 @@ def _load() -> ctypes.CDLL:
     lib.attn_kv8_decode.restype = i
     lib.attn_varlen_fwd.argtypes = [vp] * 7 + [i, ll, ll, i, i, i, ll, ll, ll, f, i, i, vp]
     lib.attn_varlen_fwd.restype = i
-    lib.attn_varlen_bwd_workspace_size.argtypes = [i, ll, i, i]
+    lib.attn_varlen_bwd_workspace_size.argtypes = [i, ll, i, i, i]
     lib.attn_varlen_bwd_workspace_size.restype = sz
     lib.attn_varlen_bwd.argtypes = [vp] * 11 + [i, ll, ll, i, i, i, ll, ll, ll, f, i, i, vp, sz, vp]
     lib.attn_varlen_bwd.restype = i
@@ -330,8 +330,8 @@ def attn_varlen_fwd(q, k, v, o, lse, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, d, q_stride
                                _stream(stream))
 
 
-def attn_varlen_bwd_workspace_size(B, Tq, Hq, d) -> int:
-    return int(lib.attn_varlen_bwd_workspace_size(B, Tq, Hq, d))
+def attn_varlen_bwd_workspace_size(B, Tq, Hq, Hkv, d) -> int:
+    return int(lib.attn_varlen_bwd_workspace_size(B, Tq, Hq, Hkv, d))
 
 
 def attn_varlen_bwd(q, k, v, o, lse, dO, dq, dk, dv, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, d, q_stride,
@@ -637,8 +637,8 @@ def varlen_bwd(q, k, v, o, lse, do, cu_q, cu_k, scale=None, causal=False, ws=Non
         _want(dk, "dk", dt, sk, dev)
         _want(dv, "dv", dt, sk, dev)
     if ws is None:
-        ws = torch.empty(attn_varlen_bwd_workspace_size(sizes[0], Tq, Hq, d), dtype=torch.uint8,
-                         device=q.device)
+        ws = torch.empty(attn_varlen_bwd_workspace_size(sizes[0], Tq, Hq, k.shape[1], d),
+                         dtype=torch.uint8, device=q.device)
     elif ws.get_device() != dev:
         raise ValueError(f"ws is on {ws.device}")
     _run(dev, stream, lib.attn_varlen_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),

@@ -914,12 +914,13 @@ namespace {
 
 // A packed [T, H, d] 16-bit tensor, `stride` elements from token to token, as
 // (d, head, row window, place): the last two dimensions both step by a token,
-// so that a box may begin up to `rows` tokens before its place and reads zeros
-// there (see attn_fwd.cu).
-int encode_packed(CUtensorMap* m, const void* ptr, long long T, int H, int d, long long stride, int rows, bool bf16) {
+// so that a box of `heads` heads and `rows` tokens may begin up to `rows` tokens
+// before its place and reads zeros there (see attn_fwd.cu).
+int encode_packed(CUtensorMap* m, const void* ptr, long long T, int H, int d, long long stride, int heads, int rows,
+                  bool bf16) {
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, 128, (cuuint64_t)T};
   const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2, (cuuint64_t)stride * 2};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)rows, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                         const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -981,19 +982,20 @@ int attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float*
   attn::FwdArgs a;
   std::memset(&a, 0, sizeof a);
   const bool bf16 = dtype == ATTN_BF16;
+  a.G = Hq / Hkv;
+  attn::fwd_varlen_shape(a.G, Tq, B, &a.Gp, &a.R);
   // (without keys no K or V tile is loaded; their maps still need an address)
-  if ((rc = encode_packed(&a.tm_q, q, Tq, Hq, d, q_stride, 128, bf16)) ||
-      (rc = encode_packed(&a.tm_k, Tk ? k : q, Tk ? Tk : 1, Hkv, d, Tk ? k_stride : hk, 128, bf16)) ||
-      (rc = encode_packed(&a.tm_v, Tk ? v : q, Tk ? Tk : 1, Hkv, d, Tk ? v_stride : hk, 128, bf16)) ||
-      (rc = encode_packed(&a.tm_o, o, Tq, Hq, d, hq, 128, bf16)))
+  if ((rc = encode_packed(&a.tm_q, q, Tq, Hq, d, q_stride, a.Gp, a.R, bf16)) ||
+      (rc = encode_packed(&a.tm_k, Tk ? k : q, Tk ? Tk : 1, Hkv, d, Tk ? k_stride : hk, 1, 128, bf16)) ||
+      (rc = encode_packed(&a.tm_v, Tk ? v : q, Tk ? Tk : 1, Hkv, d, Tk ? v_stride : hk, 1, 128, bf16)) ||
+      (rc = encode_packed(&a.tm_o, o, Tq, Hq, d, hq, a.Gp, a.R, bf16)))
     return rc;
   a.o = o;
   a.lse = lse;
   if ((rc = make_dropout(0.f, 0, 0, &a.drop))) return rc;
   a.B = B; a.H = Hq; a.N = (int)Tq; a.d = d;
   a.cu_q = cu_q; a.cu_k = cu_k;
-  a.Nk = (int)Tk; a.G = Hq / Hkv;
-  a.head_pairs = a.G % 2 == 0;
+  a.Nk = (int)Tk;
   a.causal = causal ? 1 : 0;
   a.scale = scale;
   a.bf16 = bf16;
@@ -1003,11 +1005,22 @@ int attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float*
   return e != cudaSuccess ? cuda_fail(e, "attn_varlen_fwd launch") : ATTN_OK;
 }
 
-size_t attn_varlen_bwd_workspace_size(int B, long long Tq, int Hq, int d) {
-  if (B < 1 || B > attn::kVarMaxB || Tq < 0 || Tq >= (1ll << 26) || Hq < 1 || (d != 64 && d != 128)) return 0;
+// Bytes of the partial dK, dV tiles: no tile is split while a sequence of all
+// Tq queries has no more than one chunk of steps (at least 32, or two per head
+// of the group).
+static size_t varlen_parts_bytes(long long Tq, int Hq, int Hkv, int d) {
+  const long long G = Hq / Hkv, a_min = (16 + G - 1) / G;
+  return (Tq + 63) / 64 <= 2 * a_min ? 0 : (size_t)attn::kVarMaxParts * 2 * 128 * d * 4;
+}
+
+size_t attn_varlen_bwd_workspace_size(int B, long long Tq, int Hq, int Hkv, int d) {
+  if (B < 1 || B > attn::kVarMaxB || Tq < 0 || Tq >= (1ll << 26) || Hkv < 1 || Hq < Hkv || Hq % Hkv ||
+      (d != 64 && d != 128))
+    return 0;
   const size_t rows = (size_t)varlen_padded(B, Tq) * Hq;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  return up(rows * 4) * 2 + up(rows * d * 4) + 256 + up((size_t)B * sizeof(attn::VarBwdSeq)) + up(((size_t)B + 1) * 4);
+  return up(rows * 4) * 2 + up(rows * d * 4) + 256 + up((size_t)B * sizeof(attn::VarBwdSeq)) + up(((size_t)B + 1) * 4) +
+         varlen_parts_bytes(Tq, Hq, Hkv, d);
 }
 
 int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
@@ -1024,7 +1037,7 @@ int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o, 
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(dO) ||
       !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
     return fail(ATTN_ERR_ALIGN, "all pointers must be 16-byte aligned");
-  const size_t need = attn_varlen_bwd_workspace_size(B, Tq, Hq, d);
+  const size_t need = attn_varlen_bwd_workspace_size(B, Tq, Hq, Hkv, d);
   if (!workspace || workspace_bytes < need)
     return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
   if (reinterpret_cast<uintptr_t>(workspace) & 255u)
@@ -1056,6 +1069,7 @@ int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o, 
   a.sched = reinterpret_cast<unsigned*>(ws);
   a.var_seq = reinterpret_cast<attn::VarBwdSeq*>(ws + 256);
   a.var_items = reinterpret_cast<int*>(ws + 256 + up((size_t)B * sizeof(attn::VarBwdSeq)));
+  a.var_parts = reinterpret_cast<float*>(ws + 256 + up((size_t)B * sizeof(attn::VarBwdSeq)) + up(((size_t)B + 1) * 4));
   a.dq = dq; a.dk = dk; a.dv = dv;
   a.B = B; a.H = Hq; a.N = (int)Tq; a.Npad = (int)npad; a.d = d;
   a.cu_q = cu_q; a.cu_k = cu_k;
@@ -1070,12 +1084,12 @@ int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o, 
   if (e != cudaSuccess) return cuda_fail(e, "attn_varlen_bwd preprocess launch");
   if (Tq > 0 && Tk > 0) {
     const int qrows = attn::bwd_q_rows(d);
-    if ((rc = encode_packed(&a.tm_q, q, Tq, Hq, d, q_stride, qrows, bf16)) ||
-        (rc = encode_packed(&a.tm_k, k, Tk, Hkv, d, k_stride, 128, bf16)) ||
-        (rc = encode_packed(&a.tm_v, v, Tk, Hkv, d, v_stride, 128, bf16)) ||
-        (rc = encode_packed(&a.tm_do, dO, Tq, Hq, d, hq, qrows, bf16)) ||
-        (rc = encode_packed(&a.tm_dk, dk, Tk, Hkv, d, hk, 128, bf16)) ||
-        (rc = encode_packed(&a.tm_dv, dv, Tk, Hkv, d, hk, 128, bf16)))
+    if ((rc = encode_packed(&a.tm_q, q, Tq, Hq, d, q_stride, 1, qrows, bf16)) ||
+        (rc = encode_packed(&a.tm_k, k, Tk, Hkv, d, k_stride, 1, 128, bf16)) ||
+        (rc = encode_packed(&a.tm_v, v, Tk, Hkv, d, v_stride, 1, 128, bf16)) ||
+        (rc = encode_packed(&a.tm_do, dO, Tq, Hq, d, hq, 1, qrows, bf16)) ||
+        (rc = encode_packed(&a.tm_dk, dk, Tk, Hkv, d, hk, 1, 128, bf16)) ||
+        (rc = encode_packed(&a.tm_dv, dv, Tk, Hkv, d, hk, 1, 128, bf16)))
       return rc;
     e = timed(attn::kKBwdMain, s, [&] { return attn::launch_bwd_main_varlen(a, s); });
     if (e != cudaSuccess) return cuda_fail(e, "attn_varlen_bwd main launch");

@@ -218,6 +218,26 @@ __device__ __forceinline__ void stage_row_from_tmem(uint32_t taddr, int c0, floa
   }
 }
 
+// Columns [c0, c0 + NC) of this thread's TMEM row, multiplied by `mul`, into a
+// partial tile of 128 rows kept as [column / 4][row][4] fp32, so that a warp's
+// stores are contiguous.
+template <int NC>
+__device__ __forceinline__ void store_part_from_tmem(uint32_t taddr, int c0, float mul, int row, float* part) {
+  constexpr int W = NC < 32 ? NC : 32;  // columns per TMEM load
+#pragma unroll 1
+  for (int cc = c0; cc < c0 + NC; cc += W) {
+    uint32_t r[W];
+    tmem_ld_w<W>(taddr + cc, r);
+    tmem_ld_wait();
+    reg_fence<W>(r);
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i)
+      reinterpret_cast<float4*>(part)[(cc / 4 + i) * 128 + row] =
+          make_float4(__uint_as_float(r[4 * i]) * mul, __uint_as_float(r[4 * i + 1]) * mul,
+                      __uint_as_float(r[4 * i + 2]) * mul, __uint_as_float(r[4 * i + 3]) * mul);
+  }
+}
+
 // NC 16-bit zeros to dst (16-byte aligned).
 template <int NC>
 __device__ __forceinline__ void store_zero_row(uint8_t* dst) {
@@ -237,6 +257,37 @@ __host__ __device__ inline int bwd_head_group(int N, int d, int BH) {
   const long long g = (64ll << 20) / per_head;
   return (int)(g < 1 ? 1 : (g > BH ? BH : g));
 }
+
+// How a packed batch's key tiles are cut into items.  Tile tk (from the end) of a
+// sequence has G min(nqs, 2 tk + 2) steps (causal; else G nqs); an item takes
+// 2 G a of them, so tile tk has tk / a + 1 items while the causal limit binds
+// (tk < n1) and C above, and the items before a tile have a closed form.  `a`
+// comes from the whole batch's steps (var_plan): about kVarChunks equal chunks,
+// twice the SMs, and never fewer than 32 steps in one, so that the longest item
+// is a fraction of the kernel's time however the lengths are spread (without
+// the cut the first tile of the longest sequence took as long as the rest of
+// the batch: 4096 tokens, 4 heads to a key head, 256 steps, 0.24 ms).
+struct VarSplit {
+  int nkt, n1, a, C;
+  __device__ VarSplit(int lq, int lk, int a_, int causal) {
+    const int nqs = (lq + 63) >> 6;
+    nkt = (lk + 127) >> 7;
+    n1 = causal ? min(nkt, nqs >> 1) : 0;
+    a = a_;
+    C = (nqs + 2 * a - 1) / (2 * a);
+  }
+  __device__ int items(int tk) const { return tk < n1 ? tk / a + 1 : C; }
+  __device__ int items_before(int n) const {
+    const int m = min(n, n1), k = m / a, r = m - k * a;
+    return a * (k * (k + 1) / 2) + r * (k + 1) + (n - m) * C;
+  }
+  // tiles from here on have several items
+  __device__ int first_split() const { return C >= 2 ? min(a, n1) : nkt; }
+  __device__ int parts_before(int n) const {
+    const int f = first_split();
+    return n > f ? items_before(n) - items_before(f) : 0;
+  }
+};
 
 // ALIBI: the scores carry the linear bias -m_h |i - j| (m_h = p.alibi[h]), as
 // in the forward; it is folded into the per-query -LSE*log2(e) term.
@@ -277,7 +328,10 @@ __host__ __device__ inline int bwd_head_group(int N, int d, int BH) {
 // G query heads to a key head.  An item is a 128-key tile of one sequence and
 // KEY head, and its steps run over the rows of all G query heads of the group:
 // dK and dV of a shared head are summed in the same TMEM accumulators, in a
-// fixed order, and K and V are loaded once for the group.  Tiles and steps
+// fixed order, and K and V are loaded once for the group.  A tile with many
+// steps is cut into chunks (VarSplit) that are items of their own: they leave
+// fp32 partial dK, dV in the workspace, which the post kernel adds up in order.
+// Tiles and steps
 // count from the end of their sequence (see attn_fwd.cu): key tile tk sees the
 // 64-row steps u <= 2 tk + 1, the ragged ones are the first and TMA fills their
 // missing rows with zeros.  -LSE, D and the dQ accumulator are kept in a padded
@@ -307,6 +361,7 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
   const int BH = p.B * p.H;
   const int nkb = (p.N + 127) / 128;
   const int n_items = VARLEN ? p.var_items[p.B] : nkb * BH;
+  const int var_a = VARLEN ? (int)p.sched[2] : 1;
   const int G = VARLEN ? 1 : bwd_head_group(p.N, D, BH);
   const int nq = (p.N + BQ - 1) / BQ;
   const WaitCtl wc{p.wait.status, p.wait.limit_ns};
@@ -317,6 +372,8 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
   struct Item {
     int jblk, bh, b, h, k0, i_begin, n_it;
     int kbase, qbase, lq, diag, pbase, n_steps;
+    int step0;  // (VARLEN) the item's first step
+    int part;   // its place among the partial dK, dV, or -1: it has the whole tile
   };
   auto decode = [&](int item) -> Item {
     Item it{};
@@ -341,7 +398,8 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
   // of the item counts, then, as in decode, groups of key heads whose dQ
   // accumulators fit the L2, the key tiles with the most steps (the first ones)
   // first.  Slot words: tile, key head, first query row, queries, first key row,
-  // keys, padded row of query 0.
+  // keys, padded row of query 0; behind them (npos_s) the chunk and its part.
+  volatile int* npos_s = reinterpret_cast<volatile int*>(sbase + L::kNPos);
   volatile int* var_slot = reinterpret_cast<volatile int*>(sbase + L::kQBits);
   auto var_publish = [&](int slot, int item) {
     int lo = 0, hi = p.B - 1;  // last sequence with var_items <= item
@@ -350,13 +408,24 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
       if (p.var_items[mid] <= item) lo = mid; else hi = mid - 1;
     }
     const VarBwdSeq q = p.var_seq[lo];
-    const int r = item - p.var_items[lo], nkt = (q.lk + 127) >> 7;
+    const VarSplit sp(q.lq, q.lk, var_a, p.causal);
+    const int r = item - p.var_items[lo], n_head = sp.items_before(sp.nkt);  // items of one key head
     const int gh = bwd_head_group(q.lq, D * p.G, p.Hkv);
-    const int grp = r / (gh * nkt), r_in = r - grp * gh * nkt;
+    const int grp = r / (gh * n_head), r_in = r - grp * gh * n_head;
     const int gsize = min(gh, p.Hkv - grp * gh);
+    const int e = n_head - 1 - r_in / gsize, h = grp * gh + r_in % gsize;
+    lo = 0;
+    hi = sp.nkt - 1;  // the tile of item e of the head
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sp.items_before(mid) <= e) lo = mid; else hi = mid - 1;
+    }
     volatile int* v = var_slot + 8 * slot;
-    v[0] = nkt - 1 - r_in / gsize;
-    v[1] = grp * gh + r_in % gsize;
+    v[0] = lo;
+    v[1] = h;
+    npos_s[2 * slot] = e - sp.items_before(lo);  // chunk of the tile
+    npos_s[2 * slot + 1] =
+        sp.items(lo) > 1 ? q.part0 + h * sp.parts_before(sp.nkt) + sp.parts_before(lo) + (e - sp.items_before(lo)) : -1;
     v[2] = q.q0;
     v[3] = q.lq;
     v[4] = q.k0;
@@ -376,7 +445,11 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
     it.diag = lk - it.lq;
     const int nqs = (it.lq + BQ - 1) / BQ;
     it.n_steps = p.causal ? min(nqs, 2 * tk + 2) : nqs;
-    it.n_it = it.n_steps * p.G;
+    const int cap = 2 * p.G * var_a, f0 = npos_s[2 * slot] * cap;  // first of the group's steps
+    it.n_it = min(cap, it.n_steps * p.G - f0);
+    const int g0 = f0 / it.n_steps;
+    it.step0 = (g0 << 20) | (f0 - g0 * it.n_steps);
+    it.part = npos_s[2 * slot + 1];
     return it;
   };
   // (VARLEN) a step is (query head of the group) << 20 | step of that head;
@@ -386,7 +459,6 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
   };
 
   uint32_t* qbits = reinterpret_cast<uint32_t*>(sbase + L::kQBits);
-  int* npos_s = reinterpret_cast<int*>(sbase + L::kNPos);
   // (SPARSE: one item per CTA) step `it` of the item (query rows
   // (i_begin + it) * BQ ..) is visited unless masked
   auto step_ok = [&](const Item& I, int it) -> bool {
@@ -395,7 +467,7 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
     return ((qbits[qb >> 5] >> (qb & 31)) & 1u) != 0;
   };
   auto next_step = [&](const Item& I, int it) -> int {  // the next visited step after `it` (n_it: none)
-    if constexpr (VARLEN) return it >= 0 && (it & 0xFFFFF) + 1 == I.n_steps ? ((it >> 20) + 1) << 20 : it + 1;
+    if constexpr (VARLEN) return it < 0 ? I.step0 : ((it & 0xFFFFF) + 1 == I.n_steps ? ((it >> 20) + 1) << 20 : it + 1);
     ++it;
     if constexpr (SPARSE) {
       while (it < I.n_it && !step_ok(I, it)) ++it;
@@ -978,6 +1050,11 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
                                      p.dv_acc + (((size_t)I.b * p.N + (key_ok ? key : 0)) * p.H + I.h) * D);
           tc_fence_before();
           mbar_arrive(bar(L::kBarDVEmpty));  // the next item's first dV may overwrite the columns
+        } else if (VARLEN && I.part >= 0) {
+          store_part_from_tmem<D / NWG>(tmem + lane_off + L::kColDV, hf * (D / NWG), 1.f, kl,
+                                        p.var_parts + (size_t)I.part * (2 * 128 * D));
+          tc_fence_before();
+          mbar_arrive(bar(L::kBarDVEmpty));
         } else if (VARLEN && I.k0 < 0) {
           // the ragged tile: the rows before the sequence are its neighbour's
           store_row_from_tmem<D / NWG, BF16>(tmem + lane_off + L::kColDV, hf * (D / NWG), 1.f, key_ok, dst);
@@ -1083,6 +1160,11 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
                                p.dk_acc + (((size_t)I.b * p.N + (key_ok ? key : 0)) * p.H + I.h) * D);
           tc_fence_before();
           mbar_arrive(bar(L::kBarDKEmpty));  // the next item's first dK may overwrite the columns
+        } else if (VARLEN && I.part >= 0) {
+          store_part_from_tmem<D>(tmem + lane_off + L::kColDK, 0, p.scale, ln,
+                                  p.var_parts + (size_t)I.part * (2 * 128 * D) + 128 * D);
+          tc_fence_before();
+          mbar_arrive(bar(L::kBarDKEmpty));
         } else if (VARLEN && I.k0 < 0) {  // the ragged tile, as dV's
           store_row_from_tmem<D, BF16>(tmem + lane_off + L::kColDK, 0, p.scale, key_ok, dst);
           tc_fence_before();
@@ -1260,24 +1342,26 @@ cudaError_t launch_main_t(const BwdArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // one CTA per item (block-sparse), else a persistent grid of one CTA per SM
   // (VARLEN: no more items than the worst split of the keys into sequences has)
-  const long long items = VARLEN ? ((long long)a.Nk / 128 + a.B) * a.Hkv : (long long)((a.N + 127) / 128) * a.B * a.H;
+  const long long items = VARLEN ? ((long long)a.Nk / 128 + a.B) * a.Hkv * a.G
+                                 : (long long)((a.N + 127) / 128) * a.B * a.H;
   const unsigned grid = (unsigned)(SPARSE ? items : (items < a.sms ? items : a.sms));
   e = launch_pdl(k, grid, BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, L::kSmem, stream, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // ------------------------------------------------------------ packed pre / post
-// Every CTA of these two kernels computes the sequences' descriptions for
+// Every CTA of the preprocess kernel computes the sequences' descriptions for
 // itself (B offsets from L2, one block-wide scan per 256 of them): first query
 // rows and padded starts go to shared memory, where a token's sequence is found
-// by bisection.
+// by bisection.  (The post kernel reads them as the preprocess kernel left them.)
 struct VarScan {
   int* q0;     // [B] first query row
   int* lq;     // [B]
   int* pbase;  // [B] padded row of query 0
 };
 
-// Also leaves, from CTA 0, what the main kernel reads: p.var_seq, p.var_items.
+// Also leaves, from CTA 0, what the other kernels read: p.var_seq, p.var_items,
+// the work counter, the split `a` and the number of split tiles (p.sched).
 __device__ __forceinline__ VarScan var_scan(const BwdArgs& p, uint8_t* smem, bool publish) {
   __shared__ long long wsum[8];
   VarScan v;
@@ -1304,14 +1388,14 @@ __device__ __forceinline__ VarScan var_scan(const BwdArgs& p, uint8_t* smem, boo
     __syncthreads();
     return before + inc - x;
   };
-  long long c_pad = 0, c_item = 0;
+  long long c_pad = 0, c_steps = 0;
   for (int b0 = 0; b0 < p.B; b0 += kAuxThreads) {
     const int b = b0 + threadIdx.x;
-    int q0 = 0, lq = 0, k0 = 0, lk = 0;
+    int q0 = 0, lq = 0, lk = 0;
     if (b < p.B) {
       q0 = min(max(p.cu_q[b], 0), p.N);
       lq = min(max(p.cu_q[b + 1], q0), p.N) - q0;
-      k0 = min(max(p.cu_k[b], 0), p.Nk);
+      const int k0 = min(max(p.cu_k[b], 0), p.Nk);
       lk = min(max(p.cu_k[b + 1], k0), p.Nk) - k0;
     }
     const int pad = (lq + 63) / 64 * 64;
@@ -1319,22 +1403,55 @@ __device__ __forceinline__ VarScan var_scan(const BwdArgs& p, uint8_t* smem, boo
     // (offsets that do not ascend could ask for more rows than there are: such
     // a sequence has no queries, so that nothing leaves the workspace)
     if (ps > p.Npad - pad) lq = 0;
-    const int items = lq > 0 ? (lk + 127) / 128 * p.Hkv : 0;
-    const long long is = scan(items, c_item);
+    const int pbase = lq > 0 ? (int)ps + pad - lq : 0;
     if (b < p.B) {
-      const int pbase = lq > 0 ? (int)ps + pad - lq : 0;
       v.q0[b] = q0;
       v.lq[b] = lq;
       v.pbase[b] = pbase;
-      if (publish) {
-        p.var_seq[b] = VarBwdSeq{q0, lq, k0, lk, pbase, {0, 0, 0}};
-        p.var_items[b] = (int)min(is, (long long)INT_MAX);
-      }
+    }
+    if (publish) {
+      const int nqs = (lq + 63) >> 6, nkt = (lk + 127) >> 7, n1 = p.causal ? min(nkt, nqs >> 1) : 0;
+      scan((long long)n1 * (n1 + 1) + (long long)(nkt - n1) * nqs, c_steps);
     }
   }
   __syncthreads();
-  if (publish && threadIdx.x == 0) p.var_items[p.B] = (int)min(c_item, (long long)INT_MAX);
+  if (publish) {
+    // chunks of 2 G a steps: an equal share of kVarChunks, no less than 32
+    const long long total = c_steps * p.H, unit = 2ll * p.G;
+    const int a = (int)max((16ll + p.G - 1) / p.G, (total + kVarChunks * unit - 1) / (kVarChunks * unit));
+    long long c_item = 0, c_part = 0, c_split = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kAuxThreads) {
+      const int b = b0 + threadIdx.x;
+      int k0 = 0, lk = 0, lq = 0;
+      if (b < p.B) {
+        k0 = min(max(p.cu_k[b], 0), p.Nk);
+        lk = min(max(p.cu_k[b + 1], k0), p.Nk) - k0;
+        lq = v.lq[b];
+      }
+      const VarSplit sp(lq, lk, a, p.causal);
+      const long long items = lq > 0 ? (long long)sp.items_before(sp.nkt) * p.Hkv : 0;
+      const long long parts = lq > 0 ? (long long)sp.parts_before(sp.nkt) * p.Hkv : 0;
+      const long long split = lq > 0 ? (long long)max(0, sp.nkt - sp.first_split()) * p.Hkv : 0;
+      const long long is = scan(items, c_item), pp = scan(parts, c_part), ss = scan(split, c_split);
+      if (b < p.B) {
+        p.var_seq[b] = VarBwdSeq{v.q0[b], lq, k0, lk, v.pbase[b], (int)pp, (int)min(ss, (long long)INT_MAX), 0};
+        p.var_items[b] = (int)min(is, (long long)INT_MAX);
+      }
+    }
+    if (threadIdx.x == 0) {
+      p.var_items[p.B] = (int)min(c_item, (long long)INT_MAX);
+      p.sched[0] = 0u;
+      p.sched[1] = 0u;
+      p.sched[2] = (unsigned)a;
+      p.sched[3] = (unsigned)min(c_split, (long long)INT_MAX);
+    }
+  }
   return v;
+}
+
+// r / n: a 32-bit division where it fits (see attn_bwd_pre_kernel).
+__device__ __forceinline__ int row_of(long long r, int n) {
+  return r < (1ll << 32) ? (int)((unsigned)r / (unsigned)n) : (int)(r / n);
 }
 
 // Padded row of packed query t, or -1 if no sequence has it.
@@ -1398,7 +1515,7 @@ __global__ void __launch_bounds__(kAuxThreads, kAuxBlocksPerSm) attn_var_pre_ker
       for (int off = kLanesPerRow / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
       const long long r = (g0 + j) * kRowsPerWarp + sub;
       if (part == 0 && r < rows) {
-        const int t = (int)(r / p.H), h = (int)(r - (long long)t * p.H);
+        const int t = row_of(r, p.H), h = (int)(r - (long long)t * p.H);
         const int row = var_row(v, p.B, t);
         if (row >= 0) {
           const size_t at = (size_t)h * p.Npad + row;
@@ -1429,10 +1546,6 @@ __global__ void __launch_bounds__(kAuxThreads, kAuxBlocksPerSm) attn_var_pre_ker
       reinterpret_cast<uint4*>(p.dv)[at + i] = make_uint4(0, 0, 0, 0);
     }
   }
-  if (tid == 0) {
-    p.sched[0] = 0u;
-    p.sched[1] = 0u;
-  }
   griddep_launch_dependents();
 }
 
@@ -1442,7 +1555,51 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kAuxThreads, kAuxBlocksPerSm) attn_var_post_kernel(const __grid_constant__ BwdArgs p) {
   extern __shared__ __align__(16) uint8_t var_smem[];
   griddep_wait();
-  const VarScan v = var_scan(p, var_smem, false);
+  VarScan v;
+  v.q0 = reinterpret_cast<int*>(var_smem);
+  v.lq = v.q0 + p.B;
+  v.pbase = v.lq + p.B;
+  for (int b = threadIdx.x; b < p.B; b += kAuxThreads) {
+    const VarBwdSeq q = p.var_seq[b];
+    v.q0[b] = q.q0;
+    v.lq[b] = q.lq;
+    v.pbase[b] = q.pbase;
+  }
+  __syncthreads();
+  // dK and dV of the tiles that several items share: their parts, in order.  A
+  // block takes a quarter of the columns of a tile's dV or dK, a thread eight
+  // columns of a row at a time.
+  const long long n_units = 8ll * (int)p.sched[3];
+  for (long long u = blockIdx.x; u < n_units; u += gridDim.x) {
+    const int i = (int)(u >> 3), which = (int)(u >> 2) & 1, quarter = (int)u & 3;
+    int lo = 0, hi = p.B - 1;  // last sequence with split0 <= i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.var_seq[mid].split0 <= i) lo = mid; else hi = mid - 1;
+    }
+    const VarBwdSeq q = p.var_seq[lo];
+    const VarSplit sp(q.lq, q.lk, (int)p.sched[2], p.causal);
+    const int per = sp.nkt - sp.first_split(), h = (i - q.split0) / per;
+    const int tk = sp.first_split() + (i - q.split0) - h * per, n = sp.items(tk);
+    const float4* src = reinterpret_cast<const float4*>(
+        p.var_parts + (size_t)(q.part0 + h * sp.parts_before(sp.nkt) + sp.parts_before(tk)) * (2 * 128 * D) + which * 128 * D);
+    uint8_t* dst = reinterpret_cast<uint8_t*>(which ? p.dk : p.dv);
+    const int k0 = q.lk - 128 * (tk + 1);
+    for (int j = threadIdx.x; j < 128 * D / 32; j += kAuxThreads) {
+      const int row = j & 127, c8 = quarter * (D / 32) + (j >> 7);
+      if (k0 + row < 0) continue;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 4
+      for (int t = 0; t < n; ++t) {
+        const float4 a = src[(size_t)t * (2 * 128 * D / 4) + (2 * c8) * 128 + row];
+        const float4 b = src[(size_t)t * (2 * 128 * D / 4) + (2 * c8 + 1) * 128 + row];
+        x.x += a.x; x.y += a.y; x.z += a.z; x.w += a.w;
+        y.x += b.x; y.y += b.y; y.z += b.z; y.w += b.w;
+      }
+      *reinterpret_cast<uint4*>(dst + (((size_t)(q.k0 + k0 + row) * p.Hkv + h) * D + c8 * 8) * 2) =
+          make_uint4(pack2<BF16>(x.x, x.y), pack2<BF16>(x.z, x.w), pack2<BF16>(y.x, y.y), pack2<BF16>(y.z, y.w));
+    }
+  }
   constexpr int kU = 4;
   const long long nthreads = (long long)gridDim.x * blockDim.x;
   const long long total = (long long)p.N * p.H * D / 8;
@@ -1457,7 +1614,7 @@ __global__ void __launch_bounds__(kAuxThreads, kAuxBlocksPerSm) attn_var_post_ke
       if (idx < total) {
         const int c = (int)(idx % (D / 8)) * 8;
         const long long r = idx / (D / 8);
-        const int t = (int)(r / p.H), h = (int)(r - (long long)t * p.H);
+        const int t = row_of(r, p.H), h = (int)(r - (long long)t * p.H);
         const int row = var_row(v, p.B, t);
         in[j] = row >= 0;
         if (in[j]) {

@@ -104,10 +104,13 @@ __device__ __forceinline__ bool var_find(const FwdArgs& p, int& unit, int tile_r
   int carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    int q0 = 0, lq = 0;
-    if (b < p.B) {
+    int q0 = 0, lq = 0, k0 = 0, k1 = 0;
+    if (b < p.B) {  // (all four loads in flight at once)
+      const int q1 = p.cu_q[b + 1];
+      k0 = p.cu_k[b];
+      k1 = p.cu_k[b + 1];
       q0 = min(max(p.cu_q[b], 0), p.N);
-      lq = min(max(p.cu_q[b + 1], q0), p.N) - q0;
+      lq = min(max(q1, q0), p.N) - q0;
     }
     const int n = (lq + tile_rows - 1) / tile_rows;
     int inc = n;
@@ -119,12 +122,11 @@ __device__ __forceinline__ bool var_find(const FwdArgs& p, int& unit, int tile_r
     const uint32_t hit = __ballot_sync(0xffffffffu, unit < carry + inc);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      const int bs = b0 + src;
       unit -= carry + __shfl_sync(0xffffffffu, inc - n, src);
       vs.q0 = __shfl_sync(0xffffffffu, q0, src);
       vs.lq = __shfl_sync(0xffffffffu, lq, src);
-      vs.k0 = min(max(p.cu_k[bs], 0), p.Nk);
-      vs.lk = min(max(p.cu_k[bs + 1], vs.k0), p.Nk) - vs.k0;
+      vs.k0 = min(max(__shfl_sync(0xffffffffu, k0, src), 0), p.Nk);
+      vs.lk = min(max(__shfl_sync(0xffffffffu, k1, src), vs.k0), p.Nk) - vs.k0;
       return true;
     }
     carry += __shfl_sync(0xffffffffu, inc, 31);
@@ -164,10 +166,11 @@ __device__ __forceinline__ bool var_find(const FwdArgs& p, int& unit, int tile_r
 // stride twice, as a 128-row window (r) and as its place (s), and a tile that
 // begins at row -m of its sequence is loaded at (r = -m, s = first row), where
 // TMA fills the m rows with zeros.  So nothing of another sequence, not even an
-// infinity times a zero, enters a product.  The two query tiles of a CTA are
-// the same rows of two heads of one group where the group is even (they share
-// every K/V tile, and a short prompt fills both), else neighbouring rows of
-// one head.
+// infinity times a zero, enters a product.  A query tile holds R positions of Gp
+// heads that share a key head (row = position * Gp + head, one box of the map),
+// so that a key tile serves the group and a prompt of one token fills Gp rows of
+// a tile, not one row of Gp tiles (fwd_varlen_shape); the two tiles of a CTA are
+// neighbouring positions.
 template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false, bool VARLEN = false>
 __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ FwdArgs p) {
@@ -195,27 +198,25 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
   const int n_kv_all = (p.N + 127) / 128;
   int n0 = p.causal ? min(2 * pair + 1, n_kv_all) : n_kv_all;
   int n1 = p.causal ? min(2 * pair + 2, n_kv_all) : n_kv_all;
-  // (VARLEN) the sequence, its key tiles, and per query tile its head and the
-  // position of its first row in the sequence (negative: the ragged tile)
+  // (VARLEN) the sequence, its key tiles, the tiles' first head, and the position
+  // of each query tile's first row in the sequence (negative: the ragged tile)
   VarSeq vs{};
-  int v_nk = 0, v_head[2] = {0, 0}, v_row[2] = {0, 0};
+  int v_nk = 0, v_head = 0, v_row[2] = {0, 0};
   if constexpr (VARLEN) {
-    const int n_hb = p.head_pairs ? p.H / 2 : p.H;
-    const int hb = blockIdx.x % n_hb;
-    const int tile_rows = p.head_pairs ? 128 : 256;
+    const int n_hb = p.H / p.Gp;
     int unit = (int)(blockIdx.x / n_hb);
-    if (!var_find(p, unit, tile_rows, vs)) {  // (the grid is sized for the worst split into sequences)
+    if (!var_find(p, unit, 2 * p.R, vs)) {  // (the grid is sized for the worst split into sequences)
       if (threadIdx.x == 0) griddep_launch_dependents();
       return;
     }
     v_nk = (vs.lk + 127) / 128;
-    const int tq0 = p.head_pairs ? unit : 2 * unit + 1, tq1 = p.head_pairs ? unit : 2 * unit;
-    v_head[0] = p.head_pairs ? 2 * hb : hb;
-    v_head[1] = p.head_pairs ? 2 * hb + 1 : hb;
-    v_row[0] = vs.lq - 128 * (tq0 + 1);
-    v_row[1] = vs.lq - 128 * (tq1 + 1);
-    n1 = p.causal ? max(0, v_nk - tq1) : v_nk;
-    n0 = v_row[0] <= -128 ? 0 : (p.causal ? max(0, v_nk - tq0) : v_nk);
+    v_head = (int)(blockIdx.x - (blockIdx.x / n_hb) * n_hb) * p.Gp;
+    const int tq1 = 2 * unit, tq0 = tq1 + 1;  // counted from the end
+    v_row[0] = vs.lq - p.R * (tq0 + 1);
+    v_row[1] = vs.lq - p.R * (tq1 + 1);
+    // tile tq begins R tq positions from the end: keys nearer to it are hidden
+    n1 = p.causal ? max(0, v_nk - ((p.R * tq1) >> 7)) : v_nk;
+    n0 = v_row[0] <= -p.R ? 0 : (p.causal ? max(0, v_nk - ((p.R * tq0) >> 7)) : v_nk);
   }
   const WaitCtl wc{p.wait.status, p.wait.limit_ns};
 
@@ -254,14 +255,14 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
   auto load_q = [&](int t, int s) {
     const uint32_t dst = base + L::kQ0 + t * L::kTile + s * L::kSub;
     if constexpr (VARLEN)
-      tma_load_4d(dst, &p.tm_q, bar(L::kBarQ), s * 64, v_head[t], min(v_row[t], 0), vs.q0 + max(v_row[t], 0));
+      tma_load_4d(dst, &p.tm_q, bar(L::kBarQ), s * 64, v_head, min(v_row[t], 0), vs.q0 + max(v_row[t], 0));
     else
       tma_load_4d(dst, &p.tm_q, bar(L::kBarQ), s * 64, h, q0 + t * 128, b);
   };
   auto load_kv = [&](uint32_t dst, const CUtensorMap* m, uint32_t fb, int s, int j) {
     if constexpr (VARLEN) {
       const int k0 = vs.lk - 128 * (v_nk - j);
-      tma_load_4d(dst, m, fb, s * 64, v_head[0] / p.G, min(k0, 0), vs.k0 + max(k0, 0));
+      tma_load_4d(dst, m, fb, s * 64, v_head / p.G, min(k0, 0), vs.k0 + max(k0, 0));
     } else {
       tma_load_4d(dst, m, fb, s * 64, h, kv_tile(j) * 128, b);
     }
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
       tma_prefetch(&p.tm_q);
       tma_prefetch(&p.tm_k);
       tma_prefetch(&p.tm_v);
-      mbar_expect_tx(bar(L::kBarQ), 2 * L::kTile);
+      mbar_expect_tx(bar(L::kBarQ), VARLEN ? 2 * p.Gp * p.R * D * 2 : 2 * L::kTile);
       for (int t = 0; t < 2; ++t)
         for (int s = 0; s < L::kNSub; ++s) load_q(t, s);
       for (int i = 0; i < n_early; ++i) {  // every slot starts empty
@@ -737,7 +738,7 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
     // (VARLEN: rows count from the sequence's first one; keys too, and row i is
     // aligned with key i + diag)
     const int row_lo = VARLEN ? (t ? v_row[1] : v_row[0]) : q0 + t * 128;
-    const int row = row_lo + qd * 32 + lane;
+    const int row = VARLEN ? row_lo + (qd * 32 + lane) / p.Gp : row_lo + qd * 32 + lane;
     const int diag = VARLEN ? vs.lk - vs.lq : 0;
     const int n_t = t ? len : cnt0;  // positions this query tile takes
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
@@ -786,12 +787,17 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 128; ++i) s[i] = __float_as_uint(-INFINITY);  // block removed
       }
-      const bool need_mask = VARLEN ? (kv0 < 0 || (p.causal && kv0 + 127 > row_lo + diag))
-                                    : ((kv0 + 128 > p.N) || (p.causal && kv0 + 127 > row_lo));
+      if (VARLEN && kv0 < 0) {  // the ragged tile: keys before the sequence
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          if (kv0 + i < 0) s[i] = __float_as_uint(-INFINITY);
+      }
+      const bool need_mask =
+          VARLEN ? (p.causal && kv0 + 127 > row_lo + diag) : ((kv0 + 128 > p.N) || (p.causal && kv0 + 127 > row_lo));
       if (need_mask) {
 #pragma unroll
         for (int i = 0; i < 128; ++i)
-          if (kv0 + i >= lim || (VARLEN && kv0 + i < 0)) s[i] = __float_as_uint(-INFINITY);
+          if (kv0 + i >= lim) s[i] = __float_as_uint(-INFINITY);
       }
       if constexpr (ALIBI) {
         // s <- s * scale * log2(e) - m |row - key| (log2 units).  On a tile
@@ -899,8 +905,9 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
       // a row that saw no key (possible only under a block-sparse mask) has
       // O = 0 and LSE = -inf
       const float inv_l = l > 0.f ? (DROPOUT ? p.drop.scale : 1.f) / l : 0.f;
-      const bool valid = VARLEN ? row >= 0 : row < p.N;
-      const int hq = VARLEN ? (t ? v_head[1] : v_head[0]) : h;
+      const int v_sub = VARLEN ? (qd * 32 + lane) - (row - row_lo) * p.Gp : 0;  // head of the row in its tile
+      const bool valid = VARLEN ? row >= 0 && row < row_lo + p.R : row < p.N;
+      const int hq = VARLEN ? v_head + (valid ? v_sub : 0) : h;
       const size_t o_row = VARLEN ? (size_t)vs.q0 + (valid ? row : 0) : (size_t)b * p.N + (valid ? row : 0);
       uint8_t* orow = reinterpret_cast<uint8_t*>(p.o) + ((o_row * p.H + hq) * D) * 2;
       if constexpr (ACC) {
@@ -1020,7 +1027,7 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
         for (int bx = 0; bx < L::kNSub; ++bx) {
           const uint32_t src = base + L::kQ0 + t * L::kTile + bx * L::kSub;
           if constexpr (VARLEN)
-            tma_store_4d(&p.tm_o, src, bx * 64, t ? v_head[1] : v_head[0], 0, vs.q0 + row_lo);
+            tma_store_4d(&p.tm_o, src, bx * 64, v_head, 0, vs.q0 + row_lo);
           else
             tma_store_4d(&p.tm_o, src, bx * 64, h, row_lo, b);
         }
@@ -1045,7 +1052,7 @@ cudaError_t launch_fwd_t(const FwdArgs& a, cudaStream_t stream) {
   auto* k = attn_fwd_kernel<D, BF16, ALIBI, SPARSE, DROPOUT, ACC, VARLEN>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
-  const unsigned grid = VARLEN ? (unsigned)fwd_varlen_grid(a.N, a.B, a.H, a.head_pairs)
+  const unsigned grid = VARLEN ? (unsigned)fwd_varlen_grid(a.N, a.B, a.H, a.Gp, a.R)
                                : (unsigned)(((a.N + 255) / 256) * a.B * a.H);
   e = launch_pdl(k, grid, FwdRoles<DROPOUT>::kThreads, L::kSmem, stream, a);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -1053,13 +1060,30 @@ cudaError_t launch_fwd_t(const FwdArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
+// Heads (Gp) and positions (R, a power of two, so that the causal limit of a tile
+// is a shift) of a packed query tile.  Gp is the largest power of two in the
+// group: every row of the tile is used.  Short prompts of other groups are packed
+// whole, unused rows and all, which saves more CTAs than it wastes rows.
+void fwd_varlen_shape(int G, long long Nq, int B, int* Gp, int* R) {
+  int g = 1;
+  while (g < 128 && G % (2 * g) == 0) g *= 2;
+  int r = 128 / g;
+  if (G < 128 && Nq < 128ll * B) {
+    int up = 1;
+    while (up < G) up *= 2;
+    g = G;
+    r = 128 / up;
+  }
+  *Gp = g;
+  *R = r;
+}
+
 // Blocks for N packed queries in B sequences, whatever the lengths: a sequence
-// has at most one ragged tile, and no tile is empty.
-long long fwd_varlen_grid(long long N, int B, int H, int head_pairs) {
-  const long long rows = head_pairs ? 128 : 256;
-  long long units = N / rows + B;
+// has at most one ragged pair of tiles, and no pair is empty.
+long long fwd_varlen_grid(long long N, int B, int H, int Gp, int R) {
+  long long units = N / (2 * R) + B;
   if (units > N) units = N;
-  return units * (head_pairs ? H / 2 : H);
+  return units * (H / Gp);
 }
 
 int fwd_smem_bytes(int d) {

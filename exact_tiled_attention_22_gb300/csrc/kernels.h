@@ -63,16 +63,17 @@ struct FwdArgs {
   int debug_flags;
   WaitCtlHost wait;
   // Packed variant (attn_varlen_fwd): B sequences of N queries and Nk keys in
-  // all, H query heads, G to a key head; the maps are (d, head, row, place).
+  // all, H query heads, G to a key head; query tiles of R positions of Gp heads;
+  // the maps are (d, head, row, place).
   const int* cu_q;
   const int* cu_k;
-  int Nk, G;
-  int head_pairs;  // the two query tiles of a CTA are two heads (G even)
+  int Nk, G, Gp, R;
 };
 int fwd_smem_bytes(int d);
-long long fwd_varlen_grid(long long N, int B, int H, int head_pairs);
-cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t stream);
+void fwd_varlen_shape(int G, long long Nq, int B, int* Gp, int* R);
+long long fwd_varlen_grid(long long N, int B, int H, int Gp, int R);
 cudaError_t launch_fwd_varlen(const FwdArgs& a, cudaStream_t stream);
+cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t stream);
 
 // Largest N / 128 the block-sparse variants take.
 constexpr int kMaxSparseTiles = 512;
@@ -84,9 +85,12 @@ constexpr int kMaxSparseTiles = 512;
 struct VarBwdSeq {
   int q0, lq, k0, lk;  // first rows and lengths
   int pbase;           // padded row of query 0 (a multiple of 64 rows before its last step's end)
-  int pad[3];
+  int part0, split0;   // partial tiles and split tiles before this sequence's
+  int pad;
 };
 constexpr int kVarMaxB = 8192;
+constexpr int kVarChunks = 304;                 // equal chunks a batch's steps are cut into
+constexpr int kVarMaxParts = 2 * kVarChunks;    // a split tile of n steps has < 2 n / (all steps / kVarChunks) parts
 
 struct BwdArgs {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;  // q/do boxes of bwd_q_rows(d) rows, k/v 128 rows
@@ -125,6 +129,7 @@ struct BwdArgs {
   int Nk, G, Hkv;
   VarBwdSeq* var_seq;  // [B]
   int* var_items;      // [B + 1] items before each sequence
+  float* var_parts;    // [kVarMaxParts][dV, dK][d / 4][128][4] partial tiles
 };
 cudaError_t launch_var_pre(const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_var_post(const BwdArgs& a, cudaStream_t stream);

@@ -365,7 +365,7 @@ int attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float*
                     long long Tk, int Hq, int Hkv, int d, long long q_stride,
                     long long k_stride, long long v_stride, float scale, int causal,
                     attn_dtype_t dtype, void* stream);
-size_t attn_varlen_bwd_workspace_size(int B, long long Tq, int Hq, int d);
+size_t attn_varlen_bwd_workspace_size(int B, long long Tq, int Hq, int Hkv, int d);
 int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o,
                     const float* lse, const void* dO, void* dq, void* dk, void* dv,
                     const int32_t* cu_q, const int32_t* cu_k, int B, long long Tq,

@@ -202,7 +202,7 @@ def test_captured_and_on_another_stream():
     c = offsets(lens[0])
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    ws = torch.empty(attn.attn_varlen_bwd_workspace_size(3, T, Hq, d), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(attn.attn_varlen_bwd_workspace_size(3, T, Hq, H, d), dtype=torch.uint8, device="cuda")
 
     def step():
         o, lse = attn.varlen_fwd(q, k, v, c, c, 0.125, True)
@@ -228,10 +228,40 @@ def test_captured_and_on_another_stream():
     assert attn.attn_status() == 0
 
 
+SPLIT = [
+    # long enough that key tiles are cut into several items: at the causal limit,
+    # in a prefix (more keys than queries), without a mask; odd numbers of steps
+    ([4500], [4500], 1, 1, 64, "fp16", True),
+    ([2300, 100, 1100], [2300, 100, 1100], 8, 1, 128, "bf16", True),
+    ([1900, 333], [3500, 2000], 6, 2, 64, "bf16", True),
+    ([1665, 40], [1500, 700], 4, 1, 128, "fp16", False),
+    ([2113], [1000], 3, 1, 64, "bf16", True),
+]
+
+
+@pytest.mark.parametrize("case", SPLIT, ids=lambda c: f"{c[0][0]}-{c[2]}x{c[3]}d{c[4]}{c[5]}{'c' if c[6] else ''}")
+def test_split_key_tiles(case):
+    """Gradients of batches whose key tiles are shared by several work items, with
+    a workspace full of NaN."""
+    from exact_tiled_attention_22_gb300 import attn
+    lens_q, lens_k, Hq, H, d, dtype, causal = case
+    q, k, v, do = draw(lens_q, lens_k, Hq, H, d, dtype, seed=sum(lens_q))
+    cq, ck = offsets(lens_q), offsets(lens_k)
+    n = attn.attn_varlen_bwd_workspace_size(len(lens_q), sum(lens_q), Hq, H, d)
+    ws = torch.full((n // 4 + 1,), math.nan, device="cuda").view(torch.uint8)
+    o, lse = attn.varlen_fwd(dev(q), dev(k), dev(v), cq, ck, None, causal)
+    grads = attn.varlen_bwd(dev(q), dev(k), dev(v), o, lse, dev(do), cq, ck, None, causal, ws=ws)
+    attn.check(attn.attn_status())
+    ref = plain64.packed(q.double(), k.double(), v.double(), cu(lens_q), cu(lens_k), d ** -0.5, causal, dtype,
+                         do.double())
+    for name, got in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+        plain64.check(got, *ref[name], name)
+
+
 def test_repeats_are_equal():
     """O, LSE, dK, dV do not depend on the order in which blocks finish."""
     from exact_tiled_attention_22_gb300 import attn
-    lens = [900, 40, 333]
+    lens = [3900, 40, 333]
     q, k, v, do = (x.cuda() for x in draw(lens, lens, 8, 2, 128, "bf16", seed=40))
     c = offsets(lens)
     first = None

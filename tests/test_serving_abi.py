@@ -108,7 +108,7 @@ def test_varlen_fwd_refuses(A, kw, code):
     (dict(ws=WS + 16), -3), (dict(dq=P[5]), -1), (dict(dk=P[8]), -1), (dict(ws=P[3]), -1)])
 def test_varlen_bwd_refuses(A, kw, code):
     base = dict(q=P[0], k=P[1], v=P[2], o=P[3], lse=P[4], dO=P[5], dq=P[6], dk=P[7], dv=P[8], cu_q=P[9], cu_k=P[10],
-                ws=WS, ws_bytes=A.attn_varlen_bwd_workspace_size(3, 100, 4, 64), **SIZES)
+                ws=WS, ws_bytes=A.attn_varlen_bwd_workspace_size(3, 100, 4, 2, 64), **SIZES)
     assert call(A.lib.attn_varlen_bwd, BWD, base, **kw) == code and A.last_error()
 
 
@@ -123,10 +123,13 @@ def test_nothing_to_do_is_no_error(A):
 
 def test_workspace_sizes(A):
     f = A.attn_varlen_bwd_workspace_size
-    assert f(0, 10, 1, 64) == 0 and f(1, -1, 1, 64) == 0 and f(1, 10, 0, 64) == 0 and f(1, 10, 1, 96) == 0
+    assert f(0, 10, 1, 1, 64) == 0 and f(1, -1, 1, 1, 64) == 0 and f(1, 10, 0, 1, 64) == 0
+    assert f(1, 10, 1, 1, 96) == 0 and f(1, 10, 3, 2, 64) == 0
     # three fp32 parts over every head's rows, padded by at most 64 a sequence
-    assert f(5, 1000, 8, 128) >= 8 * 1000 * (128 + 2) * 4
-    assert f(5, 1000, 8, 128) <= 8 * (1000 + 5 * 64) * (128 + 2) * 4 + 4096
+    assert f(5, 1000, 8, 8, 128) >= 8 * 1000 * (128 + 2) * 4
+    assert f(5, 1000, 8, 8, 128) <= 8 * (1000 + 5 * 64) * (128 + 2) * 4 + 4096
+    # and, where key tiles may be split, a fixed number of partial dK, dV tiles
+    assert f(1, 100000, 2, 1, 64) - 2 * 100000 * (64 + 2) * 4 <= 608 * 2 * 128 * 64 * 4 + 100000
     g = A.attn_kv8_decode_workspace_size
     assert g(0, 1, 1, 64) == 0 and g(1, 3, 2, 64) == 0 and g(1, 2, 2, 60) == 0 and g(1, 8, 1, 128) > 0
 
