@@ -1484,10 +1484,12 @@ __global__ void __launch_bounds__(kAuxThreads, kAuxBlocksPerSm) attn_var_pre_ker
   for (long long i = tid; i < nz; i += nthreads) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   const VarScan v = var_scan(p, var_smem, blockIdx.x == 0);
 
+  // (block 0, which lays out the work, takes no rows)
   const long long rows = (long long)p.N * p.H;
   const long long groups = (rows + kRowsPerWarp - 1) / kRowsPerWarp;
   const int sub = lane / kLanesPerRow, part = lane % kLanesPerRow;
-  for (long long g0 = gw * kU; g0 < groups; g0 += nwarps * kU) {
+  constexpr int kW0 = kAuxThreads / 32;  // warps of block 0
+  for (long long g0 = (gw - kW0) * kU; gw >= kW0 && g0 < groups; g0 += (nwarps - kW0) * kU) {
     uint4 ov[kU], gv[kU];
 #pragma unroll
     for (int j = 0; j < kU; ++j) {
@@ -1500,6 +1502,23 @@ __global__ void __launch_bounds__(kAuxThreads, kAuxBlocksPerSm) attn_var_pre_ker
         gv[j] = ov[j];
       }
     }
+    // Lane j of a row's lanes looks after its j-th group of the four: the row's
+    // place and LSE, on their way while O and dO are.
+    static_assert(kLanesPerRow >= kU, "a lane to a group");
+    long long at = -1;
+    float l = 0.f;
+    if (part < kU) {
+      const long long r = (g0 + part) * kRowsPerWarp + sub;
+      if (r < rows) {
+        const int t = row_of(r, p.H), h = (int)(r - (long long)t * p.H);
+        const int row = var_row(v, p.B, t);
+        if (row >= 0) {
+          at = (long long)h * p.Npad + row;
+          l = p.lse[(size_t)h * p.N + t];
+        }
+      }
+    }
+    float mine = 0.f;
 #pragma unroll
     for (int j = 0; j < kU; ++j) {
       const uint32_t* ow = &ov[j].x;
@@ -1513,18 +1532,12 @@ __global__ void __launch_bounds__(kAuxThreads, kAuxBlocksPerSm) attn_var_pre_ker
       }
 #pragma unroll
       for (int off = kLanesPerRow / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-      const long long r = (g0 + j) * kRowsPerWarp + sub;
-      if (part == 0 && r < rows) {
-        const int t = row_of(r, p.H), h = (int)(r - (long long)t * p.H);
-        const int row = var_row(v, p.B, t);
-        if (row >= 0) {
-          const size_t at = (size_t)h * p.Npad + row;
-          const float l = p.lse[(size_t)h * p.N + t];
-          const bool none = l == -INFINITY;  // a query that sees no key: its P is 0
-          p.dvec[at] = none ? 0.f : acc;
-          p.lse2[at] = none ? -INFINITY : -l * kLog2e;
-        }
-      }
+      if (part == j) mine = acc;
+    }
+    if (at >= 0) {
+      const bool none = l == -INFINITY;  // a query that sees no key: its P is 0
+      p.dvec[at] = none ? 0.f : mine;
+      p.lse2[at] = none ? -INFINITY : -l * kLog2e;
     }
   }
   // padding rows (fewer than 64 to a sequence and head), keys without queries
