@@ -402,12 +402,12 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
   volatile int* npos_s = reinterpret_cast<volatile int*>(sbase + L::kNPos);
   volatile int* var_slot = reinterpret_cast<volatile int*>(sbase + L::kQBits);
   auto var_publish = [&](int slot, int item) {
-    int lo = 0, hi = p.B - 1;  // last sequence with var_items <= item
+    int lo = 0, hi = p.B - 1;  // last sequence (in work order) with var_items <= item
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (p.var_items[mid] <= item) lo = mid; else hi = mid - 1;
     }
-    const VarBwdSeq q = p.var_seq[lo];
+    const VarBwdSeq q = p.var_seq[p.var_order[lo]];
     const VarSplit sp(q.lq, q.lk, var_a, p.causal);
     const int r = item - p.var_items[lo], n_head = sp.items_before(sp.nkt);  // items of one key head
     const int gh = bwd_head_group(q.lq, D * p.G, p.Hkv);
@@ -1360,8 +1360,8 @@ struct VarScan {
   int* pbase;  // [B] padded row of query 0
 };
 
-// Also leaves, from CTA 0, what the other kernels read: p.var_seq, p.var_items,
-// the work counter, the split `a` and the number of split tiles (p.sched).
+// Also leaves, from CTA 0, what the other kernels read: p.var_seq, p.var_order,
+// p.var_items, the work counter, the split `a` and the number of split tiles (p.sched).
 __device__ __forceinline__ VarScan var_scan(const BwdArgs& p, uint8_t* smem, bool publish) {
   __shared__ long long wsum[8];
   VarScan v;
@@ -1419,24 +1419,58 @@ __device__ __forceinline__ VarScan var_scan(const BwdArgs& p, uint8_t* smem, boo
     // chunks of 2 G a steps: an equal share of kVarChunks, no less than 32
     const long long total = c_steps * p.H, unit = 2ll * p.G;
     const int a = (int)max((16ll + p.G - 1) / p.G, (total + kVarChunks * unit - 1) / (kVarChunks * unit));
+    // Sequences with the most steps first, in half octaves (counted, then
+    // placed): the short ones fill the end of the kernel.
+    __shared__ int hist[128];
+    auto lens_of = [&](int b, int& k0, int& lq, int& lk) {
+      k0 = min(max(p.cu_k[b], 0), p.Nk);
+      lk = min(max(p.cu_k[b + 1], k0), p.Nk) - k0;
+      lq = v.lq[b];
+    };
+    auto bucket = [&](int lq, int lk) -> int {
+      const int nqs = (lq + 63) >> 6, nkt = (lk + 127) >> 7, n1 = p.causal ? min(nkt, nqs >> 1) : 0;
+      const float steps = (float)n1 * (float)(n1 + 1) + (float)(nkt - n1) * (float)nqs;
+      return 127 - min(127, (int)(2.f * __log2f(steps + 1.f)));
+    };
+    for (int i = threadIdx.x; i < 128; i += kAuxThreads) hist[i] = 0;
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.B; b += kAuxThreads) {
+      int k0, lq, lk;
+      lens_of(b, k0, lq, lk);
+      atomicAdd(&hist[bucket(lq, lk)], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int at = 0;
+      for (int i = 0; i < 128; ++i) {
+        const int n = hist[i];
+        hist[i] = at;
+        at += n;
+      }
+    }
+    __syncthreads();
     long long c_item = 0, c_part = 0, c_split = 0;
     for (int b0 = 0; b0 < p.B; b0 += kAuxThreads) {
       const int b = b0 + threadIdx.x;
       int k0 = 0, lk = 0, lq = 0;
       if (b < p.B) {
-        k0 = min(max(p.cu_k[b], 0), p.Nk);
-        lk = min(max(p.cu_k[b + 1], k0), p.Nk) - k0;
-        lq = v.lq[b];
+        lens_of(b, k0, lq, lk);
+        p.var_order[atomicAdd(&hist[bucket(lq, lk)], 1)] = b;
       }
       const VarSplit sp(lq, lk, a, p.causal);
-      const long long items = lq > 0 ? (long long)sp.items_before(sp.nkt) * p.Hkv : 0;
       const long long parts = lq > 0 ? (long long)sp.parts_before(sp.nkt) * p.Hkv : 0;
       const long long split = lq > 0 ? (long long)max(0, sp.nkt - sp.first_split()) * p.Hkv : 0;
-      const long long is = scan(items, c_item), pp = scan(parts, c_part), ss = scan(split, c_split);
-      if (b < p.B) {
-        p.var_seq[b] = VarBwdSeq{v.q0[b], lq, k0, lk, v.pbase[b], (int)pp, (int)min(ss, (long long)INT_MAX), 0};
-        p.var_items[b] = (int)min(is, (long long)INT_MAX);
-      }
+      const long long pp = scan(parts, c_part), ss = scan(split, c_split);
+      if (b < p.B) p.var_seq[b] = VarBwdSeq{v.q0[b], lq, k0, lk, v.pbase[b], (int)pp, (int)min(ss, (long long)INT_MAX), 0};
+    }
+    __syncthreads();  // (var_order is complete; this block wrote it)
+    for (int i0 = 0; i0 < p.B; i0 += kAuxThreads) {
+      const int i = i0 + threadIdx.x;
+      int k0 = 0, lk = 0, lq = 0;
+      if (i < p.B) lens_of(p.var_order[i], k0, lq, lk);
+      const VarSplit sp(lq, lk, a, p.causal);
+      const long long is = scan(lq > 0 ? (long long)sp.items_before(sp.nkt) * p.Hkv : 0, c_item);
+      if (i < p.B) p.var_items[i] = (int)min(is, (long long)INT_MAX);
     }
     if (threadIdx.x == 0) {
       p.var_items[p.B] = (int)min(c_item, (long long)INT_MAX);

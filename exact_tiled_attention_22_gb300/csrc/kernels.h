@@ -128,7 +128,8 @@ struct BwdArgs {
   const int* cu_k;
   int Nk, G, Hkv;
   VarBwdSeq* var_seq;  // [B]
-  int* var_items;      // [B + 1] items before each sequence
+  int* var_order;      // [B] sequences in the order of the work
+  int* var_items;      // [B + 1] items before each of them
   float* var_parts;    // [kVarMaxParts][dV, dK][d / 4][128][4] partial tiles
 };
 cudaError_t launch_var_pre(const BwdArgs& a, cudaStream_t stream);
