@@ -833,7 +833,7 @@ int attn_kv8_append(const void* k, const void* v, long long k_stride, long long 
   a.x_stride[0] = k_stride; a.x_stride[1] = v_stride;
   a.T = T;
   a.n_slots = (long long)P * page;
-  a.H = H; a.d = d; a.page = page; a.bf16 = dtype == ATTN_BF16;
+  a.H = H; a.d = d; a.page_shift = page_shift_of(page); a.bf16 = dtype == ATTN_BF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = timed(attn::kKKv8Append, s, [&] { return attn::launch_kv8_append(a, dev->sms, s); });
   return e != cudaSuccess ? cuda_fail(e, "attn_kv8_append launch") : ATTN_OK;

@@ -77,46 +77,50 @@ __global__ void __launch_bounds__(kAppThreads) attn_kv8_append_kernel(const __gr
   constexpr int kTok = 32 / kLanes;      // tokens per warp load
   constexpr int kU = 8;
   const int lane = threadIdx.x & 31, sub = lane / kLanes, part = lane % kLanes;
-  const long long gw = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  // (T H < 2^30: the warp's number has 31 bits; pages are powers of two)
+  const unsigned gw = (unsigned)(((unsigned long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5);
   const int kv = (int)(gw & 1);
-  const long long rest = gw >> 1;
-  const int h = (int)(rest % p.H);
-  const long long t0 = rest / p.H * chunk;
-  const int ps = p.page;
+  const unsigned ci = (gw >> 1) / (unsigned)p.H;
+  const int h = (int)((gw >> 1) - ci * (unsigned)p.H);
+  const long long t0 = (long long)ci * chunk;
+  const int ps = 1 << p.page_shift;
   auto slot_at = [&](long long t) -> long long {
     const long long s = t >= 0 && t < p.T ? p.slots[t] : -1;
     return s >= 0 && s < p.n_slots ? s : -1;
   };
-  uint32_t starts = 0;
-  long long my_slot = -1;
-  {
-    const long long t = t0 + lane;
-    bool st = false;
-    if (lane < chunk && t < p.T) {
-      my_slot = slot_at(t);
-      st = my_slot >= 0 && (slot_at(t - 1) != my_slot - 1 || my_slot % ps == 0);
-    }
-    starts = __ballot_sync(0xffffffffu, st);
-  }
+  // A lane looks at one token: whether it goes on with the run of the token
+  // before it, or begins one (only the chunk's own beginnings are taken).
+  const long long my_slot = slot_at(t0 + lane);
+  long long prev = __shfl_up_sync(0xffffffffu, my_slot, 1);
+  if (lane == 0) prev = slot_at(t0 - 1);
+  const bool goes_on = my_slot >= 0 && prev == my_slot - 1 && (my_slot & (ps - 1)) != 0;
+  const uint32_t on = __ballot_sync(0xffffffffu, goes_on);
+  uint32_t starts = __ballot_sync(0xffffffffu, my_slot >= 0 && !goes_on && lane < chunk);
   const uint8_t* x = static_cast<const uint8_t*>(p.x[kv]);
   while (starts) {
     const int bit = __ffs(starts) - 1;
     starts &= starts - 1;
     const long long t = t0 + bit, slot = __shfl_sync(0xffffffffu, my_slot, bit);
-    const long long page = slot / ps;
-    const int first = (int)(slot - page * ps);
-    int n = 1;
-    for (int i0 = 1; first + i0 < ps; i0 += 32) {  // length of the run
-      const int i = i0 + lane;
-      const uint32_t in = __ballot_sync(0xffffffffu, first + i < ps && slot_at(t + i) == slot + i);
-      const int k = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
-      n += k;
-      if (k < 32) break;
+    const long long page = slot >> p.page_shift;
+    const int first = (int)(slot & (ps - 1));
+    // length of the run: seen above, or beyond the 32 tokens
+    int n = 1 + __ffs(~(on >> bit >> 1)) - 1;
+    if (bit + n >= 32) {
+      n = 32 - bit;
+      for (; first + n < ps; n += 32) {
+        const int i = n + lane;
+        const uint32_t in = __ballot_sync(0xffffffffu, first + i < ps && slot_at(t + i) == slot + i);
+        if (in != 0xffffffffu) {
+          n += __ffs(~in) - 1;
+          break;
+        }
+      }
+      n = min(n, ps - first);
     }
     const uint8_t* src = x + ((t * p.x_stride[kv]) + (long long)h * D) * 2 + part * 16;
     const long long row_bytes = p.x_stride[kv] * 2;
     float* scale = p.scale[kv] + page * p.H + h;
-    uint8_t* dst = p.cache[kv] + ((page * p.H + h) * ps) * (long long)D;
+    uint8_t* dst = p.cache[kv] + ((page * p.H + h) << p.page_shift) * D;
     const float old = first > 0 ? *scale : 0.f;
     uint4 v[kU];
     float amax = 0.f;
@@ -188,7 +192,7 @@ template <int D, int RP, int NP>
 struct Kv8Layout {
   static constexpr int N = (RP * NP + 15) / 16 * 16;  // MMA columns (M = 128 needs a multiple of 16)
   static constexpr int kTile = 128 * D;
-  static constexpr int kCtas = RP <= 8 ? 3 : 2;       // CTAs to an SM
+  static constexpr int kCtas = RP <= 4 ? 3 : 2;       // CTAs to an SM
   static constexpr int kStages = (D == 128 ? 1 : 2) * (kCtas == 3 ? 2 : 3);
   static constexpr int kQ = 0;
   static constexpr int kP = kQ + up1024(N * D);
@@ -895,7 +899,7 @@ int kv8_rows(int R) { return R <= 4 ? 4 : (R <= 8 ? 8 : 16); }
 
 // All CTAs resident at once, no more than there can be tiles.
 int kv8_grid(int rp, int sms, long long max_units) {
-  long long g = (rp <= 8 ? 3ll : 2ll) * sms;
+  long long g = (rp <= 4 ? 3ll : 2ll) * sms;
   if (g > kKv8MaxCtas) g = kKv8MaxCtas;
   if (g > max_units) g = max_units;
   return (int)(g < 1 ? 1 : g);
@@ -921,8 +925,9 @@ cudaError_t launch_kv8_merge(const Kv8DecArgs& a, cudaStream_t stream) {
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int sms, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
   // A warp per token, head and tensor while that is few warps (decoding
-  // steps: every token starts a run of its own); a warp per 16 tokens above.
-  const int chunk = a.T * a.H * 2 <= 64ll * sms ? 1 : 16;
+  // steps: every token starts a run of its own); a warp per 32 tokens above (31749
+  // tokens of 4 heads, d = 64: 12.8 us against 13.8 with 16 and 17.3 with 8).
+  const int chunk = a.T * a.H * 2 <= 64ll * sms ? 1 : 32;
   const long long warps = (a.T + chunk - 1) / chunk * a.H * 2;
   const unsigned grid = (unsigned)((warps * 32 + kAppThreads - 1) / kAppThreads);
   cudaLaunchConfig_t cfg = {};

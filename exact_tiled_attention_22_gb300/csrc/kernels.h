@@ -200,7 +200,7 @@ struct Kv8AppendArgs {
   const long long* slots;   // [T]
   long long x_stride[2];
   long long T, n_slots;     // n_slots = P * page
-  int H, d, page, bf16;
+  int H, d, page_shift, bf16;
 };
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int sms, cudaStream_t stream);
 
