@@ -441,7 +441,8 @@ def decode(q, k, v, scale=None, causal=False, ws=None, stream=None, alibi=None):
 # A decoding step's calls are short (the kernels take a few microseconds, the
 # host's part several times that), so these wrappers look at each tensor once,
 # with the cheapest tests there are, and make few torch calls: on the GPU's Grace
-# host each allocation or view costs 2-4 us among others, each test 0.1.
+# host each allocation or view costs 2-4 us among others, each test 0.1.  Each
+# takes stream=, the stream to run on instead of the current one.
 def _want(t, name, dtype, shape, index):
     """t is a contiguous tensor of this type and shape on CUDA device `index`."""
     if (t.dtype is not dtype or t.shape != shape or t.get_device() != index or index < 0
@@ -450,22 +451,36 @@ def _want(t, name, dtype, shape, index):
                          f"device with the others, got {list(t.shape)} {t.dtype} on {t.device}")
 
 
-def _run(index, stream, fn, *args):
+def _run(index, fn, *args):
     """fn(*args, stream) with CUDA device `index` current (the library acts on the
-    current device; a None stream is that device's current one)."""
+    current device), on that device's current stream."""
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
-            return _run(index, stream, fn, *args)
-    if stream is None and _raw_stream is not None:
-        rc = fn(*args, _raw_stream(index))
-    else:
-        rc = fn(*args, _stream(stream))
+            return _run(index, fn, *args)
+    rc = fn(*args, _raw_stream(index) if _raw_stream is not None else _stream(None))
     if rc:
         check(rc)
 
 
+def _on_stream(f):
+    """A `stream` argument (a torch stream or a handle) is made the current stream
+    for the call, so that what the call allocates belongs to it."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        if isinstance(stream, int):
+            dev = args[0].device
+            stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
+                      else torch.cuda.default_stream(dev))
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
+@_on_stream
 def pages_extend(lens, add, block_table, free_pages, free_count, page, max_new, new_lens=None,
-                 free_left=None, stream=None):
+                 free_left=None):
     """Pages and slots for add[b] new tokens of each request (attn_pages_extend).
     lens, add: int32 [B]; block_table: int32 [B, width], updated in place;
     free_pages: int32 [cap], a stack of free page ids, free_count: int32 [1];
@@ -488,15 +503,16 @@ def pages_extend(lens, add, block_table, free_pages, free_count, page, max_new, 
     new_lens = new if new_lens is None else new_lens
     free_left = left if free_left is None else free_left
     slots = torch.empty(max_new, dtype=torch.int64, device=lens.device)
-    _run(dev, stream, lib.attn_pages_extend, lens.data_ptr(), add.data_ptr(), B,
+    _run(dev, lib.attn_pages_extend, lens.data_ptr(), add.data_ptr(), B,
          block_table.data_ptr(), width, free_pages.data_ptr(), free_count.data_ptr(), cap, page,
          max_new, new_lens.data_ptr(), granted.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
          free_left.data_ptr())
     return new_lens, granted, cu_new, slots, free_left
 
 
+@_on_stream
 def pages_release(lens, finished, block_table, free_pages, free_count, page, new_lens=None,
-                  free_left=None, stream=None):
+                  free_left=None):
     """Pages of the requests with finished[b] != 0 (int32 [B]) go back onto the
     stack free_pages, written in place (attn_pages_release).  Returns (new_lens, free_left)."""
     (B, width), (cap,) = block_table.shape, free_pages.shape
@@ -510,7 +526,7 @@ def pages_release(lens, finished, block_table, free_pages, free_count, page, new
     free_left = torch.empty_like(free_count) if free_left is None else free_left
     _want(new_lens, "new_lens", i32, (B,), dev)
     _want(free_left, "free_left", i32, (1,), dev)
-    _run(dev, stream, lib.attn_pages_release, lens.data_ptr(), finished.data_ptr(), B,
+    _run(dev, lib.attn_pages_release, lens.data_ptr(), finished.data_ptr(), B,
          block_table.data_ptr(), width, free_pages.data_ptr(), free_count.data_ptr(), cap, page,
          new_lens.data_ptr(), free_left.data_ptr())
     return new_lens, free_left
@@ -541,7 +557,8 @@ def _cache(k_cache, v_cache, k_scale, v_scale, dev):
     return shape
 
 
-def kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
+@_on_stream
+def kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale):
     """Rounds new keys and values [T, H, d] into their slots (int64 [T]) of the
     8-bit cache [P, H, page, d] with scales [P, H], in place (attn_kv8_append).
     k and v may be slices of a wider projection (any token stride)."""
@@ -550,7 +567,7 @@ def kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
     T = k.shape[0]
     ks, vs = _packed(k, "k", k.dtype, (T, H, d), dev), _packed(v, "v", k.dtype, (T, H, d), dev)
     _want(slots, "slots", torch.int64, (T,), dev)
-    _run(dev, stream, lib.attn_kv8_append, k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T,
+    _run(dev, lib.attn_kv8_append, k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T,
          H, d, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P,
          page, dtype_code(k.dtype))
 
@@ -560,8 +577,9 @@ def _kv8_workspace_size(Nq, Hq, H, d):
     return attn_kv8_decode_workspace_size(Nq, Hq, H, d)
 
 
+@_on_stream
 def kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=None, causal=True,
-               ws=None, stream=None):
+               ws=None):
     """(o, lse) of q [B, Nq, Hq, d], the last Nq tokens of every request, against
     the 8-bit cache (attn_kv8_decode); lens counts the Nq tokens."""
     dev = q.get_device()
@@ -578,7 +596,7 @@ def kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=N
         ws = torch.empty(_kv8_workspace_size(Nq, Hq, H, d), dtype=torch.uint8, device=q.device)
     elif ws.get_device() != dev:
         raise ValueError(f"ws is on {ws.device}")
-    _run(dev, stream, lib.attn_kv8_decode, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    _run(dev, lib.attn_kv8_decode, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
          k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
          o.data_ptr(), lse.data_ptr(), B, Nq, Hq, H, d, P, page, width, scale, 1 if causal else 0,
          code, ws.data_ptr(), ws.numel() * ws.element_size())
@@ -597,7 +615,8 @@ def _packed_args(q, k, v, cu_q, cu_k):
     return dev, (n - 1, Tq, Tk, Hq, Hkv, d, qs, ks, vs)
 
 
-def varlen_fwd(q, k, v, cu_q, cu_k, scale=None, causal=False, o=None, stream=None):
+@_on_stream
+def varlen_fwd(q, k, v, cu_q, cu_k, scale=None, causal=False, o=None):
     """(o, lse [Hq, Tq]) of packed sequences: q [Tq, Hq, d], k, v [Tk, Hkv, d]
     fp16/bf16 CUDA tensors (any token stride that is a multiple of d), cu_q, cu_k
     int32 [B + 1] row offsets on the device (attn_varlen_fwd).  o: an output to
@@ -611,13 +630,13 @@ def varlen_fwd(q, k, v, cu_q, cu_k, scale=None, causal=False, o=None, stream=Non
     else:
         _want(o, "o", q.dtype, (Tq, Hq, d), dev)
     lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
-    _run(dev, stream, lib.attn_varlen_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+    _run(dev, lib.attn_varlen_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
          lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), *sizes, scale, 1 if causal else 0, code)
     return o, lse
 
 
-def varlen_bwd(q, k, v, o, lse, do, cu_q, cu_k, scale=None, causal=False, ws=None, grads=None,
-               stream=None):
+@_on_stream
+def varlen_bwd(q, k, v, o, lse, do, cu_q, cu_k, scale=None, causal=False, ws=None, grads=None):
     """(dq, dk, dv) for the varlen_fwd that produced (o, lse).  grads: three
     contiguous tensors to write into (rows of no sequence are left as they are)."""
     dev, sizes = _packed_args(q, k, v, cu_q, cu_k)
@@ -641,7 +660,7 @@ def varlen_bwd(q, k, v, o, lse, do, cu_q, cu_k, scale=None, causal=False, ws=Non
                          dtype=torch.uint8, device=q.device)
     elif ws.get_device() != dev:
         raise ValueError(f"ws is on {ws.device}")
-    _run(dev, stream, lib.attn_varlen_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+    _run(dev, lib.attn_varlen_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
          lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
          cu_q.data_ptr(), cu_k.data_ptr(), *sizes, scale, 1 if causal else 0, code, ws.data_ptr(),
          ws.numel() * ws.element_size())

@@ -415,14 +415,17 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
           __syncwarp();
           if (lane < n_here) {
             const uint32_t k = base + L::kKV + s * 2 * L::kTile + lane * page_rows * D;
-            // (a page id outside the cache: TMA fills zeros, the scale is page 0's)
+            // (a page id outside the cache reads as zeros, its scales too)
             const bool in = here >= 0 && here < p.P;
             const int c2 = in ? here * p.H + h : -1;
-            const size_t si = in ? (size_t)here * p.H + h : (size_t)h;
+            const size_t si = in ? (size_t)here * p.H + h : 0;
+            const uint32_t sn = in ? 4 : 0;  // bytes read; the rest of the four are zeros
             tma_load_3d(k, &p.tm_k, bar(L::kBarKFull + s), 0, 0, c2);
             const uint32_t sc = base + L::kScale + s * 64 + lane * 4;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sc), "l"(p.k_scale + si) : "memory");
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sc + 32), "l"(p.v_scale + si) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sc), "l"(p.k_scale + si), "r"(sn)
+                         : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sc + 32), "l"(p.v_scale + si), "r"(sn)
+                         : "memory");
             tma_load_3d(k + L::kTile, &p.tm_v, bar(L::kBarVFull + s), 0, 0, c2);
           }
           asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar(L::kBarKFull + s)) : "memory");
@@ -618,7 +621,8 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
           for (int c = 0; c < N; c += 16) tmem_ld16(tS + (g & 1) * N + c, r_ + c);
           const float* sc = reinterpret_cast<const float*>(sbase + L::kScale + st * 64);
           const bool live = kv0 + kl < len;
-          const float ks = sc[kl >> p.page_shift], vs = live ? sc[8 + (kl >> p.page_shift)] : 1.f;
+          const float ks = sc[kl >> p.page_shift], vs_ = sc[8 + (kl >> p.page_shift)];
+          const float vs = live && vs_ != 0.f ? vs_ : 1.f;
           lv = __log2f(vs);
           inv_vs = 1.f / vs;
           tmem_ld_wait();

@@ -287,6 +287,53 @@ def test_two_calls_at_once_and_repeats():
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
+def test_pages_that_are_not_there_read_as_zeros():
+    """Page ids outside the cache within a request's length: zero keys and values
+    (the scales of page 0 may be anything)."""
+    from exact_tiled_attention_22_gb300 import attn
+    lens = [150]
+    q, kc, vc, ks, vs, table = problem(lens, 1, 4, 2, 64, 16, "bf16", seed=14)
+    gone = [1, 4, 7]
+    zk, zv = kc.clone(), vc.clone()
+    for j in gone:
+        zk.view(torch.uint8)[table[0, j]] = 0
+        zv.view(torch.uint8)[table[0, j]] = 0
+    (ro, bo), (rl, bl) = plain64.cached(q.double(), zk.double(), zv.double(), ks.double(), vs.double(), table, lens,
+                                        0.125, True, "bf16")
+    spare = [p for p in range(kc.shape[0]) if p not in table[0].tolist()][0]
+    bad = table.clone()
+    # page 0's scales are NaN, and the pages that are not there have ids -1, P, 2^31 - 1
+    keep = bad[0] == 0
+    if keep.any():  # (page 0 is in use: its contents move to a spare page)
+        for c in (kc, vc, ks, vs):
+            c[spare] = c[0].clone()
+        bad[0][keep] = spare
+    ks[0], vs[0] = math.nan, math.nan
+    for j, i in zip(gone, (-1, kc.shape[0], 2 ** 31 - 1)):
+        bad[0, j] = i
+    o, lse = attn.kv8_decode(q.cuda(), kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda(), bad.cuda(),
+                             torch.tensor(lens, dtype=torch.int32).cuda(), 0.125)
+    plain64.check(lse, rl, bl, "lse")
+    plain64.check(o, ro, bo, "o")
+
+
+def test_stream_argument():
+    """stream= as a torch stream and as a handle; what the call allocates belongs
+    to that stream."""
+    from exact_tiled_attention_22_gb300 import attn
+    lens = [700, 80]
+    args = [x.cuda() for x in problem(lens, 1, 8, 2, 64, 32, "fp16", seed=15)]
+    ln = torch.tensor(lens, dtype=torch.int32).cuda()
+    want = attn.kv8_decode(*args, ln)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a = attn.kv8_decode(*args, ln, stream=side)
+    b = attn.kv8_decode(*args, ln, stream=side.cuda_stream)
+    side.synchronize()
+    for got in (a, b):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("lens", [[127, 128, 129, 16, 17], [1, 1, 1], [3000, 5], [128] * 40])
 def test_what_the_workspace_held_does_not_matter(lens):
     """A workspace full of NaN: only parts that this call wrote are read, also

@@ -75,6 +75,48 @@ def test_forward_and_gradients(case):
         plain64.check(got, *ref[name], name)
 
 
+@pytest.mark.parametrize("first", [0, 5])
+def test_nothing_but_padding(first):
+    """Offsets that begin behind row 0, and batches whose sequences are all empty:
+    rows of no sequence keep what they held."""
+    from exact_tiled_attention_22_gb300 import attn
+    q, k, v, do = draw([40], [40], 4, 2, 64, "fp16", seed=70)
+    for ends in ([first, first, first], [first, first + 3, first + 30]):
+        c = torch.tensor(ends, dtype=torch.int32).cuda()
+        marks = [torch.full(x.shape, 7.0, dtype=x.dtype, device="cuda") for x in (q, q, k, v)]
+        o, lse = attn.varlen_fwd(dev(q), dev(k), dev(v), c, c, 0.125, True, o=marks[0])
+        grads = attn.varlen_bwd(dev(q), dev(k), dev(v), o, lse, dev(do), c, c, 0.125, True, grads=marks[1:])
+        attn.check(attn.attn_status())
+        for x in (o, *grads):
+            assert (x[:ends[0]] == 7.0).all() and (x[ends[-1]:] == 7.0).all()
+        if ends[-1] > ends[0]:
+            s = slice(ends[0], ends[-1])
+            cut = [e - ends[0] for e in ends]
+            ref = plain64.packed(*(x[s].double() for x in (q, k, v)), cut, cut, 0.125, True, "fp16", do[s].double())
+            for name, got in zip(("o", "dq", "dk", "dv"), (o, *grads)):
+                plain64.check(got[s], *ref[name], name)
+            plain64.check(lse[:, s], *ref["lse"], "lse")
+
+
+def test_offsets_that_do_not_ascend_stay_inside():
+    """Outputs are unspecified, but nothing outside the given tensors is written
+    and the next call is right."""
+    from exact_tiled_attention_22_gb300 import attn
+    q, k, v, do = (x.cuda() for x in draw([300], [300], 4, 2, 64, "bf16", seed=71))
+    for ends in ([0, 300, 10, 290, 300], [-50, 5000, 2, 300, -1], [300, 200, 100, 0, 0], [0, 300, 0, 300, 300]):
+        c = torch.tensor(ends, dtype=torch.int32).cuda()
+        room = [torch.full((400, x.shape[1], 64), 7.0, dtype=x.dtype, device="cuda") for x in (q, q, k, v)]
+        o, lse = attn.varlen_fwd(q, k, v, c, c, 0.125, True, o=room[0][50:350])
+        attn.varlen_bwd(q, k, v, o, lse, do, c, c, 0.125, True, grads=[x[50:350] for x in room[1:]])
+        attn.check(attn.attn_status())
+        for x in room:
+            assert (x[:50] == 7.0).all() and (x[350:] == 7.0).all()
+    c = offsets([300])
+    o, lse = attn.varlen_fwd(q, k, v, c, c, 0.125, True)
+    ref = plain64.packed(*(x.double().cpu() for x in (q, k, v)), [0, 300], [0, 300], 0.125, True, "bf16")
+    plain64.check(o, *ref["o"], "o")
+
+
 def test_many_short_sequences():
     """More sequences than a warp and than a block of the scans, zeros among them."""
     from exact_tiled_attention_22_gb300 import attn
