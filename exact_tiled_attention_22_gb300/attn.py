@@ -32,7 +32,8 @@ ERROR_NAMES = {0: "ATTN_OK", -1: "ATTN_ERR_INVALID", -2: "ATTN_ERR_UNSUPPORTED",
 # Kernel ids of attn_profile_end.
 KERNEL_NAMES = ["attn_fwd", "attn_bwd_pre", "attn_bwd_main", "attn_dq_post",
                 "attn_decode_split", "attn_decode_merge", "attn_pages_extend",
-                "attn_pages_release", "attn_kv8_append", "attn_kv8_split", "attn_kv8_merge"]
+                "attn_pages_release", "attn_kv8_append", "attn_kv8_split", "attn_kv8_merge",
+                "attn_varlen_merge"]
 
 
 class AttnError(RuntimeError):
@@ -107,7 +108,9 @@ def _load() -> ctypes.CDLL:
     lib.attn_kv8_decode_workspace_size.restype = sz
     lib.attn_kv8_decode.argtypes = [vp] * 9 + [i] * 8 + [f, i, i, vp, sz, vp]
     lib.attn_kv8_decode.restype = i
-    lib.attn_varlen_fwd.argtypes = [vp] * 7 + [i, ll, ll, i, i, i, ll, ll, ll, f, i, i, vp]
+    lib.attn_varlen_fwd_workspace_size.argtypes = [i, ll, ll, i, i, i]
+    lib.attn_varlen_fwd_workspace_size.restype = sz
+    lib.attn_varlen_fwd.argtypes = [vp] * 7 + [i, ll, ll, i, i, i, ll, ll, ll, f, i, i, vp, sz, vp]
     lib.attn_varlen_fwd.restype = i
     lib.attn_varlen_bwd_workspace_size.argtypes = [i, ll, i, i, i]
     lib.attn_varlen_bwd_workspace_size.restype = sz
@@ -322,12 +325,17 @@ def attn_kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o,
                                _stream(stream))
 
 
+def attn_varlen_fwd_workspace_size(B, Tq, Tk, Hq, Hkv, d) -> int:
+    return int(lib.attn_varlen_fwd_workspace_size(B, Tq, Tk, Hq, Hkv, d))
+
+
 def attn_varlen_fwd(q, k, v, o, lse, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, d, q_stride, k_stride,
-                    v_stride, scale, causal, dtype, stream=None) -> int:
+                    v_stride, scale, causal, dtype, workspace=None, workspace_bytes=0,
+                    stream=None) -> int:
     return lib.attn_varlen_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_q),
                                _ptr(cu_k), B, Tq, Tk, Hq, Hkv, d, q_stride, k_stride, v_stride,
                                float(scale), int(bool(causal)), dtype_code(dtype),
-                               _stream(stream))
+                               _ptr(workspace), int(workspace_bytes), _stream(stream))
 
 
 def attn_varlen_bwd_workspace_size(B, Tq, Hq, Hkv, d) -> int:
@@ -615,8 +623,13 @@ def _packed_args(q, k, v, cu_q, cu_k):
     return dev, (n - 1, Tq, Tk, Hq, Hkv, d, qs, ks, vs)
 
 
+@functools.lru_cache(maxsize=1024)
+def _varlen_workspace_size(B, Tq, Tk, Hq, Hkv, d):
+    return attn_varlen_fwd_workspace_size(B, Tq, Tk, Hq, Hkv, d)
+
+
 @_on_stream
-def varlen_fwd(q, k, v, cu_q, cu_k, scale=None, causal=False, o=None):
+def varlen_fwd(q, k, v, cu_q, cu_k, scale=None, causal=False, ws=None, o=None):
     """(o, lse [Hq, Tq]) of packed sequences: q [Tq, Hq, d], k, v [Tk, Hkv, d]
     fp16/bf16 CUDA tensors (any token stride that is a multiple of d), cu_q, cu_k
     int32 [B + 1] row offsets on the device (attn_varlen_fwd).  o: an output to
@@ -630,8 +643,18 @@ def varlen_fwd(q, k, v, cu_q, cu_k, scale=None, causal=False, o=None):
     else:
         _want(o, "o", q.dtype, (Tq, Hq, d), dev)
     lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
+    need = 0
+    if ws is None:
+        need = _varlen_workspace_size(*sizes[:6])
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif ws.get_device() != dev:
+        raise ValueError(f"ws is on {ws.device}")
+    else:
+        need = ws.numel() * ws.element_size()
     _run(dev, lib.attn_varlen_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-         lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), *sizes, scale, 1 if causal else 0, code)
+         lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), *sizes, scale, 1 if causal else 0, code,
+         ws.data_ptr() if ws is not None else None, need)
     return o, lse
 
 

@@ -961,9 +961,29 @@ size_t packed_bytes(long long T, long long stride, long long row) {
 
 }  // namespace
 
+// CTAs that share a pair of query tiles, and the CTAs in all.
+static int varlen_fwd_split(int B, long long Tq, long long Tk, int Hq, int Hkv, long long* ctas) {
+  int Gp, R;
+  attn::fwd_varlen_shape(Hq / Hkv, Tq, B, &Gp, &R);
+  const long long n = attn::fwd_varlen_grid(Tq, B, Hq, Gp, R);
+  const int nsplit = attn::fwd_varlen_nsplit(n, Tk);
+  *ctas = n * nsplit;
+  return nsplit;
+}
+
+size_t attn_varlen_fwd_workspace_size(int B, long long Tq, long long Tk, int Hq, int Hkv, int d) {
+  if (B < 1 || B > attn::kVarMaxB || Tq < 1 || Tk < 0 || Tq >= (1ll << 26) || Tk >= (1ll << 26) || Hkv < 1 ||
+      Hq < Hkv || Hq % Hkv || (d != 64 && d != 128))
+    return 0;
+  long long ctas = 0;
+  if (varlen_fwd_split(B, Tq, Tk, Hq, Hkv, &ctas) == 1) return 0;
+  return (size_t)ctas * 2 * 128 * (d + 2) * 4;
+}
+
 int attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_q,
                     const int32_t* cu_k, int B, long long Tq, long long Tk, int Hq, int Hkv, int d, long long q_stride,
-                    long long k_stride, long long v_stride, float scale, int causal, attn_dtype_t dtype, void* stream) {
+                    long long k_stride, long long v_stride, float scale, int causal, attn_dtype_t dtype,
+                    void* workspace, size_t workspace_bytes, void* stream) {
   t_err.clear();
   int rc = check_packed(cu_q, cu_k, B, Tq, Tk, Hq, Hkv, d, q_stride, k_stride, v_stride, scale, dtype);
   if (rc) return rc;
@@ -971,12 +991,17 @@ int attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float*
   if (!q || !o || !lse || (Tk > 0 && (!k || !v))) return fail(ATTN_ERR_INVALID, "null pointer argument");
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
     return fail(ATTN_ERR_ALIGN, "q, k, v, o and lse must be 16-byte aligned");
+  const size_t need = attn_varlen_fwd_workspace_size(B, Tq, Tk, Hq, Hkv, d);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+  if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return fail(ATTN_ERR_ALIGN, "workspace must be 256-byte aligned");
   const long long hq = (long long)Hq * d, hk = (long long)Hkv * d;
   const size_t cb = ((size_t)B + 1) * 4;
-  const Range outs[2] = {rng(o, packed_bytes(Tq, hq, hq)), rng(lse, (size_t)Tq * Hq * 4)};
+  const Range outs[3] = {rng(o, packed_bytes(Tq, hq, hq)), rng(lse, (size_t)Tq * Hq * 4), rng(workspace, need)};
   const Range ins[5] = {rng(q, packed_bytes(Tq, q_stride, hq)), rng(k, packed_bytes(Tk, k_stride, hk)),
                         rng(v, packed_bytes(Tk, v_stride, hk)), rng(cu_q, cb), rng(cu_k, cb)};
-  if ((rc = check_overlaps(outs, 2, ins, 5))) return rc;
+  if ((rc = check_overlaps(outs, 3, ins, 5))) return rc;
   DeviceInfo* dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   attn::FwdArgs a;
@@ -996,13 +1021,22 @@ int attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float*
   a.B = B; a.H = Hq; a.N = (int)Tq; a.d = d;
   a.cu_q = cu_q; a.cu_k = cu_k;
   a.Nk = (int)Tk;
+  long long ctas = 0;
+  a.nsplit = varlen_fwd_split(B, Tq, Tk, Hq, Hkv, &ctas);
+  if (need) {
+    a.ws_o = static_cast<float*>(workspace);
+    a.ws_ml = a.ws_o + (size_t)ctas * 2 * 128 * d;
+  }
   a.causal = causal ? 1 : 0;
   a.scale = scale;
   a.bf16 = bf16;
   wait_ctl(dev, &a.wait, &a.debug_flags);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = timed(attn::kKFwd, s, [&] { return attn::launch_fwd_varlen(a, s); });
-  return e != cudaSuccess ? cuda_fail(e, "attn_varlen_fwd launch") : ATTN_OK;
+  if (e != cudaSuccess) return cuda_fail(e, "attn_varlen_fwd launch");
+  if (a.nsplit == 1) return ATTN_OK;
+  e = timed(attn::kKVarMerge, s, [&] { return attn::launch_var_merge(a, s); });
+  return e != cudaSuccess ? cuda_fail(e, "attn_varlen_fwd merge launch") : ATTN_OK;
 }
 
 // Bytes of the partial dK, dV tiles: no tile is split while a sequence of all

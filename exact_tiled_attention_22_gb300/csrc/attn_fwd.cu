@@ -134,6 +134,24 @@ __device__ __forceinline__ bool var_find(const FwdArgs& p, int& unit, int tile_r
   return false;
 }
 
+// A pair of query tiles of a sequence, counted from its end: positions of their
+// first rows, the key tiles that each sees, and how the later one's are shared.
+constexpr int kVarMinChunk = 4;  // key tiles of a part, at least: a part costs about two
+struct VarPair {
+  int nk, row[2], n0, n1, chunk, parts;
+  __device__ VarPair(const FwdArgs& p, const VarSeq& vs, int unit) {
+    const int tq1 = 2 * unit, tq0 = tq1 + 1;
+    nk = (vs.lk + 127) / 128;
+    row[0] = vs.lq - p.R * (tq0 + 1);
+    row[1] = vs.lq - p.R * (tq1 + 1);
+    // tile tq begins R tq positions from the end: keys nearer to it are hidden
+    n1 = p.causal ? max(0, nk - ((p.R * tq1) >> 7)) : nk;
+    n0 = row[0] <= -p.R ? 0 : (p.causal ? max(0, nk - ((p.R * tq0) >> 7)) : nk);
+    chunk = p.nsplit > 1 ? max(kVarMinChunk, (n1 + p.nsplit - 1) / p.nsplit) : max(n1, 1);
+    parts = max(1, (n1 + chunk - 1) / chunk);
+  }
+};
+
 // ALIBI: add the linear bias -m_h |i - j| (m_h = p.alibi[h]) to the scaled
 // scores, the ALiBi of page "FlashAttention技术解析：如何让GPT训练速度提升5-9倍",
 // section 4.1.
@@ -170,7 +188,9 @@ __device__ __forceinline__ bool var_find(const FwdArgs& p, int& unit, int tile_r
 // heads that share a key head (row = position * Gp + head, one box of the map),
 // so that a key tile serves the group and a prompt of one token fills Gp rows of
 // a tile, not one row of Gp tiles (fwd_varlen_shape); the two tiles of a CTA are
-// neighbouring positions.
+// neighbouring positions.  Where the batch has too few pairs of tiles for the
+// GPU (few queries on many keys), p.nsplit CTAs share the key tiles of a pair;
+// their unnormalised O, reference max and sum meet in attn_var_merge_kernel.
 template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false, bool VARLEN = false>
 __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ FwdArgs p) {
@@ -201,22 +221,30 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
   // (VARLEN) the sequence, its key tiles, the tiles' first head, and the position
   // of each query tile's first row in the sequence (negative: the ragged tile)
   VarSeq vs{};
-  int v_nk = 0, v_head = 0, v_row[2] = {0, 0};
+  int v_nk = 0, v_head = 0, v_row[2] = {0, 0}, v_parts = 1;
   if constexpr (VARLEN) {
-    const int n_hb = p.H / p.Gp;
-    int unit = (int)(blockIdx.x / n_hb);
-    if (!var_find(p, unit, 2 * p.R, vs)) {  // (the grid is sized for the worst split into sequences)
+    const unsigned n_hb = p.H / p.Gp, pair_hb = blockIdx.x / (unsigned)p.nsplit;
+    const int part = (int)(blockIdx.x - pair_hb * p.nsplit);
+    int unit = (int)(pair_hb / n_hb);
+    bool work = var_find(p, unit, 2 * p.R, vs);  // (the grid is sized for the worst split into sequences)
+    if (work) {
+      const VarPair vp(p, vs, unit);
+      v_nk = vp.nk;
+      v_row[0] = vp.row[0];
+      v_row[1] = vp.row[1];
+      v_head = (int)(pair_hb % n_hb) * p.Gp;
+      // this CTA's key tiles, of the n1 that the later tile sees
+      v_parts = vp.parts;
+      const int j0 = part * vp.chunk;
+      n1 = min(vp.n1 - j0, vp.chunk);
+      n0 = min(max(vp.n0 - j0, 0), n1);
+      v_nk -= j0;
+      work = part < v_parts;
+    }
+    if (!work) {
       if (threadIdx.x == 0) griddep_launch_dependents();
       return;
     }
-    v_nk = (vs.lk + 127) / 128;
-    v_head = (int)(blockIdx.x - (blockIdx.x / n_hb) * n_hb) * p.Gp;
-    const int tq1 = 2 * unit, tq0 = tq1 + 1;  // counted from the end
-    v_row[0] = vs.lq - p.R * (tq0 + 1);
-    v_row[1] = vs.lq - p.R * (tq1 + 1);
-    // tile tq begins R tq positions from the end: keys nearer to it are hidden
-    n1 = p.causal ? max(0, v_nk - ((p.R * tq1) >> 7)) : v_nk;
-    n0 = v_row[0] <= -p.R ? 0 : (p.causal ? max(0, v_nk - ((p.R * tq0) >> 7)) : v_nk);
   }
   const WaitCtl wc{p.wait.status, p.wait.limit_ns};
 
@@ -960,6 +988,27 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
           }
         }
         if (valid) p.lse[lrow] = lse_out;
+      } else if (VARLEN && v_parts > 1) {
+        // A part: [column / 4][row][4] fp32 (a warp's stores are contiguous); none
+        // from a tile that sees no key of this part.
+        const int rl = qd * 32 + lane;
+        const size_t slot = (size_t)blockIdx.x * 2 + t;
+        if (n_t > 0) {
+          float4* po = reinterpret_cast<float4*>(p.ws_o + slot * (128 * D)) + rl;
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + cc, o);
+            tmem_ld_wait();
+            reg_fence<32>(o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              po[(cc / 4 + i) * 128] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                   __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+          }
+        }
+        p.ws_ml[slot * 256 + rl] = m_ref;
+        p.ws_ml[slot * 256 + 128 + rl] = l;
       } else if (VARLEN && row_lo < 0) {
         // The ragged tile: rows before the sequence belong to its neighbour, so
         // every thread stores its own row.
@@ -1023,7 +1072,7 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
     if constexpr (!ACC) {
       // The tile's four warps meet (agreeing on whether all of them got
       // here without giving up), then one thread stores the staged O.
-      if (named_bar_and(kTileBar0 + t, 128, ok) && qd == 0 && lane == 0 && !(VARLEN && row_lo < 0)) {
+      if (named_bar_and(kTileBar0 + t, 128, ok) && qd == 0 && lane == 0 && !(VARLEN && (row_lo < 0 || v_parts > 1))) {
         for (int bx = 0; bx < L::kNSub; ++bx) {
           const uint32_t src = base + L::kQ0 + t * L::kTile + bx * L::kSub;
           if constexpr (VARLEN)
@@ -1046,13 +1095,76 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
   }
 }
 
+// Joins the parts of a pair of query tiles: with M = max m_c,
+//   O = sum 2^(m_c - M) O_c / L,  L = sum 2^(m_c - M) l_c,  LSE = ln 2 (M + log2 L).
+// A block per (pair, head block), query tile and 32 columns; a thread takes 8
+// columns of a row, four parts' loads in flight, in the order of the keys.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(512) attn_var_merge_kernel(const __grid_constant__ FwdArgs p) {
+  griddep_wait();
+  const unsigned n_hb = p.H / p.Gp;
+  const int t = blockIdx.y, rl = threadIdx.x & 127, c4 = blockIdx.z * 8 + (threadIdx.x >> 7) * 2;
+  int unit = (int)(blockIdx.x / n_hb);
+  VarSeq vs{};
+  if (var_find(p, unit, 2 * p.R, vs)) {
+    const VarPair vp(p, vs, unit);
+    const int pos = rl / p.Gp, sub = rl - pos * p.Gp, row = vp.row[t] + pos;
+    if (vp.parts > 1 && row >= 0 && pos < p.R) {
+      const size_t slot0 = (size_t)blockIdx.x * p.nsplit * 2 + t;
+      float M = -INFINITY, Ls = 0.f;
+      float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+      for (int i0 = 0; i0 < vp.parts; i0 += 4) {
+        float m[4], l[4];
+        float4 x[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const size_t slot = slot0 + 2 * (size_t)min(i0 + i, vp.parts - 1);
+          const float* ml = p.ws_ml + slot * 256 + rl;
+          m[i] = i0 + i < vp.parts ? ml[0] : -INFINITY;
+          l[i] = i0 + i < vp.parts ? ml[128] : 0.f;
+          const float4* o = reinterpret_cast<const float4*>(p.ws_o + slot * (128 * D)) + rl;
+          x[i][0] = o[c4 * 128];
+          x[i][1] = o[(c4 + 1) * 128];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // (m = -inf: no visible key in this part, whose O may not be written, or
+          // nothing but NaN)
+          if (m[i] == -INFINITY) {
+            if (l[i] != l[i]) Ls = l[i];
+            continue;
+          }
+          const float mn = fmaxf(M, m[i]), a = ex2(M - mn), b = ex2(m[i] - mn);
+          M = mn;
+          Ls = fmaf(Ls, a, l[i] * b);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            acc[k].x = fmaf(acc[k].x, a, x[i][k].x * b);
+            acc[k].y = fmaf(acc[k].y, a, x[i][k].y * b);
+            acc[k].z = fmaf(acc[k].z, a, x[i][k].z * b);
+            acc[k].w = fmaf(acc[k].w, a, x[i][k].w * b);
+          }
+        }
+      }
+      const float inv = Ls != 0.f ? 1.f / Ls : 0.f;
+      const int hq = (int)(blockIdx.x % n_hb) * p.Gp + sub;
+      const size_t o_row = (size_t)vs.q0 + row;
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.o) + ((o_row * p.H + hq) * D + c4 * 4) * 2) =
+          make_uint4(pack2<BF16>(acc[0].x * inv, acc[0].y * inv), pack2<BF16>(acc[0].z * inv, acc[0].w * inv),
+                     pack2<BF16>(acc[1].x * inv, acc[1].y * inv), pack2<BF16>(acc[1].z * inv, acc[1].w * inv));
+      if (c4 == 0) p.lse[(size_t)hq * p.N + o_row] = Ls != 0.f ? (M + __log2f(Ls)) * kLn2 : -INFINITY;
+    }
+  }
+  griddep_launch_dependents();
+}
+
 template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false, bool VARLEN = false>
 cudaError_t launch_fwd_t(const FwdArgs& a, cudaStream_t stream) {
   using L = FwdLayout<D>;
   auto* k = attn_fwd_kernel<D, BF16, ALIBI, SPARSE, DROPOUT, ACC, VARLEN>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
-  const unsigned grid = VARLEN ? (unsigned)fwd_varlen_grid(a.N, a.B, a.H, a.Gp, a.R)
+  const unsigned grid = VARLEN ? (unsigned)(fwd_varlen_grid(a.N, a.B, a.H, a.Gp, a.R) * a.nsplit)
                                : (unsigned)(((a.N + 255) / 256) * a.B * a.H);
   e = launch_pdl(k, grid, FwdRoles<DROPOUT>::kThreads, L::kSmem, stream, a);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -1078,8 +1190,18 @@ void fwd_varlen_shape(int G, long long Nq, int B, int* Gp, int* R) {
   *R = r;
 }
 
-// Blocks for N packed queries in B sequences, whatever the lengths: a sequence
-// has at most one ragged pair of tiles, and no pair is empty.
+// CTAs that share the key tiles of a pair: as many as fill the SMs once where the
+// pairs alone do not, if any sequence can be long enough to be shared.  (One
+// sequence of 64 queries on 2400 keys, 12 heads: 15 us against 33 by one
+// CTA a pair.)
+int fwd_varlen_nsplit(long long ctas, long long Nk) {
+  if ((Nk + 127) / 128 < 2 * kVarMinChunk || ctas >= 152) return 1;
+  const long long n = (152 + ctas - 1) / ctas, most = (Nk + 127) / 128 / kVarMinChunk;
+  return (int)(n < most ? n : most);
+}
+
+// Pairs of tiles and head blocks of N packed queries in B sequences, whatever the
+// lengths: a sequence has at most one ragged pair, and no pair is empty.
 long long fwd_varlen_grid(long long N, int B, int H, int Gp, int R) {
   long long units = N / (2 * R) + B;
   if (units > N) units = N;
@@ -1116,6 +1238,25 @@ cudaError_t launch_fwd_varlen(const FwdArgs& a, cudaStream_t stream) {
                   : launch_fwd_t<128, false, false, false, false, false, true>(a, stream);
   return a.bf16 ? launch_fwd_t<64, true, false, false, false, false, true>(a, stream)
                 : launch_fwd_t<64, false, false, false, false, false, true>(a, stream);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_var_merge_t(const FwdArgs& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)fwd_varlen_grid(a.N, a.B, a.H, a.Gp, a.R), 2, D / 32);
+  cfg.blockDim = dim3(512);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_var_merge_kernel<D, BF16>, a);
+}
+
+cudaError_t launch_var_merge(const FwdArgs& a, cudaStream_t stream) {
+  if (a.d == 128) return a.bf16 ? launch_var_merge_t<128, true>(a, stream) : launch_var_merge_t<128, false>(a, stream);
+  return a.bf16 ? launch_var_merge_t<64, true>(a, stream) : launch_var_merge_t<64, false>(a, stream);
 }
 
 cudaError_t launch_fwd_acc(const FwdArgs& a, cudaStream_t stream) {

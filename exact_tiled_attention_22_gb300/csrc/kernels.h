@@ -11,7 +11,8 @@ namespace attn {
 // Kernel ids used by the per-kernel timing of attn_profile_*.
 enum KernelId {
   kKFwd = 0, kKBwdPre = 1, kKBwdMain = 2, kKDqPost = 3, kKDecSplit = 4, kKDecMerge = 5,
-  kKPagesExtend = 6, kKPagesRelease = 7, kKKv8Append = 8, kKKv8Split = 9, kKKv8Merge = 10, kKNum = 11
+  kKPagesExtend = 6, kKPagesRelease = 7, kKKv8Append = 8, kKKv8Split = 9, kKKv8Merge = 10, kKVarMerge = 11,
+  kKNum = 12
 };
 
 struct WaitCtlHost {
@@ -68,8 +69,13 @@ struct FwdArgs {
   const int* cu_q;
   const int* cu_k;
   int Nk, G, Gp, R;
+  int nsplit;    // CTAs that share the key tiles of a pair of query tiles
+  float* ws_o;   // [CTA][tile][d / 4][128][4] unnormalised O of shared pairs
+  float* ws_ml;  // [CTA][tile][m, l][128]
 };
 int fwd_smem_bytes(int d);
+int fwd_varlen_nsplit(long long ctas, long long Nk);
+cudaError_t launch_var_merge(const FwdArgs& a, cudaStream_t stream);
 void fwd_varlen_shape(int G, long long Nq, int B, int* Gp, int* R);
 long long fwd_varlen_grid(long long N, int B, int H, int Gp, int R);
 cudaError_t launch_fwd_varlen(const FwdArgs& a, cudaStream_t stream);

@@ -354,17 +354,21 @@ int attn_decode(const void* q, const void* k, const void* v, void* o, float* lse
  * sees no key gets O = 0, LSE = -inf, dQ = 0; a key that no query sees gets
  * dK = dV = 0.  Rows of no sequence (before cu[0], behind cu[B]) are neither read
  * nor written.  dK and dV of a key head sum over its group in a fixed order;
- * dQ as in attn_bwd.  o and lse are the forward's.  Offsets are clamped to the
+ * dQ as in attn_bwd.  o and lse are the forward's.
+ * Workspaces as attn_bwd's; the forward needs one only where its size is not 0
+ * (few queries on many keys, whose key range several blocks share).  Offsets are clamped to the
  * tensors; if they do not ascend, outputs are unspecified.
  * 1 <= B <= 8192, 0 <= Tq, Tk < 2^26, Hq / Hkv <= 1024.
  * The pages name batches of sequences only as [B, N, H, d]; the packed layout
  * and the grouped heads are an addition of this library.
  */
+size_t attn_varlen_fwd_workspace_size(int B, long long Tq, long long Tk, int Hq, int Hkv, int d);
 int attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
                     const int32_t* cu_q, const int32_t* cu_k, int B, long long Tq,
                     long long Tk, int Hq, int Hkv, int d, long long q_stride,
                     long long k_stride, long long v_stride, float scale, int causal,
-                    attn_dtype_t dtype, void* stream);
+                    attn_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                    void* stream);
 size_t attn_varlen_bwd_workspace_size(int B, long long Tq, int Hq, int Hkv, int d);
 int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o,
                     const float* lse, const void* dO, void* dq, void* dk, void* dv,
@@ -511,7 +515,8 @@ int attn_set_wait_limit(unsigned long long limit_ns, int debug_flags);
  * synchronises those events and fills, for kernel ids 0..n-1
  * (0 forward, 1 backward preprocess, 2 backward main, 3 dQ conversion,
  * 4 decode chunks, 5 decode merge, 6 pages extend, 7 pages release, 8 8-bit
- * append, 9 8-bit decode, 10 its merge),
+ * append, 9 8-bit decode, 10 its merge, 11 the
+ * packed forward's merge),
  * the number of launches and their summed device time in milliseconds.
  * Returns the number of kernel ids filled, or a negative ATTN_ERR_* code.
  */

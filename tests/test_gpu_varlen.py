@@ -300,6 +300,31 @@ def test_split_key_tiles(case):
         plain64.check(got, *ref[name], name)
 
 
+SHARED = [
+    # few queries on many keys: several blocks share the key range of a query tile
+    ([64], [2400], 12, 4, 64, "fp16", True),
+    ([1, 30], [3000, 1500], 3, 1, 128, "bf16", True),
+    ([300], [5000], 2, 2, 128, "fp16", True),
+    ([200, 5, 0], [1100, 4000, 30], 5, 1, 64, "bf16", False),
+    ([1500], [1100], 1, 1, 64, "bf16", True),   # queries that see none of the keys
+]
+
+
+@pytest.mark.parametrize("case", SHARED, ids=lambda c: f"{c[0][0]}on{c[1][0]}-{c[2]}x{c[3]}d{c[4]}{c[5]}{'c' if c[6] else ''}")
+def test_shared_key_ranges(case):
+    from exact_tiled_attention_22_gb300 import attn
+    lens_q, lens_k, Hq, H, d, dtype, causal = case
+    q, k, v, _ = draw(lens_q, lens_k, Hq, H, d, dtype, seed=sum(lens_k))
+    n = attn.attn_varlen_fwd_workspace_size(len(lens_q), sum(lens_q), sum(lens_k), Hq, H, d)
+    assert n > 0
+    ws = torch.full((n // 4,), math.nan, device="cuda").view(torch.uint8)
+    o, lse = attn.varlen_fwd(dev(q), dev(k), dev(v), offsets(lens_q), offsets(lens_k), None, causal, ws=ws)
+    attn.check(attn.attn_status())
+    ref = plain64.packed(q.double(), k.double(), v.double(), cu(lens_q), cu(lens_k), d ** -0.5, causal, dtype)
+    plain64.check(o, *ref["o"], "o")
+    plain64.check(lse, *ref["lse"], "lse")
+
+
 def test_repeats_are_equal():
     """O, LSE, dK, dV do not depend on the order in which blocks finish."""
     from exact_tiled_attention_22_gb300 import attn

@@ -87,7 +87,7 @@ def test_decode_refuses(A, kw, code):
     assert call(A.lib.attn_kv8_decode, DECODE, base, **kw) == code and A.last_error()
 
 
-FWD = "q k v o lse cu_q cu_k B Tq Tk Hq Hkv d qs ks vs scale causal dtype stream"
+FWD = "q k v o lse cu_q cu_k B Tq Tk Hq Hkv d qs ks vs scale causal dtype ws ws_bytes stream"
 BWD = ("q k v o lse dO dq dk dv cu_q cu_k B Tq Tk Hq Hkv d qs ks vs scale causal dtype ws ws_bytes stream")
 SIZES = dict(B=3, Tq=100, Tk=120, Hq=4, Hkv=2, d=64, qs=256, ks=128, vs=128, scale=0.125, causal=1, dtype=0, stream=None)
 COMMON = [
@@ -99,7 +99,18 @@ COMMON = [
 
 @pytest.mark.parametrize("kw,code", COMMON + [(dict(o=P[0]), -1), (dict(lse=P[3]), -1), (dict(lse=P[9]), -1)])
 def test_varlen_fwd_refuses(A, kw, code):
-    base = dict(q=P[0], k=P[1], v=P[2], o=P[3], lse=P[4], cu_q=P[9], cu_k=P[10], **SIZES)
+    base = dict(q=P[0], k=P[1], v=P[2], o=P[3], lse=P[4], cu_q=P[9], cu_k=P[10], ws=None, ws_bytes=0, **SIZES)
+    assert call(A.lib.attn_varlen_fwd, FWD, base, **kw) == code and A.last_error()
+
+
+@pytest.mark.parametrize("kw,code", [(dict(ws=None), -6), (dict(ws_bytes=1000), -6), (dict(ws=WS + 16), -3),
+                                     (dict(ws=P[1]), -1), (dict(o=WS), -1)])
+def test_varlen_fwd_refuses_its_workspace(A, kw, code):
+    """Few queries on many keys: a workspace is needed."""
+    sizes = {**SIZES, "Tk": 50000}
+    need = A.attn_varlen_fwd_workspace_size(3, 100, 50000, 4, 2, 64)
+    assert need > 0
+    base = dict(q=P[0], k=P[1], v=P[2], o=P[3], lse=P[4], cu_q=P[9], cu_k=P[10], ws=WS, ws_bytes=need, **sizes)
     assert call(A.lib.attn_varlen_fwd, FWD, base, **kw) == code and A.last_error()
 
 
@@ -114,9 +125,10 @@ def test_varlen_bwd_refuses(A, kw, code):
 
 def test_nothing_to_do_is_no_error(A):
     """No rows: nothing is enqueued (and no device is needed)."""
-    base = dict(q=None, k=None, v=None, o=None, lse=None, cu_q=P[9], cu_k=P[10], **{**SIZES, "Tq": 0, "Tk": 0})
+    base = dict(q=None, k=None, v=None, o=None, lse=None, cu_q=P[9], cu_k=P[10], ws=None, ws_bytes=0,
+                **{**SIZES, "Tq": 0, "Tk": 0})
     assert call(A.lib.attn_varlen_fwd, FWD, base) == 0
-    base.update(dO=None, dq=None, dk=None, dv=None, ws=None, ws_bytes=0)
+    base.update(dO=None, dq=None, dk=None, dv=None)
     assert call(A.lib.attn_varlen_bwd, BWD, base) == 0
     assert A.lib.attn_kv8_append(None, None, 0, 0, None, 0, 1, 64, None, None, None, None, 1, 16, 0, None) == 0
 
@@ -130,6 +142,9 @@ def test_workspace_sizes(A):
     assert f(5, 1000, 8, 8, 128) <= 8 * (1000 + 5 * 64) * (128 + 2) * 4 + 4096
     # and, where key tiles may be split, a fixed number of partial dK, dV tiles
     assert f(1, 100000, 2, 1, 64) - 2 * 100000 * (64 + 2) * 4 <= 608 * 2 * 128 * 64 * 4 + 100000
+    h = A.attn_varlen_fwd_workspace_size
+    assert h(4, 8192, 8192, 16, 4, 128) == 0 and h(1, 64, 500, 12, 4, 64) == 0  # enough query tiles; few keys
+    assert 0 < h(1, 64, 100000, 12, 4, 64) <= 2 * 152 * 2 * 128 * 66 * 4
     g = A.attn_kv8_decode_workspace_size
     assert g(0, 1, 1, 64) == 0 and g(1, 3, 2, 64) == 0 and g(1, 2, 2, 60) == 0 and g(1, 8, 1, 128) > 0
 
