@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import math
 import os
 
@@ -445,29 +446,23 @@ def decode(q, k, v, scale=None, causal=False, ws=None, stream=None, alibi=None):
     return o, lse
 
 
-# ---- paged key/value cache in 8 bits --------------------------------------
-# A decoding step's calls are short (the kernels take a few microseconds, the
-# host's part several times that), so these wrappers look at each tensor once,
-# with the cheapest tests there are, and make few torch calls: on the GPU's Grace
-# host each allocation or view costs 2-4 us among others, each test 0.1.  Each
-# takes stream=, the stream to run on instead of the current one.
-def _want(t, name, dtype, shape, index):
-    """t is a contiguous tensor of this type and shape on CUDA device `index`."""
-    if (t.dtype is not dtype or t.shape != shape or t.get_device() != index or index < 0
-            or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on one CUDA "
-                         f"device with the others, got {list(t.shape)} {t.dtype} on {t.device}")
+# ---- serving and packed batches ---------------------------------------------
+# The calls of attn_bind.so (csrc/attn_bind.cpp): they check the tensors (a
+# ValueError says what is wrong), allocate outputs and workspaces on the current
+# stream and call the entry points above.  Each takes stream=, the stream to run
+# on instead of the current one.
+def _load_bind():
+    path = os.path.join(os.path.dirname(LIB_PATH), "attn_bind.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is not built; run exact_tiled_attention_22_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("attn_bind", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.set_error(AttnError)
+    return mod
 
 
-def _run(index, fn, *args):
-    """fn(*args, stream) with CUDA device `index` current (the library acts on the
-    current device), on that device's current stream."""
-    if torch.cuda.current_device() != index:
-        with torch.cuda.device(index):
-            return _run(index, fn, *args)
-    rc = fn(*args, _raw_stream(index) if _raw_stream is not None else _stream(None))
-    if rc:
-        check(rc)
+_bind = _load_bind()
 
 
 def _on_stream(f):
@@ -494,28 +489,8 @@ def pages_extend(lens, add, block_table, free_pages, free_count, page, max_new, 
     free_pages: int32 [cap], a stack of free page ids, free_count: int32 [1];
     max_new: length of the slot map.  new_lens may be lens and free_left may
     be free_count.  Returns (new_lens, granted, cu_new, slots, free_left)."""
-    (B, width), (cap,) = block_table.shape, free_pages.shape
-    i32, dev = torch.int32, lens.get_device()
-    _want(lens, "lens", i32, (B,), dev)
-    _want(add, "add", i32, (B,), dev)
-    _want(block_table, "block_table", i32, (B, width), dev)
-    _want(free_pages, "free_pages", i32, (cap,), dev)
-    _want(free_count, "free_count", i32, (1,), dev)
-    if new_lens is not None:
-        _want(new_lens, "new_lens", i32, (B,), dev)
-    if free_left is not None:
-        _want(free_left, "free_left", i32, (1,), dev)
-    # one allocation for the four small outputs (views of it that no gradient sees)
-    new, granted, cu_new, left = torch.empty(3 * B + 2, dtype=i32, device=lens.device) \
-        .unsafe_split_with_sizes((B, B, B + 1, 1))
-    new_lens = new if new_lens is None else new_lens
-    free_left = left if free_left is None else free_left
-    slots = torch.empty(max_new, dtype=torch.int64, device=lens.device)
-    _run(dev, lib.attn_pages_extend, lens.data_ptr(), add.data_ptr(), B,
-         block_table.data_ptr(), width, free_pages.data_ptr(), free_count.data_ptr(), cap, page,
-         max_new, new_lens.data_ptr(), granted.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
-         free_left.data_ptr())
-    return new_lens, granted, cu_new, slots, free_left
+    return _bind.pages_extend(lens, add, block_table, free_pages, free_count, page, max_new,
+                              new_lens, free_left)
 
 
 @_on_stream
@@ -523,46 +498,8 @@ def pages_release(lens, finished, block_table, free_pages, free_count, page, new
                   free_left=None):
     """Pages of the requests with finished[b] != 0 (int32 [B]) go back onto the
     stack free_pages, written in place (attn_pages_release).  Returns (new_lens, free_left)."""
-    (B, width), (cap,) = block_table.shape, free_pages.shape
-    i32, dev = torch.int32, lens.get_device()
-    _want(lens, "lens", i32, (B,), dev)
-    _want(finished, "finished", i32, (B,), dev)
-    _want(block_table, "block_table", i32, (B, width), dev)
-    _want(free_pages, "free_pages", i32, (cap,), dev)
-    _want(free_count, "free_count", i32, (1,), dev)
-    new_lens = torch.empty_like(lens) if new_lens is None else new_lens
-    free_left = torch.empty_like(free_count) if free_left is None else free_left
-    _want(new_lens, "new_lens", i32, (B,), dev)
-    _want(free_left, "free_left", i32, (1,), dev)
-    _run(dev, lib.attn_pages_release, lens.data_ptr(), finished.data_ptr(), B,
-         block_table.data_ptr(), width, free_pages.data_ptr(), free_count.data_ptr(), cap, page,
-         new_lens.data_ptr(), free_left.data_ptr())
-    return new_lens, free_left
-
-
-def _packed(t, name, dtype, shape, index):
-    """t is [T, H, d] on CUDA device `index`, heads d apart; its token stride."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or index < 0:
-        raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} on one CUDA device with "
-                         f"the others, got {list(t.shape)} {t.dtype} on {t.device}")
-    T, H, d = shape
-    if t.is_contiguous():
-        return H * d
-    if t.stride(2) != 1 or t.stride(1) != d and H > 1:
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if T > 1 else H * d
-
-
-def _cache(k_cache, v_cache, k_scale, v_scale, dev):
-    P, H, page, d = shape = k_cache.shape
-    code = k_cache.dtype
-    if code is not torch.float8_e4m3fn and code is not torch.uint8:
-        raise ValueError(f"the caches hold float8_e4m3fn or uint8 codes, got {code}")
-    _want(k_cache, "k_cache", code, shape, dev)
-    _want(v_cache, "v_cache", code, shape, dev)
-    _want(k_scale, "k_scale", torch.float32, (P, H), dev)
-    _want(v_scale, "v_scale", torch.float32, (P, H), dev)
-    return shape
+    return _bind.pages_release(lens, finished, block_table, free_pages, free_count, page, new_lens,
+                               free_left)
 
 
 @_on_stream
@@ -570,19 +507,7 @@ def kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale):
     """Rounds new keys and values [T, H, d] into their slots (int64 [T]) of the
     8-bit cache [P, H, page, d] with scales [P, H], in place (attn_kv8_append).
     k and v may be slices of a wider projection (any token stride)."""
-    dev = k.get_device()
-    P, H, page, d = _cache(k_cache, v_cache, k_scale, v_scale, dev)
-    T = k.shape[0]
-    ks, vs = _packed(k, "k", k.dtype, (T, H, d), dev), _packed(v, "v", k.dtype, (T, H, d), dev)
-    _want(slots, "slots", torch.int64, (T,), dev)
-    _run(dev, lib.attn_kv8_append, k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T,
-         H, d, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P,
-         page, dtype_code(k.dtype))
-
-
-@functools.lru_cache(maxsize=256)
-def _kv8_workspace_size(Nq, Hq, H, d):
-    return attn_kv8_decode_workspace_size(Nq, Hq, H, d)
+    _bind.kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale)
 
 
 @_on_stream
@@ -590,42 +515,8 @@ def kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=N
                ws=None):
     """(o, lse) of q [B, Nq, Hq, d], the last Nq tokens of every request, against
     the 8-bit cache (attn_kv8_decode); lens counts the Nq tokens."""
-    dev = q.get_device()
-    P, H, page, d = _cache(k_cache, v_cache, k_scale, v_scale, dev)
-    (B, Nq, Hq, _), (_, width) = q.shape, block_table.shape
-    code = dtype_code(q.dtype)
-    _want(q, "q", q.dtype, (B, Nq, Hq, d), dev)
-    _want(block_table, "block_table", torch.int32, (B, width), dev)
-    _want(lens, "lens", torch.int32, (B,), dev)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    o = torch.empty_like(q)
-    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = torch.empty(_kv8_workspace_size(Nq, Hq, H, d), dtype=torch.uint8, device=q.device)
-    elif ws.get_device() != dev:
-        raise ValueError(f"ws is on {ws.device}")
-    _run(dev, lib.attn_kv8_decode, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-         k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
-         o.data_ptr(), lse.data_ptr(), B, Nq, Hq, H, d, P, page, width, scale, 1 if causal else 0,
-         code, ws.data_ptr(), ws.numel() * ws.element_size())
-    return o, lse
-
-
-# ---- packed batches ---------------------------------------------------------
-def _packed_args(q, k, v, cu_q, cu_k):
-    """The device index and the sizes the calls take from B to the strides."""
-    (Tq, Hq, d), (Tk, Hkv, _), (n,) = sq, _, _ = q.shape, k.shape, cu_q.shape
-    dev, dt, sk = q.get_device(), q.dtype, (Tk, Hkv, d)
-    qs, ks, vs = (_packed(q, "q", dt, sq, dev), _packed(k, "k", dt, sk, dev),
-                  _packed(v, "v", dt, sk, dev))
-    _want(cu_q, "cu_q", torch.int32, (n,), dev)
-    _want(cu_k, "cu_k", torch.int32, (n,), dev)
-    return dev, (n - 1, Tq, Tk, Hq, Hkv, d, qs, ks, vs)
-
-
-@functools.lru_cache(maxsize=1024)
-def _varlen_workspace_size(B, Tq, Tk, Hq, Hkv, d):
-    return attn_varlen_fwd_workspace_size(B, Tq, Tk, Hq, Hkv, d)
+    return _bind.kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale, causal,
+                            ws)
 
 
 @_on_stream
@@ -634,60 +525,15 @@ def varlen_fwd(q, k, v, cu_q, cu_k, scale=None, causal=False, ws=None, o=None):
     fp16/bf16 CUDA tensors (any token stride that is a multiple of d), cu_q, cu_k
     int32 [B + 1] row offsets on the device (attn_varlen_fwd).  o: an output to
     write into; rows of no sequence are left as they are there."""
-    dev, sizes = _packed_args(q, k, v, cu_q, cu_k)
-    Tq, Hq, d = q.shape
-    code = dtype_code(q.dtype)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    if o is None:
-        o = torch.empty((Tq, Hq, d), dtype=q.dtype, device=q.device)
-    else:
-        _want(o, "o", q.dtype, (Tq, Hq, d), dev)
-    lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
-    need = 0
-    if ws is None:
-        need = _varlen_workspace_size(*sizes[:6])
-        if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif ws.get_device() != dev:
-        raise ValueError(f"ws is on {ws.device}")
-    else:
-        need = ws.numel() * ws.element_size()
-    _run(dev, lib.attn_varlen_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-         lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), *sizes, scale, 1 if causal else 0, code,
-         ws.data_ptr() if ws is not None else None, need)
-    return o, lse
+    return _bind.varlen_fwd(q, k, v, cu_q, cu_k, scale, causal, ws, o)
 
 
 @_on_stream
 def varlen_bwd(q, k, v, o, lse, do, cu_q, cu_k, scale=None, causal=False, ws=None, grads=None):
     """(dq, dk, dv) for the varlen_fwd that produced (o, lse).  grads: three
     contiguous tensors to write into (rows of no sequence are left as they are)."""
-    dev, sizes = _packed_args(q, k, v, cu_q, cu_k)
-    Tq, Hq, d = q.shape
-    dt, sq, sk = q.dtype, (Tq, Hq, d), tuple(k.shape)
-    code = dtype_code(dt)
-    _want(o, "o", dt, sq, dev)
-    _want(do, "do", dt, sq, dev)
-    _want(lse, "lse", torch.float32, (Hq, Tq), dev)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    if grads is None:
-        dq = torch.empty(sq, dtype=dt, device=q.device)
-        dk, dv = (torch.empty(sk, dtype=dt, device=q.device) for _ in range(2))
-    else:
-        dq, dk, dv = grads
-        _want(dq, "dq", dt, sq, dev)
-        _want(dk, "dk", dt, sk, dev)
-        _want(dv, "dv", dt, sk, dev)
-    if ws is None:
-        ws = torch.empty(attn_varlen_bwd_workspace_size(sizes[0], Tq, Hq, k.shape[1], d),
-                         dtype=torch.uint8, device=q.device)
-    elif ws.get_device() != dev:
-        raise ValueError(f"ws is on {ws.device}")
-    _run(dev, lib.attn_varlen_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-         lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-         cu_q.data_ptr(), cu_k.data_ptr(), *sizes, scale, 1 if causal else 0, code, ws.data_ptr(),
-         ws.numel() * ws.element_size())
-    return dq, dk, dv
+    dq, dk, dv = (None, None, None) if grads is None else grads
+    return _bind.varlen_bwd(q, k, v, o, lse, do, cu_q, cu_k, scale, causal, ws, dq, dk, dv)
 
 
 # ---- autograd -------------------------------------------------------------

@@ -317,6 +317,33 @@ def test_pages_that_are_not_there_read_as_zeros():
     plain64.check(o, ro, bo, "o")
 
 
+def test_errors_of_the_calls():
+    """What the tensors cannot be raises ValueError, what the library refuses
+    AttnError with its code; nothing is enqueued and the next call works."""
+    from exact_tiled_attention_22_gb300 import attn
+    lens = [20, 40]
+    q, kc, vc, ks, vs, table = (x.cuda() for x in problem(lens, 1, 4, 2, 64, 16, "fp16", seed=16))
+    ln = torch.tensor(lens, dtype=torch.int32).cuda()
+    want = attn.kv8_decode(q, kc, vc, ks, vs, table, ln)
+    for bad in (dict(q=q.float()), dict(q=q[0]), dict(q=q.transpose(0, 1)), dict(q=q.cpu()), dict(kc=kc.float()),
+                dict(vc=vc[:-1]), dict(ks=ks.half()), dict(table=table.long()), dict(table=table[:1]),
+                dict(ln=ln.cpu()), dict(ln=[20, 40]), dict(ws=torch.zeros(8))):
+        a = dict(q=q, kc=kc, vc=vc, ks=ks, vs=vs, table=table, ln=ln, ws=None)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            attn.kv8_decode(a["q"], a["kc"], a["vc"], a["ks"], a["vs"], a["table"], a["ln"], ws=a["ws"])
+    for bad, code in ((dict(q=q[:, :, :3].contiguous()), attn.ATTN_ERR_INVALID), (dict(scale=-1.0), attn.ATTN_ERR_INVALID),
+                      (dict(ws=torch.zeros(1024, device="cuda")), attn.ATTN_ERR_WORKSPACE)):
+        with pytest.raises(attn.AttnError) as e:
+            attn.kv8_decode(bad.get("q", q), kc, vc, ks, vs, table, ln, bad.get("scale"), ws=bad.get("ws"))
+        assert e.value.code == code and str(e.value)
+    with pytest.raises(attn.AttnError):
+        attn.kv8_append(q[0, :, :2], q[0, :, :2], torch.zeros(1, dtype=torch.int64, device="cuda"), kc[:, :, :8].contiguous(),
+                        vc[:, :, :8].contiguous(), ks, vs)
+    got = attn.kv8_decode(q, kc, vc, ks, vs, table, ln)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_stream_argument():
     """stream= as a torch stream and as a handle; what the call allocates belongs
     to that stream."""
