@@ -63,6 +63,17 @@ __device__ __forceinline__ int scale_exp(float amax) {
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// Pairwise max(a, |w|) of two 16-bit values.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max2_abs(uint32_t a, uint32_t w) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(w & 0x7fff7fffu));
+  else
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(w & 0x7fff7fffu));
+  return r;
+}
+
 constexpr int kAppThreads = 256;
 
 // One warp per (chunk of `chunk` tokens, head, K or V): it takes the runs of
@@ -123,7 +134,7 @@ __global__ void __launch_bounds__(kAppThreads) attn_kv8_append_kernel(const __gr
     uint8_t* dst = p.cache[kv] + ((page * p.H + h) << p.page_shift) * D;
     const float old = first > 0 ? *scale : 0.f;
     uint4 v[kU];
-    float amax = 0.f;
+    uint32_t top = 0;  // largest magnitudes, a pair of 16-bit values (NaN ignored)
     auto load = [&](int i0) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
@@ -137,13 +148,11 @@ __global__ void __launch_bounds__(kAppThreads) attn_kv8_append_kernel(const __gr
       for (int u = 0; u < kU; ++u) {
         const uint32_t* w = &v[u].x;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = unpack2<BF16>(w[j]);
-          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
+        for (int j = 0; j < 4; ++j) top = max2_abs<BF16>(top, w[j]);
       }
     }
-    amax = warp_max(amax);
+    const float2 top2 = unpack2<BF16>(top);
+    const float amax = warp_max(fmaxf(top2.x, top2.y));
     const float now = fmaxf(pow2f(scale_exp(amax)), old);
     const float inv = 1.f / now;
     if (first > 0 && now > old) {  // the tokens before the run, rounded again
@@ -771,12 +780,13 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
   }
 }
 
-// One CTA per (request, query row and head): joins the parts of a segment that
-// several CTAs share; requests without keys get O = 0, LSE = -inf.  The parts
-// are dealt to the four warps, a lane holding D / 32 columns, eight parts'
-// loads in flight, and the warps' sums meet in shared memory: always in the
-// same order.
-template <int D, bool BF16>
+// Joins the parts of a segment that several CTAs share; requests without keys get
+// O = 0, LSE = -inf.  A lane holds D / 32 columns, eight parts' loads in flight.
+// WPR = 4: a block per query row, whose parts are dealt to its four warps (few
+// rows, many parts: one row of four long requests has 19 parts each).  WPR = 1: a
+// warp per row, four rows of a segment to a block (many rows: most segments are
+// one CTA's, and their blocks only find that out).  Always in the same order.
+template <int D, bool BF16, int WPR>
 __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_constant__ Kv8DecArgs p) {
   __shared__ long long sums[4][2];
   __shared__ float xo[4][D];
@@ -785,8 +795,12 @@ __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_consta
   constexpr int kPer = D / 32, kU = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int Hr = p.H * p.n_rb, R = p.Nq * p.G;
-  const int b = blockIdx.x / (p.H * R), hi = blockIdx.x % (p.H * R);
-  const int h = hi / R, idx = hi % R, rb = idx / p.rp, r = idx % p.rp;
+  // a block's rows: one, or four of one row block
+  const unsigned per = WPR == 4 ? 1 : 4, n_in = (p.rp + per - 1) / per;
+  const unsigned blk = blockIdx.x / n_in;  // (b, head, row block)
+  const int b = (int)(blk / (unsigned)Hr), hr = (int)(blk - (unsigned)b * Hr);
+  const int h = hr / p.n_rb, rb = hr - h * p.n_rb;
+  const int r = (int)((blockIdx.x - blk * n_in) * per) + (WPR == 4 ? 0 : warp), idx = rb * p.rp + r;
   long long before = 0, total = 0;
   for (int i = threadIdx.x; i < p.B; i += 128) {
     const int n = seg_units((kv8_len(p, i) + 127) >> 7);
@@ -807,24 +821,27 @@ __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_consta
   total = sums[0][1] + sums[1][1] + sums[2][1] + sums[3][1];
   const int nt = (kv8_len(p, b) + 127) >> 7;
   const long long units = total * Hr, n_cta = min((long long)p.grid, units);
-  const long long u0 = before * Hr + (long long)(h * p.n_rb + rb) * seg_units(nt);
+  const long long u0 = before * Hr + (long long)hr * seg_units(nt);
   const int c0 = nt ? (int)range_owner(u0 + kSegCost, units, n_cta) : 0;
   const int c1 = nt ? (int)range_owner(u0 + kSegCost + nt - 1, units, n_cta) : 0;
-  if (nt == 0 || c0 != c1) {
+  if ((nt == 0 || c0 != c1) && (WPR == 1 || idx < R)) {
     // the first CTA's part is in its second slot if its range began earlier
     const int s0 = nt && range_start(c0, units, n_cta) < u0 ? 1 : 0;
     auto part = [&](int c) -> size_t { return ((size_t)c * 2 + (c == c0 ? s0 : 0)) * p.rp + r; };
+    const bool live = idx < R;  // (WPR = 1: a warp may have no row)
     float acc[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
     float M = -INFINITY, Ls = 0.f;
-    if (nt) {
-      for (int c = c0 + (int)threadIdx.x; c <= c1; c += 128) M = fmaxf(M, p.ws_ml[part(c) * 2]);
+    if (nt && live) {
+      for (int c = c0 + (WPR == 4 ? (int)threadIdx.x : lane); c <= c1; c += 32 * WPR) M = fmaxf(M, p.ws_ml[part(c) * 2]);
       M = warp_max(M);
-      if (lane == 0) xml[warp][0] = M;
-      __syncthreads();
-      M = fmaxf(fmaxf(xml[0][0], xml[1][0]), fmaxf(xml[2][0], xml[3][0]));
-      for (int cb = c0 + warp * kU; cb <= c1; cb += 4 * kU) {
+      if constexpr (WPR == 4) {
+        if (lane == 0) xml[warp][0] = M;
+        __syncthreads();
+        M = fmaxf(fmaxf(xml[0][0], xml[1][0]), fmaxf(xml[2][0], xml[3][0]));
+      }
+      for (int cb = c0 + (WPR == 4 ? warp * kU : 0); cb <= c1; cb += WPR * kU) {
         float wgt = 0.f;
         if (lane < kU && cb + lane <= c1) {
           const size_t at = part(cb + lane) * 2;
@@ -861,23 +878,30 @@ __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_consta
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
-      if (lane == 0) xml[warp][1] = Ls;
+      if constexpr (WPR == 4) {
+        if (lane == 0) xml[warp][1] = Ls;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) xo[warp][lane * kPer + k] = acc[k];
-      __syncthreads();
-      Ls = (xml[0][1] + xml[1][1]) + (xml[2][1] + xml[3][1]);
+        for (int k = 0; k < kPer; ++k) xo[warp][lane * kPer + k] = acc[k];
+        __syncthreads();
+        Ls = (xml[0][1] + xml[1][1]) + (xml[2][1] + xml[3][1]);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int c = lane * kPer + k;
+          acc[k] = (xo[0][c] + xo[1][c]) + (xo[2][c] + xo[3][c]);
+        }
+      }
     }
-    const int i = idx / p.G, hq = h * p.G + idx % p.G;
-    if (threadIdx.x < D / 2) {
-      const int c = 2 * threadIdx.x;
+    if (live && (WPR == 1 || warp == 0)) {
+      const int i = idx / p.G, hq = h * p.G + idx - i * p.G;
       const float inv = Ls != 0.f ? 1.f / Ls : 0.f;
-      float a[2] = {0.f, 0.f};
-      if (nt)
-        for (int k = 0; k < 2; ++k) a[k] = ((xo[0][c + k] + xo[1][c + k]) + (xo[2][c + k] + xo[3][c + k])) * inv;
-      reinterpret_cast<uint32_t*>(p.o)[((((size_t)b * p.Nq + i) * p.Hq + hq) * D + c) / 2] = pack2<BF16>(a[0], a[1]);
+      uint32_t wv[kPer / 2];
+#pragma unroll
+      for (int k = 0; k < kPer / 2; ++k) wv[k] = pack2<BF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+      uint8_t* dst = static_cast<uint8_t*>(p.o) + ((((size_t)b * p.Nq + i) * p.Hq + hq) * D + lane * kPer) * 2;
+      if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(wv[0], wv[1]);
+      else *reinterpret_cast<uint32_t*>(dst) = wv[0];
+      if (lane == 0) p.lse[((size_t)b * p.Hq + hq) * p.Nq + i] = Ls != 0.f ? (M + __log2f(Ls)) * kLn2 : -INFINITY;
     }
-    if (threadIdx.x == 0)
-      p.lse[((size_t)b * p.Hq + hq) * p.Nq + i] = Ls != 0.f ? (M + __log2f(Ls)) * kLn2 : -INFINITY;
   }
   griddep_launch_dependents();
 }
@@ -917,13 +941,19 @@ cudaError_t launch_kv8_split(const Kv8DecArgs& a, cudaStream_t stream) {
                    : (a.rp == 8 ? launch_split_n<64, 8>(a, stream) : launch_split_n<64, 16>(a, stream));
 }
 
+template <int D, bool BF16>
+static cudaError_t launch_merge_t(const Kv8DecArgs& a, cudaStream_t stream) {
+  const long long segs = (long long)a.B * a.H * a.n_rb;
+  // parts of a segment: about a.grid / segs + 1 (64 requests of 8 heads: 51 us with a
+  // warp per row, 52 with a block; 17 requests of 2 heads and 3 row blocks: 20 and 19)
+  if (a.grid >= 2 * segs)
+    return launch_pdl(attn_kv8_merge_kernel<D, BF16, 4>, (unsigned)(segs * a.rp), 128, 0, stream, a);
+  return launch_pdl(attn_kv8_merge_kernel<D, BF16, 1>, (unsigned)(segs * ((a.rp + 3) / 4)), 128, 0, stream, a);
+}
+
 cudaError_t launch_kv8_merge(const Kv8DecArgs& a, cudaStream_t stream) {
-  const unsigned grid = (unsigned)((long long)a.B * a.Hq * a.Nq);
-  if (a.d == 128)
-    return a.bf16 ? launch_pdl(attn_kv8_merge_kernel<128, true>, grid, 128, 0, stream, a)
-                  : launch_pdl(attn_kv8_merge_kernel<128, false>, grid, 128, 0, stream, a);
-  return a.bf16 ? launch_pdl(attn_kv8_merge_kernel<64, true>, grid, 128, 0, stream, a)
-                : launch_pdl(attn_kv8_merge_kernel<64, false>, grid, 128, 0, stream, a);
+  if (a.d == 128) return a.bf16 ? launch_merge_t<128, true>(a, stream) : launch_merge_t<128, false>(a, stream);
+  return a.bf16 ? launch_merge_t<64, true>(a, stream) : launch_merge_t<64, false>(a, stream);
 }
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int sms, cudaStream_t stream) {
