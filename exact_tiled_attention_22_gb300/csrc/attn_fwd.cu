@@ -178,8 +178,8 @@ struct VarPair {
 // VARLEN (with none of the above): packed sequences of different lengths, with
 // Hq / Hkv query heads to a key head (p.cu_q, p.cu_k; VarSeq below).  Query and
 // key tiles are counted from the END of their sequence, so that the ragged tile
-// is the first one and the causal diagonal, aligned at the ends, always runs
-// through tile corners whatever the two lengths are.  The ragged tile's rows
+// is the first one and the causal diagonal, which is aligned at the ends, crosses
+// the tiles in the same places whatever the two lengths are.  The ragged tile's rows
 // before the sequence would be its neighbour's: the tensor maps have the row
 // stride twice, as a 128-row window (r) and as its place (s), and a tile that
 // begins at row -m of its sequence is loaded at (r = -m, s = first row), where
@@ -191,6 +191,16 @@ struct VarPair {
 // neighbouring positions.  Where the batch has too few pairs of tiles for the
 // GPU (few queries on many keys), p.nsplit CTAs share the key tiles of a pair;
 // their unnormalised O, reference max and sum meet in attn_var_merge_kernel.
+// Bound as the plain kernel where sequences are long (15813 tokens in five of 700 to
+// 8192, 16 / 4 heads, d 128, causal: 270 us, 1300 TFLOP/s, the tensor pipe 57 %
+// busy, the dense kernel's rate), by the chain of a CTA where they are short (24
+// prompts of 1 to 400 tokens on up to 2197 keys, 12 / 4 heads, d 64: 31 us, the 18
+// key tiles of the longest).  Tried and not kept: persistent CTAs with equal shares
+// of all key tiles (as in attn_kv8.cu), which took 12 us off batches of short
+// prompts but 308 us on the long batch and 53 against 43 on a ragged one (the block
+// scheduler balances long tiles better, and parts of shared tiles cost traffic and
+// a merge); the sequences ordered by length, 274 against 270 us and 21 against 17
+// on 96 prompts of one token.
 template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false, bool VARLEN = false>
 __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ FwdArgs p) {
@@ -1175,7 +1185,9 @@ cudaError_t launch_fwd_t(const FwdArgs& a, cudaStream_t stream) {
 // Heads (Gp) and positions (R, a power of two, so that the causal limit of a tile
 // is a shift) of a packed query tile.  Gp is the largest power of two in the
 // group: every row of the tile is used.  Short prompts of other groups are packed
-// whole, unused rows and all, which saves more CTAs than it wastes rows.
+// whole, unused rows and all, which saves more CTAs than it wastes rows (groups of
+// 3: 96 prompts of one token 17 us against 44, 24 of 64 tokens on 420 keys 12
+// against 21; prompts that fill their tiles would only lose the rows).
 void fwd_varlen_shape(int G, long long Nq, int B, int* Gp, int* R) {
   int g = 1;
   while (g < 128 && G % (2 * g) == 0) g *= 2;
@@ -1193,7 +1205,8 @@ void fwd_varlen_shape(int G, long long Nq, int B, int* Gp, int* R) {
 // CTAs that share the key tiles of a pair: as many as fill the SMs once where the
 // pairs alone do not, if any sequence can be long enough to be shared.  (One
 // sequence of 64 queries on 2400 keys, 12 heads: 15 us against 33 by one
-// CTA a pair.)
+// CTA a pair.  Sharing beyond one CTA an SM, up to 304 or 456, made 24 prompts of 64
+// tokens on 420 keys 19 us instead of 12.)
 int fwd_varlen_nsplit(long long ctas, long long Nk) {
   if ((Nk + 127) / 128 < 2 * kVarMinChunk || ctas >= 152) return 1;
   const long long n = (152 + ctas - 1) / ctas, most = (Nk + 127) / 128 / kVarMinChunk;

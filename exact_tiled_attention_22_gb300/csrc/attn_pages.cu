@@ -15,7 +15,8 @@
 // CTAs: each CTA computes the prefix sums for itself (B values, from L2), then
 // they share the tokens and table rows; the cluster barrier between the reads
 // of the lengths and their update lets new_lens be lens and left be
-// free_count.
+// free_count.  Measured (graph replay): one token for each of 256 requests
+// 5.8 us, 28005 tokens of 48 prompts 6.9 us.
 #include <climits>
 
 #include "kernels.h"
