@@ -466,16 +466,20 @@ _bind = _load_bind()
 
 
 def _on_stream(f):
-    """A `stream` argument (a torch stream or a handle) is made the current stream
-    for the call, so that what the call allocates belongs to it."""
+    """A `stream` argument (a torch stream or a handle, of the tensors' device) is
+    made the current stream for the call, so that what the call allocates belongs to it."""
     @functools.wraps(f)
     def call(*args, stream=None, **kw):
         if stream is None:
             return f(*args, **kw)
+        dev = next((x.device for x in (*args, *kw.values()) if isinstance(x, torch.Tensor)), None)
+        if dev is None or dev.type != "cuda":
+            return f(*args, **kw)  # refused there
         if isinstance(stream, int):
-            dev = args[0].device
             stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
                       else torch.cuda.default_stream(dev))
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
         with torch.cuda.stream(stream):
             return f(*args, **kw)
     return call
@@ -589,5 +593,9 @@ class VarlenAttentionFunction(torch.autograd.Function):
 
 
 def attention_varlen(q, k, v, cu_q, cu_k, scale=None, causal=False):
-    """Differentiable attention on packed sequences (see varlen_fwd)."""
+    """Differentiable attention on packed sequences (see varlen_fwd).  A training
+    step may be captured into a CUDA graph, forward and backward together; as for
+    every torch operator, no autograd graph of the same leaves from before the
+    capture may still be alive then (drop its loss first): torch would run their
+    gradient accumulation on the stream of that graph, outside the capture."""
     return VarlenAttentionFunction.apply(q, k, v, cu_q, cu_k, scale, causal)

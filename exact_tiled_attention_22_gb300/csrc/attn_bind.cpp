@@ -100,10 +100,9 @@ attn_dtype_t dtype16(const at::Tensor& t, const char* name) {
   refuse(std::string(name) + " must be fp16 or bf16, got " + say(t));
 }
 
-int64_t whole(PyObject* o, const char* name) {
+int64_t whole(PyObject* o) {
   const long long v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw Refused();
-  (void)name;
   return v;
 }
 
@@ -171,7 +170,7 @@ PyObject* pages_extend(PyObject* const* a, Py_ssize_t n) {
                    &free_pages = tensor(a[3], "free_pages"), &count = tensor(a[4], "free_count");
   const Call c(lens, "lens");
   c.want(lens, "lens", at::kInt, {-1});
-  const int64_t B = lens.size(0), T = whole(a[6], "max_new");
+  const int64_t B = lens.size(0), T = whole(a[6]);
   c.want(add, "add", at::kInt, {B});
   c.want(table, "block_table", at::kInt, {B, -1});
   c.want(free_pages, "free_pages", at::kInt, {-1});
@@ -194,7 +193,7 @@ PyObject* pages_extend(PyObject* const* a, Py_ssize_t n) {
   const at::Tensor granted = c.empty({B}, at::kInt), cu = c.empty({B + 1}, at::kInt), slots = c.empty({T}, at::kLong);
   check(attn_pages_extend(ptr<int>(lens), ptr<int>(add), narrow(B, "B"), ptr<int>(table), narrow(table.size(1), "width"),
                           ptr<int>(free_pages), ptr<int>(count), narrow(free_pages.size(0), "free_pages"),
-                          narrow(whole(a[5], "page"), "page"), T, ptr<int>(new_lens), ptr<int>(granted), ptr<int>(cu),
+                          narrow(whole(a[5]), "page"), T, ptr<int>(new_lens), ptr<int>(granted), ptr<int>(cu),
                           ptr<int64_t>(slots), ptr<int>(left), c.stream()));
   return tuple({new_lens, granted, cu, slots, left});
 }
@@ -217,7 +216,7 @@ PyObject* pages_release(PyObject* const* a, Py_ssize_t n) {
   c.want(left, "free_left", at::kInt, {1});
   check(attn_pages_release(ptr<int>(lens), ptr<int>(done), narrow(B, "B"), ptr<int>(table), narrow(table.size(1), "width"),
                            ptr<int>(free_pages), ptr<int>(count), narrow(free_pages.size(0), "free_pages"),
-                           narrow(whole(a[5], "page"), "page"), ptr<int>(new_lens), ptr<int>(left), c.stream()));
+                           narrow(whole(a[5]), "page"), ptr<int>(new_lens), ptr<int>(left), c.stream()));
   return tuple({new_lens, left});
 }
 

@@ -1422,9 +1422,10 @@ __device__ __forceinline__ VarScan var_scan(const BwdArgs& p, uint8_t* smem, boo
   }
   __syncthreads();
   if (publish) {
-    // chunks of 2 G a steps: an equal share of kVarChunks, no less than 32
+    // chunks of 2 G a steps: an equal share of kVarChunks, no less than 32 (and no
+    // more than the 2^20 steps of the longest sequence)
     const long long total = c_steps * p.H, unit = 2ll * p.G;
-    const int a = (int)max((16ll + p.G - 1) / p.G, (total + kVarChunks * unit - 1) / (kVarChunks * unit));
+    const int a = (int)min(1ll << 19, max((16ll + p.G - 1) / p.G, (total + kVarChunks * unit - 1) / (kVarChunks * unit)));
     // Sequences with the most steps first, in half octaves (counted, then
     // placed): the short ones fill the end of the kernel.
     __shared__ int hist[128];

@@ -942,7 +942,9 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
       tc_fence_after();
       // a row that saw no key (possible only under a block-sparse mask) has
       // O = 0 and LSE = -inf
-      const float inv_l = l > 0.f ? (DROPOUT ? p.drop.scale : 1.f) / l : 0.f;
+      // (VARLEN: a row that is not a number, l = NaN, has a NaN for its LSE)
+      const bool some = VARLEN ? l != 0.f : l > 0.f;
+      const float inv_l = some ? (DROPOUT ? p.drop.scale : 1.f) / l : 0.f;
       const int v_sub = VARLEN ? (qd * 32 + lane) - (row - row_lo) * p.Gp : 0;  // head of the row in its tile
       const bool valid = VARLEN ? row >= 0 && row < row_lo + p.R : row < p.N;
       const int hq = VARLEN ? v_head + (valid ? v_sub : 0) : h;
@@ -1043,7 +1045,7 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
             for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           }
         }
-        if (valid) p.lse[(size_t)hq * p.N + o_row] = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
+        if (valid) p.lse[(size_t)hq * p.N + o_row] = some ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
       } else {
       // O/l rounded to 16-bit into this tile's Q buffer (no S of the tile
       // reads Q any more: its last S completed before its last P), laid out
@@ -1075,7 +1077,7 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
       }
       if (valid)
         p.lse[VARLEN ? (size_t)hq * p.N + o_row : (size_t)bh * p.N + row] =
-            l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
+            some ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
       fence_proxy_async_smem();
       }
     }

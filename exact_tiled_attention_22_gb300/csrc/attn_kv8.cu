@@ -574,7 +574,6 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
         const bool bad = top >= 0x7f800000u;
 #pragma unroll
         for (int j = 0; j < E; ++j) f[j] *= mul;
-        float s16 = 1.f;
 #pragma unroll
         for (int t = 0; t < NP; ++t) {
           uint32_t cw[E / 4];
@@ -594,9 +593,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
             *reinterpret_cast<uint4*>(sbase + L::kQ + swz) = make_uint4(cw[0], cw[1], cw[2], cw[3]);
           else
             *reinterpret_cast<uint2*>(sbase + L::kQ + swz) = make_uint2(cw[0], cw[1]);
-          s16 *= 0.0625f;
         }
-        (void)s16;
         if (c == 0) {
           qs_s[r] = bad ? __uint_as_float(0x7fc00000u) : pow2f(e) * p.scale * kLog2e;
           qi_s[r] = i;

@@ -353,11 +353,14 @@ int attn_decode(const void* q, const void* k, const void* v, void* o, float* lse
  * lq positions (lk > lq: a prompt that goes on after cached keys).  A query that
  * sees no key gets O = 0, LSE = -inf, dQ = 0; a key that no query sees gets
  * dK = dV = 0.  Rows of no sequence (before cu[0], behind cu[B]) are neither read
- * nor written.  dK and dV of a key head sum over its group in a fixed order;
+ * nor written.  Values (and for the gradients queries and dO) must be finite: as in
+ * any matrix product a NaN or an infinity there may reach the sequence's rows
+ * that the mask keeps from it; one in a query or key reaches the rows that see
+ * it only.  dK and dV of a key head sum over its group in a fixed order;
  * dQ as in attn_bwd.  o and lse are the forward's.
  * Workspaces as attn_bwd's; the forward needs one only where its size is not 0
- * (few queries on many keys, whose key range several blocks share).  Offsets are clamped to the
- * tensors; if they do not ascend, outputs are unspecified.
+ * (few queries on many keys, whose key range several blocks share).  Offsets are
+ * clamped to the tensors; if they do not ascend, outputs are unspecified.
  * 1 <= B <= 8192, 0 <= Tq, Tk < 2^26, Hq / Hkv <= 1024.
  * The pages name batches of sequences only as [B, N, H, d]; the packed layout
  * and the grouped heads are an addition of this library.
@@ -440,7 +443,8 @@ int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o,
  * not further apart than 2^124, and that far only for values beyond 2^46).
  * Lengths are clamped to [0, width * page]; codes behind a request's last token
  * and entries of block_table behind its last page are not used; a page id
- * outside [0, P) reads as zeros.  Query and key products carry fp16 / bf16
+ * outside [0, P) reads as zeros.  A NaN among a request's cached values may reach
+ * all its queries, also with causal those before it.  Query and key products carry fp16 / bf16
  * queries exactly up to 2^-21 of a row's largest element; probabilities are
  * rounded to 2^-14 (fp16) or 2^-9 (bf16) of their value.
  * workspace: as attn_decode's, size from attn_kv8_decode_workspace_size.

@@ -463,3 +463,22 @@ def test_a_serving_run():
         plain64.check(o, ro, bo, f"step {i}")
         plain64.check(lse, rl, bl, f"lse of step {i}")
     assert attn.attn_status() == 0
+
+
+def test_stream_handle_with_keyword_arguments():
+    """A handle says nothing of its device: that is the tensors', wherever they stand
+    among the arguments."""
+    from exact_tiled_attention_22_gb300 import attn
+    lens = [90]
+    q, kc, vc, ks, vs, table = (x.cuda() for x in problem(lens, 1, 4, 2, 64, 32, "bf16", seed=16))
+    ln = torch.tensor(lens, dtype=torch.int32).cuda()
+    want = attn.kv8_decode(q, kc, vc, ks, vs, table, ln)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side.cuda_stream, 0):
+        o, lse = attn.kv8_decode(q=q, k_cache=kc, v_cache=vc, k_scale=ks, v_scale=vs, block_table=table, lens=ln,
+                                 stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    with pytest.raises(ValueError):
+        attn.kv8_decode(q.cpu(), kc, vc, ks, vs, table, ln, stream=side.cuda_stream)

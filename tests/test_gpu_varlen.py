@@ -360,3 +360,68 @@ def test_wait_limit_reports_a_timeout():
         attn.attn_set_wait_limit(0, 0)
     o2, lse2 = attn.varlen_fwd(q, k, v, c, c, None, True)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("lens_q,lens_k", [([70, 40], [70, 40]), ([5, 64], [2000, 1500])])
+def test_not_numbers_reach_their_rows_only(lens_q, lens_k):
+    """A NaN query has a NaN row of O and of LSE, a NaN key those of the queries
+    that see it (causal), whether a pair of tiles is one block's or several share it;
+    all other rows keep their bits."""
+    from exact_tiled_attention_22_gb300 import attn
+    Hq, H, d = 4, 2, 64
+    q, k, v, _ = draw(lens_q, lens_k, Hq, H, d, "bf16", seed=40)
+    clean, clean_lse = attn.varlen_fwd(q.cuda(), k.cuda(), v.cuda(), offsets(lens_q), offsets(lens_k), None, True)
+    q[2, 1, 5] = math.nan                      # query 2 of sequence 0, head 1
+    hidden = 7                                 # the key that the last 7 queries of sequence 1 see
+    k[sum(lens_k) - hidden, 1, 9] = math.nan   # key head 1: query heads 2, 3
+    o, lse = attn.varlen_fwd(q.cuda(), k.cuda(), v.cuda(), offsets(lens_q), offsets(lens_k), None, True)
+    bad = torch.zeros(sum(lens_q), Hq, dtype=torch.bool)
+    bad[2, 1] = True
+    bad[sum(lens_q) - hidden:, 2:] = True
+    bad = bad.cuda()
+    assert torch.equal(torch.isnan(o).all(-1), bad) and torch.equal(torch.isnan(o).any(-1), bad)
+    assert torch.equal(torch.isnan(lse), bad.t())
+    assert torch.equal(o[~bad], clean[~bad]) and torch.equal(lse[~bad.t()], clean_lse[~bad.t()])
+    assert attn.attn_status() == 0
+
+
+def test_a_captured_training_step():
+    """attention_varlen and its backward captured together, replayed on other
+    values and lengths: the eager results (dQ is summed in no fixed order)."""
+    from exact_tiled_attention_22_gb300 import attn
+    Hq, H, d, T = 4, 2, 128, 300
+    lens = [[100, 150, 50], [3, 290, 0]]       # the second leaves seven rows of padding
+    xs = [draw([T], [T], Hq, H, d, "bf16", seed=50 + i) for i in range(2)]
+    q, k, v = (x.cuda().requires_grad_() for x in xs[0][:3])
+    w = xs[0][3].cuda()
+    c = offsets(lens[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        o = attn.attention_varlen(q, k, v, c, c, None, True)
+        return (o, *torch.autograd.grad(o, (q, k, v), w))
+
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = [x.detach() for x in step()]
+    for i in (1, 0):
+        with torch.no_grad():
+            for t, x in zip((q, k, v, w), xs[i]):
+                t.copy_(x.cuda())
+        c.copy_(offsets(lens[i]))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in out]
+        want = [x.detach() for x in step()]
+        assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])
+        # |dQ|: two fp32 sums of the same terms in different orders, then one bf16 rounding each
+        assert (got[1].float() - want[1].float()).abs().max() <= 2.0 ** -7 * want[1].float().abs().max()
+        n = sum(lens[i])
+        for x in got:
+            assert (x[n:] == 0).all()
+    assert attn.attn_status() == 0
