@@ -1447,12 +1447,21 @@ __device__ __forceinline__ VarScan var_scan(const BwdArgs& p, uint8_t* smem, boo
       atomicAdd(&hist[bucket(lq, lk)], 1);
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      int at = 0;
-      for (int i = 0; i < 128; ++i) {
-        const int n = hist[i];
-        hist[i] = at;
-        at += n;
+    if (threadIdx.x < 32) {  // exclusive sums, four buckets to a lane
+      int n[4], own = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) own += n[i] = hist[4 * lane + i];
+      int at = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += x;
+      }
+      at -= own;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        hist[4 * lane + i] = at;
+        at += n[i];
       }
     }
     __syncthreads();

@@ -196,8 +196,8 @@ struct VarPair {
 // busy, the dense kernel's rate), by the chain of a CTA where they are short (24
 // prompts of 1 to 400 tokens on up to 2197 keys, 12 / 4 heads, d 64: 31 us, the 18
 // key tiles of the longest).  Tried and not kept: persistent CTAs with equal shares
-// of all key tiles (as in attn_kv8.cu), which took 12 us off batches of short
-// prompts but 308 us on the long batch and 53 against 43 on a ragged one (the block
+// of all key tiles (as in attn_kv8.cu), faster only for many short prompts: 308 us
+// on the long batch, and 53 against 43 on 16 texts of 16 to 2048 tokens (the block
 // scheduler balances long tiles better, and parts of shared tiles cost traffic and
 // a merge); the sequences ordered by length, 274 against 270 us and 21 against 17
 // on 96 prompts of one token.

@@ -85,18 +85,20 @@ __device__ __forceinline__ uint32_t max2_abs(uint32_t a, uint32_t w) {
   return r;
 }
 
-constexpr int kAppThreads = 256;
+constexpr int kAppThreads = 128;
 
 // One warp per (chunk of `chunk` tokens, head, K or V): it takes the runs of
 // consecutive slots in one page that begin in its chunk.  Two passes over a
 // run: largest magnitude, then codes; the first 16 (d = 128) or 32 (d = 64)
 // tokens stay in registers between them.  Bound by HBM for prompts (the 16-bit
 // values in, the codes out), by latency for a decoding step: the chain slot,
-// values and old scale, codes.  Measured: 31749 tokens of 4 heads, d = 64, page 16
-// (49 MB) 11.8 us or 4.1 TB/s, the schedulers 60 % busy with conversions; one
-// token of each of 256 requests, 8 heads, d = 128, 4.3 us.
+// values and old scale, codes.  Blocks of 128 threads, six or more to an SM (48 %
+// more warps than blocks of 256 at the same 72 registers).  Measured: 31749 tokens of
+// 4 heads, d = 64, page 16 (49 MB) 11.1 us or 4.4 TB/s (12.0 with blocks of 256, 11.6
+// with eight to an SM at 64 registers); one token of each of 256 requests, 8 heads,
+// d = 128, 4.3 us.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kAppThreads) attn_kv8_append_kernel(const __grid_constant__ Kv8AppendArgs p,
+__global__ void __launch_bounds__(kAppThreads, 6) attn_kv8_append_kernel(const __grid_constant__ Kv8AppendArgs p,
                                                                      int chunk) {
   griddep_wait();
   constexpr int kLanes = D / 8;          // lanes of 16 bytes to a token

@@ -16,7 +16,7 @@
 // they share the tokens and table rows; the cluster barrier between the reads
 // of the lengths and their update lets new_lens be lens and left be
 // free_count.  Measured (graph replay): one token for each of 256 requests
-// 5.8 us, 28005 tokens of 48 prompts 6.9 us.
+// 4.8 us, 28005 tokens of 48 prompts 6.8 us.
 #include <climits>
 
 #include "kernels.h"
@@ -26,10 +26,10 @@ namespace attn {
 namespace {
 
 constexpr int kPgThreads = 1024;
-constexpr int kPgWarps = kPgThreads / 32;
 
 // Exclusive prefix sums of x and y over the block's threads, added to the
-// carries, which become the totals.  wx, wy: shared [kPgWarps].
+// carries, which become the totals.  wx, wy: shared, NW warps.
+template <int NW>
 __device__ __forceinline__ void block_scan2(long long& x, long long& y, long long& cx, long long& cy, long long* wx,
                                             long long* wy) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -49,7 +49,7 @@ __device__ __forceinline__ void block_scan2(long long& x, long long& y, long lon
   __syncthreads();
   long long bx = 0, by = 0, tx = 0, ty = 0;
   {
-    const long long vx = wx[lane], vy = wy[lane];  // kPgWarps = 32
+    const long long vx = lane < NW ? wx[lane] : 0, vy = lane < NW ? wy[lane] : 0;
     long long sx = vx, sy = vy;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -81,16 +81,18 @@ struct PageReq {
   int cu, off, len;
 };
 
-__global__ void __launch_bounds__(kPgThreads, 1) attn_pages_extend_kernel(const __grid_constant__ PagesArgs p) {
+template <int NT>
+__global__ void __launch_bounds__(NT, 1) attn_pages_extend_kernel(const __grid_constant__ PagesArgs p) {
+  constexpr int NW = NT / 32;
   extern __shared__ __align__(16) uint8_t pg_smem[];
   PageReq* req = reinterpret_cast<PageReq*>(pg_smem);
-  __shared__ long long wx[kPgWarps], wy[kPgWarps];
+  __shared__ long long wx[NW], wy[NW];
   griddep_wait();
   const int ps = 1 << p.page_shift;
   const int n_cta = gridDim.x, cta = blockIdx.x;
   const int count = min(max(*p.free_count, 0), p.free_cap);
   long long c_need = 0, c_add = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kPgThreads) {
+  for (int b0 = 0; b0 < p.B; b0 += NT) {
     const int b = b0 + threadIdx.x;
     int len = 0, add = 0;
     if (b < p.B) {
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) attn_pages_extend_kernel(const 
     const int p_old = valid ? (int)(((long long)len + ps - 1) >> p.page_shift) : 0;
     const long long need = valid ? ((end + ps - 1) >> p.page_shift) - p_old : 0;
     long long sn = need, sa = add > 0 ? add : 0;
-    block_scan2(sn, sa, c_need, c_add, wx, wy);
+    block_scan2<NW>(sn, sa, c_need, c_add, wx, wy);
     const bool served = valid && b < p.B && (need == 0 || sn + need <= count);
     if (b < p.B) {
       const int cu = (int)min(sa, (long long)INT_MAX);
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) attn_pages_extend_kernel(const 
 
   // Block table rows: a warp per request.
   const int lane = threadIdx.x & 31;
-  const int gw = (cta * kPgThreads + (int)threadIdx.x) >> 5, n_gw = n_cta * kPgWarps;
+  const int gw = (cta * NT + (int)threadIdx.x) >> 5, n_gw = n_cta * NW;
   for (int b = gw; b < p.B; b += n_gw) {
     const PageReq r = req[b];
     if (r.off < 0) continue;
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) attn_pages_extend_kernel(const 
     for (int j = j0 + lane; j < j1; j += 32) row[j] = p.free_pages[count - 1 - (r.off + (j - j0))];
   }
   // Slots: a thread per new token; its request by bisection of cu.
-  for (long long t = (long long)cta * kPgThreads + threadIdx.x; t < p.T; t += (long long)n_cta * kPgThreads) {
+  for (long long t = (long long)cta * NT + threadIdx.x; t < p.T; t += (long long)n_cta * NT) {
     long long slot = -1;
     if (t < total) {
       int lo = 0, hi = p.B - 1;  // last request with cu <= t
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) attn_pages_extend_kernel(const 
   cluster_sync_all();
   if (cta == 0) {
     long long taken = 0;
-    for (int b = threadIdx.x; b < p.B; b += kPgThreads) {
+    for (int b = threadIdx.x; b < p.B; b += NT) {
       const PageReq r = req[b];
       const int add = p.add[b];
       const int g = r.off >= 0 ? add : 0;
@@ -163,12 +165,12 @@ __global__ void __launch_bounds__(kPgThreads, 1) attn_pages_extend_kernel(const 
     // Pages taken: the served needs are a prefix of all of them (a refused
     // request's inclusive sum is above the count, and so is every later one
     // that needs a page), so it is the largest served inclusive sum.
-    __shared__ long long most[kPgWarps];
+    __shared__ long long most[NW];
     for (int o = 16; o > 0; o >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, o));
     if (lane == 0) most[threadIdx.x >> 5] = taken;
     __syncthreads();
     if (threadIdx.x < 32) {
-      long long v = most[threadIdx.x];
+      long long v = threadIdx.x < NW ? most[threadIdx.x] : 0;
       for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
       if (threadIdx.x == 0) {
         p.cu_new[p.B] = total;
@@ -182,9 +184,10 @@ __global__ void __launch_bounds__(kPgThreads, 1) attn_pages_extend_kernel(const 
 // Pages of the finished requests go back on the stack, in the order of the
 // requests and of their pages; their lengths become 0.  One CTA.
 __global__ void __launch_bounds__(kPgThreads, 1) attn_pages_release_kernel(const __grid_constant__ PagesArgs p) {
+  constexpr int NW = kPgThreads / 32;
   extern __shared__ __align__(16) uint8_t pg_smem[];
   int* off = reinterpret_cast<int*>(pg_smem);  // [B] stack offset of the request's first page, -1: kept
-  __shared__ long long wx[kPgWarps], wy[kPgWarps];
+  __shared__ long long wx[NW], wy[NW];
   griddep_wait();
   const int ps = 1 << p.page_shift, lane = threadIdx.x & 31;
   const int count = min(max(*p.free_count, 0), p.free_cap);
@@ -199,11 +202,11 @@ __global__ void __launch_bounds__(kPgThreads, 1) attn_pages_release_kernel(const
       if (gone && len > 0) n = min(((long long)len + ps - 1) >> p.page_shift, (long long)p.width);
     }
     const long long own = n;
-    block_scan2(n, z, c_n, c_z, wx, wy);
+    block_scan2<NW>(n, z, c_n, c_z, wx, wy);
     if (b < p.B) off[b] = gone && own > 0 ? (int)min(n, (long long)INT_MAX) : -1;
   }
   __syncthreads();
-  for (int b = threadIdx.x >> 5; b < p.B; b += kPgWarps) {
+  for (int b = threadIdx.x >> 5; b < p.B; b += NW) {
     if (off[b] < 0) continue;
     const int n = (int)min(((long long)p.lens[b] + ps - 1) >> p.page_shift, (long long)p.width);
     const int* row = p.table + (size_t)b * p.width;
@@ -220,17 +223,18 @@ __global__ void __launch_bounds__(kPgThreads, 1) attn_pages_release_kernel(const
 
 }  // namespace
 
-cudaError_t launch_pages_extend(const PagesArgs& a, cudaStream_t stream) {
-  auto* k = attn_pages_extend_kernel;
+template <int NT>
+static cudaError_t launch_extend_t(const PagesArgs& a, cudaStream_t stream) {
+  auto* k = attn_pages_extend_kernel<NT>;
   const size_t smem = sizeof(PageReq) * (size_t)a.B;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(PageReq) * kPagesMaxB);
   if (e != cudaSuccess) return e;
   // one CTA for a decoding step, up to eight (a portable cluster) for prompts
-  const long long want = ((a.T > 4ll * a.B ? (long long)a.T : 4ll * a.B) + kPgThreads - 1) / kPgThreads;
+  const long long want = ((a.T > 4ll * a.B ? (long long)a.T : 4ll * a.B) + NT - 1) / NT;
   const unsigned n = (unsigned)(want >= 8 ? 8 : (want >= 4 ? 4 : (want >= 2 ? 2 : 1)));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(n);
-  cfg.blockDim = dim3(kPgThreads);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -243,6 +247,14 @@ cudaError_t launch_pages_extend(const PagesArgs& a, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+// Blocks of 256 threads while they take one look at the requests and four at the
+// tokens (a token for each of 256 requests: 4.8 us, 5.7 with 1024 threads, whose
+// scans and barriers are longer), of 1024 above (28005 tokens of 48 prompts: 6.8 us, 9.7
+// with 256).
+cudaError_t launch_pages_extend(const PagesArgs& a, cudaStream_t stream) {
+  return a.B <= 256 && a.T <= 1024 ? launch_extend_t<256>(a, stream) : launch_extend_t<kPgThreads>(a, stream);
 }
 
 cudaError_t launch_pages_release(const PagesArgs& a, cudaStream_t stream) {
