@@ -78,7 +78,7 @@ def link_bind(obj: str) -> None:
     lib = os.path.join(_torch_dir(), "lib")
     tmp = BIND + f".tmp{os.getpid()}"
     _run([shutil.which("g++") or "g++", "-shared", obj, "-o", tmp, f"-L{HERE}", "-l:libattn.so", "-Wl,-rpath,$ORIGIN",
-          f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "link of attn_bind.so failed")
+          f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], "link of attn_bind.so failed")
     os.replace(tmp, BIND)
 
 

@@ -8,6 +8,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -15,6 +17,7 @@
 
 #include <cmath>
 #include <string>
+#include <vector>
 
 #include "attn.h"
 
@@ -85,8 +88,25 @@ struct Call {
     if (t.stride(2) != 1 || (t.stride(1) != d && H > 1)) refuse(std::string(name) + ": the heads of a token must be contiguous");
     return T > 1 ? t.stride(0) : H * d;
   }
+  // (the allocation behind torch.empty, without its dispatch: 0.55 against 0.77 us)
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+    return at::detail::empty_cuda(shape, type, dev, std::nullopt);
+  }
+  // Small int32 vectors in one allocation (0.2 us each instead of 0.6), 16 bytes aligned.
+  std::vector<at::Tensor> vectors(std::initializer_list<int64_t> lens) const {
+    int64_t n = 0;
+    for (int64_t x : lens) n += (x + 3) / 4 * 4;
+    const at::Tensor all = empty({n}, at::kInt);
+    std::vector<at::Tensor> out;
+    int64_t at = 0;
+    for (int64_t x : lens) {
+      at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+      t.unsafeGetTensorImpl()->set_storage_offset(at);
+      t.unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(&x, 1));
+      out.push_back(std::move(t));
+      at += (x + 3) / 4 * 4;
+    }
+    return out;
   }
   void* stream() const { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 };
@@ -142,20 +162,20 @@ PyObject* tuple(std::initializer_list<at::Tensor> ts) {
 // The caller's workspace, or one of `need` bytes for the call (freed after it: the
 // allocator hands its memory on in stream order).
 struct Workspace {
-  at::Tensor t;
+  c10::DataPtr own;
   void* p = nullptr;
   size_t n = 0;
   Workspace(const Call& c, PyObject* o, size_t need) {
     if (o != Py_None) {
-      t = tensor(o, "ws");
+      const at::Tensor& t = tensor(o, "ws");
       if (t.device() != c.dev || !t.is_contiguous()) refuse("ws must be contiguous on " + c.dev.str() + ", got " + say(t));
+      p = t.data_ptr();
+      n = t.nbytes();
     } else if (need) {
-      t = c.empty({(int64_t)need}, at::kByte);
-    } else {
-      return;
+      own = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+      p = own.get();
+      n = need;
     }
-    p = t.data_ptr();
-    n = t.nbytes();
   }
 };
 
@@ -177,20 +197,13 @@ PyObject* pages_extend(PyObject* const* a, Py_ssize_t n) {
   c.want(count, "free_count", at::kInt, {1});
   if (T < 0) refuse("max_new must not be negative");
   c10::cuda::CUDAGuard guard(c.dev);
-  at::Tensor new_lens, left;
-  if (a[7] != Py_None) {
-    new_lens = tensor(a[7], "new_lens");
-    c.want(new_lens, "new_lens", at::kInt, {B});
-  } else {
-    new_lens = c.empty({B}, at::kInt);
-  }
-  if (a[8] != Py_None) {
-    left = tensor(a[8], "free_left");
-    c.want(left, "free_left", at::kInt, {1});
-  } else {
-    left = c.empty({1}, at::kInt);
-  }
-  const at::Tensor granted = c.empty({B}, at::kInt), cu = c.empty({B + 1}, at::kInt), slots = c.empty({T}, at::kLong);
+  const std::vector<at::Tensor> v = c.vectors({B, B + 1, a[7] != Py_None ? 0 : B, a[8] != Py_None ? 0 : 1});
+  const at::Tensor &granted = v[0], &cu = v[1];
+  const at::Tensor &new_lens = a[7] != Py_None ? tensor(a[7], "new_lens") : v[2],
+                   &left = a[8] != Py_None ? tensor(a[8], "free_left") : v[3];
+  c.want(new_lens, "new_lens", at::kInt, {B});
+  c.want(left, "free_left", at::kInt, {1});
+  const at::Tensor slots = c.empty({T}, at::kLong);
   check(attn_pages_extend(ptr<int>(lens), ptr<int>(add), narrow(B, "B"), ptr<int>(table), narrow(table.size(1), "width"),
                           ptr<int>(free_pages), ptr<int>(count), narrow(free_pages.size(0), "free_pages"),
                           narrow(whole(a[5]), "page"), T, ptr<int>(new_lens), ptr<int>(granted), ptr<int>(cu),
@@ -210,8 +223,9 @@ PyObject* pages_release(PyObject* const* a, Py_ssize_t n) {
   c.want(free_pages, "free_pages", at::kInt, {-1});
   c.want(count, "free_count", at::kInt, {1});
   c10::cuda::CUDAGuard guard(c.dev);
-  const at::Tensor new_lens = a[6] != Py_None ? tensor(a[6], "new_lens") : c.empty({B}, at::kInt);
-  const at::Tensor left = a[7] != Py_None ? tensor(a[7], "free_left") : c.empty({1}, at::kInt);
+  const std::vector<at::Tensor> o = c.vectors({a[6] != Py_None ? 0 : B, a[7] != Py_None ? 0 : 1});
+  const at::Tensor &new_lens = a[6] != Py_None ? tensor(a[6], "new_lens") : o[0],
+                   &left = a[7] != Py_None ? tensor(a[7], "free_left") : o[1];
   c.want(new_lens, "new_lens", at::kInt, {B});
   c.want(left, "free_left", at::kInt, {1});
   check(attn_pages_release(ptr<int>(lens), ptr<int>(done), narrow(B, "B"), ptr<int>(table), narrow(table.size(1), "width"),
@@ -270,7 +284,7 @@ PyObject* kv8_decode(PyObject* const* a, Py_ssize_t n) {
   const float scale = scale_of(a[7], m.d);
   const int causal = flag(a[8]), nq = narrow(Nq, "Nq"), hq = narrow(Hq, "Hq"), h = narrow(m.H, "H"), d = narrow(m.d, "d");
   c10::cuda::CUDAGuard guard(c.dev);
-  const at::Tensor o = at::empty_like(q), lse = c.empty({B, Hq, Nq}, at::kFloat);
+  const at::Tensor o = c.empty({B, Nq, Hq, m.d}, q.scalar_type()), lse = c.empty({B, Hq, Nq}, at::kFloat);
   const Workspace ws(c, a[9], attn_kv8_decode_workspace_size(nq, hq, h, d));
   check(attn_kv8_decode(ptr<void>(q), ptr<uint8_t>(kc), ptr<uint8_t>(vc), ptr<float>(ks), ptr<float>(vs), ptr<int>(table),
                         ptr<int>(lens), ptr<void>(o), ptr<float>(lse), narrow(B, "B"), nq, hq, h, d, narrow(m.P, "P"),

@@ -227,8 +227,10 @@ template <int NT>
 static cudaError_t launch_extend_t(const PagesArgs& a, cudaStream_t stream) {
   auto* k = attn_pages_extend_kernel<NT>;
   const size_t smem = sizeof(PageReq) * (size_t)a.B;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(PageReq) * kPagesMaxB);
-  if (e != cudaSuccess) return e;
+  if (smem > 40 * 1024) {  // (48 KB, the static part included, need no attribute)
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(PageReq) * kPagesMaxB);
+    if (e != cudaSuccess) return e;
+  }
   // one CTA for a decoding step, up to eight (a portable cluster) for prompts
   const long long want = ((a.T > 4ll * a.B ? (long long)a.T : 4ll * a.B) + NT - 1) / NT;
   const unsigned n = (unsigned)(want >= 8 ? 8 : (want >= 4 ? 4 : (want >= 2 ? 2 : 1)));
