@@ -1604,13 +1604,17 @@ __global__ void __launch_bounds__(kAuxThreads, kAuxBlocksPerSm) attn_var_pre_ker
       p.dvec[at] = 0.f;
     }
   }
-  for (int b = 0; b < p.B; ++b) {
-    if (v.lq[b] > 0) continue;
-    const int k0 = min(max(p.cu_k[b], 0), p.Nk), lk = min(max(p.cu_k[b + 1], k0), p.Nk) - k0;
-    const long long n = (long long)lk * p.Hkv * D / 8, at = (long long)k0 * p.Hkv * D / 8;
-    for (long long i = tid; i < n; i += nthreads) {
-      reinterpret_cast<uint4*>(p.dk)[at + i] = make_uint4(0, 0, 0, 0);
-      reinterpret_cast<uint4*>(p.dv)[at + i] = make_uint4(0, 0, 0, 0);
+  for (int b0 = 0; b0 < p.B; b0 += 32) {  // (a warp looks at 32 sequences at a time)
+    uint32_t none = __ballot_sync(0xffffffffu, b0 + lane < p.B && v.lq[b0 + lane] == 0);
+    while (none) {
+      const int b = b0 + __ffs(none) - 1;
+      none &= none - 1;
+      const int k0 = min(max(p.cu_k[b], 0), p.Nk), lk = min(max(p.cu_k[b + 1], k0), p.Nk) - k0;
+      const long long n = (long long)lk * p.Hkv * D / 8, at = (long long)k0 * p.Hkv * D / 8;
+      for (long long i = tid; i < n; i += nthreads) {
+        reinterpret_cast<uint4*>(p.dk)[at + i] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4*>(p.dv)[at + i] = make_uint4(0, 0, 0, 0);
+      }
     }
   }
   griddep_launch_dependents();

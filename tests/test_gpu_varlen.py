@@ -425,3 +425,23 @@ def test_a_captured_training_step():
         for x in got:
             assert (x[n:] == 0).all()
     assert attn.attn_status() == 0
+
+
+@pytest.mark.parametrize("B", [64, 65, 257, 300, 330])
+def test_searches_over_many_sequences(B):
+    """Around the places where the search for a block's sequence changes its width:
+    queries, keys or both missing in some, the last ones among them."""
+    from exact_tiled_attention_22_gb300 import attn
+    g = torch.Generator().manual_seed(B)
+    lq = torch.randint(0, 40, (B,), generator=g)
+    lk = torch.randint(0, 40, (B,), generator=g)
+    lq[torch.rand(B, generator=g) < 0.3] = 0
+    lk[torch.rand(B, generator=g) < 0.2] = 0
+    lq[-1], lk[-1], lq[0] = 5, 9, 0
+    lq, lk = lq.tolist(), lk.tolist()
+    q, k, v, do = draw(lq, lk, 2, 2, 64, "bf16", seed=60)
+    o, lse = attn.varlen_fwd(dev(q), dev(k), dev(v), offsets(lq), offsets(lk), 0.125, True)
+    grads = attn.varlen_bwd(dev(q), dev(k), dev(v), o, lse, dev(do), offsets(lq), offsets(lk), 0.125, True)
+    ref = plain64.packed(q.double(), k.double(), v.double(), cu(lq), cu(lk), 0.125, True, "bf16", do.double())
+    for name, got in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+        plain64.check(got, *ref[name], name)
