@@ -97,10 +97,11 @@ struct VarSeq {
 // The sequence that holds work unit `unit` when a sequence of lq queries has
 // ceil(lq / tile_rows) of them; `unit` becomes its index there.  Every warp
 // searches by itself (no shared memory, no barrier), 32 sequences at a time, whose
-// offsets are then at hand, or 256 of many (8192 sequences of 3 tokens, a block each:
-// 0.7 ms instead of 2.2; out of line, since inlined it costs every block 0.4 us even
-// where it is not called).  Offsets are clamped to the tensors, so that wrong ones
-// read and write nothing outside them.
+// offsets are then at hand, 0.3 us a look; or 256 of more than 256 (1000 sequences of
+// 32 tokens, 4 heads: 191 us, 281 with 32; 96 of 64, 12 heads: 55 us, 53 with 32).  The
+// latter stay out of line: inlined they cost every block 0.4 us even where they are
+// not called.  Offsets are clamped to the tensors, so that wrong ones read and
+// write nothing outside them.
 __device__ __noinline__ bool var_find_many(const FwdArgs& p, int& unit, int tile_rows, VarSeq& vs) {
   constexpr int S = 8;  // sequences to a lane
   const int lane = threadIdx.x & 31, sh = __ffs(tile_rows) - 1;  // (a power of two)
@@ -149,7 +150,7 @@ __device__ __noinline__ bool var_find_many(const FwdArgs& p, int& unit, int tile
   return false;
 }
 __device__ __forceinline__ bool var_find(const FwdArgs& p, int& unit, int tile_rows, VarSeq& vs) {
-  if (p.B > 64) return var_find_many(p, unit, tile_rows, vs);
+  if (p.B > 256) return var_find_many(p, unit, tile_rows, vs);
   const int lane = threadIdx.x & 31;
   int carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {

@@ -427,7 +427,7 @@ def test_a_captured_training_step():
     assert attn.attn_status() == 0
 
 
-@pytest.mark.parametrize("B", [64, 65, 257, 300, 330])
+@pytest.mark.parametrize("B", [64, 65, 256, 257, 300, 513])
 def test_searches_over_many_sequences(B):
     """Around the places where the search for a block's sequence changes its width:
     queries, keys or both missing in some, the last ones among them."""
