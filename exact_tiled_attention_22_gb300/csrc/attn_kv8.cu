@@ -801,8 +801,9 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
 // O = 0, LSE = -inf.  A lane holds D / 32 columns, eight parts' loads in flight.
 // WPR = 4: a block per query row, whose parts are dealt to its four warps (few
 // rows, many parts: one row of four long requests has 19 parts each).  WPR = 1: a
-// warp per row, four rows of a segment to a block (many rows: most segments are
-// one CTA's, and their blocks only find that out).  Always in the same order.
+// warp per row, four rows of a segment at a time, p.merge_run times (many rows: most
+// segments are one CTA's, and their blocks only find that out).  Always in the same
+// order.
 template <int D, bool BF16, int WPR>
 __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_constant__ Kv8DecArgs p) {
   __shared__ long long sums[4][2];
@@ -812,12 +813,11 @@ __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_consta
   constexpr int kPer = D / 32, kU = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int Hr = p.H * p.n_rb, R = p.Nq * p.G;
-  // a block's rows: one, or four of one row block
+  // a block's units: one row, or p.merge_run times four rows of one row block
   const unsigned per = WPR == 4 ? 1 : 4, n_in = (p.rp + per - 1) / per;
-  const unsigned blk = blockIdx.x / n_in;  // (b, head, row block)
-  const int b = (int)(blk / (unsigned)Hr), hr = (int)(blk - (unsigned)b * Hr);
-  const int h = hr / p.n_rb, rb = hr - h * p.n_rb;
-  const int r = (int)((blockIdx.x - blk * n_in) * per) + (WPR == 4 ? 0 : warp), idx = rb * p.rp + r;
+  const unsigned run = WPR == 4 ? 1 : p.merge_run, units_all = (unsigned)p.B * Hr * n_in;
+  const unsigned first = blockIdx.x * run;
+  int b = (int)(first / n_in / (unsigned)Hr);
   long long before = 0, total = 0;
   for (int i = threadIdx.x; i < p.B; i += 128) {
     const int n = seg_units((kv8_len(p, i) + 127) >> 7);
@@ -836,88 +836,98 @@ __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_consta
   __syncthreads();
   before = sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0];
   total = sums[0][1] + sums[1][1] + sums[2][1] + sums[3][1];
-  const int nt = (kv8_len(p, b) + 127) >> 7;
   const long long units = total * Hr, n_cta = min((long long)p.grid, units);
-  const long long u0 = before * Hr + (long long)hr * seg_units(nt);
-  const int c0 = nt ? (int)range_owner(u0 + kSegCost, units, n_cta) : 0;
-  const int c1 = nt ? (int)range_owner(u0 + kSegCost + nt - 1, units, n_cta) : 0;
-  if ((nt == 0 || c0 != c1) && (WPR == 1 || idx < R)) {
-    // the first CTA's part is in its second slot if its range began earlier
-    const int s0 = nt && range_start(c0, units, n_cta) < u0 ? 1 : 0;
-    auto part = [&](int c) -> size_t { return ((size_t)c * 2 + (c == c0 ? s0 : 0)) * p.rp + r; };
-    const bool live = idx < R;  // (WPR = 1: a warp may have no row)
-    float acc[kPer];
+  int nt = (kv8_len(p, b) + 127) >> 7;
+  for (unsigned unit = first; unit < min(first + run, units_all); ++unit) {
+    const unsigned blk = unit / n_in;  // (b, head, row block)
+    if ((int)(blk / (unsigned)Hr) != b) {
+      before += seg_units(nt);
+      nt = (kv8_len(p, ++b) + 127) >> 7;
+    }
+    const int hr = (int)(blk - (unsigned)b * Hr);
+    const int h = hr / p.n_rb, rb = hr - h * p.n_rb;
+    const int r = (int)((unit - blk * n_in) * per) + (WPR == 4 ? 0 : warp), idx = rb * p.rp + r;
+    const long long u0 = before * Hr + (long long)hr * seg_units(nt);
+    const int c0 = nt ? (int)range_owner(u0 + kSegCost, units, n_cta) : 0;
+    const int c1 = nt ? (int)range_owner(u0 + kSegCost + nt - 1, units, n_cta) : 0;
+    if ((nt == 0 || c0 != c1) && (WPR == 1 || idx < R)) {
+      // the first CTA's part is in its second slot if its range began earlier
+      const int s0 = nt && range_start(c0, units, n_cta) < u0 ? 1 : 0;
+      auto part = [&](int c) -> size_t { return ((size_t)c * 2 + (c == c0 ? s0 : 0)) * p.rp + r; };
+      const bool live = idx < R;  // (WPR = 1: a warp may have no row)
+      float acc[kPer];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-    float M = -INFINITY, Ls = 0.f;
-    if (nt && live) {
-      for (int c = c0 + (WPR == 4 ? (int)threadIdx.x : lane); c <= c1; c += 32 * WPR) M = fmaxf(M, p.ws_ml[part(c) * 2]);
-      M = warp_max(M);
-      if constexpr (WPR == 4) {
-        if (lane == 0) xml[warp][0] = M;
-        __syncthreads();
-        M = fmaxf(fmaxf(xml[0][0], xml[1][0]), fmaxf(xml[2][0], xml[3][0]));
-      }
-      for (int cb = c0 + (WPR == 4 ? warp * kU : 0); cb <= c1; cb += WPR * kU) {
-        float wgt = 0.f;
-        if (lane < kU && cb + lane <= c1) {
-          const size_t at = part(cb + lane) * 2;
-          const float mc = p.ws_ml[at], lc = p.ws_ml[at + 1];
-          wgt = mc == -INFINITY ? 0.f : ex2(mc - M);
-          // (a part whose every score is NaN has m = -inf and a NaN sum)
-          Ls += lc != lc ? lc : wgt * lc;
+      for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+      float M = -INFINITY, Ls = 0.f;
+      if (nt && live) {
+        for (int c = c0 + (WPR == 4 ? (int)threadIdx.x : lane); c <= c1; c += 32 * WPR) M = fmaxf(M, p.ws_ml[part(c) * 2]);
+        M = warp_max(M);
+        if constexpr (WPR == 4) {
+          if (lane == 0) xml[warp][0] = M;
+          __syncthreads();
+          M = fmaxf(fmaxf(xml[0][0], xml[1][0]), fmaxf(xml[2][0], xml[3][0]));
         }
-        float4 v[kU];
+        for (int cb = c0 + (WPR == 4 ? warp * kU : 0); cb <= c1; cb += WPR * kU) {
+          float wgt = 0.f;
+          if (lane < kU && cb + lane <= c1) {
+            const size_t at = part(cb + lane) * 2;
+            const float mc = p.ws_ml[at], lc = p.ws_ml[at + 1];
+            wgt = mc == -INFINITY ? 0.f : ex2(mc - M);
+            // (a part whose every score is NaN has m = -inf and a NaN sum)
+            Ls += lc != lc ? lc : wgt * lc;
+          }
+          float4 v[kU];
 #pragma unroll
-        for (int k = 0; k < kU; ++k) {
-          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (cb + k <= c1) {
-            const float* o = p.ws_o + part(cb + k) * D + lane * kPer;
+          for (int k = 0; k < kU; ++k) {
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (cb + k <= c1) {
+              const float* o = p.ws_o + part(cb + k) * D + lane * kPer;
+              if constexpr (kPer == 4) {
+                v[k] = *reinterpret_cast<const float4*>(o);
+              } else {
+                const float2 v2 = *reinterpret_cast<const float2*>(o);
+                v[k].x = v2.x;
+                v[k].y = v2.y;
+              }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kU; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, wgt, k);
+            acc[0] = fmaf(wk, v[k].x, acc[0]);
+            acc[1] = fmaf(wk, v[k].y, acc[1]);
             if constexpr (kPer == 4) {
-              v[k] = *reinterpret_cast<const float4*>(o);
-            } else {
-              const float2 v2 = *reinterpret_cast<const float2*>(o);
-              v[k].x = v2.x;
-              v[k].y = v2.y;
+              acc[2] = fmaf(wk, v[k].z, acc[2]);
+              acc[3] = fmaf(wk, v[k].w, acc[3]);
             }
           }
         }
 #pragma unroll
-        for (int k = 0; k < kU; ++k) {
-          const float wk = __shfl_sync(0xffffffffu, wgt, k);
-          acc[0] = fmaf(wk, v[k].x, acc[0]);
-          acc[1] = fmaf(wk, v[k].y, acc[1]);
-          if constexpr (kPer == 4) {
-            acc[2] = fmaf(wk, v[k].z, acc[2]);
-            acc[3] = fmaf(wk, v[k].w, acc[3]);
+        for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+        if constexpr (WPR == 4) {
+          if (lane == 0) xml[warp][1] = Ls;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) xo[warp][lane * kPer + k] = acc[k];
+          __syncthreads();
+          Ls = (xml[0][1] + xml[1][1]) + (xml[2][1] + xml[3][1]);
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int c = lane * kPer + k;
+            acc[k] = (xo[0][c] + xo[1][c]) + (xo[2][c] + xo[3][c]);
           }
         }
       }
+      if (live && (WPR == 1 || warp == 0)) {
+        const int i = idx / p.G, hq = h * p.G + idx - i * p.G;
+        const float inv = Ls != 0.f ? 1.f / Ls : 0.f;
+        uint32_t wv[kPer / 2];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
-      if constexpr (WPR == 4) {
-        if (lane == 0) xml[warp][1] = Ls;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) xo[warp][lane * kPer + k] = acc[k];
-        __syncthreads();
-        Ls = (xml[0][1] + xml[1][1]) + (xml[2][1] + xml[3][1]);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const int c = lane * kPer + k;
-          acc[k] = (xo[0][c] + xo[1][c]) + (xo[2][c] + xo[3][c]);
-        }
+        for (int k = 0; k < kPer / 2; ++k) wv[k] = pack2<BF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+        uint8_t* dst = static_cast<uint8_t*>(p.o) + ((((size_t)b * p.Nq + i) * p.Hq + hq) * D + lane * kPer) * 2;
+        if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(wv[0], wv[1]);
+        else *reinterpret_cast<uint32_t*>(dst) = wv[0];
+        if (lane == 0) p.lse[((size_t)b * p.Hq + hq) * p.Nq + i] = Ls != 0.f ? (M + __log2f(Ls)) * kLn2 : -INFINITY;
       }
-    }
-    if (live && (WPR == 1 || warp == 0)) {
-      const int i = idx / p.G, hq = h * p.G + idx - i * p.G;
-      const float inv = Ls != 0.f ? 1.f / Ls : 0.f;
-      uint32_t wv[kPer / 2];
-#pragma unroll
-      for (int k = 0; k < kPer / 2; ++k) wv[k] = pack2<BF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-      uint8_t* dst = static_cast<uint8_t*>(p.o) + ((((size_t)b * p.Nq + i) * p.Hq + hq) * D + lane * kPer) * 2;
-      if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(wv[0], wv[1]);
-      else *reinterpret_cast<uint32_t*>(dst) = wv[0];
-      if (lane == 0) p.lse[((size_t)b * p.Hq + hq) * p.Nq + i] = Ls != 0.f ? (M + __log2f(Ls)) * kLn2 : -INFINITY;
     }
   }
   griddep_launch_dependents();
@@ -958,14 +968,21 @@ cudaError_t launch_kv8_split(const Kv8DecArgs& a, cudaStream_t stream) {
                    : (a.rp == 8 ? launch_split_n<64, 8>(a, stream) : launch_split_n<64, 16>(a, stream));
 }
 
+constexpr long long kMergeBlocks = 2 * 1216;  // (8 blocks fit an SM)
+
 template <int D, bool BF16>
-static cudaError_t launch_merge_t(const Kv8DecArgs& a, cudaStream_t stream) {
+static cudaError_t launch_merge_t(Kv8DecArgs a, cudaStream_t stream) {
   const long long segs = (long long)a.B * a.H * a.n_rb;
   // parts of a segment: about a.grid / segs + 1 (64 requests of 8 heads: 51 us with a
   // warp per row, 52 with a block; 17 requests of 2 heads and 3 row blocks: 20 and 19)
   if (a.grid >= 2 * segs)
     return launch_pdl(attn_kv8_merge_kernel<D, BF16, 4>, (unsigned)(segs * a.rp), 128, 0, stream, a);
-  return launch_pdl(attn_kv8_merge_kernel<D, BF16, 1>, (unsigned)(segs * ((a.rp + 3) / 4)), 128, 0, stream, a);
+  // Every block sums all the lengths, so with many rows a block takes several, two
+  // waves of blocks in all (4096 requests of 30 to 60 tokens, 8 heads: the merge 43 us, 127
+  // with a block for every four rows).
+  const long long rows4 = segs * ((a.rp + 3) / 4);
+  a.merge_run = (int)((rows4 + kMergeBlocks - 1) / kMergeBlocks);
+  return launch_pdl(attn_kv8_merge_kernel<D, BF16, 1>, (unsigned)((rows4 + a.merge_run - 1) / a.merge_run), 128, 0, stream, a);
 }
 
 cudaError_t launch_kv8_merge(const Kv8DecArgs& a, cudaStream_t stream) {

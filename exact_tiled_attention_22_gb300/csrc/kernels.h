@@ -225,6 +225,7 @@ struct Kv8DecArgs {
   int B, Nq, Hq, H, G, d, width, page_shift, P;
   int rp, n_rb;            // rows of a row block, row blocks
   int grid;
+  int merge_run;           // groups of four rows to a block of the merge: the launcher's choice
   int causal, bf16;
   float scale;
   int debug_flags;

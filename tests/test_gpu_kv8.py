@@ -482,3 +482,14 @@ def test_stream_handle_with_keyword_arguments():
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     with pytest.raises(ValueError):
         attn.kv8_decode(q.cpu(), kc, vc, ks, vs, table, ln, stream=side.cuda_stream)
+
+
+def test_more_rows_than_blocks_of_the_merge():
+    """So many requests that a block of the merge takes several rows of several of
+    them, empty ones and ones that several blocks of the split share among them."""
+    g = torch.Generator().manual_seed(17)
+    lens = torch.randint(0, 4, (1000,), generator=g)
+    lens[torch.tensor([0, 1, 399, 700, 999])] = torch.tensor([1500, 0, 3000, 257, 0], dtype=lens.dtype)
+    lens = lens.tolist()
+    args = problem(lens, 1, 5, 5, 64, 16, "bf16", seed=18)
+    decode_and_check(args, lens, 0.125, True, "bf16")
