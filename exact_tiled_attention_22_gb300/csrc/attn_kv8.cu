@@ -92,11 +92,12 @@ constexpr int kAppThreads = 128;
 // run: largest magnitude, then codes; the first 16 (d = 128) or 32 (d = 64)
 // tokens stay in registers between them.  Bound by HBM for prompts (the 16-bit
 // values in, the codes out), by latency for a decoding step: the chain slot,
-// values and old scale, codes.  Blocks of 128 threads, six or more to an SM (48 %
-// more warps than blocks of 256 at the same 72 registers).  Measured: 31749 tokens of
-// 4 heads, d = 64, page 16 (49 MB) 11.1 us or 4.4 TB/s (12.0 with blocks of 256, 11.6
-// with eight to an SM at 64 registers); one token of each of 256 requests, 8 heads,
-// d = 128, 4.3 us.
+// values and old scale, codes.  Blocks of 128 threads, six to an SM at 80 registers:
+// a block whose warps have done their runs makes room sooner than a larger one.
+// Measured: 31749 tokens of 4 heads, d = 64, page 16 (49 MB) 11.1 us or 4.4 TB/s (12.0
+// with blocks of 256, three to an SM; 11.6 with eight at 64 registers), 15 us with
+// the values in HBM, the schedulers 58 % busy; one token of each of 256 requests, 8
+// heads, d = 128, 4.3 us.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kAppThreads, 6) attn_kv8_append_kernel(const __grid_constant__ Kv8AppendArgs p,
                                                                      int chunk) {
