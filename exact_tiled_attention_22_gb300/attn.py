@@ -467,13 +467,17 @@ _bind = _load_bind()
 
 def _on_stream(f):
     """A `stream` argument (a torch stream or a handle, of the tensors' device) is
-    made the current stream for the call, so that what the call allocates belongs to it."""
+    made the current stream for the call, so that what the call allocates belongs to it;
+    tensors of other streams are marked as used there, so that freeing one after the
+    call does not hand its memory on before the kernels have read it."""
     @functools.wraps(f)
     def call(*args, stream=None, **kw):
         if stream is None:
             return f(*args, **kw)
-        dev = next((x.device for x in (*args, *kw.values()) if isinstance(x, torch.Tensor)), None)
-        if dev is None or dev.type != "cuda":
+        given = [x for a in (*args, *kw.values()) for x in (a if isinstance(a, (tuple, list)) else (a,))
+                 if isinstance(x, torch.Tensor)]
+        dev = given[0].device if given else None
+        if dev is None or any(x.device != dev or dev.type != "cuda" for x in given):
             return f(*args, **kw)  # refused there
         if isinstance(stream, int):
             stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
@@ -481,7 +485,10 @@ def _on_stream(f):
         if stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
         with torch.cuda.stream(stream):
-            return f(*args, **kw)
+            out = f(*args, **kw)
+        for x in given:
+            x.record_stream(stream)
+        return out
     return call
 
 

@@ -493,3 +493,27 @@ def test_more_rows_than_blocks_of_the_merge():
     lens = lens.tolist()
     args = problem(lens, 1, 5, 5, 64, 16, "bf16", seed=18)
     decode_and_check(args, lens, 0.125, True, "bf16")
+
+
+def test_tensors_freed_after_a_call_on_another_stream():
+    """The memory of a query that is dropped after the call is not handed on while
+    the call still waits for its stream."""
+    from exact_tiled_attention_22_gb300 import attn
+    lens = [300] * 64
+    q, kc, vc, ks, vs, table = (x.cuda() for x in problem(lens, 1, 32, 4, 128, 32, "bf16", seed=19))
+    ln = torch.tensor(lens, dtype=torch.int32).cuda()
+    want = attn.kv8_decode(q, kc, vc, ks, vs, table, ln)
+    side = torch.cuda.Stream()
+    big = torch.randn(8192, 8192, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(4):
+            big @ big                       # the call waits behind these
+    mine = q.clone()
+    torch.cuda.current_stream().synchronize()
+    o, lse = attn.kv8_decode(mine, kc, vc, ks, vs, table, ln, stream=side)
+    del mine
+    others = [torch.full_like(q, math.nan) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    del others
