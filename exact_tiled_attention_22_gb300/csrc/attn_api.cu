@@ -1047,6 +1047,9 @@ static size_t varlen_parts_bytes(long long Tq, int Hq, int Hkv, int d) {
   return (Tq + 63) / 64 <= 2 * a_min ? 0 : (size_t)attn::kVarMaxParts * 2 * 128 * d * 4;
 }
 
+// Integers of the item counts and the order of the sequences.
+static size_t varlen_items(int B) { return (size_t)attn::kVarClasses * B + 1 + B; }
+
 size_t attn_varlen_bwd_workspace_size(int B, long long Tq, int Hq, int Hkv, int d) {
   if (B < 1 || B > attn::kVarMaxB || Tq < 0 || Tq >= (1ll << 26) || Hkv < 1 || Hq < Hkv || Hq % Hkv ||
       (d != 64 && d != 128))
@@ -1054,7 +1057,7 @@ size_t attn_varlen_bwd_workspace_size(int B, long long Tq, int Hq, int Hkv, int 
   const size_t rows = (size_t)varlen_padded(B, Tq) * Hq;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   return up(rows * 4) * 2 + up(rows * d * 4) + 256 + up((size_t)B * sizeof(attn::VarBwdSeq)) +
-         up((2 * (size_t)B + 1) * 4) + varlen_parts_bytes(Tq, Hq, Hkv, d);
+         up(varlen_items(B) * 4) + varlen_parts_bytes(Tq, Hq, Hkv, d);
 }
 
 int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
@@ -1103,8 +1106,8 @@ int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o, 
   a.sched = reinterpret_cast<unsigned*>(ws);
   a.var_seq = reinterpret_cast<attn::VarBwdSeq*>(ws + 256);
   a.var_items = reinterpret_cast<int*>(ws + 256 + up((size_t)B * sizeof(attn::VarBwdSeq)));
-  a.var_order = a.var_items + B + 1;
-  a.var_parts = reinterpret_cast<float*>(ws + 256 + up((size_t)B * sizeof(attn::VarBwdSeq)) + up((2 * (size_t)B + 1) * 4));
+  a.var_order = a.var_items + varlen_items(B) - B;
+  a.var_parts = reinterpret_cast<float*>(ws + 256 + up((size_t)B * sizeof(attn::VarBwdSeq)) + up(varlen_items(B) * 4));
   a.dq = dq; a.dk = dk; a.dv = dv;
   a.B = B; a.H = Hq; a.N = (int)Tq; a.Npad = (int)npad; a.d = d;
   a.cu_q = cu_q; a.cu_k = cu_k;

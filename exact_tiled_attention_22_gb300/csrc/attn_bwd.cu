@@ -269,27 +269,81 @@ __host__ __device__ inline int bwd_head_group(int N, int d, int BH) {
 // is a fraction of the kernel's time however the lengths are spread (without
 // the cut the first tile of the longest sequence took as long as the rest of
 // the batch: 4096 tokens, 4 heads to a key head, 256 steps, 0.24 ms).
+// With heads that share a key head, where most of the work is in split tiles, items
+// are numbered by classes of their length, kVarClasses in all: whole chunks of 2 G a
+// steps first, then what is left of the tiles, by eighths of a chunk from the longest
+// on.  (The blocks take two or three items each, so a chunk that is claimed after
+// short rests makes the last ones late: 8192 tokens, 8 / 2 heads, d 128, 291 us tile by
+// tile, 249 by classes; three texts of 3000 141 and 124.)  Others are numbered tile by
+// tile, which are found sooner: few of their tiles are split, and the classes gained them
+// nothing (4096 tokens, 12 heads with keys of their own, d 64: 88 us, 90 by classes).
 struct VarSplit {
-  int nkt, n1, a, C;
-  __device__ VarSplit(int lq, int lk, int a_, int causal) {
-    const int nqs = (lq + 63) >> 6;
+  int nkt, n1, a, C, nqs;
+  __host__ __device__ VarSplit(int lq, int lk, int a_, int causal) {
+    nqs = (lq + 63) >> 6;
     nkt = (lk + 127) >> 7;
     n1 = causal ? min(nkt, nqs >> 1) : 0;
     a = a_;
     C = (nqs + 2 * a - 1) / (2 * a);
   }
-  __device__ int items(int tk) const { return tk < n1 ? tk / a + 1 : C; }
-  __device__ int items_before(int n) const {
+  // of a tile beyond the causal limit: whole chunks, and the eighths (1 .. 8) of its rest or 0
+  __host__ __device__ int fC() const { return nqs == C * 2 * a ? C : C - 1; }
+  __host__ __device__ int lC() const { return ((nqs - fC() * 2 * a) * 4 + a - 1) / a; }
+  // whole chunks of the tiles before tile n
+  __host__ __device__ int full_before(int n) const {
+    const int m = min(n, n1), k = m / a, r = m - k * a;
+    return a * (k * (k - 1) / 2) + k * (r + 1) + (n - m) * fC();
+  }
+  __host__ __device__ int full(int tk) const { return tk < n1 ? (tk + 1) / a : fC(); }
+  // rests of class c: (tk + 1) % a in (lo, hi], l = 9 - c eighths
+  __host__ __device__ int lo(int l) const { return (l - 1) * a / 8; }
+  __host__ __device__ int hi(int l) const { return l == 8 ? a - 1 : l * a / 8; }
+  __host__ __device__ int count1(int l) const {  // of the tiles at the causal limit
+    const int w = hi(l) - lo(l), k = n1 / a, r = n1 - k * a;
+    return k * w + min(max(r - lo(l), 0), w);
+  }
+  // items of class c, or of all (c = -1)
+  __host__ __device__ int count(int c) const {
+    if (c < 0) return items_before(nkt);
+    return c == 0 ? full_before(nkt) : count1(9 - c) + (nkt > n1 && lC() == 9 - c ? nkt - n1 : 0);
+  }
+  // tile and chunk of the e-th of them, the first tiles first
+  __host__ __device__ void pick(int c, int e, int* tk, int* chunk) const {
+    if (c <= 0) {
+      int at = 0, end = nkt - 1;
+      while (at < end) {
+        const int mid = (at + end + 1) >> 1;
+        if ((c < 0 ? items_before(mid) : full_before(mid)) <= e) at = mid; else end = mid - 1;
+      }
+      *tk = at;
+      *chunk = e - (c < 0 ? items_before(at) : full_before(at));
+    } else {
+      const int l = 9 - c, n = count1(l), w = hi(l) - lo(l);
+      *tk = e < n ? e / w * a + lo(l) + e % w : n1 + e - n;
+      *chunk = full(*tk);
+    }
+  }
+  __host__ __device__ int items(int tk) const { return tk < n1 ? tk / a + 1 : C; }
+  __host__ __device__ int items_before(int n) const {
     const int m = min(n, n1), k = m / a, r = m - k * a;
     return a * (k * (k + 1) / 2) + r * (k + 1) + (n - m) * C;
   }
   // tiles from here on have several items
-  __device__ int first_split() const { return C >= 2 ? min(a, n1) : nkt; }
-  __device__ int parts_before(int n) const {
+  __host__ __device__ int first_split() const { return C >= 2 ? min(a, n1) : nkt; }
+  __host__ __device__ int parts_before(int n) const {
     const int f = first_split();
     return n > f ? items_before(n) - items_before(f) : 0;
   }
 };
+
+// VarSplit's count and pick, out of line: inlined they cost batches that need neither
+// (16 texts of 512, 12 heads, d 64: 47 us, 49 inlined).
+__device__ __noinline__ int var_count(VarSplit sp, int c) { return sp.count(c); }
+__device__ __noinline__ int2 var_pick(VarSplit sp, int c, int e) {
+  int2 r;
+  sp.pick(c, e, &r.x, &r.y);
+  return r;
+}
 
 // ALIBI: the scores carry the linear bias -m_h |i - j| (m_h = p.alibi[h]), as
 // in the forward; it is folded into the per-query -LSE*log2(e) term.
@@ -340,10 +394,10 @@ struct VarSplit {
 // The producer finds an item's sequence and publishes its description with it
 // (sequences without queries have no items; those with the most steps come first).
 // Measured: 7457 tokens in five sequences, the longest 4096, 16 / 4 heads, d 128,
-// causal: 187 us, the tensor pipe 59 % busy (263 us without the chunks, 206 without
-// the order); chunks of a 456th or 608th of all steps instead of a 304th made it
+// causal: 181 us, the tensor pipe 60 % busy (263 us without the chunks, 206 without
+// the order of the sequences, 187 without the classes of VarSplit); chunks of a 456th or 608th of all steps instead of a 304th made it
 // about 10 us faster and the sum of the parts 5 to 9 us slower.  16 sequences of 16
-// to 2048 tokens, 12 heads, d 64: 66 us, bound by the items' starts and ends.
+// to 2048 tokens, 12 heads, d 64: 64 us, bound by the items' starts and ends.
 template <int D, bool BF16, bool ALIBI, bool SPARSE, bool DROPOUT, bool ACC = false, bool VARLEN = false>
 __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
     attn_bwd_main_kernel(const __grid_constant__ BwdArgs p) {
@@ -366,7 +420,9 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
   griddep_wait();  // (programmatic serialization: see griddep_wait)
   const int BH = p.B * p.H;
   const int nkb = (p.N + 127) / 128;
-  const int n_items = VARLEN ? p.var_items[p.B] : nkb * BH;
+  const bool var_split = VARLEN && p.sched[3] != 0;  // some tile has several items
+  const int var_cls = var_split && p.G > 1 ? kVarClasses : 1;
+  const int n_items = VARLEN ? p.var_items[var_cls * p.B] : nkb * BH;
   const int var_a = VARLEN ? (int)p.sched[2] : 1;
   const int G = VARLEN ? 1 : bwd_head_group(p.N, D, BH);
   const int nq = (p.N + BQ - 1) / BQ;
@@ -400,38 +456,39 @@ __global__ void __launch_bounds__(BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, 1)
   auto do_addr = [&](int st) -> uint32_t { return q_addr(st) + L::kQT; };
   volatile int* item_slot = reinterpret_cast<volatile int*>(sbase + L::kItemSlot);
 
-  // (VARLEN) The item `item` described for its slot: the sequence by bisection
-  // of the item counts, then, as in decode, groups of key heads whose dQ
+  // (VARLEN) The item `item` described for its slot: class and sequence by
+  // bisection of the item counts, then, as in decode, groups of key heads whose dQ
   // accumulators fit the L2, the key tiles with the most steps (the first ones)
   // first.  Slot words: tile, key head, first query row, queries, first key row,
   // keys, padded row of query 0; behind them (npos_s) the chunk and its part.
   volatile int* npos_s = reinterpret_cast<volatile int*>(sbase + L::kNPos);
   volatile int* var_slot = reinterpret_cast<volatile int*>(sbase + L::kQBits);
   auto var_publish = [&](int slot, int item) {
-    int lo = 0, hi = p.B - 1;  // last sequence (in work order) with var_items <= item
+    int lo = 0, hi = var_cls * p.B - 1;  // last class and sequence (in work order) with var_items <= item
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (p.var_items[mid] <= item) lo = mid; else hi = mid - 1;
     }
-    const VarBwdSeq q = p.var_seq[p.var_order[lo]];
+    const int c = var_cls > 1 ? lo / p.B : -1;
+    const VarBwdSeq q = p.var_seq[p.var_order[lo - max(c, 0) * p.B]];
     const VarSplit sp(q.lq, q.lk, var_a, p.causal);
-    const int r = item - p.var_items[lo], n_head = sp.items_before(sp.nkt);  // items of one key head
+    const int r = item - p.var_items[lo], n_head = var_split ? var_count(sp, c) : sp.nkt;  // items of one key head
     const int gh = bwd_head_group(q.lq, D * p.G, p.Hkv);
     const int grp = r / (gh * n_head), r_in = r - grp * gh * n_head;
     const int gsize = min(gh, p.Hkv - grp * gh);
-    const int e = n_head - 1 - r_in / gsize, h = grp * gh + r_in % gsize;
-    lo = 0;
-    hi = sp.nkt - 1;  // the tile of item e of the head
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (sp.items_before(mid) <= e) lo = mid; else hi = mid - 1;
+    const int h = grp * gh + r_in % gsize;
+    int tk = n_head - 1 - r_in / gsize, chunk = 0;
+    if (var_split) {
+      const int2 t = var_pick(sp, c, tk);
+      tk = t.x;
+      chunk = t.y;
     }
     volatile int* v = var_slot + 8 * slot;
-    v[0] = lo;
+    v[0] = tk;
     v[1] = h;
-    npos_s[2 * slot] = e - sp.items_before(lo);  // chunk of the tile
+    npos_s[2 * slot] = chunk;
     npos_s[2 * slot + 1] =
-        sp.items(lo) > 1 ? q.part0 + h * sp.parts_before(sp.nkt) + sp.parts_before(lo) + (e - sp.items_before(lo)) : -1;
+        var_split && sp.items(tk) > 1 ? q.part0 + h * sp.parts_before(sp.nkt) + sp.parts_before(tk) + chunk : -1;
     v[2] = q.q0;
     v[3] = q.lq;
     v[4] = q.k0;
@@ -1480,16 +1537,32 @@ __device__ __forceinline__ VarScan var_scan(const BwdArgs& p, uint8_t* smem, boo
       if (b < p.B) p.var_seq[b] = VarBwdSeq{v.q0[b], lq, k0, lk, v.pbase[b], (int)pp, (int)min(ss, (long long)INT_MAX), 0};
     }
     __syncthreads();  // (var_order is complete; this block wrote it)
-    for (int i0 = 0; i0 < p.B; i0 += kAuxThreads) {
-      const int i = i0 + threadIdx.x;
-      int k0 = 0, lk = 0, lq = 0;
-      if (i < p.B) lens_of(p.var_order[i], k0, lq, lk);
-      const VarSplit sp(lq, lk, a, p.causal);
-      const long long is = scan(lq > 0 ? (long long)sp.items_before(sp.nkt) * p.Hkv : 0, c_item);
-      if (i < p.B) p.var_items[i] = (int)min(is, (long long)INT_MAX);
+    const bool cls = c_split > 0 && p.G > 1;
+    const int n_cls = (cls ? kVarClasses : 1) * p.B, K = n_cls > 4 * kAuxThreads ? 8 : 1;  // counts to a thread
+    for (int i0 = 0; i0 < n_cls; i0 += kAuxThreads * K) {
+      const int i = i0 + threadIdx.x * K;
+      long long n[8], own = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        n[k] = 0;
+        if (k < K && i + k < n_cls) {
+          const int c = (i + k) / p.B;
+          int k0, lk, lq;
+          lens_of(p.var_order[i + k - c * p.B], k0, lq, lk);
+          const VarSplit sp(lq, lk, a, p.causal);
+          if (lq > 0) n[k] = (long long)sp.count(cls ? c : -1) * p.Hkv;
+        }
+        own += n[k];
+      }
+      long long at = scan(own, c_item);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k < K && i + k < n_cls) p.var_items[i + k] = (int)min(at, (long long)INT_MAX);
+        at += n[k];
+      }
     }
     if (threadIdx.x == 0) {
-      p.var_items[p.B] = (int)min(c_item, (long long)INT_MAX);
+      p.var_items[n_cls] = (int)min(c_item, (long long)INT_MAX);
       p.sched[0] = 0u;
       p.sched[1] = 0u;
       p.sched[2] = (unsigned)a;

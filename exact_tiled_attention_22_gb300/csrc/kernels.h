@@ -95,6 +95,7 @@ struct VarBwdSeq {
   int pad;
 };
 constexpr int kVarMaxB = 8192;
+constexpr int kVarClasses = 9;                  // classes of items by length: whole chunks, eighths of one
 constexpr int kVarChunks = 304;                 // equal chunks a batch's steps are cut into
 constexpr int kVarMaxParts = 2 * kVarChunks;    // a split tile of n steps has < 2 n / (all steps / kVarChunks) parts
 
@@ -135,7 +136,7 @@ struct BwdArgs {
   int Nk, G, Hkv;
   VarBwdSeq* var_seq;  // [B]
   int* var_order;      // [B] sequences in the order of the work
-  int* var_items;      // [B + 1] items before each of them
+  int* var_items;      // [kVarClasses][B], 1: items before each class and sequence (in that order)
   float* var_parts;    // [kVarMaxParts][dV, dK][d / 4][128][4] partial tiles
 };
 cudaError_t launch_var_pre(const BwdArgs& a, cudaStream_t stream);
