@@ -394,7 +394,7 @@ __device__ __noinline__ int2 var_pick(VarSplit sp, int c, int e) {
 // The producer finds an item's sequence and publishes its description with it
 // (sequences without queries have no items; those with the most steps come first).
 // Measured: 7457 tokens in five sequences, the longest 4096, 16 / 4 heads, d 128,
-// causal: 181 us, the tensor pipe 60 % busy (263 us without the chunks, 206 without
+// causal: 181 us, the tensor pipe 57 % busy (263 us without the chunks, 206 without
 // the order of the sequences, 187 without the classes of VarSplit); chunks of a 456th or 608th of all steps instead of a 304th made it
 // about 10 us faster and the sum of the parts 5 to 9 us slower.  16 sequences of 16
 // to 2048 tokens, 12 heads, d 64: 64 us, bound by the items' starts and ends.
