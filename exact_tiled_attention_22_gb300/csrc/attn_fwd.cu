@@ -985,14 +985,18 @@ __global__ void __launch_bounds__(FwdRoles<DROPOUT>::kThreads, 1)
       const float2 s01 = add2(add2(sk[0], sk[1]), add2(sk[2], sk[3]));
       l = l * alpha + (s01.x + s01.y);
     }
-    // (a query tile with no position has no O_t to wait for: it writes O = 0)
+    // (a query tile with no position has no O_t to wait for: it writes O = 0.  But
+    // where its pair has positions the producer has loaded its Q all the same, and
+    // the zeros are staged in Q's place: not before the copy is complete.)
     if (ok && n_t > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarOFull + t), 0, wc));
+    if ((SPARSE || VARLEN) && ok && n_t == 0 && len > 0)
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQ), 0, wc));
     if (ok) {
       // the last PV of this tile has read V_{n_t-1}
       if (n_t > 0) release(n_t - 1, 2 * n_t - 1);
       tc_fence_after();
-      // a row that saw no key (possible only under a block-sparse mask) has
-      // O = 0 and LSE = -inf
+      // a row that saw no key (under a block-sparse mask, or in a packed sequence of
+      // more queries than keys) has O = 0 and LSE = -inf
       // (VARLEN: a row that is not a number, l = NaN, has a NaN for its LSE)
       const bool some = VARLEN ? l != 0.f : l > 0.f;
       const float inv_l = some ? (DROPOUT ? p.drop.scale : 1.f) / l : 0.f;

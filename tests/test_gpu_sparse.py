@@ -226,3 +226,26 @@ def test_sparse_max_length(oracle):
                            ("dv", g["dv"][0, keys, 0, :], dv_r)):
         err = rel_l2(got, ref)
         assert err <= TOL_GRAD, f"{name} rel L2 {err:.3e}"
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_sparse_empty_tile_beside_a_full_one(oracle, d):
+    """Even query blocks keep no key block, odd ones keep them all: in every pair of
+    query tiles the first sees nothing while the second one does.  Its rows are zeros
+    in every head and every time, whenever its queries arrive."""
+    from exact_tiled_attention_22_gb300 import attn
+    B, N, H, dtype = 4, 2048, 8, "bf16"
+    x = make_inputs(B, N, H, d, dtype, seed=4900 + d)
+    nb = N // 128
+    mask = torch.zeros((H, nb, nb), dtype=torch.uint8)
+    mask[:, 1::2] = 1
+    dev = torch.device("cuda:0")
+    q, k, v = (x[n].to(dev) for n in ("q", "k", "v"))
+    scale = default_scale(d)
+    for _ in range(20):
+        o, lse = attn.fwd(q, k, v, scale, False, block_mask=mask.to(dev))
+        assert (o.view(B, nb, 128, H, d)[:, ::2] == 0).all()
+        assert torch.isneginf(lse.view(B, H, nb, 128)[:, :, ::2]).all()
+    attn.check(attn.attn_status())
+    g = {"o": o.float().cpu().numpy(), "lse": lse.cpu().numpy()}
+    check_head(oracle, {n: t.double().numpy() for n, t in x.items()}, g, 1, 3, scale, False, dtype, mask[3].numpy())

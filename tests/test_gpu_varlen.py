@@ -445,3 +445,29 @@ def test_searches_over_many_sequences(B):
     ref = plain64.packed(q.double(), k.double(), v.double(), cu(lq), cu(lk), 0.125, True, "bf16", do.double())
     for name, got in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
         plain64.check(got, *ref[name], name)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,H", [(1, 1), (3, 1)])
+def test_whole_query_tiles_without_keys(Hq, H, d):
+    """256 queries on 100 keys, causal, where a tile is 128 positions of one head: the
+    first tile of every pair sees nothing while the second one does.  Its rows are
+    zeros in every sequence and every time, whenever its queries arrive."""
+    from exact_tiled_attention_22_gb300 import attn
+    B, lq, lk = 200, 256, 100
+    q, k, v, _ = draw([lq] * B, [lk] * B, Hq, H, d, "bf16", seed=d + Hq)
+    cq, ck = offsets([lq] * B), offsets([lk] * B)
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    first = None
+    for _ in range(20):
+        o, lse = attn.varlen_fwd(q, k, v, cq, ck, None, True)
+        assert (o.view(B, lq, Hq, d)[:, :lq - lk] == 0).all()
+        assert (lse.view(Hq, B, lq)[:, :, :lq - lk] == -math.inf).all()
+        assert first is None or (torch.equal(o, first[0]) and torch.equal(lse, first[1]))
+        first = (o, lse)
+    attn.check(attn.attn_status())
+    n = 3  # sequences in 64 bits
+    ref = plain64.packed(q[:n * lq].double().cpu(), k[:n * lk].double().cpu(), v[:n * lk].double().cpu(),
+                         cu([lq] * n), cu([lk] * n), d ** -0.5, True, "bf16")
+    plain64.check(o[:n * lq], *ref["o"], "o")
+    plain64.check(lse[:, :n * lq], *ref["lse"], "lse")
