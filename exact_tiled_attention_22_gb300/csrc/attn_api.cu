@@ -1039,12 +1039,9 @@ int attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float*
   return e != cudaSuccess ? cuda_fail(e, "attn_varlen_fwd merge launch") : ATTN_OK;
 }
 
-// Bytes of the partial dK, dV tiles: no tile is split while a sequence of all
-// Tq queries has no more than one chunk of steps (at least 32, or two per head
-// of the group).
+// Bytes of the partial dK, dV tiles.
 static size_t varlen_parts_bytes(long long Tq, int Hq, int Hkv, int d) {
-  const long long G = Hq / Hkv, a_min = (16 + G - 1) / G;
-  return (Tq + 63) / 64 <= 2 * a_min ? 0 : (size_t)attn::kVarMaxParts * 2 * 128 * d * 4;
+  return attn::var_may_split(Tq, Hq / Hkv) ? (size_t)attn::kVarMaxParts * 2 * 128 * d * 4 : 0;
 }
 
 // Integers of the item counts and the order of the sequences.

@@ -260,82 +260,6 @@ __host__ __device__ inline int bwd_head_group(int N, int d, int BH) {
   return (int)(g < 1 ? 1 : (g > BH ? BH : g));
 }
 
-// How a packed batch's key tiles are cut into items.  Tile tk (from the end) of a
-// sequence has G min(nqs, 2 tk + 2) steps (causal; else G nqs); an item takes
-// 2 G a of them, so tile tk has tk / a + 1 items while the causal limit binds
-// (tk < n1) and C above, and the items before a tile have a closed form.  `a`
-// comes from the whole batch's steps (var_plan): about kVarChunks equal chunks,
-// twice the SMs, and never fewer than 32 steps in one, so that the longest item
-// is a fraction of the kernel's time however the lengths are spread (without
-// the cut the first tile of the longest sequence took as long as the rest of
-// the batch: 4096 tokens, 4 heads to a key head, 256 steps, 0.24 ms).
-// With heads that share a key head, where most of the work is in split tiles, items
-// are numbered by classes of their length, kVarClasses in all: whole chunks of 2 G a
-// steps first, then what is left of the tiles, by eighths of a chunk from the longest
-// on.  (The blocks take two or three items each, so a chunk that is claimed after
-// short rests makes the last ones late: 8192 tokens, 8 / 2 heads, d 128, 291 us tile by
-// tile, 249 by classes; three texts of 3000 141 and 124.)  Others are numbered tile by
-// tile, which are found sooner: few of their tiles are split, and the classes gained them
-// nothing (4096 tokens, 12 heads with keys of their own, d 64: 88 us, 90 by classes).
-struct VarSplit {
-  int nkt, n1, a, C, nqs;
-  __host__ __device__ VarSplit(int lq, int lk, int a_, int causal) {
-    nqs = (lq + 63) >> 6;
-    nkt = (lk + 127) >> 7;
-    n1 = causal ? min(nkt, nqs >> 1) : 0;
-    a = a_;
-    C = (nqs + 2 * a - 1) / (2 * a);
-  }
-  // of a tile beyond the causal limit: whole chunks, and the eighths (1 .. 8) of its rest or 0
-  __host__ __device__ int fC() const { return nqs == C * 2 * a ? C : C - 1; }
-  __host__ __device__ int lC() const { return ((nqs - fC() * 2 * a) * 4 + a - 1) / a; }
-  // whole chunks of the tiles before tile n
-  __host__ __device__ int full_before(int n) const {
-    const int m = min(n, n1), k = m / a, r = m - k * a;
-    return a * (k * (k - 1) / 2) + k * (r + 1) + (n - m) * fC();
-  }
-  __host__ __device__ int full(int tk) const { return tk < n1 ? (tk + 1) / a : fC(); }
-  // rests of class c: (tk + 1) % a in (lo, hi], l = 9 - c eighths
-  __host__ __device__ int lo(int l) const { return (l - 1) * a / 8; }
-  __host__ __device__ int hi(int l) const { return l == 8 ? a - 1 : l * a / 8; }
-  __host__ __device__ int count1(int l) const {  // of the tiles at the causal limit
-    const int w = hi(l) - lo(l), k = n1 / a, r = n1 - k * a;
-    return k * w + min(max(r - lo(l), 0), w);
-  }
-  // items of class c, or of all (c = -1)
-  __host__ __device__ int count(int c) const {
-    if (c < 0) return items_before(nkt);
-    return c == 0 ? full_before(nkt) : count1(9 - c) + (nkt > n1 && lC() == 9 - c ? nkt - n1 : 0);
-  }
-  // tile and chunk of the e-th of them, the first tiles first
-  __host__ __device__ void pick(int c, int e, int* tk, int* chunk) const {
-    if (c <= 0) {
-      int at = 0, end = nkt - 1;
-      while (at < end) {
-        const int mid = (at + end + 1) >> 1;
-        if ((c < 0 ? items_before(mid) : full_before(mid)) <= e) at = mid; else end = mid - 1;
-      }
-      *tk = at;
-      *chunk = e - (c < 0 ? items_before(at) : full_before(at));
-    } else {
-      const int l = 9 - c, n = count1(l), w = hi(l) - lo(l);
-      *tk = e < n ? e / w * a + lo(l) + e % w : n1 + e - n;
-      *chunk = full(*tk);
-    }
-  }
-  __host__ __device__ int items(int tk) const { return tk < n1 ? tk / a + 1 : C; }
-  __host__ __device__ int items_before(int n) const {
-    const int m = min(n, n1), k = m / a, r = m - k * a;
-    return a * (k * (k + 1) / 2) + r * (k + 1) + (n - m) * C;
-  }
-  // tiles from here on have several items
-  __host__ __device__ int first_split() const { return C >= 2 ? min(a, n1) : nkt; }
-  __host__ __device__ int parts_before(int n) const {
-    const int f = first_split();
-    return n > f ? items_before(n) - items_before(f) : 0;
-  }
-};
-
 // VarSplit's count and pick, out of line: inlined they cost batches that need neither
 // (16 texts of 512, 12 heads, d 64: 47 us, 49 inlined).
 __device__ __noinline__ int var_count(VarSplit sp, int c) { return sp.count(c); }
@@ -1404,10 +1328,9 @@ cudaError_t launch_main_t(const BwdArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   // one CTA per item (block-sparse), else a persistent grid of one CTA per SM
-  // (VARLEN: no more items than the worst split of the keys into sequences has)
-  const long long items = VARLEN ? ((long long)a.Nk / 128 + a.B) * a.Hkv * a.G
-                                 : (long long)((a.N + 127) / 128) * a.B * a.H;
-  const unsigned grid = (unsigned)(SPARSE ? items : (items < a.sms ? items : a.sms));
+  const long long items = (long long)((a.N + 127) / 128) * a.B * a.H;
+  const unsigned grid = VARLEN ? (unsigned)bwd_varlen_grid(a.B, a.N, a.Nk, a.G, a.Hkv, a.sms)
+                               : (unsigned)(SPARSE ? items : (items < a.sms ? items : a.sms));
   e = launch_pdl(k, grid, BwdRoles<BwdNwg<DROPOUT>::value>::kThreads, L::kSmem, stream, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -1473,16 +1396,12 @@ __device__ __forceinline__ VarScan var_scan(const BwdArgs& p, uint8_t* smem, boo
       v.pbase[b] = pbase;
     }
     if (publish) {
-      const int nqs = (lq + 63) >> 6, nkt = (lk + 127) >> 7, n1 = p.causal ? min(nkt, nqs >> 1) : 0;
-      scan((long long)n1 * (n1 + 1) + (long long)(nkt - n1) * nqs, c_steps);
+      scan(var_steps(lq, lk, p.causal), c_steps);
     }
   }
   __syncthreads();
   if (publish) {
-    // chunks of 2 G a steps: an equal share of kVarChunks, no less than 32 (and no
-    // more than the 2^20 steps of the longest sequence)
-    const long long total = c_steps * p.H, unit = 2ll * p.G;
-    const int a = (int)min(1ll << 19, max((16ll + p.G - 1) / p.G, (total + kVarChunks * unit - 1) / (kVarChunks * unit)));
+    const int a = var_chunk(c_steps, p.H, p.G);  // chunks of 2 G a steps
     // Sequences with the most steps first, in half octaves (counted, then
     // placed): the short ones fill the end of the kernel.
     __shared__ int hist[128];
@@ -1492,9 +1411,7 @@ __device__ __forceinline__ VarScan var_scan(const BwdArgs& p, uint8_t* smem, boo
       lq = v.lq[b];
     };
     auto bucket = [&](int lq, int lk) -> int {
-      const int nqs = (lq + 63) >> 6, nkt = (lk + 127) >> 7, n1 = p.causal ? min(nkt, nqs >> 1) : 0;
-      const float steps = (float)n1 * (float)(n1 + 1) + (float)(nkt - n1) * (float)nqs;
-      return 127 - min(127, (int)(2.f * __log2f(steps + 1.f)));
+      return 127 - min(127, (int)(2.f * __log2f((float)var_steps(lq, lk, p.causal) + 1.f)));
     };
     for (int i = threadIdx.x; i < 128; i += kAuxThreads) hist[i] = 0;
     __syncthreads();

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "var_split.h"
+
 namespace attn {
 
 // Kernel ids used by the per-kernel timing of attn_profile_*.
@@ -95,9 +97,6 @@ struct VarBwdSeq {
   int pad;
 };
 constexpr int kVarMaxB = 8192;
-constexpr int kVarClasses = 9;                  // classes of items by length: whole chunks, eighths of one
-constexpr int kVarChunks = 304;                 // equal chunks a batch's steps are cut into
-constexpr int kVarMaxParts = 2 * kVarChunks;    // a split tile of n steps has < 2 n / (all steps / kVarChunks) parts
 
 struct BwdArgs {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;  // q/do boxes of bwd_q_rows(d) rows, k/v 128 rows
