@@ -548,6 +548,33 @@ def varlen_bwd(q, k, v, o, lse, do, cu_q, cu_k, scale=None, causal=False, ws=Non
 
 
 # ---- autograd -------------------------------------------------------------
+class _SecondDerivative(torch.autograd.Function):
+    """Hands gradients on unchanged; whoever differentiates them gets an error."""
+
+    @staticmethod
+    def forward(ctx, dq, dk, dv, *sources):
+        return dq.view_as(dq), dk.view_as(dk), dv.view_as(dv)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("attention can be differentiated once, not twice: its backward is a kernel "
+                           "without a derivative")
+
+
+def _once(backward):
+    """A backward pass whose results refuse to be differentiated.  (torch's
+    once_differentiable lets them pass as constants where the incoming gradient is
+    one, although they depend on q, k and v.)"""
+    @functools.wraps(backward)
+    def call(ctx, do):
+        with torch.no_grad():
+            grads = backward(ctx, do)
+        if torch.is_grad_enabled():  # create_graph=True
+            grads = (*_SecondDerivative.apply(*grads[:3], do, *ctx.saved_tensors[:3]), *grads[3:])
+        return grads
+    return call
+
+
 class AttentionFunction(torch.autograd.Function):
     """O = attention(q, k, v) with the backward of the library (attn_bwd_ex):
     saves q, k, v, O and LSE (O(N) extra state), never P."""
@@ -561,6 +588,7 @@ class AttentionFunction(torch.autograd.Function):
         return o
 
     @staticmethod
+    @_once
     def backward(ctx, do):
         q, k, v, o, lse = ctx.saved_tensors
         scale, causal, alibi, block_mask, dropout_p, seed, offset = ctx.opts
@@ -572,7 +600,8 @@ class AttentionFunction(torch.autograd.Function):
 def attention(q, k, v, scale=None, causal=False, alibi=None, block_mask=None, dropout_p=0.0,
               seed=0, offset=0):
     """Differentiable attention on contiguous [B, N, H, d] fp16/bf16 CUDA
-    tensors (forward and backward in the library's kernels)."""
+    tensors (forward and backward in the library's kernels).  The backward has no
+    derivative of its own: asking for a second one raises."""
     return AttentionFunction.apply(q, k, v, scale, causal, alibi, block_mask, dropout_p, seed,
                                    offset)
 
@@ -591,6 +620,7 @@ class VarlenAttentionFunction(torch.autograd.Function):
         return o
 
     @staticmethod
+    @_once
     def backward(ctx, do):
         q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
         grads = [torch.zeros(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v)]
@@ -600,7 +630,8 @@ class VarlenAttentionFunction(torch.autograd.Function):
 
 
 def attention_varlen(q, k, v, cu_q, cu_k, scale=None, causal=False):
-    """Differentiable attention on packed sequences (see varlen_fwd).  A training
+    """Differentiable attention on packed sequences (see varlen_fwd), once: asking
+    for a second derivative raises.  A training
     step may be captured into a CUDA graph, forward and backward together; as for
     every torch operator, no autograd graph of the same leaves from before the
     capture may still be alive then (drop its loss first): torch would run their
