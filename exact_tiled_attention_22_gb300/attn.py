@@ -451,7 +451,10 @@ def decode(q, k, v, scale=None, causal=False, ws=None, stream=None, alibi=None):
 # ValueError says what is wrong), allocate outputs and workspaces on the current
 # stream and call the entry points above.  Each takes stream=, the stream to run
 # on instead of the current one.
-def _load_bind():
+# The module is loaded at the first of these calls: the dense calls need libattn.so
+# only, not a torch whose C++ interface the module was built for.
+@functools.cache
+def _bind():
     path = os.path.join(os.path.dirname(LIB_PATH), "attn_bind.so")
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is not built; run exact_tiled_attention_22_gb300.build.build()")
@@ -460,9 +463,6 @@ def _load_bind():
     spec.loader.exec_module(mod)
     mod.set_error(AttnError)
     return mod
-
-
-_bind = _load_bind()
 
 
 def _on_stream(f):
@@ -500,8 +500,8 @@ def pages_extend(lens, add, block_table, free_pages, free_count, page, max_new, 
     free_pages: int32 [cap], a stack of free page ids, free_count: int32 [1];
     max_new: length of the slot map.  new_lens may be lens and free_left may
     be free_count.  Returns (new_lens, granted, cu_new, slots, free_left)."""
-    return _bind.pages_extend(lens, add, block_table, free_pages, free_count, page, max_new,
-                              new_lens, free_left)
+    return _bind().pages_extend(lens, add, block_table, free_pages, free_count, page, max_new,
+                                new_lens, free_left)
 
 
 @_on_stream
@@ -509,8 +509,8 @@ def pages_release(lens, finished, block_table, free_pages, free_count, page, new
                   free_left=None):
     """Pages of the requests with finished[b] != 0 (int32 [B]) go back onto the
     stack free_pages, written in place (attn_pages_release).  Returns (new_lens, free_left)."""
-    return _bind.pages_release(lens, finished, block_table, free_pages, free_count, page, new_lens,
-                               free_left)
+    return _bind().pages_release(lens, finished, block_table, free_pages, free_count, page, new_lens,
+                                 free_left)
 
 
 @_on_stream
@@ -518,7 +518,7 @@ def kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale):
     """Rounds new keys and values [T, H, d] into their slots (int64 [T]) of the
     8-bit cache [P, H, page, d] with scales [P, H], in place (attn_kv8_append).
     k and v may be slices of a wider projection (any token stride)."""
-    _bind.kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+    _bind().kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale)
 
 
 @_on_stream
@@ -526,8 +526,8 @@ def kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=N
                ws=None):
     """(o, lse) of q [B, Nq, Hq, d], the last Nq tokens of every request, against
     the 8-bit cache (attn_kv8_decode); lens counts the Nq tokens."""
-    return _bind.kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale, causal,
-                            ws)
+    return _bind().kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale, causal,
+                              ws)
 
 
 @_on_stream
@@ -536,7 +536,7 @@ def varlen_fwd(q, k, v, cu_q, cu_k, scale=None, causal=False, ws=None, o=None):
     fp16/bf16 CUDA tensors (any token stride that is a multiple of d), cu_q, cu_k
     int32 [B + 1] row offsets on the device (attn_varlen_fwd).  o: an output to
     write into; rows of no sequence are left as they are there."""
-    return _bind.varlen_fwd(q, k, v, cu_q, cu_k, scale, causal, ws, o)
+    return _bind().varlen_fwd(q, k, v, cu_q, cu_k, scale, causal, ws, o)
 
 
 @_on_stream
@@ -544,7 +544,7 @@ def varlen_bwd(q, k, v, o, lse, do, cu_q, cu_k, scale=None, causal=False, ws=Non
     """(dq, dk, dv) for the varlen_fwd that produced (o, lse).  grads: three
     contiguous tensors to write into (rows of no sequence are left as they are)."""
     dq, dk, dv = (None, None, None) if grads is None else grads
-    return _bind.varlen_bwd(q, k, v, o, lse, do, cu_q, cu_k, scale, causal, ws, dq, dk, dv)
+    return _bind().varlen_bwd(q, k, v, o, lse, do, cu_q, cu_k, scale, causal, ws, dq, dk, dv)
 
 
 # ---- autograd -------------------------------------------------------------
