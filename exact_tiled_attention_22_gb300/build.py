@@ -22,6 +22,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libattn.so")
 BIND = os.path.join(HERE, "attn_bind.so")
 BIND_SRC = os.path.join(CSRC, "attn_bind.cpp")
+STAMP = os.path.join(BUILD, "attn_bind.stamp")
 SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_decode.cu", "attn_noalloc.cu", "attn_diag.cu",
            "attn_pages.cu", "attn_kv8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -29,26 +30,47 @@ FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", 
          f"-I{os.path.join(ROOT, 'include')}"] + ARCH
 
 
+def _nvcc_path() -> str:
+    return shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+
+
 def nvcc() -> str:
-    exe = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    exe = _nvcc_path()
     if not os.path.exists(exe):
         raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libattn.so")
     return exe
 
 
-def _inputs():
+def _newer(lib, files) -> bool:
+    return os.path.exists(lib) and all(os.path.getmtime(f) <= os.path.getmtime(lib) for f in files)
+
+
+def _headers():
+    return glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
+
+
+def lib_up_to_date() -> bool:
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-    files += glob.glob(os.path.join(ROOT, "include", "*.h"))
-    files += [os.path.abspath(__file__), BIND_SRC]
-    return files
+    return _newer(LIB, files + _headers())
+
+
+def _stamp() -> str:
+    """What attn_bind.so was built for besides its sources: this torch (its version.py
+    names version, commit and CUDA), this Python and this toolkit."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return "\n".join([sysconfig.get_config_var("SOABI") or "", _torch_dir(), _nvcc_path(), f.read()])
+
+
+def bind_up_to_date() -> bool:
+    if not _newer(BIND, [BIND_SRC] + _headers()) or not os.path.exists(STAMP):
+        return False
+    with open(STAMP) as f:
+        return f.read() == _stamp()
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return lib_up_to_date() and bind_up_to_date()
 
 
 def _run(cmd, what):
@@ -80,36 +102,36 @@ def link_bind(obj: str) -> None:
     _run([shutil.which("g++") or "g++", "-shared", obj, "-o", tmp, f"-L{HERE}", "-l:libattn.so", "-Wl,-rpath,$ORIGIN",
           f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], "link of attn_bind.so failed")
     os.replace(tmp, BIND)
+    with open(STAMP, "w") as f:
+        f.write(_stamp())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
+    """Builds what is not up to date.  libattn.so is in place before an error in
+    attn_bind.so's build (a torch without its C++ headers, say) is raised."""
+    todo_lib, todo_bind = force or not lib_up_to_date(), force or not bind_up_to_date()
+    if not todo_lib and not todo_bind:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    exe = nvcc()
+    bind_obj = os.path.join(BUILD, "attn_bind.o")
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-        cmd = [exe] + FLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        r = _run([nvcc()] + FLAGS + ["-c", os.path.join(CSRC, src), "-o", obj], f"nvcc failed on {src}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr)
         return obj
 
-    bind_obj = os.path.join(BUILD, "attn_bind.o")
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        bind = ex.submit(compile_bind, bind_obj)
-        objs = list(ex.map(compile_one, SOURCES))
-        bind.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [exe, "-shared"] + ARCH + ["-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    link_bind(bind_obj)
+        bind = ex.submit(compile_bind, bind_obj) if todo_bind else None
+        if todo_lib:
+            objs = list(ex.map(compile_one, SOURCES))
+            tmp = LIB + f".tmp{os.getpid()}"
+            _run([nvcc(), "-shared"] + ARCH + ["-o", tmp] + objs, "link failed")
+            os.replace(tmp, LIB)
+        if bind is not None:
+            bind.result()
+            link_bind(bind_obj)
     return LIB
 
 

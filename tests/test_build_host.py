@@ -16,6 +16,9 @@ def copy(tmp_path):
     from exact_tiled_attention_22_gb300 import build
     build.build()
     shutil.copytree(os.path.join(ROOT, PKG), tmp_path / PKG, ignore=shutil.ignore_patterns("__pycache__"))
+    shutil.copytree(os.path.join(ROOT, "include"), tmp_path / "include")
+    os.makedirs(tmp_path / "_build")
+    shutil.copy(os.path.join(ROOT, "_build", "attn_bind.stamp"), tmp_path / "_build")
     return tmp_path
 
 
@@ -40,5 +43,54 @@ for _ in range(2):
         assert "attn_bind.so" in str(e), e
     else:
         raise SystemExit("no error")
+""")
+    assert r.returncode == 0, r.stderr
+
+
+def test_the_binding_is_built_again_for_another_torch(copy):
+    """Another torch, Python or toolkit than the module was built for: attn_bind.so is
+    built again, libattn.so, which does not know them, is not."""
+    r = python(copy, f"""
+import os
+from {PKG} import build
+assert build.up_to_date()
+old = os.stat(build.LIB).st_mtime_ns
+with open(build.STAMP) as f:
+    kept = f.read()
+assert kept == build._stamp() and "version" in kept
+for text in (kept.replace("version", "another version", 1), None):
+    if text is None:
+        os.remove(build.STAMP)
+    else:
+        with open(build.STAMP, "w") as f:
+            f.write(text)
+    assert build.lib_up_to_date() and not build.bind_up_to_date() and not build.up_to_date()
+did = []
+build.compile_bind = lambda obj: did.append("compile")
+build.link_bind = lambda obj: did.append("link")
+build.build()
+assert did == ["compile", "link"] and os.stat(build.LIB).st_mtime_ns == old
+""")
+    assert r.returncode == 0, r.stderr
+
+
+def test_libattn_is_in_place_before_the_binding_fails(copy):
+    """A torch without C++ headers: build() says so, and the dense calls have their library."""
+    r = python(copy, f"""
+import os
+from {PKG} import build
+os.remove(build.LIB)
+os.remove(build.BIND)
+build.SOURCES[:] = ["attn_diag.cu"]  # (one small file stands for them all)
+def fail(obj):
+    raise RuntimeError("no headers")
+build.compile_bind = fail
+try:
+    build.build()
+except RuntimeError as e:
+    assert "no headers" in str(e)
+else:
+    raise SystemExit("no error")
+assert os.path.exists(build.LIB) and not os.path.exists(build.BIND) and build.lib_up_to_date()
 """)
     assert r.returncode == 0, r.stderr
