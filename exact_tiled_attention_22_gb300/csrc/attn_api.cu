@@ -862,8 +862,9 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   const int shift = page_shift_of(page);
   if (shift < 0) return fail(ATTN_ERR_UNSUPPORTED, "page must be 16, 32, 64 or 128 (got %d)", page);
   if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_INVALID, "scale must be finite and > 0");
-  if ((long long)P * H >= (1ll << 31) || (long long)width * page >= (1ll << 31) || (long long)B * Nq * Hq >= (1ll << 31))
-    return fail(ATTN_ERR_INVALID, "P * H, width * page and B * Nq * Hq must be < 2^31");
+  // (the kernels round a length up to whole tiles of 128 keys in 32 bits)
+  if ((long long)P * H >= (1ll << 31) || (long long)width * page > (1ll << 31) - 128 || (long long)B * Nq * Hq >= (1ll << 31))
+    return fail(ATTN_ERR_INVALID, "P * H and B * Nq * Hq must be < 2^31, width * page at most 2^31 - 128");
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(lse))
     return fail(ATTN_ERR_ALIGN, "q, o, lse and the caches must be 16-byte aligned");
   if (!aligned4(k_scale) || !aligned4(v_scale) || !aligned4(block_table) || !aligned4(lens))

@@ -448,6 +448,7 @@ int attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o,
  * queries exactly up to 2^-21 of a row's largest element; probabilities are
  * rounded to 2^-14 (fp16) or 2^-9 (bf16) of their value.
  * workspace: as attn_decode's, size from attn_kv8_decode_workspace_size.
+ * 1 <= Nq <= 128; P * H and B * Nq * Hq below 2^31, width * page at most 2^31 - 128.
  */
 int attn_pages_extend(const int32_t* lens, const int32_t* add, int B, int32_t* block_table,
                       int width, const int32_t* free_pages, const int32_t* free_count,

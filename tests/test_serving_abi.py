@@ -164,3 +164,13 @@ def test_conveniences_refuse_other_tensors(A):
         A.pages_extend(z(3).int(), z(3).int(), z(3, 4).int(), z(9).int(), z(1).int(), 16, 3)
     with pytest.raises(ValueError):
         A.pages_release(z(3).int(), z(3).int(), z(3, 4).int(), z(9).int(), z(1).int(), 16)
+
+
+@pytest.mark.parametrize("width,page", [((1 << 27) - 1, 16), ((1 << 27) - 7, 16), ((1 << 26) - 3, 32), ((1 << 25) - 1, 64)])
+def test_decode_refuses_lengths_that_do_not_round_up(A, width, page):
+    """Tables of more than 2^31 - 128 tokens: the last tile's end would not fit 32 bits."""
+    assert (1 << 31) - 128 < width * page < 1 << 31
+    base = dict(q=P[0], kc=P[1], vc=P[2], sk=P[3], sv=P[4], table=P[5], lens=P[6], o=P[7], lse=P[8], B=1, Nq=1, Hq=4,
+                H=2, d=64, P=9, page=page, width=width, scale=0.125, causal=1, dtype=A.ATTN_BF16, ws=WS,
+                ws_bytes=A.attn_kv8_decode_workspace_size(1, 4, 2, 64), stream=None)
+    assert call(A.lib.attn_kv8_decode, DECODE, base) == -1 and "width * page" in A.last_error()
