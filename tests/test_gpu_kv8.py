@@ -517,3 +517,31 @@ def test_tensors_freed_after_a_call_on_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     del others
+
+
+@pytest.mark.parametrize("H,d,page,T", [(8, 128, 16, 640), (8, 64, 64, 1000), (1, 128, 32, 5000), (3, 64, 128, 1700)])
+def test_append_single_tokens_of_many_requests(H, d, page, T):
+    """A decoding step of many requests, where a warp looks after 32 tokens and every one
+    is a run of its own: at any place of its page, the scale growing or not, skipped ones
+    and a few short prompts among them."""
+    from exact_tiled_attention_22_gb300 import attn
+    assert T * H * 2 > 64 * 152               # the launcher's border
+    g = torch.Generator().manual_seed(T)
+    P = T + 40
+    kc, ks = cache(P, H, page, d, g)
+    vc, vs = cache(P, H, page, d, g)
+    pages = torch.randperm(P, generator=g)
+    place = torch.randint(0, page, (T,), generator=g)
+    place[::3] = 0
+    slots = pages[:T] * page + place
+    slots[5::50] = -1
+    n = min(page, 17)
+    for i, t in enumerate(range(64, T - 64, 320)):            # a run over the end of a warp's 32 tokens
+        slots[t + 25:t + 25 + n] = pages[T + i] * page + torch.arange(n)
+    x = [(torch.randn((T, H, d), generator=g) * torch.exp2(torch.randint(-6, 7, (T, 1, 1), generator=g).float())).to(
+        DT["bf16"]) for _ in range(2)]
+    dk, dv, dks, dvs = kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda()
+    attn.kv8_append(x[0].cuda(), x[1].cuda(), slots.cuda(), dk, dv, dks, dvs)
+    for t, c, s, got, got_s in ((x[0], kc, ks, dk, dks), (x[1], vc, vs, dv, dvs)):
+        val, sc = plain64.append(t.double(), slots.tolist(), c.double(), s.double())
+        assert torch.equal(got_s.double().cpu(), sc) and torch.equal(got.cpu().double(), val)

@@ -140,3 +140,29 @@ def test_extend_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert (ln.tolist(), slots.tolist(), cnt.item(), tb.tolist()) == (lens, want, count, table)
+
+
+@pytest.mark.parametrize("B", [1023, 1024, 1025, 3000, 8192])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_release_of_many(B, in_place):
+    """Around one pass of the block's threads and far beyond, lengths past the table's row
+    and negative ones among them."""
+    from exact_tiled_attention_22_gb300 import attn
+    page, width, count = 16, 3, 7
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(-2, page * width + 20, (B,), generator=g).tolist()
+    done = torch.randint(0, 3, (B,), generator=g).tolist()   # any number but 0 is a yes
+    table = torch.randperm(B * width, generator=g).view(B, width).tolist()
+    want = list(range(-count, 0))
+    for b in range(B):
+        if done[b]:
+            want += table[b][:max(0, min(width, -(-lens[b] // page)))]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    for cap in (count + B * width, len(want), len(want) - 5):
+        stack = i32((want[:count] + [-7] * cap)[:cap])
+        ln, cnt = i32(lens), i32([count])
+        new, left = attn.pages_release(ln, i32(done), i32(table), stack, cnt, page, new_lens=ln if in_place else None,
+                                       free_left=cnt if in_place else None)
+        kept = want[:cap]
+        assert left.item() == len(kept) and stack.tolist() == kept + [-7] * (cap - len(kept))
+        assert new.tolist() == [0 if f else n for n, f in zip(lens, done)]

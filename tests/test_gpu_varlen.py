@@ -471,3 +471,29 @@ def test_whole_query_tiles_without_keys(Hq, H, d):
                          cu([lq] * n), cu([lk] * n), d ** -0.5, True, "bf16")
     plain64.check(o[:n * lq], *ref["o"], "o")
     plain64.check(lse[:, :n * lq], *ref["lse"], "lse")
+
+
+GROUPS = [
+    # (lens_q, lens_k, Hq, Hkv, d, dtype, causal): groups above 8, with a ragged first tile.  A
+    # batch of 128 queries or more a sequence takes tiles of the largest power of two in
+    # the group (48: 16 heads of 8 positions), a shorter one the whole group (48: 2 positions)
+    ([300, 40], [300, 40], 16, 1, 64, "bf16", True),
+    ([70, 33], [70, 51], 32, 2, 128, "fp16", True),
+    ([150, 130], [150, 259], 48, 1, 64, "fp16", True),
+    ([21, 90], [130, 90], 48, 1, 128, "bf16", False),
+    ([200], [333], 64, 1, 128, "bf16", True),
+    ([150, 129], [150, 129], 65, 1, 64, "bf16", True),
+    ([60, 5, 30], [60, 200, 1], 65, 1, 128, "fp16", True),
+    ([20, 90], [20, 300], 127, 1, 64, "bf16", False),
+    ([140, 3], [140, 3], 128, 1, 128, "fp16", True),
+    ([130, 3], [260, 3], 256, 1, 64, "bf16", True),
+    ([135], [70], 256, 1, 128, "bf16", True),       # the first tiles see no key
+    # few keys: one key tile of many steps, which are cut into chunks
+    ([6000], [128], 2, 2, 64, "bf16", False),
+    ([3100, 5], [100, 260], 32, 1, 64, "fp16", False),
+]
+
+
+@pytest.mark.parametrize("case", GROUPS, ids=lambda c: f"{c[0][0]}on{c[1][0]}-{c[2]}x{c[3]}d{c[4]}{c[5]}{'c' if c[6] else ''}")
+def test_large_groups(case):
+    test_forward_and_gradients(case)
