@@ -405,11 +405,11 @@ cudaError_t launch_merge_t(const DecArgs& a, cudaStream_t stream) {
 
 int decode_n_split(int B, int H, int Nk) {
   // Chunks of whole 128-key tiles, at least two tiles each, about two CTAs
-  // per SM of a GB300 (152 SMs) in total, at most kDecodeMaxSplit per head;
+  // per SM (kSms) in total, at most kDecodeMaxSplit per head;
   // then as few chunks as the resulting chunk length needs (none empty).
   const int tiles = (Nk + 127) / 128;
   const long long bh = (long long)B * H;
-  long long want = (2 * 152 + bh - 1) / bh;
+  long long want = (2 * kSms + bh - 1) / bh;
   if (want > (tiles + 1) / 2) want = (tiles + 1) / 2;
   if (want > kDecodeMaxSplit) want = kDecodeMaxSplit;
   if (want < 1) want = 1;

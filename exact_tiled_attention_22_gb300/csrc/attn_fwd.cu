@@ -1265,8 +1265,8 @@ void fwd_varlen_shape(int G, long long Nq, int B, int* Gp, int* R) {
 // CTA a pair.  Sharing beyond one CTA an SM, up to 304 or 456, made 24 prompts of 64
 // tokens on 420 keys 19 us instead of 12.)
 int fwd_varlen_nsplit(long long ctas, long long Nk) {
-  if ((Nk + 127) / 128 < 2 * kVarMinChunk || ctas >= 152) return 1;
-  const long long n = (152 + ctas - 1) / ctas, most = (Nk + 127) / 128 / kVarMinChunk;
+  if ((Nk + 127) / 128 < 2 * kVarMinChunk || ctas >= kSms) return 1;
+  const long long n = (kSms + ctas - 1) / ctas, most = (Nk + 127) / 128 / kVarMinChunk;
   return (int)(n < most ? n : most);
 }
 

@@ -969,7 +969,7 @@ cudaError_t launch_kv8_split(const Kv8DecArgs& a, cudaStream_t stream) {
                    : (a.rp == 8 ? launch_split_n<64, 8>(a, stream) : launch_split_n<64, 16>(a, stream));
 }
 
-constexpr long long kMergeBlocks = 2 * 1216;  // (8 blocks fit an SM)
+constexpr long long kMergeBlocks = 2 * 8 * kSms;  // two waves of eight blocks to an SM
 
 template <int D, bool BF16>
 static cudaError_t launch_merge_t(Kv8DecArgs a, cudaStream_t stream) {

@@ -11,8 +11,12 @@
 
 namespace attn {
 
+// SMs of a GB300, for what must not depend on the device of a call: sizes of workspaces,
+// the split of the work (and with it the order of sums).
+constexpr int kSms = 152;
+
 constexpr int kVarClasses = 9;                // classes of items by length: whole chunks, eighths of one
-constexpr int kVarChunks = 304;               // equal chunks a batch's steps are cut into
+constexpr int kVarChunks = 2 * kSms;          // equal chunks a batch's steps are cut into
 constexpr int kVarMaxParts = 2 * kVarChunks;  // a split tile of n steps has < 2 n / (all steps / kVarChunks) parts
 
 template <typename T>
