@@ -98,7 +98,7 @@ struct VarSeq {
 // ceil(lq / tile_rows) of them; `unit` becomes its index there.  Every warp
 // searches by itself (no shared memory, no barrier), 32 sequences at a time, whose
 // offsets are then at hand, 0.3 us a look; or 256 of more than 256 (1000 sequences of
-// 32 tokens, 4 heads: 191 us, 281 with 32; 96 of 64, 12 heads: 55 us, 53 with 32).  The
+// 32 tokens, 4 heads, d 64: 188 us, 281 with 32; 96 of 64, 12 heads: 55 us, 53 with 32).  The
 // latter stay out of line: inlined they cost every block 0.4 us even where they are
 // not called.  Offsets are clamped to the tensors, so that wrong ones read and
 // write nothing outside them.

@@ -90,10 +90,11 @@ constexpr int kAppThreads = 128;
 // One warp per (chunk of `chunk` tokens, head, K or V): it takes the runs of
 // consecutive slots in one page that begin in its chunk.  Two passes over a
 // run: largest magnitude, then codes; the first 16 (d = 128) or 32 (d = 64)
-// tokens stay in registers between them.  Bound by HBM for prompts (the 16-bit
-// values in, the codes out), by latency for a decoding step: the chain slot,
-// values and old scale, codes.  Blocks of 128 threads, six to an SM at 80 registers:
-// a block whose warps have done their runs makes room sooner than a larger one.
+// tokens stay in registers between them.  Bound by its own instructions for prompts
+// (conversions and the search for runs: issue slots 58 %, DRAM 25 %), by latency for a
+// decoding step: the chain slot, values and old scale, codes.  Blocks of 128 threads,
+// six to an SM at 80 registers: a block whose warps have done their runs makes room
+// sooner than a larger one.
 // Measured: 31749 tokens of 4 heads, d = 64, page 16 (49 MB) 11.1 us or 4.4 TB/s (12.0
 // with blocks of 256, three to an SM; 11.6 with eight at 64 registers), 15 us with
 // the values in HBM, the schedulers 58 % busy; one token of each of 256 requests, 8
@@ -993,9 +994,15 @@ cudaError_t launch_kv8_merge(const Kv8DecArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int sms, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
-  // A warp per token, head and tensor while that is few warps (decoding
-  // steps: every token starts a run of its own); a warp per 32 tokens above (31749
-  // tokens of 4 heads, d = 64: 12.8 us against 13.8 with 16 and 17.3 with 8).
+  // A warp per token, head and tensor while that is few warps, a warp per 32 tokens
+  // above.  The rule sees how many tokens there are, not whether they are prompts, whose
+  // runs a warp takes whole, or single tokens of many requests, which it takes one after
+  // the other.  Prompts, us with 1 and with 32 (8 heads, d = 128, page 64): 300 tokens 5.5
+  // and 5.3, 608 (the last with 1) 7.2 and 5.5, 2000 13.1 and 6.4; 31749 of 4 heads, d = 64,
+  // page 16: 66 and 10.7 (12.8 with 32 when 16 took 13.8 and 8 took 17.3).  Single tokens:
+  // 256 requests 4.2 and 25.6, 608 7.2 and 25.5, 640 (the first with 32) 7.6 and 25.6, 1024
+  // 10.9 and 25.6, 4096 38 and 41, 8192 75 and 69: steps of 608 to about 4500 requests of 8
+  // heads pay for the prompts.
   const int chunk = a.T * a.H * 2 <= 64ll * sms ? 1 : 32;
   const long long warps = (a.T + chunk - 1) / chunk * a.H * 2;
   const unsigned grid = (unsigned)((warps * 32 + kAppThreads - 1) / kAppThreads);

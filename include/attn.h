@@ -352,8 +352,8 @@ int attn_decode(const void* q, const void* k, const void* v, void* o, float* lse
  * sequence, or with `causal` the keys j <= lk - lq + i: the queries are the last
  * lq positions (lk > lq: a prompt that goes on after cached keys).  A query that
  * sees no key gets O = 0, LSE = -inf, dQ = 0; a key that no query sees gets
- * dK = dV = 0.  Rows of no sequence (before cu[0], behind cu[B]) are neither read
- * nor written.  Values (and for the gradients queries and dO) must be finite: as in
+ * dK = dV = 0.  Rows of no sequence (before cu[0], behind cu[B]) are not written,
+ * and what they hold does not matter.  Values (and for the gradients queries and dO) must be finite: as in
  * any matrix product a NaN or an infinity there may reach the sequence's rows
  * that the mask keeps from it; one in a query or key reaches the rows that see
  * it only.  dK and dV of a key head sum over its group in a fixed order;
