@@ -567,10 +567,11 @@ def _once(backward):
     one, although they depend on q, k and v.)"""
     @functools.wraps(backward)
     def call(ctx, do):
+        saved = ctx.saved_tensors  # (once: a checkpointed forward hands them out only once)
         with torch.no_grad():
-            grads = backward(ctx, do)
+            grads = backward(ctx, do, *saved)
         if torch.is_grad_enabled():  # create_graph=True
-            grads = (*_SecondDerivative.apply(*grads[:3], do, *ctx.saved_tensors[:3]), *grads[3:])
+            grads = (*_SecondDerivative.apply(*grads[:3], do, *saved[:3]), *grads[3:])
         return grads
     return call
 
@@ -589,8 +590,7 @@ class AttentionFunction(torch.autograd.Function):
 
     @staticmethod
     @_once
-    def backward(ctx, do):
-        q, k, v, o, lse = ctx.saved_tensors
+    def backward(ctx, do, q, k, v, o, lse):
         scale, causal, alibi, block_mask, dropout_p, seed, offset = ctx.opts
         dq, dk, dv = bwd(q, k, v, o, lse, do.contiguous(), scale, causal, alibi=alibi,
                          block_mask=block_mask, dropout_p=dropout_p, seed=seed, offset=offset)
@@ -623,8 +623,7 @@ class VarlenAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     @_once
-    def backward(ctx, do):
-        q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
+    def backward(ctx, do, q, k, v, o, lse, cu_q, cu_k):
         grads = [torch.zeros(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v)]
         dq, dk, dv = varlen_bwd(q, k, v, o, lse, do.contiguous(), cu_q, cu_k, *ctx.opts,
                                 grads=grads)

@@ -2,6 +2,7 @@
 one is refused, not dropped (CPU: the library's calls replaced by formulas in torch)."""
 import pytest
 import torch
+import torch.utils.checkpoint
 
 
 @pytest.fixture()
@@ -39,3 +40,15 @@ def test_second_derivatives_are_refused(A, packed):
     with torch.no_grad():
         out = call()
     assert torch.equal(gy, 2 * out * y)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("create_graph", [False, True])
+def test_in_a_checkpointed_block(A, packed, create_graph):
+    """A recomputed forward hands each saved tensor out once."""
+    shape = (5, 2, 4) if packed else (1, 5, 2, 4)
+    x = [torch.randn(shape, requires_grad=True) for _ in range(3)]
+    call = (lambda *t: A.attention_varlen(*t, None, None)) if packed else A.attention
+    out = torch.utils.checkpoint.checkpoint(call, *x, use_reentrant=False)
+    grads = torch.autograd.grad(out.sum(), x, create_graph=create_graph)
+    assert all(torch.equal(g, 2 * t) for g, t in zip(grads, x))
