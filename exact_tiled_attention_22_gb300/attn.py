@@ -34,7 +34,8 @@ ERROR_NAMES = {0: "ATTN_OK", -1: "ATTN_ERR_INVALID", -2: "ATTN_ERR_UNSUPPORTED",
 KERNEL_NAMES = ["attn_fwd", "attn_bwd_pre", "attn_bwd_main", "attn_dq_post",
                 "attn_decode_split", "attn_decode_merge", "attn_pages_extend",
                 "attn_pages_release", "attn_kv8_append", "attn_kv8_split", "attn_kv8_merge",
-                "attn_varlen_merge"]
+                "attn_varlen_merge", "attn_kv4_append", "attn_kv4_split", "attn_kv4_merge",
+                "attn_kv_read"]
 
 
 class AttnError(RuntimeError):
@@ -109,6 +110,10 @@ def _load() -> ctypes.CDLL:
     lib.attn_kv8_decode_workspace_size.restype = sz
     lib.attn_kv8_decode.argtypes = [vp] * 9 + [i] * 8 + [f, i, i, vp, sz, vp]
     lib.attn_kv8_decode.restype = i
+    lib.attn_kv4_append.argtypes = lib.attn_kv8_append.argtypes
+    lib.attn_kv4_append.restype = i
+    lib.attn_kv_read.argtypes = [vp] * 9 + [i, ll] + [i] * 7 + [vp]
+    lib.attn_kv_read.restype = i
     lib.attn_varlen_fwd_workspace_size.argtypes = [i, ll, ll, i, i, i]
     lib.attn_varlen_fwd_workspace_size.restype = sz
     lib.attn_varlen_fwd.argtypes = [vp] * 7 + [i, ll, ll, i, i, i, ll, ll, ll, f, i, i, vp, sz, vp]
@@ -326,6 +331,20 @@ def attn_kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o,
                                _stream(stream))
 
 
+def attn_kv4_append(k, v, k_stride, v_stride, slots, T, H, d, k_cache, v_cache, k_scale, v_scale,
+                    P, page, dtype, stream=None) -> int:
+    return lib.attn_kv4_append(_ptr(k), _ptr(v), k_stride, v_stride, _ptr(slots), T, H, d,
+                               _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), P, page,
+                               dtype_code(dtype), _stream(stream))
+
+
+def attn_kv_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, cu, k, v, B, T, H, d, P, page,
+                 width, bits, dtype, stream=None) -> int:
+    return lib.attn_kv_read(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                            _ptr(block_table), _ptr(lens), _ptr(cu), _ptr(k), _ptr(v), B, T, H, d, P,
+                            page, width, bits, dtype_code(dtype), _stream(stream))
+
+
 def attn_varlen_fwd_workspace_size(B, Tq, Tk, Hq, Hkv, d) -> int:
     return int(lib.attn_varlen_fwd_workspace_size(B, Tq, Tk, Hq, Hkv, d))
 
@@ -528,6 +547,34 @@ def kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=N
     the 8-bit cache (attn_kv8_decode); lens counts the Nq tokens."""
     return _bind().kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale, causal,
                               ws)
+
+
+@_on_stream
+def kv4_append(k, v, slots, k_cache, v_cache, k_scale, v_scale):
+    """Rounds new keys and values [T, H, d] into their slots (int64 [T]) of the
+    4-bit cache, uint8 [P, H, page, d / 2] with bf16 scales [P, H, page, d / 32], in place
+    (attn_kv4_append).  k and v may be slices of a wider projection (any token
+    stride that is a multiple of 8)."""
+    _bind().kv4_append(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+
+
+@_on_stream
+def kv4_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, cu, total, dtype=torch.bfloat16,
+             k=None, v=None):
+    """(k, v) [total, H, d]: the cached tokens of every request as packed rows of
+    dtype, request b's from row cu[b] (int32 [B + 1]) on, for varlen_fwd
+    (attn_kv_read).  k, v: outputs to write into; rows of no cached token are left
+    as they are there (a request's new tokens, say), and hold anything otherwise."""
+    return _bind().kv4_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, cu, total,
+                            dtype_code(dtype), k, v)
+
+
+@_on_stream
+def kv8_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, cu, total, dtype=torch.bfloat16,
+             k=None, v=None):
+    """The same from the 8-bit cache (attn_kv_read)."""
+    return _bind().kv8_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, cu, total,
+                            dtype_code(dtype), k, v)
 
 
 @_on_stream

@@ -24,7 +24,7 @@ BIND = os.path.join(HERE, "attn_bind.so")
 BIND_SRC = os.path.join(CSRC, "attn_bind.cpp")
 STAMP = os.path.join(BUILD, "attn_bind.stamp")
 SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_decode.cu", "attn_noalloc.cu", "attn_diag.cu",
-           "attn_pages.cu", "attn_kv8.cu"]
+           "attn_pages.cu", "attn_kv8.cu", "attn_kv4.cu", "attn_kvread.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          f"-I{os.path.join(ROOT, 'include')}"] + ARCH

@@ -797,6 +797,98 @@ int attn_pages_release(const int32_t* lens, const int32_t* finished, int B, cons
   return e != cudaSuccess ? cuda_fail(e, "attn_pages_release launch") : ATTN_OK;
 }
 
+// What the calls on a cache in `bits` bits ask of it.  (In 4 bits its rows are copied by TMA,
+// which unpacks them: 32-byte aligned.)
+static int check_cache(const uint8_t* k_cache, const uint8_t* v_cache, const void* k_scale, const void* v_scale, int H,
+                       int d, int P, int page, attn_dtype_t dtype, int bits) {
+  if (!k_cache || !v_cache || !k_scale || !v_scale) return fail(ATTN_ERR_INVALID, "null pointer argument");
+  if (H < 1 || P < 1) return fail(ATTN_ERR_INVALID, "H >= 1, P >= 1 needed (got %d, %d)", H, P);
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim d=%d not supported (64 or 128)", d);
+  if (dtype != ATTN_F16 && dtype != ATTN_BF16) return fail(ATTN_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
+  if (page_shift_of(page) < 0) return fail(ATTN_ERR_UNSUPPORTED, "page must be 16, 32, 64 or 128 (got %d)", page);
+  if ((long long)P * H >= (1ll << 31) || (long long)H * d >= (1ll << 32))
+    return fail(ATTN_ERR_INVALID, "P * H must be < 2^31, H * d < 2^32");
+  const uintptr_t c = reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache);
+  const uintptr_t s = reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale);
+  if (c & (bits == 4 ? 31u : 15u)) return fail(ATTN_ERR_ALIGN, "the caches must be %d-byte aligned", bits == 4 ? 32 : 16);
+  if (s & (bits == 4 ? 15u : 3u)) return fail(ATTN_ERR_ALIGN, "scales must be %d-byte aligned", bits == 4 ? 16 : 4);
+  return ATTN_OK;
+}
+static size_t code_bytes(int P, int H, int page, int d, int bits) { return (size_t)P * H * page * (d * bits / 8); }
+static size_t scale_bytes(int P, int H, int page, int d, int bits) {
+  return (size_t)P * H * (bits == 4 ? (size_t)page * (d / 32) * 2 : 4);
+}
+
+int attn_kv4_append(const void* k, const void* v, long long k_stride, long long v_stride, const int64_t* slots,
+                    long long T, int H, int d, uint8_t* k_cache, uint8_t* v_cache, uint16_t* k_scale,
+                    uint16_t* v_scale, int P, int page, attn_dtype_t dtype, void* stream) {
+  t_err.clear();
+  if (T == 0) return ATTN_OK;
+  if (!k || !v || !slots) return fail(ATTN_ERR_INVALID, "null pointer argument");
+  int rc = check_cache(k_cache, v_cache, k_scale, v_scale, H, d, P, page, dtype, 4);
+  if (rc) return rc;
+  if (T < 0 || T >= (1ll << 31) || T * H >= (1ll << 30)) return fail(ATTN_ERR_INVALID, "T * H must be in [0, 2^30)");
+  const long long hd = (long long)H * d;
+  if (k_stride < hd || v_stride < hd || k_stride % 8 || v_stride % 8 || k_stride >= (1ll << 32) || v_stride >= (1ll << 32))
+    return fail(ATTN_ERR_INVALID, "token strides must be multiples of 8, at least H * d, below 2^32");
+  if (!aligned16(k) || !aligned16(v)) return fail(ATTN_ERR_ALIGN, "k and v must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(slots) & 7u) return fail(ATTN_ERR_ALIGN, "slots must be 8-byte aligned");
+  const size_t cb = code_bytes(P, H, page, d, 4), sb = scale_bytes(P, H, page, d, 4);
+  const Range outs[4] = {rng(k_cache, cb), rng(v_cache, cb), rng(k_scale, sb), rng(v_scale, sb)};
+  const Range ins[3] = {rng(k, ((size_t)(T - 1) * k_stride + hd) * 2), rng(v, ((size_t)(T - 1) * v_stride + hd) * 2),
+                        rng(slots, (size_t)T * 8)};
+  if ((rc = check_overlaps(outs, 4, ins, 3))) return rc;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  attn::Kv4AppendArgs a = {};
+  a.x[0] = k; a.x[1] = v;
+  a.cache[0] = k_cache; a.cache[1] = v_cache;
+  a.scale[0] = k_scale; a.scale[1] = v_scale;
+  a.slots = reinterpret_cast<const long long*>(slots);
+  a.x_stride[0] = k_stride; a.x_stride[1] = v_stride;
+  a.T = T;
+  a.n_slots = (long long)P * page;
+  a.H = H; a.d = d; a.page_shift = page_shift_of(page); a.bf16 = dtype == ATTN_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = timed(attn::kKKv4Append, s, [&] { return attn::launch_kv4_append(a, dev->sms, s); });
+  return e != cudaSuccess ? cuda_fail(e, "attn_kv4_append launch") : ATTN_OK;
+}
+
+int attn_kv_read(const uint8_t* k_cache, const uint8_t* v_cache, const void* k_scale, const void* v_scale,
+                 const int32_t* block_table, const int32_t* lens, const int32_t* cu, void* k, void* v, int B,
+                 long long T, int H, int d, int P, int page, int width, int bits, attn_dtype_t dtype, void* stream) {
+  t_err.clear();
+  if (bits != 8 && bits != 4) return fail(ATTN_ERR_UNSUPPORTED, "caches hold 8 or 4 bits (got %d)", bits);
+  int rc = check_cache(k_cache, v_cache, k_scale, v_scale, H, d, P, page, dtype, bits);
+  if (rc) return rc;
+  if (!block_table || !lens || !cu || (T > 0 && (!k || !v))) return fail(ATTN_ERR_INVALID, "null pointer argument");
+  if (B < 1 || width < 1) return fail(ATTN_ERR_INVALID, "B >= 1, width >= 1 needed (got %d, %d)", B, width);
+  if (T < 0 || T >= (1ll << 31) || T * H >= (1ll << 33)) return fail(ATTN_ERR_INVALID, "T must be in [0, 2^31), T * H below 2^33");
+  if ((long long)width * page >= (1ll << 31)) return fail(ATTN_ERR_INVALID, "width * page must be < 2^31");
+  if (!aligned16(k) || !aligned16(v)) return fail(ATTN_ERR_ALIGN, "k and v must be 16-byte aligned");
+  if (!aligned4(block_table) || !aligned4(lens) || !aligned4(cu))
+    return fail(ATTN_ERR_ALIGN, "block_table, lens and cu must be 4-byte aligned");
+  if (T == 0) return ATTN_OK;
+  const size_t cb = code_bytes(P, H, page, d, bits), sb = scale_bytes(P, H, page, d, bits), ob = (size_t)T * H * d * 2;
+  const Range outs[2] = {rng(k, ob), rng(v, ob)};
+  const Range ins[7] = {rng(k_cache, cb), rng(v_cache, cb), rng(k_scale, sb), rng(v_scale, sb),
+                        rng(block_table, (size_t)B * width * 4), rng(lens, (size_t)B * 4), rng(cu, (size_t)B * 4 + 4)};
+  if ((rc = check_overlaps(outs, 2, ins, 7))) return rc;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  attn::KvReadArgs a = {};
+  a.cache[0] = k_cache; a.cache[1] = v_cache;
+  a.scale[0] = k_scale; a.scale[1] = v_scale;
+  a.out[0] = k; a.out[1] = v;
+  a.table = block_table; a.lens = lens; a.cu = cu;
+  a.T = T;
+  a.B = B; a.H = H; a.d = d; a.P = P; a.page_shift = page_shift_of(page); a.width = width;
+  a.bf16 = dtype == ATTN_BF16; a.bits = bits;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = timed(attn::kKKvRead, s, [&] { return attn::launch_kv_read(a, dev->sms, s); });
+  return e != cudaSuccess ? cuda_fail(e, "attn_kv_read launch") : ATTN_OK;
+}
+
 int attn_kv8_append(const void* k, const void* v, long long k_stride, long long v_stride, const int64_t* slots,
                     long long T, int H, int d, uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale,
                     int P, int page, attn_dtype_t dtype, void* stream) {
@@ -841,7 +933,7 @@ int attn_kv8_append(const void* k, const void* v, long long k_stride, long long 
 
 size_t attn_kv8_decode_workspace_size(int Nq, int Hq, int H, int d) {
   if (Nq < 1 || H < 1 || Hq < H || Hq % H || (d != 64 && d != 128)) return 0;
-  const size_t rows = (size_t)attn::kKv8MaxCtas * 2 * attn::kv8_rows(Nq * (Hq / H));
+  const size_t rows = (size_t)attn::kKvMaxCtas * 2 * attn::kv8_rows(Nq * (Hq / H));
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   return up(rows * d * 4) + up(rows * 2 * 4);
 }
@@ -882,7 +974,7 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   if (rc) return rc;
   DeviceInfo* dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
-  attn::Kv8DecArgs a;
+  attn::KvDecArgs a;
   std::memset(&a, 0, sizeof a);
   if ((rc = encode_pages(&a.tm_k, k_cache, (long long)P * H, page, d)) ||
       (rc = encode_pages(&a.tm_v, v_cache, (long long)P * H, page, d)))
@@ -893,6 +985,7 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   a.width = width; a.page_shift = shift; a.P = P;
   const int R = Nq * a.G;
   a.rp = attn::kv8_rows(R);
+  a.tile_shift = 7;
   a.n_rb = (R + a.rp - 1) / a.rp;
   a.causal = causal ? 1 : 0;
   a.bf16 = dtype == ATTN_BF16;
@@ -901,12 +994,12 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   a.grid = attn::kv8_grid(a.rp, dev->sms, tiles * B * H * a.n_rb);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.ws_o = reinterpret_cast<float*>(ws);
-  a.ws_ml = reinterpret_cast<float*>(ws + ((size_t)attn::kKv8MaxCtas * 2 * a.rp * d * 4 + 255) / 256 * 256);
+  a.ws_ml = reinterpret_cast<float*>(ws + ((size_t)attn::kKvMaxCtas * 2 * a.rp * d * 4 + 255) / 256 * 256);
   wait_ctl(dev, &a.wait, &a.debug_flags);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = timed(attn::kKKv8Split, s, [&] { return attn::launch_kv8_split(a, s); });
   if (e != cudaSuccess) return cuda_fail(e, "attn_kv8_decode launch");
-  e = timed(attn::kKKv8Merge, s, [&] { return attn::launch_kv8_merge(a, s); });
+  e = timed(attn::kKKv8Merge, s, [&] { return attn::launch_kv_merge(a, s); });
   return e != cudaSuccess ? cuda_fail(e, "attn_kv8_decode merge launch") : ATTN_OK;
 }
 

@@ -292,6 +292,75 @@ PyObject* kv8_decode(PyObject* const* a, Py_ssize_t n) {
   return tuple({o, lse});
 }
 
+// ------------------------------------------------------------------ 4-bit cache
+struct Cache4 {
+  int64_t P, H, page, d;
+  Cache4(const Call& c, const at::Tensor& k, const at::Tensor& v, const at::Tensor& ks, const at::Tensor& vs) {
+    c.want(k, "k_cache", at::kByte, {-1, -1, -1, -1});
+    P = k.size(0);
+    H = k.size(1);
+    page = k.size(2);
+    d = k.size(3) * 2;
+    c.want(v, "v_cache", at::kByte, {P, H, page, d / 2});
+    c.want(ks, "k_scale", at::kBFloat16, {P, H, page, d / 32});
+    c.want(vs, "v_scale", at::kBFloat16, {P, H, page, d / 32});
+  }
+};
+
+PyObject* kv4_append(PyObject* const* a, Py_ssize_t n) {
+  count_args(n, 7);
+  const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &slots = tensor(a[2], "slots"),
+                   &kc = tensor(a[3], "k_cache"), &vc = tensor(a[4], "v_cache"), &ks = tensor(a[5], "k_scale"),
+                   &vs = tensor(a[6], "v_scale");
+  const Call c(k, "k");
+  const Cache4 m(c, kc, vc, ks, vs);
+  const attn_dtype_t dt = dtype16(k, "k");
+  const int64_t T = k.dim() ? k.size(0) : 0;
+  const int64_t k_st = c.packed(k, "k", k.scalar_type(), T, m.H, m.d), v_st = c.packed(v, "v", k.scalar_type(), T, m.H, m.d);
+  c.want(slots, "slots", at::kLong, {T});
+  c10::cuda::CUDAGuard guard(c.dev);
+  check(attn_kv4_append(ptr<void>(k), ptr<void>(v), k_st, v_st, ptr<int64_t>(slots), T, narrow(m.H, "H"),
+                        narrow(m.d, "d"), ptr<uint8_t>(kc), ptr<uint8_t>(vc), ptr<uint16_t>(ks), ptr<uint16_t>(vs),
+                        narrow(m.P, "P"), narrow(m.page, "page"), dt, c.stream()));
+  Py_RETURN_NONE;
+}
+
+// ------------------------------------------------------------------ reading back
+template <int BITS>
+PyObject* kv_read(PyObject* const* a, Py_ssize_t n) {
+  count_args(n, 11);
+  const at::Tensor &kc = tensor(a[0], "k_cache"), &vc = tensor(a[1], "v_cache"), &ks = tensor(a[2], "k_scale"),
+                   &vs = tensor(a[3], "v_scale"), &table = tensor(a[4], "block_table"), &lens = tensor(a[5], "lens"),
+                   &cu = tensor(a[6], "cu");
+  const Call c(kc, "k_cache");
+  int64_t P, H, page, d;
+  if constexpr (BITS == 8) {
+    const Cache m(c, kc, vc, ks, vs);
+    P = m.P, H = m.H, page = m.page, d = m.d;
+  } else {
+    const Cache4 m(c, kc, vc, ks, vs);
+    P = m.P, H = m.H, page = m.page, d = m.d;
+  }
+  c.want(lens, "lens", at::kInt, {-1});
+  const int64_t B = lens.size(0), T = whole(a[7]);
+  c.want(table, "block_table", at::kInt, {B, -1});
+  c.want(cu, "cu", at::kInt, {B + 1});
+  if (T < 0) refuse("total must not be negative");
+  const int64_t code = whole(a[8]);
+  const at::ScalarType type = code == ATTN_BF16 ? at::kBFloat16 : at::kHalf;
+  c10::cuda::CUDAGuard guard(c.dev);
+  const at::Tensor k = a[9] != Py_None ? tensor(a[9], "k") : c.empty({T, H, d}, type);
+  const at::Tensor v = a[10] != Py_None ? tensor(a[10], "v") : c.empty({T, H, d}, type);
+  c.want(k, "k", type, {T, H, d});
+  c.want(v, "v", type, {T, H, d});
+  const int b = narrow(B, "B"), h = narrow(H, "H"), dd = narrow(d, "d"), pp = narrow(P, "P"), pg = narrow(page, "page"),
+            width = narrow(table.size(1), "width");
+  check(attn_kv_read(ptr<uint8_t>(kc), ptr<uint8_t>(vc), ks.data_ptr(), vs.data_ptr(), ptr<int>(table), ptr<int>(lens),
+                     ptr<int>(cu), ptr<void>(k), ptr<void>(v), b, T, h, dd, pp, pg, width, BITS, (attn_dtype_t)code,
+                     c.stream()));
+  return tuple({k, v});
+}
+
 // ------------------------------------------------------------------ packed batches
 struct Packed {
   int64_t B, Tq, Tk, Hq, Hkv, d, qs, ks, vs;
@@ -387,6 +456,8 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(&entry<f>)), METH_FASTCALL
 PyMethodDef methods[] = {{"pages_extend", FAST(pages_extend), nullptr}, {"pages_release", FAST(pages_release), nullptr},
                          {"kv8_append", FAST(kv8_append), nullptr},     {"kv8_decode", FAST(kv8_decode), nullptr},
+                         {"kv4_append", FAST(kv4_append), nullptr},     {"kv4_read", FAST(kv_read<4>), nullptr},
+                         {"kv8_read", FAST(kv_read<8>), nullptr},
                          {"varlen_fwd", FAST(varlen_fwd), nullptr},     {"varlen_bwd", FAST(varlen_bwd), nullptr},
                          {"set_error", set_error, METH_O, nullptr},     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "attn_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -8,7 +8,8 @@
 //
 // attn_kv8_append_kernel   rounds new keys and values into their slots.
 // attn_kv8_split_kernel    O = softmax(s q K^T) V over the cache, split.
-// attn_kv8_merge_kernel    joins the parts of a split (request, head).
+// attn_kv_merge_kernel     joins the parts of a split (request, head), of this cache
+//                          and of the one in 4 bits.
 //
 // Decoding streams the codes once, 2 d bytes a key and head, and is bound by
 // HBM.  The codes go from TMA to shared memory to the tensor core as they
@@ -56,6 +57,7 @@
 #include <cuda_fp16.h>
 
 #include "kernels.h"
+#include "kv_split.cuh"
 #include "sm103_ptx.cuh"
 
 namespace attn {
@@ -254,67 +256,8 @@ struct Kv8Layout {
   static_assert(kBar % 8 == 0 && kStart % 8 == 0 && kScan % 8 == 0, "alignment");
 };
 
-// What a segment (a request's tiles of one head group) costs besides its tiles,
-// in tiles: its query terms, the first S and the last O^T, during which nothing
-// else of the CTA runs.  Units are counted with it, tile t of a segment being
-// unit kSegCost + t, so that a CTA with many short requests gets fewer tiles (64
-// ragged requests: 65, 53, 52, 53 us with a cost of 0 to 3).
-constexpr int kSegCost = 2;
-
-__device__ __forceinline__ int seg_units(int nt) { return nt > 0 ? nt + kSegCost : 0; }
-
-// The units are dealt to min(grid, units) CTAs, so that none of those has an
-// empty range (the merge kernel reads a part from each CTA of a segment).
-__host__ __device__ inline long long range_start(long long c, long long units, long long grid) { return c * units / grid; }
-// The CTA whose range holds unit u.
-__device__ __forceinline__ long long range_owner(long long u, long long units, long long grid) {
-  return ((u + 1) * grid - 1) / units;
-}
-
-__device__ __forceinline__ int kv8_len(const Kv8DecArgs& p, int b) {
-  const long long cap = (long long)p.width << p.page_shift;
-  return (int)min(max((long long)p.lens[b], 0ll), cap);
-}
-
-// Walks the (request, head, row block) segments of a CTA's range: `left` units
-// from unit v of segment (b, hr) on.
-struct Walk {
-  int b, hr, v;
-  long long left;
-};
-// The next segment of which the range holds tiles [t0, t1); false at the end.
-struct Seg {
-  int b, hr, len, nt, t0, t1;
-};
-__device__ __forceinline__ bool next_seg(const Kv8DecArgs& p, int Hr, Walk& w, Seg& s) {
-  while (w.left > 0) {
-    s.len = kv8_len(p, w.b);
-    s.nt = (s.len + 127) >> 7;
-    const int n = seg_units(s.nt);
-    if (n == 0) {  // (a request without tokens has no units)
-      ++w.b;
-      w.hr = 0;
-      w.v = 0;
-      continue;
-    }
-    const int end = (int)min((long long)n, w.v + w.left);
-    s.b = w.b;
-    s.hr = w.hr;
-    s.t0 = max(0, w.v - kSegCost);
-    s.t1 = max(0, end - kSegCost);
-    w.left -= end - w.v;
-    w.v = 0;
-    if (++w.hr == Hr) {
-      w.hr = 0;
-      ++w.b;
-    }
-    if (s.t0 < s.t1) return true;
-  }
-  return false;
-}
-
 template <int D, int RP, int NP>
-__global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn_kv8_split_kernel(const __grid_constant__ Kv8DecArgs p) {
+__global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn_kv8_split_kernel(const __grid_constant__ KvDecArgs p) {
   using L = Kv8Layout<D, RP, NP>;
   constexpr bool BF16 = NP == 2;
   constexpr int N = L::N;
@@ -348,66 +291,13 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
     tmem_relinquish();
   }
   griddep_wait();
-  // The CTA's range of tiles [u0, u1) and where it starts: every thread sums
-  // the tiles of a run of requests, a scan finds the thread whose run holds u0.
-  {
-    long long* wsum = reinterpret_cast<long long*>(sbase + L::kScan);
-    const int per = (p.B + kDecThreads - 1) / kDecThreads;
-    const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seg_units((kv8_len(p, b) + 127) >> 7);
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long a = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += a;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    long long before = inc - mine, total = 0;
-    for (int w = 0; w < kDecThreads / 32; ++w) {
-      if (w < warp) before += wsum[w];
-      total += wsum[w];
-    }
-    const long long units = total * Hr;
-    const long long n_cta = min((long long)p.grid, units);
-    const bool has = blockIdx.x < n_cta;
-    const long long u0 = has ? range_start(blockIdx.x, units, n_cta) : 0;
-    const long long u1 = has ? range_start(blockIdx.x + 1ll, units, n_cta) : 0;
-    long long* st = reinterpret_cast<long long*>(sbase + L::kStart);
-    if (threadIdx.x == 0) {
-      st[0] = u0;
-      st[1] = u1;
-    }
-    if (u0 < u1 && before * Hr <= u0 && u0 < (before + mine) * Hr) {
-      long long at = before;
-      for (int b = b0; b < b1; ++b) {
-        const int n = seg_units((kv8_len(p, b) + 127) >> 7);
-        if (u0 < (at + n) * Hr) {
-          const long long in = u0 - at * Hr;
-          int* w = reinterpret_cast<int*>(st + 2);
-          w[0] = b;
-          w[1] = (int)(in / n);
-          w[2] = (int)(in % n);
-          break;
-        }
-        at += n;
-      }
-    }
-  }
+  deal_range<7, kDecThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
+                             reinterpret_cast<long long*>(sbase + L::kStart));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sbase + L::kTmemSlot);
-  Walk w0;
-  {
-    const long long* st = reinterpret_cast<const long long*>(sbase + L::kStart);
-    const int* w = reinterpret_cast<const int*>(st + 2);
-    w0.left = st[1] - st[0];
-    w0.b = w[0];
-    w0.hr = w[1];
-    w0.v = w[2];
-  }
+  const Walk w0 = first_walk(reinterpret_cast<const long long*>(sbase + L::kStart));
   const int page_rows = 1 << p.page_shift;
   const int tile_pages = 128 >> p.page_shift;
 
@@ -420,7 +310,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
       bool ok = true;
       Walk w = w0;
       Seg sg;
-      while (ok && next_seg(p, Hr, w, sg)) {
+      while (ok && next_seg<7>(p, Hr, w, sg)) {
         const int len = sg.len;
         const int h = sg.hr / p.n_rb;
         const int pages = (len + page_rows - 1) >> p.page_shift;
@@ -502,7 +392,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
     int g = 0, seg = 0;
     Walk w = w0;
     Seg sg;
-    while (ok && next_seg(p, Hr, w, sg)) {
+    while (ok && next_seg<7>(p, Hr, w, sg)) {
       const int cnt = sg.t1 - sg.t0;
       ok = wt(L::kBarQFull, seg & 1) && wt(L::kBarKFull + g % L::kStages, (g / L::kStages) & 1);
       if (!ok) break;
@@ -540,7 +430,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
     int g = 0, seg = 0;
     Walk w = w0;
     Seg sg;
-    while (ok && next_seg(p, Hr, w, sg)) {
+    while (ok && next_seg<7>(p, Hr, w, sg)) {
       const int len = sg.len;
       const int h = sg.hr / p.n_rb, rb = sg.hr % p.n_rb;
       // ---- the q terms of the row block: eight lanes to a row
@@ -806,8 +696,8 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
 // warp per row, four rows of a segment at a time, p.merge_run times (many rows: most
 // segments are one CTA's, and their blocks only find that out).  Always in the same
 // order.
-template <int D, bool BF16, int WPR>
-__global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_constant__ Kv8DecArgs p) {
+template <int D, bool BF16, int WPR, int TS>
+__global__ void __launch_bounds__(128) attn_kv_merge_kernel(const __grid_constant__ KvDecArgs p) {
   __shared__ long long sums[4][2];
   __shared__ float xo[4][D];
   __shared__ float xml[4][2];
@@ -822,7 +712,7 @@ __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_consta
   int b = (int)(first / n_in / (unsigned)Hr);
   long long before = 0, total = 0;
   for (int i = threadIdx.x; i < p.B; i += 128) {
-    const int n = seg_units((kv8_len(p, i) + 127) >> 7);
+    const int n = seg_units(kv_tiles<TS>(kv_len(p, i)));
     total += n;
     if (i < b) before += n;
   }
@@ -839,12 +729,12 @@ __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_consta
   before = sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0];
   total = sums[0][1] + sums[1][1] + sums[2][1] + sums[3][1];
   const long long units = total * Hr, n_cta = min((long long)p.grid, units);
-  int nt = (kv8_len(p, b) + 127) >> 7;
+  int nt = kv_tiles<TS>(kv_len(p, b));
   for (unsigned unit = first; unit < min(first + run, units_all); ++unit) {
     const unsigned blk = unit / n_in;  // (b, head, row block)
     if ((int)(blk / (unsigned)Hr) != b) {
       before += seg_units(nt);
-      nt = (kv8_len(p, ++b) + 127) >> 7;
+      nt = kv_tiles<TS>(kv_len(p, ++b));
     }
     const int hr = (int)(blk - (unsigned)b * Hr);
     const int h = hr / p.n_rb, rb = hr - h * p.n_rb;
@@ -936,7 +826,7 @@ __global__ void __launch_bounds__(128) attn_kv8_merge_kernel(const __grid_consta
 }
 
 template <int D, int RP, int NP>
-cudaError_t launch_split_t(const Kv8DecArgs& a, cudaStream_t stream) {
+cudaError_t launch_split_t(const KvDecArgs& a, cudaStream_t stream) {
   using L = Kv8Layout<D, RP, NP>;
   auto* k = attn_kv8_split_kernel<D, RP, NP>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
@@ -945,7 +835,7 @@ cudaError_t launch_split_t(const Kv8DecArgs& a, cudaStream_t stream) {
 }
 
 template <int D, int RP>
-cudaError_t launch_split_n(const Kv8DecArgs& a, cudaStream_t stream) {
+cudaError_t launch_split_n(const KvDecArgs& a, cudaStream_t stream) {
   return a.bf16 ? launch_split_t<D, RP, 2>(a, stream) : launch_split_t<D, RP, 3>(a, stream);
 }
 
@@ -957,12 +847,12 @@ int kv8_rows(int R) { return R <= 4 ? 4 : (R <= 8 ? 8 : 16); }
 // All CTAs resident at once, no more than there can be tiles.
 int kv8_grid(int rp, int sms, long long max_units) {
   long long g = (rp <= 4 ? 3ll : 2ll) * sms;
-  if (g > kKv8MaxCtas) g = kKv8MaxCtas;
+  if (g > kKvMaxCtas) g = kKvMaxCtas;
   if (g > max_units) g = max_units;
   return (int)(g < 1 ? 1 : g);
 }
 
-cudaError_t launch_kv8_split(const Kv8DecArgs& a, cudaStream_t stream) {
+cudaError_t launch_kv8_split(const KvDecArgs& a, cudaStream_t stream) {
   if (a.d == 128)
     return a.rp == 4 ? launch_split_n<128, 4>(a, stream)
                      : (a.rp == 8 ? launch_split_n<128, 8>(a, stream) : launch_split_n<128, 16>(a, stream));
@@ -972,24 +862,25 @@ cudaError_t launch_kv8_split(const Kv8DecArgs& a, cudaStream_t stream) {
 
 constexpr long long kMergeBlocks = 2 * 8 * kSms;  // two waves of eight blocks to an SM
 
-template <int D, bool BF16>
-static cudaError_t launch_merge_t(Kv8DecArgs a, cudaStream_t stream) {
+template <int D, bool BF16, int TS>
+static cudaError_t launch_merge_t(KvDecArgs a, cudaStream_t stream) {
   const long long segs = (long long)a.B * a.H * a.n_rb;
   // parts of a segment: about a.grid / segs + 1 (64 requests of 8 heads: 51 us with a
   // warp per row, 52 with a block; 17 requests of 2 heads and 3 row blocks: 20 and 19)
   if (a.grid >= 2 * segs)
-    return launch_pdl(attn_kv8_merge_kernel<D, BF16, 4>, (unsigned)(segs * a.rp), 128, 0, stream, a);
+    return launch_pdl(attn_kv_merge_kernel<D, BF16, 4, TS>, (unsigned)(segs * a.rp), 128, 0, stream, a);
   // Every block sums all the lengths, so with many rows a block takes several, two
   // waves of blocks in all (4096 requests of 30 to 60 tokens, 8 heads: the merge 43 us, 127
   // with a block for every four rows).
   const long long rows4 = segs * ((a.rp + 3) / 4);
   a.merge_run = (int)((rows4 + kMergeBlocks - 1) / kMergeBlocks);
-  return launch_pdl(attn_kv8_merge_kernel<D, BF16, 1>, (unsigned)((rows4 + a.merge_run - 1) / a.merge_run), 128, 0, stream, a);
+  return launch_pdl(attn_kv_merge_kernel<D, BF16, 1, TS>, (unsigned)((rows4 + a.merge_run - 1) / a.merge_run), 128, 0, stream, a);
 }
 
-cudaError_t launch_kv8_merge(const Kv8DecArgs& a, cudaStream_t stream) {
-  if (a.d == 128) return a.bf16 ? launch_merge_t<128, true>(a, stream) : launch_merge_t<128, false>(a, stream);
-  return a.bf16 ? launch_merge_t<64, true>(a, stream) : launch_merge_t<64, false>(a, stream);
+cudaError_t launch_kv_merge(const KvDecArgs& a, cudaStream_t stream) {
+  if (a.d == 128) return a.bf16 ? launch_merge_t<128, true, 7>(a, stream) : launch_merge_t<128, false, 7>(a, stream);
+  if (a.tile_shift == 8) return a.bf16 ? launch_merge_t<64, true, 8>(a, stream) : launch_merge_t<64, false, 8>(a, stream);
+  return a.bf16 ? launch_merge_t<64, true, 7>(a, stream) : launch_merge_t<64, false, 7>(a, stream);
 }
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int sms, cudaStream_t stream) {

@@ -14,7 +14,8 @@ namespace attn {
 enum KernelId {
   kKFwd = 0, kKBwdPre = 1, kKBwdMain = 2, kKDqPost = 3, kKDecSplit = 4, kKDecMerge = 5,
   kKPagesExtend = 6, kKPagesRelease = 7, kKKv8Append = 8, kKKv8Split = 9, kKKv8Merge = 10, kKVarMerge = 11,
-  kKNum = 12
+  kKKv4Append = 12, kKKv4Split = 13, kKKv4Merge = 14, kKKvRead = 15,
+  kKNum = 16
 };
 
 struct WaitCtlHost {
@@ -210,22 +211,25 @@ struct Kv8AppendArgs {
 };
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int sms, cudaStream_t stream);
 
-constexpr int kKv8MaxCtas = 640;  // workspace bound of the decode grid
-struct Kv8DecArgs {
-  CUtensorMap tm_k, tm_v;  // (d, page, P * H), one page of one head a box
-  const void* q;           // [B, Nq, Hq, d]
+constexpr int kKvMaxCtas = 640;  // workspace bound of the decode grids
+// Decoding from a paged cache, in 8 bits or in 4.
+struct KvDecArgs {
+  CUtensorMap tm_k, tm_v;    // one page of one head a box: (d, page, P * H), in 4 bits (128, page * d / 128, P * H)
+  CUtensorMap tm_ks, tm_vs;  // 4 bits: scales of 128 channels as one element, (page * d / 128, P * H)
+  const void* q;             // [B, Nq, Hq, d]
   void* o;
-  float* lse;              // [B, Hq, Nq]
-  const float* k_scale;
+  float* lse;                // [B, Hq, Nq]
+  const float* k_scale;      // 8 bits: [P][H]
   const float* v_scale;
-  const int* table;        // [B][width]
-  const int* lens;         // [B]
-  float* ws_o;             // [CTA][2][rows][d]
-  float* ws_ml;            // [CTA][2][rows][2]
+  const int* table;          // [B][width]
+  const int* lens;           // [B]
+  float* ws_o;               // [CTA][2][rows][d]
+  float* ws_ml;              // [CTA][2][rows][2]
   int B, Nq, Hq, H, G, d, width, page_shift, P;
-  int rp, n_rb;            // rows of a row block, row blocks
+  int rp, n_rb;              // rows of a row block, row blocks
+  int tile_shift;            // a tile is 2^tile_shift tokens
   int grid;
-  int merge_run;           // groups of four rows to a block of the merge: the launcher's choice
+  int merge_run;             // groups of four rows to a block of the merge: the launcher's choice
   int causal, bf16;
   float scale;
   int debug_flags;
@@ -234,8 +238,46 @@ struct Kv8DecArgs {
 // Rows of one row block for R = Nq * Hq / H query rows of a key head.
 int kv8_rows(int R);
 int kv8_grid(int rp, int sms, long long max_units);
-cudaError_t launch_kv8_split(const Kv8DecArgs& a, cudaStream_t stream);
-cudaError_t launch_kv8_merge(const Kv8DecArgs& a, cudaStream_t stream);
+cudaError_t launch_kv8_split(const KvDecArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_merge(const KvDecArgs& a, cudaStream_t stream);
+
+// Cache in 4 bits (attn_kv4.cu): codes [P][H][page][d / 2], two to a byte, scales
+// bf16 [P][H][page][d / 32].
+struct Kv4AppendArgs {
+  const void* x[2];         // new keys, values: token stride x_stride elements, heads d apart
+  uint8_t* cache[2];
+  uint16_t* scale[2];
+  const long long* slots;   // [T]
+  long long x_stride[2];
+  long long T, n_slots;     // n_slots = P * page
+  int H, d, page_shift, bf16;
+  int tok;                  // tokens of a block
+  uint32_t h_magic;         // row / H of a block's (token, head) rows is row * h_magic >> 31
+};
+// Tokens of a block, `tok` if its (token, head) rows stay below 2^15: there the product with
+// ceil(2^31 / H) divides them by H.
+template <typename Args>
+void kv_rows(Args* a, long long tok) {
+  if (tok * a->H > 32767) tok = 32767 / a->H;
+  a->tok = tok < 1 ? 1 : (int)tok;
+  a->h_magic = a->tok == 1 ? 0 : (uint32_t)(((1ull << 31) + a->H - 1) / a->H);
+}
+cudaError_t launch_kv4_append(Kv4AppendArgs a, int sms, cudaStream_t stream);
+
+// Cached keys and values as packed 16-bit rows (attn_kvread.cu).
+struct KvReadArgs {
+  const uint8_t* cache[2];
+  const void* scale[2];     // fp32 [P][H] (8 bits) or bf16 [P][H][page][d / 32] (4 bits)
+  void* out[2];             // [T][H][d]
+  const int* table;         // [B][width]
+  const int* lens;          // [B]
+  const int* cu;            // [B + 1]
+  long long T;
+  int B, H, d, P, page_shift, width, bf16, bits;
+  int tok;                  // tokens of a block
+  uint32_t h_magic;         // as above
+};
+cudaError_t launch_kv_read(KvReadArgs a, int sms, cudaStream_t stream);
 
 // Id of the calling thread's current CUDA context (unique for the life of
 // the process, unlike the CUcontext handle, which a new context may reuse).

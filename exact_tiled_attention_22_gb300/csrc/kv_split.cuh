@@ -1,0 +1,139 @@
+// kv_split.cuh -- how decoding from a paged cache deals its work to the CTAs:
+// shared by the cache in 8 bits (attn_kv8.cu) and in 4 bits (attn_kv4.cu), whose
+// parts one merge kernel joins.
+//
+// All tiles (2^TS tokens of one head group of one request) are numbered and every
+// CTA takes an equal consecutive range, whatever the lengths are; the range may
+// begin and end inside a (request, head), whose parts then meet in the merge
+// kernel.
+#pragma once
+
+#include "kernels.h"
+
+namespace attn {
+namespace {
+
+// What a segment (a request's tiles of one head group) costs besides its tiles,
+// in tiles: its query terms, the first S and the last O^T, during which nothing
+// else of the CTA runs.  Units are counted with it, tile t of a segment being
+// unit kSegCost + t, so that a CTA with many short requests gets fewer tiles (64
+// ragged requests: 65, 53, 52, 53 us with a cost of 0 to 3).
+constexpr int kSegCost = 2;
+
+__device__ __forceinline__ int seg_units(int nt) { return nt > 0 ? nt + kSegCost : 0; }
+
+// The units are dealt to min(grid, units) CTAs, so that none of those has an
+// empty range (the merge kernel reads a part from each CTA of a segment).
+__host__ __device__ inline long long range_start(long long c, long long units, long long grid) { return c * units / grid; }
+// The CTA whose range holds unit u.
+__device__ __forceinline__ long long range_owner(long long u, long long units, long long grid) {
+  return ((u + 1) * grid - 1) / units;
+}
+
+__device__ __forceinline__ int kv_len(const KvDecArgs& p, int b) {
+  const long long cap = (long long)p.width << p.page_shift;
+  return (int)min(max((long long)p.lens[b], 0ll), cap);
+}
+
+// Tiles of a request of `len` tokens.
+template <int TS>
+__device__ __forceinline__ int kv_tiles(int len) { return (len + (1 << TS) - 1) >> TS; }
+
+// Walks the (request, head, row block) segments of a CTA's range: `left` units
+// from unit v of segment (b, hr) on.
+struct Walk {
+  int b, hr, v;
+  long long left;
+};
+// The next segment of which the range holds tiles [t0, t1); false at the end.
+struct Seg {
+  int b, hr, len, nt, t0, t1;
+};
+template <int TS>
+__device__ __forceinline__ bool next_seg(const KvDecArgs& p, int Hr, Walk& w, Seg& s) {
+  while (w.left > 0) {
+    s.len = kv_len(p, w.b);
+    s.nt = kv_tiles<TS>(s.len);
+    const int n = seg_units(s.nt);
+    if (n == 0) {  // (a request without tokens has no units)
+      ++w.b;
+      w.hr = 0;
+      w.v = 0;
+      continue;
+    }
+    const int end = (int)min((long long)n, w.v + w.left);
+    s.b = w.b;
+    s.hr = w.hr;
+    s.t0 = max(0, w.v - kSegCost);
+    s.t1 = max(0, end - kSegCost);
+    w.left -= end - w.v;
+    w.v = 0;
+    if (++w.hr == Hr) {
+      w.hr = 0;
+      ++w.b;
+    }
+    if (s.t0 < s.t1) return true;
+  }
+  return false;
+}
+
+// The CTA's range of units [u0, u1) and where it starts: every thread sums the units
+// of a run of requests, a scan finds the thread whose run holds u0.  wsum: [THREADS / 32]
+// and st: [4] in shared memory; st is valid behind the caller's next barrier.
+template <int TS, int THREADS>
+__device__ __forceinline__ void deal_range(const KvDecArgs& p, int Hr, long long* wsum, long long* st) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (p.B + THREADS - 1) / THREADS;
+  const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += seg_units(kv_tiles<TS>(kv_len(p, b)));
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += a;
+  }
+  if (lane == 31) wsum[warp] = inc;
+  __syncthreads();
+  long long before = inc - mine, total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += wsum[w];
+    total += wsum[w];
+  }
+  const long long units = total * Hr;
+  const long long n_cta = min((long long)p.grid, units);
+  const bool has = blockIdx.x < n_cta;
+  const long long u0 = has ? range_start(blockIdx.x, units, n_cta) : 0;
+  const long long u1 = has ? range_start(blockIdx.x + 1ll, units, n_cta) : 0;
+  if (threadIdx.x == 0) {
+    st[0] = u0;
+    st[1] = u1;
+  }
+  if (u0 < u1 && before * Hr <= u0 && u0 < (before + mine) * Hr) {
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int n = seg_units(kv_tiles<TS>(kv_len(p, b)));
+      if (u0 < (at + n) * Hr) {
+        const long long in = u0 - at * Hr;
+        int* w = reinterpret_cast<int*>(st + 2);
+        w[0] = b;
+        w[1] = (int)(in / n);
+        w[2] = (int)(in % n);
+        break;
+      }
+      at += n;
+    }
+  }
+}
+__device__ __forceinline__ Walk first_walk(const long long* st) {
+  const int* w = reinterpret_cast<const int*>(st + 2);
+  Walk w0;
+  w0.left = st[1] - st[0];
+  w0.b = w[0];
+  w0.hr = w[1];
+  w0.v = w[2];
+  return w0;
+}
+
+}  // namespace
+}  // namespace attn

@@ -470,10 +470,44 @@ __device__ __forceinline__ float2 unpack_e4m3(uint32_t w) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
+// Two fp32 values to e2m1 (RNE, saturating at +-6): `lo` in bits 0-3, `hi` in
+// bits 4-7.
+__device__ __forceinline__ uint32_t pack_e2m1(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b, z;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
+      "mov.b32 {z, _, _, _}, 0;\n\t"
+      "mov.b32 %0, {b, z, z, z};\n\t}"
+      : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Eight e2m1 values, four bits each from bit 0 up, as fp16 pairs (exact).
+__device__ __forceinline__ void unpack_e2m1(uint32_t w, uint32_t h[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+
 // Maximum of v over the warp's lanes (NaN ignored unless every lane has one).
 __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// pack2 with values beyond the type's largest brought to it (NaN stays one).
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2_sat(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16) {
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  } else {
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  }
   return r;
 }
 

@@ -472,6 +472,44 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
                     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The same paged cache in 4 bits: k_cache, v_cache : [P, H, page, d / 2] bytes, two
+ * e2m1 codes each (channel 2 i in the low half of byte i; a code is sign, two bits of
+ * exponent, one of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), and
+ * k_scale, v_scale : bf16 [P, H, page, d / 32], a scale for every 32 channels of a
+ * token and head: a cached key is scale * code.  Block tables, lengths and slots are those of
+ * the cache in 8 bits.  The caches are 32-byte, the scales 16-byte aligned; P * H < 2^31,
+ * H * d < 2^32.  (The pages that the survey covers name no cache of fewer bits; formats and
+ * rules are an addition of this library.)
+ *
+ * attn_kv4_append -- rounds T new keys and values into their slots.
+ *   k, v, strides, slots : as attn_kv8_append; slots may come in any order.  A slot that
+ *   stands in the list twice holds a mixture of its tokens.
+ * s = max |x| / 6 over the 32 channels, rounded to bf16, in [2^-64, 2^60]; codes are x / s
+ * rounded to the nearest, ties to the even code, saturating at 6 (a zero keeps its sign).
+ * A NaN makes its group's scale a NaN: all 32 channels read as NaN.  Other tokens' codes and
+ * scales are left as they are.  T * H < 2^30.
+ *
+ * attn_kv_read -- cached keys and values as packed 16-bit rows, for a prompt that goes on
+ * after a cached prefix (attn_varlen_fwd takes the rows).
+ *   bits : 8 or 4, which cache it is (its layout and scales as above)
+ *   cu   : device int32 [B + 1], ascending: request b has rows cu[b] .. cu[b + 1] - 1
+ *   k, v : [T, H, d] of dtype; row cu[b] + i becomes token i of request b, for i < lens[b] and
+ *          within the request's rows and the T.  All other rows are left as they are, those
+ *          behind the cached tokens of a request among them (its new tokens go there)
+ * Values are scale * code, rounded to nearest even, at most the type's largest (NaN stays
+ * one).  A page id outside [0, P) reads as zeros; lengths are clamped to [0, width * page].
+ * 0 <= T < 2^31, T * H < 2^33, width * page < 2^31.
+ */
+int attn_kv4_append(const void* k, const void* v, long long k_stride, long long v_stride,
+                    const int64_t* slots, long long T, int H, int d, uint8_t* k_cache,
+                    uint8_t* v_cache, uint16_t* k_scale, uint16_t* v_scale, int P, int page,
+                    attn_dtype_t dtype, void* stream);
+int attn_kv_read(const uint8_t* k_cache, const uint8_t* v_cache, const void* k_scale,
+                 const void* v_scale, const int32_t* block_table, const int32_t* lens,
+                 const int32_t* cu, void* k, void* v, int B, long long T, int H, int d, int P,
+                 int page, int width, int bits, attn_dtype_t dtype, void* stream);
+
+/*
  * attn_philox4x32_10 -- diagnostic: the dropout decisions' generator itself.
  * Runs the kernels' Philox4x32-10 (Salmon et al., SC 2011, section 3.2; the
  * generator named under attn_fwd_ex) on n caller-given inputs, one GPU thread
@@ -521,7 +559,8 @@ int attn_set_wait_limit(unsigned long long limit_ns, int debug_flags);
  * (0 forward, 1 backward preprocess, 2 backward main, 3 dQ conversion,
  * 4 decode chunks, 5 decode merge, 6 pages extend, 7 pages release, 8 8-bit
  * append, 9 8-bit decode, 10 its merge, 11 the
- * packed forward's merge),
+ * packed forward's merge, 12 4-bit append, 13 4-bit decode, 14 its merge, 15 reading a
+ * cache back),
  * the number of launches and their summed device time in milliseconds.
  * Returns the number of kernel ids filled, or a negative ATTN_ERR_* code.
  */
