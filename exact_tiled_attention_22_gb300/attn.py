@@ -112,6 +112,10 @@ def _load() -> ctypes.CDLL:
     lib.attn_kv8_decode.restype = i
     lib.attn_kv4_append.argtypes = lib.attn_kv8_append.argtypes
     lib.attn_kv4_append.restype = i
+    lib.attn_kv4_decode_workspace_size.argtypes = [i, i, i, i]
+    lib.attn_kv4_decode_workspace_size.restype = sz
+    lib.attn_kv4_decode.argtypes = lib.attn_kv8_decode.argtypes
+    lib.attn_kv4_decode.restype = i
     lib.attn_kv_read.argtypes = [vp] * 9 + [i, ll] + [i] * 7 + [vp]
     lib.attn_kv_read.restype = i
     lib.attn_varlen_fwd_workspace_size.argtypes = [i, ll, ll, i, i, i]
@@ -338,6 +342,20 @@ def attn_kv4_append(k, v, k_stride, v_stride, slots, T, H, d, k_cache, v_cache, 
                                dtype_code(dtype), _stream(stream))
 
 
+def attn_kv4_decode_workspace_size(Nq, Hq, H, d) -> int:
+    return int(lib.attn_kv4_decode_workspace_size(Nq, Hq, H, d))
+
+
+def attn_kv4_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o, lse, B, Nq, Hq, H,
+                    d, P, page, width, scale, causal, dtype, workspace, workspace_bytes,
+                    stream=None) -> int:
+    return lib.attn_kv4_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                               _ptr(v_scale), _ptr(block_table), _ptr(lens), _ptr(o), _ptr(lse),
+                               B, Nq, Hq, H, d, P, page, width, float(scale), int(bool(causal)),
+                               dtype_code(dtype), _ptr(workspace), int(workspace_bytes),
+                               _stream(stream))
+
+
 def attn_kv_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, cu, k, v, B, T, H, d, P, page,
                  width, bits, dtype, stream=None) -> int:
     return lib.attn_kv_read(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
@@ -556,6 +574,15 @@ def kv4_append(k, v, slots, k_cache, v_cache, k_scale, v_scale):
     (attn_kv4_append).  k and v may be slices of a wider projection (any token
     stride that is a multiple of 8)."""
     _bind().kv4_append(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+
+
+@_on_stream
+def kv4_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=None, causal=True,
+               ws=None):
+    """(o, lse) of q [B, Nq, Hq, d], the last Nq tokens of every request, against
+    the 4-bit cache (attn_kv4_decode); lens counts the Nq tokens."""
+    return _bind().kv4_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale, causal,
+                              ws)
 
 
 @_on_stream

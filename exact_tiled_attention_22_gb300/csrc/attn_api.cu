@@ -854,6 +854,83 @@ int attn_kv4_append(const void* k, const void* v, long long k_stride, long long 
   return e != cudaSuccess ? cuda_fail(e, "attn_kv4_append launch") : ATTN_OK;
 }
 
+size_t attn_kv4_decode_workspace_size(int Nq, int Hq, int H, int d) {
+  if (Nq < 1 || Nq > 128 || H < 1 || Hq < H || Hq % H || Hq / H > (1 << 23) || (d != 64 && d != 128)) return 0;
+  const size_t rows = (size_t)attn::kKvMaxCtas * 2 * attn::kv4_rows(Nq * (Hq / H), true);
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  return up(rows * d * 4) + up(rows * 2 * 4);
+}
+
+// A page of one head a box, rows of 128 channels, unpacked by the copy.
+static int encode_pages4(CUtensorMap* m, const void* ptr, long long PH, int page, int d) {
+  const cuuint32_t rows = (cuuint32_t)(page * d / 128);
+  const cuuint64_t dims[3] = {128, rows, (cuuint64_t)PH}, strides[2] = {64, (cuuint64_t)rows * 64};
+  const cuuint32_t box[3] = {128, rows, 1}, estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return ATTN_OK;
+}
+
+int attn_kv4_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cache, const uint16_t* k_scale,
+                    const uint16_t* v_scale, const int32_t* block_table, const int32_t* lens, void* o, float* lse, int B,
+                    int Nq, int Hq, int H, int d, int P, int page, int width, float scale, int causal,
+                    attn_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  t_err.clear();
+  if (!q || !block_table || !lens || !o || !lse) return fail(ATTN_ERR_INVALID, "null pointer argument");
+  int rc = check_cache(k_cache, v_cache, k_scale, v_scale, H, d, P, page, dtype, 4);
+  if (rc) return rc;
+  if (B < 1 || Nq < 1 || Hq < 1 || width < 1) return fail(ATTN_ERR_INVALID, "B, Nq, Hq, width must be >= 1");
+  if (Hq % H) return fail(ATTN_ERR_INVALID, "Hq = %d is no multiple of H = %d", Hq, H);
+  if (Nq > 128) return fail(ATTN_ERR_UNSUPPORTED, "decode takes at most 128 query rows (got %d)", Nq);
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_INVALID, "scale must be finite and > 0");
+  // (the kernels round a length up to whole tiles of 256 tokens in 32 bits)
+  if ((long long)width * page > (1ll << 31) - 256 || (long long)B * Nq * Hq >= (1ll << 31) || Hq / H > (1 << 23))
+    return fail(ATTN_ERR_INVALID, "B * Nq * Hq must be < 2^31, Hq / H at most 2^23, width * page at most 2^31 - 256");
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return fail(ATTN_ERR_ALIGN, "q, o and lse must be 16-byte aligned");
+  if (!aligned4(block_table) || !aligned4(lens)) return fail(ATTN_ERR_ALIGN, "block_table and lens must be 4-byte aligned");
+  const size_t need = attn_kv4_decode_workspace_size(Nq, Hq, H, d);
+  if (!workspace || workspace_bytes < need)
+    return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(ATTN_ERR_ALIGN, "workspace must be 256-byte aligned");
+  const size_t qb = (size_t)B * Nq * Hq * d * 2, cb = code_bytes(P, H, page, d, 4), sb = scale_bytes(P, H, page, d, 4);
+  const Range outs[3] = {rng(o, qb), rng(lse, (size_t)B * Nq * Hq * 4), rng(workspace, need)};
+  const Range ins[7] = {rng(q, qb), rng(k_cache, cb), rng(v_cache, cb), rng(k_scale, sb), rng(v_scale, sb),
+                        rng(block_table, (size_t)B * width * 4), rng(lens, (size_t)B * 4)};
+  if ((rc = check_overlaps(outs, 3, ins, 7))) return rc;
+  DeviceInfo* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  attn::KvDecArgs a;
+  std::memset(&a, 0, sizeof a);
+  if ((rc = encode_pages4(&a.tm_k, k_cache, (long long)P * H, page, d)) ||
+      (rc = encode_pages4(&a.tm_v, v_cache, (long long)P * H, page, d)))
+    return rc;
+  a.q = q; a.o = o; a.lse = lse;
+  a.k_scale16 = k_scale; a.v_scale16 = v_scale; a.table = block_table; a.lens = lens;
+  a.B = B; a.Nq = Nq; a.Hq = Hq; a.H = H; a.G = Hq / H; a.d = d;
+  a.width = width; a.page_shift = page_shift_of(page); a.P = P;
+  const int R = Nq * a.G;
+  a.bf16 = dtype == ATTN_BF16;
+  a.rp = attn::kv4_rows(R, a.bf16);
+  a.n_rb = (R + a.rp - 1) / a.rp;
+  a.tile_shift = d == 128 ? 7 : 8;
+  a.causal = causal ? 1 : 0;
+  a.scale = scale;
+  const long long tile = 1ll << a.tile_shift, tiles = ((long long)width * page + tile - 1) / tile;
+  a.grid = attn::kv4_grid(dev->sms, tiles * B * H * a.n_rb);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.ws_o = reinterpret_cast<float*>(ws);
+  a.ws_ml = reinterpret_cast<float*>(ws + ((size_t)attn::kKvMaxCtas * 2 * a.rp * d * 4 + 255) / 256 * 256);
+  wait_ctl(dev, &a.wait, &a.debug_flags);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = timed(attn::kKKv4Split, s, [&] { return attn::launch_kv4_split(a, s); });
+  if (e != cudaSuccess) return cuda_fail(e, "attn_kv4_decode launch");
+  e = timed(attn::kKKv4Merge, s, [&] { return attn::launch_kv_merge(a, s); });
+  return e != cudaSuccess ? cuda_fail(e, "attn_kv4_decode merge launch") : ATTN_OK;
+}
+
 int attn_kv_read(const uint8_t* k_cache, const uint8_t* v_cache, const void* k_scale, const void* v_scale,
                  const int32_t* block_table, const int32_t* lens, const int32_t* cu, void* k, void* v, int B,
                  long long T, int H, int d, int P, int page, int width, int bits, attn_dtype_t dtype, void* stream) {

@@ -325,6 +325,30 @@ PyObject* kv4_append(PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+PyObject* kv4_decode(PyObject* const* a, Py_ssize_t n) {
+  count_args(n, 10);
+  const at::Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache"),
+                   &ks = tensor(a[3], "k_scale"), &vs = tensor(a[4], "v_scale"), &table = tensor(a[5], "block_table"),
+                   &lens = tensor(a[6], "lens");
+  const Call c(q, "q");
+  const Cache4 m(c, kc, vc, ks, vs);
+  const attn_dtype_t dt = dtype16(q, "q");
+  c.want(q, "q", q.scalar_type(), {-1, -1, -1, m.d});
+  const int64_t B = q.size(0), Nq = q.size(1), Hq = q.size(2);
+  c.want(table, "block_table", at::kInt, {B, -1});
+  c.want(lens, "lens", at::kInt, {B});
+  const float scale = scale_of(a[7], m.d);
+  const int causal = flag(a[8]), nq = narrow(Nq, "Nq"), hq = narrow(Hq, "Hq"), h = narrow(m.H, "H"), d = narrow(m.d, "d");
+  c10::cuda::CUDAGuard guard(c.dev);
+  const at::Tensor o = c.empty({B, Nq, Hq, m.d}, q.scalar_type()), lse = c.empty({B, Hq, Nq}, at::kFloat);
+  const Workspace ws(c, a[9], attn_kv4_decode_workspace_size(nq, hq, h, d));
+  check(attn_kv4_decode(ptr<void>(q), ptr<uint8_t>(kc), ptr<uint8_t>(vc), ptr<uint16_t>(ks), ptr<uint16_t>(vs),
+                        ptr<int>(table), ptr<int>(lens), ptr<void>(o), ptr<float>(lse), narrow(B, "B"), nq, hq, h, d,
+                        narrow(m.P, "P"), narrow(m.page, "page"), narrow(table.size(1), "width"), scale, causal, dt, ws.p,
+                        ws.n, c.stream()));
+  return tuple({o, lse});
+}
+
 // ------------------------------------------------------------------ reading back
 template <int BITS>
 PyObject* kv_read(PyObject* const* a, Py_ssize_t n) {
@@ -456,8 +480,8 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(&entry<f>)), METH_FASTCALL
 PyMethodDef methods[] = {{"pages_extend", FAST(pages_extend), nullptr}, {"pages_release", FAST(pages_release), nullptr},
                          {"kv8_append", FAST(kv8_append), nullptr},     {"kv8_decode", FAST(kv8_decode), nullptr},
-                         {"kv4_append", FAST(kv4_append), nullptr},     {"kv4_read", FAST(kv_read<4>), nullptr},
-                         {"kv8_read", FAST(kv_read<8>), nullptr},
+                         {"kv4_append", FAST(kv4_append), nullptr},     {"kv4_decode", FAST(kv4_decode), nullptr},
+                         {"kv4_read", FAST(kv_read<4>), nullptr},       {"kv8_read", FAST(kv_read<8>), nullptr},
                          {"varlen_fwd", FAST(varlen_fwd), nullptr},     {"varlen_bwd", FAST(varlen_bwd), nullptr},
                          {"set_error", set_error, METH_O, nullptr},     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "attn_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -6,6 +6,8 @@
 // in the cache is ever rounded again.
 //
 // attn_kv4_append_kernel   rounds new keys and values into their slots.
+// attn_kv4_split_kernel    O = softmax(s q K^T) V over the cache, split (joined by
+//                          attn_kv_merge_kernel).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -18,6 +20,9 @@ namespace {
 
 // ------------------------------------------------------------------ append
 constexpr int kAppThreads = 256;
+
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -96,6 +101,605 @@ __global__ void __launch_bounds__(kAppThreads) attn_kv4_append_kernel(const __gr
   if (threadIdx.x == 0) griddep_launch_dependents();
 }
 
+// ------------------------------------------------------------------ decode
+constexpr int kDecThreads = 224;  // warps 0-3 softmax, 4 producer, 5 MMA, 6 scales
+constexpr int kWarpProd = 4, kWarpMma = 5, kWarpScale = 6;
+constexpr uint32_t kWgBar = 1;    // named barrier of the softmax warps
+
+__host__ __device__ constexpr int up1024(int x) { return (x + 1023) / 1024 * 1024; }
+
+// A row is 128 channels: a token (d = 128) or two (d = 64).  A tile is 128 rows.
+template <int D, int RP, int NP>
+struct Kv4Layout {
+  static constexpr int TPR = 128 / D;                 // tokens to a row
+  static constexpr int kTileShift = D == 128 ? 7 : 8; // tokens to a tile
+  static constexpr int NG = RP * NP;                  // operand rows: query rows times terms
+  static constexpr int NS = (NG + 15) / 16 * 16;      // MMA columns of S^T (M = 128 needs a multiple of 16)
+  static constexpr int NO = 4 * NG;                   // of O^T: one set for each group of 32 channels
+  static constexpr int PW = NO <= 32 ? 32 : (NO <= 64 ? 64 : 128);  // bytes of a P row, and its swizzle
+  static constexpr int kCtas = 2;
+  static constexpr int kCode = 128 * 128;             // bytes of a tile's codes: 16 to 16 bytes, 8 of them filled
+  static constexpr int kScl = 128 * 8;                // bytes of its scales: four bf16 a row
+  static constexpr int kStages = PW == 32 ? 3 : 2;
+  static constexpr int kQ = 0;
+  static constexpr int kP = kQ + up1024(NS * 128);
+  static constexpr int kKV = kP + up1024(128 * PW);   // stage s: K codes at + s * 2 kCode, V codes behind them
+  static constexpr int kSc = kKV + kStages * 2 * kCode;   // stage s: K scales at + s * 2 kScl, V scales behind them
+  static constexpr int kNorm = kSc + kStages * 2 * kScl;  // [stages][4] 2^-e, [4] 2^e: powers above the groups' largest V scale
+  static constexpr int kXm = kNorm + kStages * 32;    // [2][4][RP] fp32 row maxima of the warps
+  static constexpr int kXl = kXm + 2 * 4 * RP * 4;    // [4][RP] fp32 row sums
+  static constexpr int kQs = kXl + 4 * RP * 4;        // [RP] fp32 row factors
+  static constexpr int kQi = kQs + RP * 4;            // [RP] int query index of the row
+  static constexpr int kBar = kQi + RP * 4;
+  static constexpr int kBarKFull = 0;
+  static constexpr int kBarVFull = kBarKFull + kStages;
+  static constexpr int kBarNFull = kBarVFull + kStages;
+  static constexpr int kBarEmpty = kBarNFull + kStages;
+  static constexpr int kBarSFull = kBarEmpty + kStages;  // [2]
+  static constexpr int kBarPFull = kBarSFull + 2;
+  static constexpr int kBarOFull = kBarPFull + 1;
+  static constexpr int kBarQFull = kBarOFull + 1;
+  static constexpr int kBarDrain = kBarQFull + 1;
+  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kTmemSlot = kBar + kNumBars * 8;
+  static constexpr int kStart = kTmemSlot + 16;       // start of the CTA's range: long long u0, u1; int b, hr, t
+  static constexpr int kScan = kStart + 32;           // [7] warp sums
+  static constexpr int kBytes = kScan + 8 * 8;
+  static constexpr int kSmem = kBytes + 1024;
+  // TMEM: two buffers of S^T (four groups) and of O^T where 256 columns hold them, else one
+  static constexpr int kBufs = 2 * (4 * NS + NO) <= 256 ? 2 : 1;
+  static constexpr int kCols = kBufs * (4 * NS + NO) <= 128 ? 128 : 256;
+  static constexpr int kColS = 0, kColO = kBufs * 4 * NS;
+  static_assert(kBufs * (4 * NS + NO) <= kCols && kCols * kCtas <= 512, "TMEM budget");
+  static_assert((kSmem + 1024) * kCtas <= 228 * 1024, "shared memory budget");
+  static_assert(NO % 16 == 0 && NO <= PW, "P rows");
+  static_assert(kBar % 8 == 0 && kNorm % 16 == 0 && kXm % 16 == 0 && kStart % 8 == 0, "alignment");
+};
+
+// Descriptor of the MN-major P operand: rows (keys) of PW bytes, PW-byte swizzle, 8-key
+// groups 8 PW bytes apart.
+template <int PW>
+__device__ __forceinline__ uint64_t make_pdesc(uint32_t saddr) {
+  constexpr uint64_t layout = PW == 128 ? 2 : (PW == 64 ? 4 : 6);
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(8 * PW >> 4) << 16) | ((uint64_t)(8 * PW >> 4) << 32) |
+         (1ull << 46) | (layout << 61);
+}
+
+// Byte of 16-byte chunk c in P row k.
+template <int PW>
+__device__ __forceinline__ uint32_t p_off(uint32_t k, uint32_t c) {
+  const uint32_t x = PW == 128 ? (k & 7) : (PW == 64 ? ((k >> 1) & 3) : ((k >> 2) & 1));
+  return k * PW + ((c ^ x) << 4);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+template <int D, int RP, int NP>
+__global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn_kv4_split_kernel(const __grid_constant__ KvDecArgs p) {
+  using L = Kv4Layout<D, RP, NP>;
+  constexpr bool BF16 = NP == 2;
+  constexpr int TPR = L::TPR, TS = L::kTileShift, NB = L::kBufs;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int Hr = p.H * p.n_rb;
+  const WaitCtl wc{p.wait.status, p.wait.limit_ns};
+  auto bar = [&](int i) -> uint32_t { return base + L::kBar + 8u * i; };
+
+  if (warp == kWarpProd && lane == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(bar(L::kBarKFull + s), 1);
+      mbar_init(bar(L::kBarVFull + s), 1);
+      mbar_init(bar(L::kBarNFull + s), 1);
+      mbar_init(bar(L::kBarEmpty + s), 1);
+    }
+    mbar_init(bar(L::kBarSFull), 1);
+    mbar_init(bar(L::kBarSFull + 1), 1);
+    mbar_init(bar(L::kBarPFull), 128);
+    mbar_init(bar(L::kBarOFull), 1);
+    mbar_init(bar(L::kBarQFull), 128);
+    mbar_init(bar(L::kBarDrain), 1);
+    fence_mbar_init();
+    tma_prefetch(&p.tm_k);
+    tma_prefetch(&p.tm_v);
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(base + L::kTmemSlot, L::kCols);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  deal_range<TS, kDecThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
+                              reinterpret_cast<long long*>(sbase + L::kStart));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sbase + L::kTmemSlot);
+  const Walk w0 = first_walk(reinterpret_cast<const long long*>(sbase + L::kStart));
+
+  if (warp == kWarpProd) {
+    // ------------------------------------------------------------ producer
+    // Lane i takes page i of a tile: its id (read a tile ahead), the copies of its
+    // codes and scales.
+    const int tile_pages = 1 << (TS - p.page_shift);
+    const int page_rows = (1 << p.page_shift) / TPR;
+    if (!(p.debug_flags & 16)) {
+      int g = 0;
+      bool ok = true;
+      Walk w = w0;
+      Seg sg;
+      while (ok && next_seg<TS>(p, Hr, w, sg)) {
+        const int h = sg.hr / p.n_rb;
+        const int pages = (sg.len + (1 << p.page_shift) - 1) >> p.page_shift;
+        const int* row = p.table + (size_t)sg.b * p.width;
+        auto page_id = [&](int t) -> int {
+          const int j = t * tile_pages + lane;
+          return lane < tile_pages && j < pages ? row[j] : -1;
+        };
+        int id = page_id(sg.t0);
+        for (int t = sg.t0; t < sg.t1; ++t, ++g) {
+          const int here = id;
+          const int n_here = min(tile_pages, pages - t * tile_pages);
+          if (t + 1 < sg.t1) id = page_id(t + 1);
+          const int s = g % L::kStages;
+          const uint32_t ph = (g / L::kStages) & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarEmpty + s), ph ^ 1, wc));
+          if (!ok) break;
+          const uint32_t k = base + L::kKV + s * 2 * L::kCode + lane * page_rows * 128;
+          const uint32_t sc = L::kSc + s * 2 * L::kScl + lane * page_rows * 8;
+          // (a page id outside the cache reads as zeros: its copies fill with them, its scales are written)
+          const bool in = lane < n_here && here >= 0 && here < p.P;
+          const uint32_t n_in = __popc(__ballot_sync(0xffffffffu, in));
+          if (!in && lane < n_here) {
+            for (int i = 0; i < page_rows * 8; i += 16) {
+              *reinterpret_cast<uint4*>(sbase + sc + i) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(sbase + sc + L::kScl + i) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) {  // (a row of codes counts as its 64 bytes in memory)
+            mbar_expect_tx(bar(L::kBarKFull + s), (n_here * 64 + n_in * 16) * page_rows);
+            mbar_expect_tx(bar(L::kBarVFull + s), n_here * 64 * page_rows);
+          }
+          __syncwarp();
+          if (lane < n_here) {
+            const int ph2 = in ? here * p.H + h : -1;
+            tma_load_3d(k, &p.tm_k, bar(L::kBarKFull + s), 0, 0, ph2);
+            if (in) {
+              const size_t at = (size_t)ph2 * page_rows * 4;
+              bulk_load(base + sc, p.k_scale16 + at, page_rows * 8, bar(L::kBarKFull + s));
+              bulk_load(base + sc + L::kScl, p.v_scale16 + at, page_rows * 8, bar(L::kBarKFull + s));
+            }
+            tma_load_3d(k + L::kCode, &p.tm_v, bar(L::kBarVFull + s), 0, 0, ph2);
+          }
+        }
+      }
+      if (!ok) {
+        for (int i = max(0, g - L::kStages); i < g; ++i) {
+          mbar_wait_drain(bar(L::kBarKFull + i % L::kStages), (i / L::kStages) & 1, wc.limit_ns);
+          mbar_wait_drain(bar(L::kBarVFull + i % L::kStages), (i / L::kStages) & 1, wc.limit_ns);
+        }
+      }
+    }
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------------ MMA warp
+    constexpr uint32_t idesc_s = make_idesc_e2m1_e4m3(128, L::NS, false, false);
+    constexpr uint32_t idesc_o = make_idesc_e2m1_e4m3(128, L::NO, true, true);
+    auto wt = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, wc)); };
+    auto kaddr = [&](int g) { return base + L::kKV + (g % L::kStages) * 2 * L::kCode; };
+    auto issue_s = [&](int g) {  // S^T = K (q terms)^T, the four groups of 32 channels apart
+      const uint32_t k = kaddr(g), d_t = tmem + L::kColS + (g % NB) * 4 * L::NS;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        mma_ss_f8(d_t + ks * L::NS, make_sdesc(k + ks * 32, 16, 1024), make_sdesc(base + L::kQ + ks * 32, 16, 1024),
+                  idesc_s, 0);
+      tc_commit(bar(L::kBarSFull + (g & 1)));
+    };
+    auto issue_o = [&](int g) {  // O^T = V^T (p terms)^T over the tile's rows
+      const uint32_t v = kaddr(g) + L::kCode, d_t = tmem + L::kColO + (g % NB) * L::NO;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        mma_ss_f8(d_t, make_sdesc(v + ks * 32 * 128, 16, 1024), make_pdesc<L::PW>(base + L::kP + ks * 32 * L::PW), idesc_o,
+                  ks > 0);
+      tc_commit(bar(L::kBarEmpty + g % L::kStages));
+      tc_commit(bar(L::kBarOFull));
+    };
+    bool ok = true;
+    int g = 0, seg = 0;
+    Walk w = w0;
+    Seg sg;
+    while (ok && next_seg<TS>(p, Hr, w, sg)) {
+      const int cnt = sg.t1 - sg.t0;
+      ok = wt(L::kBarQFull, seg & 1) && wt(L::kBarKFull + g % L::kStages, (g / L::kStages) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      issue_s(g);
+      for (int i = 0; i < cnt; ++i, ++g) {
+        auto next_s = [&] {
+          if (i + 1 < cnt) {
+            ok = wt(L::kBarKFull + (g + 1) % L::kStages, ((g + 1) / L::kStages) & 1);
+            if (!ok) return;
+            tc_fence_after();
+            issue_s(g + 1);
+          }
+        };
+        if (NB == 2) next_s();  // (with one buffer S of this tile has to be read first: P says so)
+        if (!ok) break;
+        ok = wt(L::kBarPFull, g & 1) && wt(L::kBarVFull + g % L::kStages, (g / L::kStages) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        issue_o(g);
+        if (NB == 1) next_s();
+        if (!ok) break;
+      }
+      ++seg;
+    }
+    tc_commit(bar(L::kBarDrain));
+    mbar_wait_drain(bar(L::kBarDrain), 0, wc.limit_ns);
+  } else if (warp == kWarpScale) {
+    // ------------------------------------------------------------ scale warp
+    // The power of two above the largest V scale of each group of channels in the
+    // tile.  (Rows behind the request's end hold anything.)
+    bool ok = true;
+    int g = 0;
+    Walk w = w0;
+    Seg sg;
+    while (ok && next_seg<TS>(p, Hr, w, sg)) {
+      for (int t = sg.t0; t < sg.t1; ++t, ++g) {
+        const int s = g % L::kStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarKFull + s), (g / L::kStages) & 1, wc));
+        if (!ok) break;
+        const uint4* sc = reinterpret_cast<const uint4*>(sbase + L::kSc + s * 2 * L::kScl + L::kScl);
+        const int live = sg.len - (t << TS);  // tokens of the tile that there are, or more
+        uint32_t a = 0, b = 0;                // largest magnitudes of groups 0 and 1, 2 and 3, as bits
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 v = sc[i * 32 + lane];  // rows 2 (32 i + lane) and the next
+          const int tok = 2 * (i * 32 + lane) * TPR;
+          if (tok < live) a = max_u16x2(a, v.x & 0x7fff7fffu);
+          if (tok + TPR - 1 < live) b = max_u16x2(b, v.y & 0x7fff7fffu);
+          if (tok + TPR < live) a = max_u16x2(a, v.z & 0x7fff7fffu);
+          if (tok + 2 * TPR - 1 < live) b = max_u16x2(b, v.w & 0x7fff7fffu);
+        }
+        const uint32_t top[4] = {__reduce_max_sync(0xffffffffu, a & 0xffffu), __reduce_max_sync(0xffffffffu, a >> 16),
+                                 __reduce_max_sync(0xffffffffu, b & 0xffffu), __reduce_max_sync(0xffffffffu, b >> 16)};
+        if (lane < 4) {
+          const uint32_t m = lane == 0 ? top[0] : (lane == 1 ? top[1] : (lane == 2 ? top[2] : top[3]));
+          // (a NaN among them says nothing of the others: its own scale makes its group a NaN)
+          const int e = min(max((int)(m >> 7) - 126, -100), 100);
+          float* n = reinterpret_cast<float*>(sbase + L::kNorm + s * 32);
+          n[lane] = pow2f(-e);
+          n[4 + lane] = pow2f(e);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarNFull + s));
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int kl = threadIdx.x;  // row of the tile = TMEM lane of S^T; channel of the row = lane of O^T
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t tS = tmem + lane_off + L::kColS, tO = tmem + lane_off + L::kColO + warp * L::NG;
+    float* xm = reinterpret_cast<float*>(sbase + L::kXm);
+    float* xl = reinterpret_cast<float*>(sbase + L::kXl);
+    float* qs_s = reinterpret_cast<float*>(sbase + L::kQs);
+    int* qi_s = reinterpret_cast<int*>(sbase + L::kQi);
+    const int R = p.Nq * p.G;
+    uint8_t* prow = sbase + L::kP;
+    bool ok = true;
+    int g = 0, seg = 0;
+    Walk w = w0;
+    Seg sg;
+    while (ok && next_seg<TS>(p, Hr, w, sg)) {
+      const int len = sg.len;
+      const int h = sg.hr / p.n_rb, rb = sg.hr % p.n_rb;
+      // ---- the q terms of the row block: eight lanes to a row
+      if (kl < RP * 8) {
+        constexpr int E = D / 8;  // elements per lane
+        const int r = kl >> 3, c = kl & 7, idx = rb * RP + r;
+        const int i = idx / p.G, hq = h * p.G + idx % p.G;
+        float f[E];
+        if (idx < R) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) +
+                                                            ((((size_t)sg.b * p.Nq + i) * p.Hq + hq) * D + c * E) * 2);
+#pragma unroll
+          for (int j = 0; j < E / 8; ++j) {
+            const uint4 v = src[j];
+            const uint32_t* wv = &v.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 x = unpack2<BF16>(wv[e]);
+              f[j * 8 + 2 * e] = x.x;
+              f[j * 8 + 2 * e + 1] = x.y;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j) f[j] = 0.f;
+        }
+        uint32_t top = 0;  // largest magnitude, as bits (inf and NaN above all numbers)
+#pragma unroll
+        for (int j = 0; j < E; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // 2^-e brings the row's largest into [128, 256)
+        const int e = min(max((int)(top >> 23) - 127 - 7, -100), 119);
+        const float mul = pow2f(-e);
+        const bool bad = top >= 0x7f800000u;
+#pragma unroll
+        for (int j = 0; j < E; ++j) f[j] *= mul;
+#pragma unroll
+        for (int t = 0; t < NP; ++t) {
+          uint32_t cw[E / 4];
+#pragma unroll
+          for (int j = 0; j < E; j += 4) {
+            const uint32_t lo = pack_e4m3(f[j], f[j + 1]), hi = pack_e4m3(f[j + 2], f[j + 3]);
+            const float2 a = unpack_e4m3(lo), b = unpack_e4m3(hi);
+            f[j] = (f[j] - a.x) * 16.f;  // exact: what the term leaves, for the next one
+            f[j + 1] = (f[j + 1] - a.y) * 16.f;
+            f[j + 2] = (f[j + 2] - b.x) * 16.f;
+            f[j + 3] = (f[j + 3] - b.y) * 16.f;
+            cw[j / 4] = lo | (hi << 16);
+          }
+#pragma unroll
+          for (int half = 0; half < TPR; ++half) {  // (d = 64: against both tokens of a row)
+            uint32_t off = (uint32_t)((t * RP + r) * 128 + half * 64 + c * E);
+            off ^= ((off >> 7) & 7u) << 4;
+            if constexpr (E == 16)
+              *reinterpret_cast<uint4*>(sbase + L::kQ + off) = make_uint4(cw[0], cw[1], cw[2], cw[3]);
+            else
+              *reinterpret_cast<uint2*>(sbase + L::kQ + off) = make_uint2(cw[0], cw[1]);
+          }
+        }
+        if (c == 0) {
+          qs_s[r] = bad ? __uint_as_float(0x7fc00000u) : pow2f(e) * p.scale * kLog2e;
+          qi_s[r] = i;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(L::kBarQFull));
+      ok = named_bar_and(kWgBar, 128, ok);
+      if (!ok) break;
+      float m[RP], l[RP], acc[RP];
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+        acc[r] = 0.f;
+      }
+      const int lim0 = p.causal ? len - p.Nq : len - 1;  // tokens <= lim0 are seen by every row
+      // O^T of a tile is added a tile later, while the tensor core works on the
+      // next one: be is the factor of the tile whose O^T is outstanding (acc is
+      // already on that tile's scale), the power of two of its V scales in it.
+      float be[RP];
+      auto add_o = [&](int go) {
+        tc_fence_after();
+        uint32_t r_[L::NG];
+        tmem_ld_n<L::NG>(tO + (go % NB) * L::NO, r_);
+        tmem_ld_wait();
+        reg_fence<L::NG>(r_);
+        tc_fence_before();
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          float o = __uint_as_float(r_[r]), c = __uint_as_float(r_[RP + r]);
+          if constexpr (NP == 3) c = fmaf(__uint_as_float(r_[2 * RP + r]), 0.0625f, c);
+          o = fmaf(c, 0.0625f, o);
+          acc[r] = fmaf(o, be[r], acc[r]);
+        }
+      };
+      for (int t = sg.t0; t < sg.t1; ++t, ++g) {
+        const int st = g % L::kStages, kv0 = (t << TS) + kl * TPR;  // first token of this row
+        const bool later = t > sg.t0;  // the tile before is of this segment, its O^T outstanding
+        const uint32_t ph = (g / L::kStages) & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarSFull + (g & 1)), (g >> 1) & 1, wc) &&
+                                         mbar_wait(bar(L::kBarKFull + st), ph, wc) && mbar_wait(bar(L::kBarNFull + st), ph, wc));
+        float x[TPR][RP];  // scores in log2 units
+        float f[4], lv[TPR], mul = 0.f;
+        if (ok) {
+          tc_fence_after();
+          const uint2 kw = *reinterpret_cast<const uint2*>(sbase + L::kSc + st * 2 * L::kScl + kl * 8);
+          const uint2 vw = *reinterpret_cast<const uint2*>(sbase + L::kSc + st * 2 * L::kScl + L::kScl + kl * 8);
+          const float4 inv = *reinterpret_cast<const float4*>(sbase + L::kNorm + st * 32);
+          mul = *reinterpret_cast<const float*>(sbase + L::kNorm + st * 32 + 16 + warp * 4);
+          const float ks[4] = {bf16_lo(kw.x), bf16_hi(kw.x), bf16_lo(kw.y), bf16_hi(kw.y)};
+          f[0] = bf16_lo(vw.x) * inv.x;
+          f[1] = bf16_hi(vw.x) * inv.y;
+          f[2] = bf16_lo(vw.y) * inv.z;
+          f[3] = bf16_hi(vw.y) * inv.w;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // (a token behind the end has no weight, whatever its scales hold)
+            if (kv0 + k * TPR / 4 >= len) f[k] = 0.f;
+          // the largest weight of each token's value, at most 1
+          if constexpr (TPR == 1) {
+            lv[0] = __log2f(fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), 0x1p-30f));
+          } else {
+            lv[0] = __log2f(fmaxf(fmaxf(f[0], f[1]), 0x1p-30f));
+            lv[1] = __log2f(fmaxf(fmaxf(f[2], f[3]), 0x1p-30f));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t r_[L::NG];
+            tmem_ld_n<L::NG>(tS + (g % NB) * 4 * L::NS + k * L::NS, r_);
+            tmem_ld_wait();
+            reg_fence<L::NG>(r_);
+            constexpr int per = 4 / TPR;
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+              float s = __uint_as_float(r_[r]), c = __uint_as_float(r_[RP + r]);
+              if constexpr (NP == 3) c = fmaf(__uint_as_float(r_[2 * RP + r]), 0.0625f, c);
+              s = fmaf(c, 0.0625f, s);
+              x[k / per][r] = k % per == 0 ? s * ks[k] : fmaf(s, ks[k], x[k / per][r]);
+            }
+          }
+          tc_fence_before();
+#pragma unroll
+          for (int j = 0; j < TPR; ++j)
+#pragma unroll
+            for (int r = 0; r < RP; ++r) x[j][r] *= qs_s[r];
+          if ((t << TS) + (1 << TS) - 1 > lim0) {
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+              const int lim = p.causal ? min(len - 1, len - p.Nq + qi_s[r]) : len - 1;
+#pragma unroll
+              for (int j = 0; j < TPR; ++j)
+                if (kv0 + j > lim) x[j][r] = -INFINITY;
+            }
+          }
+          float* mine = xm + ((g & 1) * 4 + warp) * RP;
+#pragma unroll
+          for (int r0 = 0; r0 < RP; r0 += 4) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float y = x[0][r0 + j] + lv[0];
+              if constexpr (TPR == 2) y = fmaxf(y, x[1][r0 + j] + lv[1]);
+              v[j] = warp_max(y);
+            }
+            if (lane == 0) *reinterpret_cast<float4*>(mine + r0) = make_float4(v[0], v[1], v[2], v[3]);
+          }
+        }
+        // (the O^T outstanding is complete: its MMA has read P, which is written again below)
+        if (ok && later) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarOFull), (g - 1) & 1, wc));
+        ok = named_bar_and(kWgBar, 128, ok);
+        if (!ok) break;
+        if (NB == 1 && later) add_o(g - 1);  // (before P lets the next O^T overwrite it)
+        float al_t[RP], be_t[RP];
+        uint32_t code[4][NP][RP / 4];  // terms of p f for the four groups, four rows to a word
+#pragma unroll
+        for (int r0 = 0; r0 < RP; r0 += 4) {
+          float4 v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const float4*>(xm + ((g & 1) * 4 + q) * RP + r0);
+          const float mt4[4] = {fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x)),
+                                fmaxf(fmaxf(v[0].y, v[1].y), fmaxf(v[2].y, v[3].y)),
+                                fmaxf(fmaxf(v[0].z, v[1].z), fmaxf(v[2].z, v[3].z)),
+                                fmaxf(fmaxf(v[0].w, v[1].w), fmaxf(v[2].w, v[3].w))};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = r0 + j;
+            const float mt = mt4[j];
+            // running maximum: one of the factors of the old and the new part is 1
+            const float e = ex2(mt > m[r] ? m[r] - mt : mt - m[r]);
+            al_t[r] = mt > m[r] ? e : 1.f;
+            be_t[r] = (mt < m[r] ? e : 1.f) * 0.00390625f;  // p below carries 2^8
+            m[r] = fmaxf(m[r], mt);
+            const float ref = mt == -INFINITY ? 0.f : mt - 8.f;
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < TPR; ++k) {
+              x[k][r] = ex2(x[k][r] - ref);  // p 2^8
+              sum += x[k][r];
+            }
+            l[r] = fmaf(sum, be_t[r], l[r] * al_t[r]);
+            be_t[r] *= mul;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float* pr = x[k * TPR / 4] + r0;
+            float2 a = make_float2(pr[0] * f[k], pr[1] * f[k]), b = make_float2(pr[2] * f[k], pr[3] * f[k]);
+#pragma unroll
+            for (int t2 = 0; t2 < NP; ++t2) {
+              const uint32_t lo = pack_e4m3(a.x, a.y), hi = pack_e4m3(b.x, b.y);
+              code[k][t2][r0 / 4] = lo | (hi << 16);
+              if (t2 + 1 < NP) {
+                const float2 d0 = unpack_e4m3(lo), d1 = unpack_e4m3(hi);
+                a = make_float2((a.x - d0.x) * 16.f, (a.y - d0.y) * 16.f);
+                b = make_float2((b.x - d1.x) * 16.f, (b.y - d1.y) * 16.f);
+              }
+            }
+          }
+        }
+        // row kl of P: column (group, term, row) one byte each
+        const uint32_t* cw = &code[0][0][0];
+#pragma unroll
+        for (int c = 0; c < L::NO / 16; ++c)
+          *reinterpret_cast<uint4*>(prow + p_off<L::PW>(kl, c)) = make_uint4(cw[4 * c], cw[4 * c + 1], cw[4 * c + 2], cw[4 * c + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar(L::kBarPFull));
+        if (NB == 2 && later) add_o(g - 1);
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          acc[r] *= al_t[r];
+          be[r] = be_t[r];
+        }
+      }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarOFull), (g - 1) & 1, wc));
+      if (ok) add_o(g - 1);
+      // ---- end of the segment: row sums over the tile's rows, then O
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+        if (lane == 0) xl[warp * RP + r] = l[r];
+      }
+      // (d = 64: lanes 64 to 127 hold the second token's part; P's rows are free)
+      float* half = reinterpret_cast<float*>(prow);
+      if (TPR == 2 && kl >= 64) {
+#pragma unroll
+        for (int r = 0; r < RP; ++r) half[r * 64 + kl - 64] = acc[r];
+      }
+      ok = named_bar_and(kWgBar, 128, ok);
+      if (!ok) break;
+      const bool whole = sg.t1 - sg.t0 == sg.nt;
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        const int idx = rb * RP + r;
+        if (idx >= R) break;
+        const float lt = (xl[r] + xl[RP + r]) + (xl[2 * RP + r] + xl[3 * RP + r]);
+        const float sum = TPR == 2 && kl < 64 ? acc[r] + half[r * 64 + kl] : acc[r];
+        if (whole) {
+          const int i = idx / p.G, hq = h * p.G + idx % p.G;
+          const float v = lt != 0.f ? sum / lt : 0.f;
+          if (kl < D) {
+            const uint32_t c = pack2<BF16>(v, 0.f);
+            reinterpret_cast<uint16_t*>(p.o)[(((size_t)sg.b * p.Nq + i) * p.Hq + hq) * D + kl] = (uint16_t)c;
+          }
+          if (kl == 0)
+            p.lse[((size_t)sg.b * p.Hq + hq) * p.Nq + i] = lt != 0.f ? (m[r] + __log2f(lt)) * kLn2 : -INFINITY;
+        } else {
+          const size_t part = ((size_t)blockIdx.x * 2 + (seg > 0 ? 1 : 0)) * RP + r;
+          if (kl < D) p.ws_o[part * D + kl] = sum;
+          if (kl == 0) {
+            p.ws_ml[part * 2] = m[r];
+            p.ws_ml[part * 2 + 1] = lt;
+          }
+        }
+      }
+      // (the next segment's P and row sums are written behind the barrier of its first tile)
+      ++seg;
+    }
+  }
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kCols);
+  }
+}
+
+template <int D, int RP, int NP>
+cudaError_t launch_split_t(const KvDecArgs& a, cudaStream_t stream) {
+  using L = Kv4Layout<D, RP, NP>;
+  auto* k = attn_kv4_split_kernel<D, RP, NP>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, (unsigned)a.grid, kDecThreads, L::kSmem, stream, a);
+}
+
+template <int D>
+cudaError_t launch_split_d(const KvDecArgs& a, cudaStream_t stream) {
+  if (a.bf16)
+    return a.rp == 4 ? launch_split_t<D, 4, 2>(a, stream)
+                     : (a.rp == 8 ? launch_split_t<D, 8, 2>(a, stream) : launch_split_t<D, 16, 2>(a, stream));
+  return a.rp == 4 ? launch_split_t<D, 4, 3>(a, stream) : launch_split_t<D, 8, 3>(a, stream);
+}
+
 }  // namespace
 
 template <int U>
@@ -122,6 +726,22 @@ cudaError_t launch_kv4_append(Kv4AppendArgs a, int sms, cudaStream_t stream) {
   const int u = a.T * per_tok * 2 > 4ll * sms * 2048 ? 4 : 1;
   kv_rows(&a, (long long)kAppThreads * u / per_tok);
   return u == 4 ? launch_append_u<4>(a, stream) : launch_append_u<1>(a, stream);
+}
+
+// Row blocks of 4, 8 or, in bf16, 16 rows: the work per tile grows with the rows.  (16 rows of
+// fp16 in three terms would take 384 columns of TMEM.)
+int kv4_rows(int R, bool bf16) { return R <= 4 ? 4 : (R <= 8 || !bf16 ? 8 : 16); }
+
+// All CTAs resident at once, no more than there can be tiles.
+int kv4_grid(int sms, long long max_units) {
+  long long g = 2ll * sms;
+  if (g > kKvMaxCtas) g = kKvMaxCtas;
+  if (g > max_units) g = max_units;
+  return (int)(g < 1 ? 1 : g);
+}
+
+cudaError_t launch_kv4_split(const KvDecArgs& a, cudaStream_t stream) {
+  return a.d == 128 ? launch_split_d<128>(a, stream) : launch_split_d<64>(a, stream);
 }
 
 }  // namespace attn

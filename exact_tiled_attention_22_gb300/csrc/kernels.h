@@ -215,12 +215,13 @@ constexpr int kKvMaxCtas = 640;  // workspace bound of the decode grids
 // Decoding from a paged cache, in 8 bits or in 4.
 struct KvDecArgs {
   CUtensorMap tm_k, tm_v;    // one page of one head a box: (d, page, P * H), in 4 bits (128, page * d / 128, P * H)
-  CUtensorMap tm_ks, tm_vs;  // 4 bits: scales of 128 channels as one element, (page * d / 128, P * H)
   const void* q;             // [B, Nq, Hq, d]
   void* o;
   float* lse;                // [B, Hq, Nq]
   const float* k_scale;      // 8 bits: [P][H]
   const float* v_scale;
+  const uint16_t* k_scale16; // 4 bits: bf16 [P][H][page][d / 32]
+  const uint16_t* v_scale16;
   const int* table;          // [B][width]
   const int* lens;           // [B]
   float* ws_o;               // [CTA][2][rows][d]
@@ -263,6 +264,9 @@ void kv_rows(Args* a, long long tok) {
   a->h_magic = a->tok == 1 ? 0 : (uint32_t)(((1ull << 31) + a->H - 1) / a->H);
 }
 cudaError_t launch_kv4_append(Kv4AppendArgs a, int sms, cudaStream_t stream);
+int kv4_rows(int R, bool bf16);
+int kv4_grid(int sms, long long max_units);
+cudaError_t launch_kv4_split(const KvDecArgs& a, cudaStream_t stream);
 
 // Cached keys and values as packed 16-bit rows (attn_kvread.cu).
 struct KvReadArgs {

@@ -312,6 +312,12 @@ __host__ __device__ constexpr uint32_t make_idesc_e4m3(int M, int N, bool a_mn, 
   return make_idesc(false, M, N, a_mn, b_mn);
 }
 
+// The same with an e2m1 A operand (type 5) and an e4m3 B operand.  e2m1 values lie in
+// shared memory as TMA unpacks them: 16 of them in 8 bytes, then 8 unused bytes.
+__host__ __device__ constexpr uint32_t make_idesc_e2m1_e4m3(int M, int N, bool a_mn, bool b_mn) {
+  return make_idesc(false, M, N, a_mn, b_mn) | (5u << 7);
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle, version 1.
 //   bits 0-13 start >> 4; 16-29 leading byte offset >> 4;
 //   32-45 stride byte offset >> 4; 46-47 version (1); 61-63 layout (2 = 128B).
@@ -370,10 +376,35 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
       : ATTN_R8(0), ATTN_R8(8)
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : ATTN_R8(0) : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
                ATTN_W8(0)
                : "memory");
+}
+// N columns of this thread's TMEM lane, N a multiple of 4 below 64
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t* r) {
+  static_assert(N % 4 == 0 && N < 64, "width");
+  if constexpr (N >= 32) {
+    tmem_ld32(taddr, r);
+    if constexpr (N > 32) tmem_ld_n<N - 32>(taddr + 32, r + 32);
+  } else if constexpr (N >= 16) {
+    tmem_ld16(taddr, r);
+    if constexpr (N > 16) tmem_ld_n<N - 16>(taddr + 16, r + 16);
+  } else if constexpr (N >= 8) {
+    tmem_ld8(taddr, r);
+    if constexpr (N > 8) tmem_ld_n<N - 8>(taddr + 8, r + 8);
+  } else {
+    tmem_ld4(taddr, r);
+  }
 }
 // 32 or 16 columns of this thread's TMEM lane, by width
 template <int W>

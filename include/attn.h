@@ -489,6 +489,17 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
  * A NaN makes its group's scale a NaN: all 32 channels read as NaN.  Other tokens' codes and
  * scales are left as they are.  T * H < 2^30.
  *
+ * attn_kv4_decode -- attention of the last Nq tokens of every request to all of its cached
+ * tokens: arguments, shapes, masks and workspace as attn_kv8_decode (the size from
+ * attn_kv4_decode_workspace_size).  Codes and scales behind a request's last token are not used; a
+ * page id outside [0, P) reads as zeros.  Scales must be finite and >= 0; a NaN among a
+ * request's cached values may reach all its queries.  Query and key products carry
+ * queries exactly up to 2^-21 of a row's largest element; a probability times its value's scale
+ * is rounded to 2^-14 (fp16) or 2^-9 (bf16) of itself, and by no more than 2^-25 or 2^-21 of
+ * the largest such product in its tile of 128 (d = 128) or 256 tokens, every group of 32
+ * channels measured by its own largest scale there.
+ * width * page at most 2^31 - 256, Hq / H at most 2^23.
+ *
  * attn_kv_read -- cached keys and values as packed 16-bit rows, for a prompt that goes on
  * after a cached prefix (attn_varlen_fwd takes the rows).
  *   bits : 8 or 4, which cache it is (its layout and scales as above)
@@ -504,6 +515,13 @@ int attn_kv4_append(const void* k, const void* v, long long k_stride, long long 
                     const int64_t* slots, long long T, int H, int d, uint8_t* k_cache,
                     uint8_t* v_cache, uint16_t* k_scale, uint16_t* v_scale, int P, int page,
                     attn_dtype_t dtype, void* stream);
+size_t attn_kv4_decode_workspace_size(int Nq, int Hq, int H, int d);
+int attn_kv4_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                    const uint16_t* k_scale, const uint16_t* v_scale,
+                    const int32_t* block_table, const int32_t* lens, void* o, float* lse,
+                    int B, int Nq, int Hq, int H, int d, int P, int page, int width,
+                    float scale, int causal, attn_dtype_t dtype, void* workspace,
+                    size_t workspace_bytes, void* stream);
 int attn_kv_read(const uint8_t* k_cache, const uint8_t* v_cache, const void* k_scale,
                  const void* v_scale, const int32_t* block_table, const int32_t* lens,
                  const int32_t* cu, void* k, void* v, int B, long long T, int H, int d, int P,
@@ -544,7 +562,7 @@ const char* attn_last_error_string(void);
  * hold back its copies, so that its consumers' waits run out (used to test
  * the timeout path without faulting the GPU): bit 0 the forward (no loads),
  * bit 1 the backward main kernel (K and V, but no query steps), bit 2 the
- * decoding chunk kernel (no loads), bit 4 attn_kv8_decode (no loads).  Bit 3 changes no result: the
+ * decoding chunk kernel (no loads), bit 4 attn_kv8_decode and attn_kv4_decode (no loads).  Bit 3 changes no result: the
  * backward's preprocess and dQ conversion kernels split row indices with
  * 64-bit arithmetic, the form they take by themselves only when
  * B * H * N (N rounded up to 128) reaches 2^31.  Process-wide.

@@ -79,12 +79,14 @@ def decoded(q, kval, vc, vs, table, lens, scale, causal, dtype):
 
     P times a value's scale is carried by two (bf16) or three (fp16) e4m3 terms: off by 2^-9 or
     2^-14 of itself, for bf16 by another 2^-11 (its rounding to fp16 before the second term), and by
-    2^-22 or 2^-26 of the largest p u s_g of its tile where it falls among the subnormal codes; u is
-    the largest of a token's scales, each against the largest s_g of its group of channels in the tile.
+    2^-21 or 2^-25 of the largest p u s_g of its tile where it falls among the subnormal codes (half of
+    their step is 2^-22 or 2^-26 of the largest product, whose scales are measured by a power of two up to
+    twice the largest s_g); u is the largest of a token's scales, each against the largest s_g of its group
+    of channels in the tile.
     Tiles hold 128 tokens (d = 128) or 256 (d = 64).  The scores see the query within 2^-21 of its
     row's largest element."""
     u, tiny = plain64.U[dtype], plain64.TINY[dtype]
-    up, floor = (2.0 ** -9 + 2.0 ** -11, 2.0 ** -22) if dtype == "bf16" else (2.0 ** -14, 2.0 ** -26)
+    up, floor = (2.0 ** -9 + 2.0 ** -11, 2.0 ** -21) if dtype == "bf16" else (2.0 ** -14, 2.0 ** -25)
     B, Nq, Hq, d = q.shape
     P, H, page, _ = kval.shape
     G, tile = Hq // H, 128 * 128 // d

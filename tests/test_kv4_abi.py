@@ -123,3 +123,33 @@ def test_conveniences_refuse_other_tensors(A):
         with pytest.raises(ValueError):
             A.kv8_read(z(3, 2, 16, 64).byte(), z(3, 2, 16, 64).byte(), z(3, 2), z(3, 2), z(1, 4).int(), z(1).int(),
                        z(2).int(), 3, dtype)
+
+
+DECODE = "q kc vc sk sv table lens o lse B Nq Hq H d P page width scale causal dtype ws ws_bytes stream"
+
+
+@pytest.mark.parametrize("kw,code", CACHE + [
+    (dict(q=None), -1), (dict(table=None), -1), (dict(lse=None), -1), (dict(B=0), -1), (dict(Nq=0), -1), (dict(Hq=3), -1),
+    (dict(Hq=0), -1), (dict(Nq=129), -2), (dict(scale=0.0), -1), (dict(scale=float("nan")), -1),
+    (dict(scale=float("inf")), -1), (dict(width=1 << 27), -1), (dict(width=(1 << 27) - 15), -1), (dict(width=0), -1),
+    (dict(B=1 << 29), -1), (dict(Hq=1 << 25), -1), (dict(o=P[7] + 8), -3), (dict(lens=P[2] + 1), -3), (dict(ws=None), -6),
+    (dict(ws=WS + 128), -3), (dict(ws_bytes=100), -6), (dict(o=P[0]), -1), (dict(lse=P[7]), -1), (dict(ws=P[3]), -1),
+    (dict(o=P[5]), -1)])
+def test_decode_refuses(A, kw, code):
+    base = dict(q=P[0], kc=P[3], vc=P[4], sk=P[5], sv=P[6], table=P[1], lens=P[2], o=P[7], lse=P[8], B=2, Nq=1, Hq=4,
+                H=2, d=64, P=9, page=16, width=4, scale=0.125, causal=1, dtype=A.ATTN_BF16, ws=WS,
+                ws_bytes=A.attn_kv4_decode_workspace_size(1, 4, 2, 64), stream=None)
+    assert call(A.lib.attn_kv4_decode, DECODE, base, kw) == code and A.last_error()
+
+
+def test_decode_workspace_sizes(A):
+    f = A.attn_kv4_decode_workspace_size
+    assert f(0, 1, 1, 64) == 0 and f(1, 3, 2, 64) == 0 and f(1, 2, 2, 60) == 0 and f(129, 1, 1, 64) == 0
+    assert 0 < f(1, 4, 1, 64) < f(1, 8, 1, 64) < f(1, 16, 1, 64) == f(128, 64, 1, 64) < f(1, 16, 1, 128)
+
+
+def test_decode_convenience_refuses_other_tensors(A):
+    z = torch.zeros
+    kc, ks = z(3, 2, 16, 32).byte(), z(3, 2, 16, 2).bfloat16()
+    with pytest.raises(ValueError):
+        A.kv4_decode(z(1, 1, 2, 64).half(), kc, kc, ks, ks, z(1, 4).int(), z(1).int())
