@@ -919,7 +919,7 @@ int attn_kv4_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   a.causal = causal ? 1 : 0;
   a.scale = scale;
   const long long tile = 1ll << a.tile_shift, tiles = ((long long)width * page + tile - 1) / tile;
-  a.grid = attn::kv4_grid(dev->sms, tiles * B * H * a.n_rb);
+  a.grid = attn::kv4_grid(a.rp, a.bf16, dev->sms, tiles * B * H * a.n_rb);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.ws_o = reinterpret_cast<float*>(ws);
   a.ws_ml = reinterpret_cast<float*>(ws + ((size_t)attn::kKvMaxCtas * 2 * a.rp * d * 4 + 255) / 256 * 256);

@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kAppThreads) attn_kv4_append_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ decode
-constexpr int kDecThreads = 224;  // warps 0-3 softmax, 4 producer, 5 MMA, 6 scales
-constexpr int kWarpProd = 4, kWarpMma = 5, kWarpScale = 6;
+constexpr int kDecThreads = 192;  // warps 0-3 softmax, 4 producer, 5 MMA, query terms and scales
+constexpr int kWarpProd = 4, kWarpMma = 5;
 constexpr uint32_t kWgBar = 1;    // named barrier of the softmax warps
 
 __host__ __device__ constexpr int up1024(int x) { return (x + 1023) / 1024 * 1024; }
@@ -114,17 +114,24 @@ struct Kv4Layout {
   static constexpr int TPR = 128 / D;                 // tokens to a row
   static constexpr int kTileShift = D == 128 ? 7 : 8; // tokens to a tile
   static constexpr int NG = RP * NP;                  // operand rows: query rows times terms
-  static constexpr int NS = (NG + 15) / 16 * 16;      // MMA columns of S^T (M = 128 needs a multiple of 16)
-  static constexpr int NO = 4 * NG;                   // of O^T: one set for each group of 32 channels
+  // S^T has a set of NG columns for each group of 32 channels.  M = 128 takes columns by 16: eight are
+  // written by twos, a set with the next one (the other's rows of the query operand are zeros there).
+  static constexpr bool kPair = NG == 8;
+  static constexpr int NS = kPair ? 16 : (NG + 15) / 16 * 16;  // MMA columns
+  static constexpr int kSet = kPair ? 8 : NS;         // columns from one set to the next
+  static constexpr int NO = 4 * NG;                   // O^T: likewise a set for each group
   static constexpr int PW = NO <= 32 ? 32 : (NO <= 64 ? 64 : 128);  // bytes of a P row, and its swizzle
-  static constexpr int kCtas = 2;
+  // CTAs to an SM, by what shared memory, TMEM and registers leave
+  static constexpr int kCtas = PW == 32 ? 3 : 2;
+  static constexpr int kStages = PW == 64 ? 3 : 2;
   static constexpr int kCode = 128 * 128;             // bytes of a tile's codes: 16 to 16 bytes, 8 of them filled
   static constexpr int kScl = 128 * 8;                // bytes of its scales: four bf16 a row
-  static constexpr int kStages = PW == 32 ? 3 : 2;
   static constexpr int kQ = 0;
   static constexpr int kP = kQ + up1024(NS * 128);
-  static constexpr int kKV = kP + up1024(128 * PW);   // stage s: K codes at + s * 2 kCode, V codes behind them
-  static constexpr int kSc = kKV + kStages * 2 * kCode;   // stage s: K scales at + s * 2 kScl, V scales behind them
+  // three rings: K codes, V codes, scales (stage s: K's at + s * 2 kScl, V's behind them)
+  static constexpr int kK = kP + up1024(128 * PW);
+  static constexpr int kV = kK + kStages * kCode;
+  static constexpr int kSc = kV + kStages * kCode;
   static constexpr int kNorm = kSc + kStages * 2 * kScl;  // [stages][4] 2^-e, [4] 2^e: powers above the groups' largest V scale
   static constexpr int kXm = kNorm + kStages * 32;    // [2][4][RP] fp32 row maxima of the warps
   static constexpr int kXl = kXm + 2 * 4 * RP * 4;    // [4][RP] fp32 row sums
@@ -132,10 +139,13 @@ struct Kv4Layout {
   static constexpr int kQi = kQs + RP * 4;            // [RP] int query index of the row
   static constexpr int kBar = kQi + RP * 4;
   static constexpr int kBarKFull = 0;
-  static constexpr int kBarVFull = kBarKFull + kStages;
-  static constexpr int kBarNFull = kBarVFull + kStages;
-  static constexpr int kBarEmpty = kBarNFull + kStages;
-  static constexpr int kBarSFull = kBarEmpty + kStages;  // [2]
+  static constexpr int kBarKEmpty = kBarKFull + kStages;
+  static constexpr int kBarVFull = kBarKEmpty + kStages;
+  static constexpr int kBarVEmpty = kBarVFull + kStages;
+  static constexpr int kBarCFull = kBarVEmpty + kStages;   // scales
+  static constexpr int kBarCEmpty = kBarCFull + kStages;
+  static constexpr int kBarNFull = kBarCEmpty + kStages;
+  static constexpr int kBarSFull = kBarNFull + kStages;  // [2]
   static constexpr int kBarPFull = kBarSFull + 2;
   static constexpr int kBarOFull = kBarPFull + 1;
   static constexpr int kBarQFull = kBarOFull + 1;
@@ -143,17 +153,17 @@ struct Kv4Layout {
   static constexpr int kNumBars = kBarDrain + 1;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kStart = kTmemSlot + 16;       // start of the CTA's range: long long u0, u1; int b, hr, t
-  static constexpr int kScan = kStart + 32;           // [7] warp sums
-  static constexpr int kBytes = kScan + 8 * 8;
-  static constexpr int kSmem = kBytes + 1024;
-  // TMEM: two buffers of S^T (four groups) and of O^T where 256 columns hold them, else one
-  static constexpr int kBufs = 2 * (4 * NS + NO) <= 256 ? 2 : 1;
-  static constexpr int kCols = kBufs * (4 * NS + NO) <= 128 ? 128 : 256;
-  static constexpr int kColS = 0, kColO = kBufs * 4 * NS;
-  static_assert(kBufs * (4 * NS + NO) <= kCols && kCols * kCtas <= 512, "TMEM budget");
+  static constexpr int kScan = kStart + 32;           // [6] warp sums
+  static constexpr int kSmem = kScan + 6 * 8;
+  // TMEM: two buffers of S^T and of O^T where the columns are there, else one
+  static constexpr int kMaxCols = kCtas == 3 ? 128 : 256;
+  static constexpr int kBufs = 2 * (4 * kSet + NO) <= kMaxCols ? 2 : 1;
+  static constexpr int kCols = kBufs * (4 * kSet + NO) <= 128 ? 128 : 256;
+  static constexpr int kColS = 0, kColO = kBufs * 4 * kSet;
+  static_assert(kBufs * (4 * kSet + NO) <= kCols && kCols * kCtas <= 512, "TMEM budget");
   static_assert((kSmem + 1024) * kCtas <= 228 * 1024, "shared memory budget");
   static_assert(NO % 16 == 0 && NO <= PW, "P rows");
-  static_assert(kBar % 8 == 0 && kNorm % 16 == 0 && kXm % 16 == 0 && kStart % 8 == 0, "alignment");
+  static_assert(kBar % 8 == 0 && kNorm % 16 == 0 && kXm % 16 == 0 && kStart % 8 == 0 && kScan % 8 == 0, "alignment");
 };
 
 // Descriptor of the MN-major P operand: rows (keys) of PW bytes, PW-byte swizzle, 8-key
@@ -176,15 +186,32 @@ __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// e4m3 of (h16 - 16 t) for a pair: h16 fp16, t the e4m3 pair in the low 16 bits of w.
+__device__ __forceinline__ uint32_t rest_e4m3(uint32_t h16, uint32_t w) {
+  uint16_t r;
+  asm("{\n\t.reg .b32 t, m;\n\t"
+      "cvt.rn.f16x2.e4m3x2 t, %2;\n\t"
+      "mov.b32 m, 0xcc00cc00;\n\t"  // -16
+      "fma.rn.f16x2 t, t, m, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 %0, t;\n\t}"
+      : "=h"(r) : "r"(h16), "h"((uint16_t)w));
+  return r;
+}
+
 template <int D, int RP, int NP>
 __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn_kv4_split_kernel(const __grid_constant__ KvDecArgs p) {
   using L = Kv4Layout<D, RP, NP>;
   constexpr bool BF16 = NP == 2;
   constexpr int TPR = L::TPR, TS = L::kTileShift, NB = L::kBufs;
+  // (dynamic shared memory begins behind the 1024 bytes the system keeps: aligned as declared.
+  // Three CTAs leave no room to align it here; a launch that it does not hold for gives up.)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* sbase = smem_raw + (base - raw);
+  const uint32_t base = smem_u32(smem_raw);
+  uint8_t* sbase = smem_raw;
+  if (base & 1023u) {
+    if (threadIdx.x == 0) atomicCAS(p.wait.status, kDevOk, kDevTimeout);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hr = p.H * p.n_rb;
   const WaitCtl wc{p.wait.status, p.wait.limit_ns};
@@ -193,15 +220,18 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
   if (warp == kWarpProd && lane == 0) {
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(bar(L::kBarKFull + s), 1);
+      mbar_init(bar(L::kBarKEmpty + s), 1);
       mbar_init(bar(L::kBarVFull + s), 1);
+      mbar_init(bar(L::kBarVEmpty + s), 1);
+      mbar_init(bar(L::kBarCFull + s), 32);
+      mbar_init(bar(L::kBarCEmpty + s), 1);
       mbar_init(bar(L::kBarNFull + s), 1);
-      mbar_init(bar(L::kBarEmpty + s), 1);
     }
     mbar_init(bar(L::kBarSFull), 1);
     mbar_init(bar(L::kBarSFull + 1), 1);
     mbar_init(bar(L::kBarPFull), 128);
     mbar_init(bar(L::kBarOFull), 1);
-    mbar_init(bar(L::kBarQFull), 128);
+    mbar_init(bar(L::kBarQFull), 32);
     mbar_init(bar(L::kBarDrain), 1);
     fence_mbar_init();
     tma_prefetch(&p.tm_k);
@@ -222,13 +252,54 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
 
   if (warp == kWarpProd) {
     // ------------------------------------------------------------ producer
-    // Lane i takes page i of a tile: its id (read a tile ahead), the copies of its
-    // codes and scales.
+    // Lane i takes page i of a tile: its id (read a tile ahead) and the copies of its
+    // codes.  K is let go when S is there, V and the scales a tile's softmax later: K runs
+    // a tile ahead of them.
     const int tile_pages = 1 << (TS - p.page_shift);
-    const int page_rows = (1 << p.page_shift) / TPR;
+    const int row_shift = p.page_shift - (TPR - 1), page_rows = 1 << row_shift;
     if (!(p.debug_flags & 16)) {
-      int g = 0;
+      int gk = 0, gv = 0;  // tiles whose K, whose V and scales were asked for
       bool ok = true;
+      int ph = -1, n_pages = 0;  // the tile whose V is next: (page, head) of the lane's page, pages
+      auto load_k = [&] {
+        const int s = gk % L::kStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarKEmpty + s), ((gk / L::kStages) & 1) ^ 1, wc));
+        if (!ok) return;
+        // (a row of codes counts as its 64 bytes in memory)
+        if (lane == 0) mbar_expect_tx(bar(L::kBarKFull + s), n_pages * page_rows * 64);
+        __syncwarp();
+        if (lane < n_pages)
+          tma_load_3d(base + L::kK + s * L::kCode + lane * page_rows * 128, &p.tm_k, bar(L::kBarKFull + s), 0, 0, ph);
+        __syncwarp();
+        ++gk;
+      };
+      auto load_v = [&](int ph_v, int n_v) {
+        const int s = gv % L::kStages;
+        const uint32_t par = ((gv / L::kStages) & 1) ^ 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarCEmpty + s), par, wc));
+        if (!ok) return;
+        // scales, two rows (16 bytes) a lane and copy; of pages that are not there zeros
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = 2 * (i * 32 + lane), pg = row >> row_shift;
+          const int at_page = __shfl_sync(0xffffffffu, ph_v, pg);
+          if (pg < n_v) {
+            const size_t at = at_page < 0 ? 0 : (((size_t)at_page << row_shift) + (row & (page_rows - 1))) * 4;
+            const uint32_t n = at_page < 0 ? 0 : 16, dst = base + L::kSc + s * 2 * L::kScl + row * 8;
+            cp_async16(dst, p.k_scale16 + at, n);
+            cp_async16(dst + L::kScl, p.v_scale16 + at, n);
+          }
+        }
+        cp_async_arrive(bar(L::kBarCFull + s));
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarVEmpty + s), par, wc));
+        if (!ok) return;
+        if (lane == 0) mbar_expect_tx(bar(L::kBarVFull + s), n_v * page_rows * 64);
+        __syncwarp();
+        if (lane < n_v)
+          tma_load_3d(base + L::kV + s * L::kCode + lane * page_rows * 128, &p.tm_v, bar(L::kBarVFull + s), 0, 0, ph_v);
+        __syncwarp();
+        ++gv;
+      };
       Walk w = w0;
       Seg sg;
       while (ok && next_seg<TS>(p, Hr, w, sg)) {
@@ -240,49 +311,24 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
           return lane < tile_pages && j < pages ? row[j] : -1;
         };
         int id = page_id(sg.t0);
-        for (int t = sg.t0; t < sg.t1; ++t, ++g) {
-          const int here = id;
-          const int n_here = min(tile_pages, pages - t * tile_pages);
+        for (int t = sg.t0; t < sg.t1; ++t) {
+          const int here = id, ph_v = ph, n_v = n_pages;
           if (t + 1 < sg.t1) id = page_id(t + 1);
-          const int s = g % L::kStages;
-          const uint32_t ph = (g / L::kStages) & 1;
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarEmpty + s), ph ^ 1, wc));
+          n_pages = min(tile_pages, pages - t * tile_pages);
+          // (a page id outside the cache reads as zeros: the copies fill with them)
+          ph = lane < n_pages && here >= 0 && here < p.P ? here * p.H + h : -1;
+          load_k();
+          if (ok && gk > 1) load_v(ph_v, n_v);
           if (!ok) break;
-          const uint32_t k = base + L::kKV + s * 2 * L::kCode + lane * page_rows * 128;
-          const uint32_t sc = L::kSc + s * 2 * L::kScl + lane * page_rows * 8;
-          // (a page id outside the cache reads as zeros: its copies fill with them, its scales are written)
-          const bool in = lane < n_here && here >= 0 && here < p.P;
-          const uint32_t n_in = __popc(__ballot_sync(0xffffffffu, in));
-          if (!in && lane < n_here) {
-            for (int i = 0; i < page_rows * 8; i += 16) {
-              *reinterpret_cast<uint4*>(sbase + sc + i) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(sbase + sc + L::kScl + i) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) {  // (a row of codes counts as its 64 bytes in memory)
-            mbar_expect_tx(bar(L::kBarKFull + s), (n_here * 64 + n_in * 16) * page_rows);
-            mbar_expect_tx(bar(L::kBarVFull + s), n_here * 64 * page_rows);
-          }
-          __syncwarp();
-          if (lane < n_here) {
-            const int ph2 = in ? here * p.H + h : -1;
-            tma_load_3d(k, &p.tm_k, bar(L::kBarKFull + s), 0, 0, ph2);
-            if (in) {
-              const size_t at = (size_t)ph2 * page_rows * 4;
-              bulk_load(base + sc, p.k_scale16 + at, page_rows * 8, bar(L::kBarKFull + s));
-              bulk_load(base + sc + L::kScl, p.v_scale16 + at, page_rows * 8, bar(L::kBarKFull + s));
-            }
-            tma_load_3d(k + L::kCode, &p.tm_v, bar(L::kBarVFull + s), 0, 0, ph2);
-          }
         }
       }
-      if (!ok) {
-        for (int i = max(0, g - L::kStages); i < g; ++i) {
+      if (ok && gk > gv) load_v(ph, n_pages);
+      if (!ok) {  // copies in flight end before shared memory is left
+        for (int i = max(0, gk - L::kStages); i < gk; ++i)
           mbar_wait_drain(bar(L::kBarKFull + i % L::kStages), (i / L::kStages) & 1, wc.limit_ns);
+        for (int i = max(0, gv - L::kStages); i < gv; ++i)
           mbar_wait_drain(bar(L::kBarVFull + i % L::kStages), (i / L::kStages) & 1, wc.limit_ns);
-        }
+        cp_async_wait_all();
       }
     }
   } else if (warp == kWarpMma) {
@@ -290,136 +336,88 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
     constexpr uint32_t idesc_s = make_idesc_e2m1_e4m3(128, L::NS, false, false);
     constexpr uint32_t idesc_o = make_idesc_e2m1_e4m3(128, L::NO, true, true);
     auto wt = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, wc)); };
-    auto kaddr = [&](int g) { return base + L::kKV + (g % L::kStages) * 2 * L::kCode; };
     auto issue_s = [&](int g) {  // S^T = K (q terms)^T, the four groups of 32 channels apart
-      const uint32_t k = kaddr(g), d_t = tmem + L::kColS + (g % NB) * 4 * L::NS;
+      const uint32_t k = base + L::kK + (g % L::kStages) * L::kCode, d_t = tmem + L::kColS + (g % NB) * 4 * L::kSet;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        mma_ss_f8(d_t + ks * L::NS, make_sdesc(k + ks * 32, 16, 1024), make_sdesc(base + L::kQ + ks * 32, 16, 1024),
-                  idesc_s, 0);
+        mma_ss_f8(d_t + (L::kPair ? ks / 2 * L::NS : ks * L::NS), make_sdesc(k + ks * 32, 16, 1024),
+                  make_sdesc(base + L::kQ + ks * 32, 16, 1024), idesc_s, L::kPair ? ks & 1 : 0);
       tc_commit(bar(L::kBarSFull + (g & 1)));
+      tc_commit(bar(L::kBarKEmpty + g % L::kStages));
     };
     auto issue_o = [&](int g) {  // O^T = V^T (p terms)^T over the tile's rows
-      const uint32_t v = kaddr(g) + L::kCode, d_t = tmem + L::kColO + (g % NB) * L::NO;
+      const uint32_t v = base + L::kV + (g % L::kStages) * L::kCode, d_t = tmem + L::kColO + (g % NB) * L::NO;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
         mma_ss_f8(d_t, make_sdesc(v + ks * 32 * 128, 16, 1024), make_pdesc<L::PW>(base + L::kP + ks * 32 * L::PW), idesc_o,
                   ks > 0);
-      tc_commit(bar(L::kBarEmpty + g % L::kStages));
       tc_commit(bar(L::kBarOFull));
+      tc_commit(bar(L::kBarVEmpty + g % L::kStages));
     };
-    bool ok = true;
-    int g = 0, seg = 0;
-    Walk w = w0;
-    Seg sg;
-    while (ok && next_seg<TS>(p, Hr, w, sg)) {
-      const int cnt = sg.t1 - sg.t0;
-      ok = wt(L::kBarQFull, seg & 1) && wt(L::kBarKFull + g % L::kStages, (g / L::kStages) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      issue_s(g);
-      for (int i = 0; i < cnt; ++i, ++g) {
-        auto next_s = [&] {
-          if (i + 1 < cnt) {
-            ok = wt(L::kBarKFull + (g + 1) % L::kStages, ((g + 1) / L::kStages) & 1);
-            if (!ok) return;
-            tc_fence_after();
-            issue_s(g + 1);
-          }
-        };
-        if (NB == 2) next_s();  // (with one buffer S of this tile has to be read first: P says so)
-        if (!ok) break;
-        ok = wt(L::kBarPFull, g & 1) && wt(L::kBarVFull + g % L::kStages, (g / L::kStages) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        issue_o(g);
-        if (NB == 1) next_s();
-        if (!ok) break;
-      }
-      ++seg;
-    }
-    tc_commit(bar(L::kBarDrain));
-    mbar_wait_drain(bar(L::kBarDrain), 0, wc.limit_ns);
-  } else if (warp == kWarpScale) {
-    // ------------------------------------------------------------ scale warp
-    // The power of two above the largest V scale of each group of channels in the
-    // tile.  (Rows behind the request's end hold anything.)
-    bool ok = true;
-    int g = 0;
-    Walk w = w0;
-    Seg sg;
-    while (ok && next_seg<TS>(p, Hr, w, sg)) {
-      for (int t = sg.t0; t < sg.t1; ++t, ++g) {
-        const int s = g % L::kStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarKFull + s), (g / L::kStages) & 1, wc));
-        if (!ok) break;
-        const uint4* sc = reinterpret_cast<const uint4*>(sbase + L::kSc + s * 2 * L::kScl + L::kScl);
-        const int live = sg.len - (t << TS);  // tokens of the tile that there are, or more
-        uint32_t a = 0, b = 0;                // largest magnitudes of groups 0 and 1, 2 and 3, as bits
+    // The power of two above the largest V scale of each group of channels in tile t.
+    // (Rows behind the request's end hold anything.)
+    auto norms = [&](int g, const Seg& sg, int t) {
+      const int s = g % L::kStages;
+      if (!wt(L::kBarCFull + s, (g / L::kStages) & 1)) return false;
+      const uint4* sc = reinterpret_cast<const uint4*>(sbase + L::kSc + s * 2 * L::kScl + L::kScl);
+      const int live = sg.len - (t << TS);  // tokens of the tile that there are, or more
+      uint32_t a = 0, b = 0;                // largest magnitudes of groups 0 and 1, 2 and 3, as bits
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 v = sc[i * 32 + lane];  // rows 2 (32 i + lane) and the next
-          const int tok = 2 * (i * 32 + lane) * TPR;
-          if (tok < live) a = max_u16x2(a, v.x & 0x7fff7fffu);
-          if (tok + TPR - 1 < live) b = max_u16x2(b, v.y & 0x7fff7fffu);
-          if (tok + TPR < live) a = max_u16x2(a, v.z & 0x7fff7fffu);
-          if (tok + 2 * TPR - 1 < live) b = max_u16x2(b, v.w & 0x7fff7fffu);
-        }
-        const uint32_t top[4] = {__reduce_max_sync(0xffffffffu, a & 0xffffu), __reduce_max_sync(0xffffffffu, a >> 16),
-                                 __reduce_max_sync(0xffffffffu, b & 0xffffu), __reduce_max_sync(0xffffffffu, b >> 16)};
-        if (lane < 4) {
-          const uint32_t m = lane == 0 ? top[0] : (lane == 1 ? top[1] : (lane == 2 ? top[2] : top[3]));
-          // (a NaN among them says nothing of the others: its own scale makes its group a NaN)
-          const int e = min(max((int)(m >> 7) - 126, -100), 100);
-          float* n = reinterpret_cast<float*>(sbase + L::kNorm + s * 32);
-          n[lane] = pow2f(-e);
-          n[4 + lane] = pow2f(e);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kBarNFull + s));
+      for (int i = 0; i < 2; ++i) {
+        const uint4 v = sc[i * 32 + lane];  // rows 2 (32 i + lane) and the next
+        const int tok = 2 * (i * 32 + lane) * TPR;
+        if (tok < live) a = max_u16x2(a, v.x & 0x7fff7fffu);
+        if (tok + TPR - 1 < live) b = max_u16x2(b, v.y & 0x7fff7fffu);
+        if (tok + TPR < live) a = max_u16x2(a, v.z & 0x7fff7fffu);
+        if (tok + 2 * TPR - 1 < live) b = max_u16x2(b, v.w & 0x7fff7fffu);
       }
-    }
-  } else {
-    // ------------------------------------------------------------ softmax
-    const int kl = threadIdx.x;  // row of the tile = TMEM lane of S^T; channel of the row = lane of O^T
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    const uint32_t tS = tmem + lane_off + L::kColS, tO = tmem + lane_off + L::kColO + warp * L::NG;
-    float* xm = reinterpret_cast<float*>(sbase + L::kXm);
-    float* xl = reinterpret_cast<float*>(sbase + L::kXl);
-    float* qs_s = reinterpret_cast<float*>(sbase + L::kQs);
-    int* qi_s = reinterpret_cast<int*>(sbase + L::kQi);
-    const int R = p.Nq * p.G;
-    uint8_t* prow = sbase + L::kP;
-    bool ok = true;
-    int g = 0, seg = 0;
-    Walk w = w0;
-    Seg sg;
-    while (ok && next_seg<TS>(p, Hr, w, sg)) {
-      const int len = sg.len;
+      const uint32_t top[4] = {__reduce_max_sync(0xffffffffu, a & 0xffffu), __reduce_max_sync(0xffffffffu, a >> 16),
+                               __reduce_max_sync(0xffffffffu, b & 0xffffu), __reduce_max_sync(0xffffffffu, b >> 16)};
+      if (lane < 4) {
+        const uint32_t m = lane == 0 ? top[0] : (lane == 1 ? top[1] : (lane == 2 ? top[2] : top[3]));
+        // (a NaN among them says nothing of the others: its own scale makes its group a NaN)
+        const int e = min(max((int)(m >> 7) - 126, -100), 100);
+        float* n = reinterpret_cast<float*>(sbase + L::kNorm + s * 32);
+        n[lane] = pow2f(-e);
+        n[4 + lane] = pow2f(e);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kBarNFull + s));
+      return true;
+    };
+    // The q terms of a segment's row block, eight lanes to a row: loaded (early), then
+    // written where the last segment's products are done.
+    constexpr int E = D / 8, kPass = RP / 4;  // elements per lane; four rows a pass
+    uint4 qv[kPass][E / 8];
+    auto load_q = [&](const Seg& sg) {
       const int h = sg.hr / p.n_rb, rb = sg.hr % p.n_rb;
-      // ---- the q terms of the row block: eight lanes to a row
-      if (kl < RP * 8) {
-        constexpr int E = D / 8;  // elements per lane
-        const int r = kl >> 3, c = kl & 7, idx = rb * RP + r;
-        const int i = idx / p.G, hq = h * p.G + idx % p.G;
+#pragma unroll
+      for (int ps = 0; ps < kPass; ++ps) {
+        const int idx = rb * RP + ps * 4 + (lane >> 3), i = idx / p.G, hq = h * p.G + idx % p.G;
+#pragma unroll
+        for (int j = 0; j < E / 8; ++j) {
+          qv[ps][j] = make_uint4(0, 0, 0, 0);
+          if (idx < p.Nq * p.G)
+            qv[ps][j] = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) +
+                                                       ((((size_t)sg.b * p.Nq + i) * p.Hq + hq) * D + (lane & 7) * E) * 2)[j];
+        }
+      }
+    };
+    auto put_q = [&](const Seg& sg) {
+      const int rb = sg.hr % p.n_rb, c = lane & 7;
+#pragma unroll
+      for (int ps = 0; ps < kPass; ++ps) {
+        const int r = ps * 4 + (lane >> 3);
         float f[E];
-        if (idx < R) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) +
-                                                            ((((size_t)sg.b * p.Nq + i) * p.Hq + hq) * D + c * E) * 2);
 #pragma unroll
-          for (int j = 0; j < E / 8; ++j) {
-            const uint4 v = src[j];
-            const uint32_t* wv = &v.x;
+        for (int j = 0; j < E / 8; ++j) {
+          const uint32_t* wv = &qv[ps][j].x;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 x = unpack2<BF16>(wv[e]);
-              f[j * 8 + 2 * e] = x.x;
-              f[j * 8 + 2 * e + 1] = x.y;
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = unpack2<BF16>(wv[e]);
+            f[j * 8 + 2 * e] = x.x;
+            f[j * 8 + 2 * e + 1] = x.y;
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < E; ++j) f[j] = 0.f;
         }
         uint32_t top = 0;  // largest magnitude, as bits (inf and NaN above all numbers)
 #pragma unroll
@@ -447,7 +445,10 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
           }
 #pragma unroll
           for (int half = 0; half < TPR; ++half) {  // (d = 64: against both tokens of a row)
-            uint32_t off = (uint32_t)((t * RP + r) * 128 + half * 64 + c * E);
+            const uint32_t byte = half * 64 + c * E;
+            // (sets by twos: rows 0-7 hold the even groups, 8-15 the odd ones)
+            const uint32_t row = t * RP + r + (L::kPair ? ((byte >> 5) & 1) * 8 : 0);
+            uint32_t off = row * 128 + byte;
             off ^= ((off >> 7) & 7u) << 4;
             if constexpr (E == 16)
               *reinterpret_cast<uint4*>(sbase + L::kQ + off) = make_uint4(cw[0], cw[1], cw[2], cw[3]);
@@ -456,14 +457,77 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
           }
         }
         if (c == 0) {
-          qs_s[r] = bad ? __uint_as_float(0x7fc00000u) : pow2f(e) * p.scale * kLog2e;
-          qi_s[r] = i;
+          reinterpret_cast<float*>(sbase + L::kQs)[r] = bad ? __uint_as_float(0x7fc00000u) : pow2f(e) * p.scale * kLog2e;
+          reinterpret_cast<int*>(sbase + L::kQi)[r] = (rb * RP + r) / p.G;
         }
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(L::kBarQFull));
-      ok = named_bar_and(kWgBar, 128, ok);
+      __syncwarp();
+    };
+    if constexpr (L::kPair) {  // (the zeros of the sets by twos stay)
+      for (int i = lane; i < L::NS * 128 / 16; i += 32) reinterpret_cast<uint4*>(sbase + L::kQ)[i] = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+    }
+    bool ok = true;
+    int g = 0;
+    Walk w = w0;
+    Seg sg;
+    bool more = next_seg<TS>(p, Hr, w, sg);
+    if (more) load_q(sg);
+    while (more) {
+      put_q(sg);
+      ok = wt(L::kBarKFull + g % L::kStages, (g / L::kStages) & 1);
       if (!ok) break;
+      tc_fence_after();
+      issue_s(g);
+      ok = norms(g, sg, sg.t0);
+      if (!ok) break;
+      const Seg now = sg;
+      more = next_seg<TS>(p, Hr, w, sg);
+      if (more) load_q(sg);
+      for (int t = now.t0; t < now.t1; ++t, ++g) {
+        auto next_s = [&] {
+          if (t + 1 < now.t1) {
+            ok = wt(L::kBarKFull + (g + 1) % L::kStages, ((g + 1) / L::kStages) & 1);
+            if (!ok) return;
+            tc_fence_after();
+            issue_s(g + 1);
+            ok = norms(g + 1, now, t + 1);
+          }
+        };
+        if (NB == 2) next_s();  // (with one buffer S of this tile has to be read first: P says so)
+        if (!ok) break;
+        ok = wt(L::kBarPFull, g & 1) && wt(L::kBarVFull + g % L::kStages, (g / L::kStages) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        issue_o(g);
+        if (NB == 1) next_s();
+        if (!ok) break;
+      }
+      if (!ok) break;
+    }
+    tc_commit(bar(L::kBarDrain));
+    mbar_wait_drain(bar(L::kBarDrain), 0, wc.limit_ns);
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int kl = threadIdx.x;  // row of the tile = TMEM lane of S^T; channel of the row = lane of O^T
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t tS = tmem + lane_off + L::kColS, tO = tmem + lane_off + L::kColO + warp * L::NG;
+    float* xm = reinterpret_cast<float*>(sbase + L::kXm);
+    float* xl = reinterpret_cast<float*>(sbase + L::kXl);
+    float* qs_s = reinterpret_cast<float*>(sbase + L::kQs);
+    int* qi_s = reinterpret_cast<int*>(sbase + L::kQi);
+    const int R = p.Nq * p.G;
+    uint8_t* prow = sbase + L::kP;
+    bool ok = true;
+    int g = 0, seg = 0;
+    Walk w = w0;
+    Seg sg;
+    while (ok && next_seg<TS>(p, Hr, w, sg)) {
+      const int len = sg.len;
+      const int h = sg.hr / p.n_rb, rb = sg.hr % p.n_rb;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQFull), seg & 1, wc));  // (row factors and indices)
       float m[RP], l[RP], acc[RP];
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
@@ -495,9 +559,9 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
         const int st = g % L::kStages, kv0 = (t << TS) + kl * TPR;  // first token of this row
         const bool later = t > sg.t0;  // the tile before is of this segment, its O^T outstanding
         const uint32_t ph = (g / L::kStages) & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarSFull + (g & 1)), (g >> 1) & 1, wc) &&
-                                         mbar_wait(bar(L::kBarKFull + st), ph, wc) && mbar_wait(bar(L::kBarNFull + st), ph, wc));
-        float x[TPR][RP];  // scores in log2 units
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarSFull + (g & 1)), (g >> 1) & 1, wc) &&
+                                         mbar_wait(bar(L::kBarCFull + st), ph, wc) && mbar_wait(bar(L::kBarNFull + st), ph, wc));
+        __align__(8) float x[TPR][RP];  // scores in log2 units
         float f[4], lv[TPR], mul = 0.f;
         if (ok) {
           tc_fence_after();
@@ -520,26 +584,49 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
             lv[0] = __log2f(fmaxf(fmaxf(f[0], f[1]), 0x1p-30f));
             lv[1] = __log2f(fmaxf(fmaxf(f[2], f[3]), 0x1p-30f));
           }
+          constexpr int kAt = L::NG <= 12 ? 4 : (L::NG <= 16 ? 2 : 1);  // groups loaded at a time
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t r_[L::NG];
-            tmem_ld_n<L::NG>(tS + (g % NB) * 4 * L::NS + k * L::NS, r_);
+          for (int k0 = 0; k0 < 4; k0 += kAt) {
+            uint32_t r_[kAt * L::NG];
+            const uint32_t from = tS + (g % NB) * 4 * L::kSet + k0 * L::kSet;
+            if constexpr (L::kSet == L::NG) {
+              tmem_ld_n<kAt * L::NG>(from, r_);
+            } else {
+#pragma unroll
+              for (int k = 0; k < kAt; ++k) tmem_ld_n<L::NG>(from + k * L::kSet, r_ + k * L::NG);
+            }
             tmem_ld_wait();
-            reg_fence<L::NG>(r_);
+            reg_fence<kAt * L::NG>(r_);
             constexpr int per = 4 / TPR;
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
-              float s = __uint_as_float(r_[r]), c = __uint_as_float(r_[RP + r]);
-              if constexpr (NP == 3) c = fmaf(__uint_as_float(r_[2 * RP + r]), 0.0625f, c);
-              s = fmaf(c, 0.0625f, s);
-              x[k / per][r] = k % per == 0 ? s * ks[k] : fmaf(s, ks[k], x[k / per][r]);
+            for (int k = 0; k < kAt; ++k) {
+              const int j = (k0 + k) / per;
+              const float2 k2 = make_float2(ks[k0 + k], ks[k0 + k]);
+#pragma unroll
+              for (int r = 0; r < RP; r += 2) {
+                auto term = [&](int t2) {
+                  const uint32_t* z = r_ + k * L::NG + t2 * RP + r;
+                  return make_float2(__uint_as_float(z[0]), __uint_as_float(z[1]));
+                };
+                const float2 sixteenth = make_float2(0.0625f, 0.0625f);
+                float2 c = term(1);
+                if constexpr (NP == 3) c = fma2(term(2), sixteenth, c);
+                const float2 s2 = fma2(c, sixteenth, term(0));
+                float2* to = reinterpret_cast<float2*>(&x[j][r]);
+                *to = (k0 + k) % per == 0 ? mul2(s2, k2) : fma2(s2, k2, *to);
+              }
             }
           }
           tc_fence_before();
 #pragma unroll
-          for (int j = 0; j < TPR; ++j)
+          for (int r = 0; r < RP; r += 2) {
+            const float2 q2 = *reinterpret_cast<const float2*>(qs_s + r);
 #pragma unroll
-            for (int r = 0; r < RP; ++r) x[j][r] *= qs_s[r];
+            for (int j = 0; j < TPR; ++j) {
+              float2* to = reinterpret_cast<float2*>(&x[j][r]);
+              *to = mul2(*to, q2);
+            }
+          }
           if ((t << TS) + (1 << TS) - 1 > lim0) {
 #pragma unroll
             for (int r = 0; r < RP; ++r) {
@@ -566,6 +653,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
         if (ok && later) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarOFull), (g - 1) & 1, wc));
         ok = named_bar_and(kWgBar, 128, ok);
         if (!ok) break;
+        if (threadIdx.x == 0) mbar_arrive(bar(L::kBarCEmpty + st));  // (every warp has its scales)
         if (NB == 1 && later) add_o(g - 1);  // (before P lets the next O^T overwrite it)
         float al_t[RP], be_t[RP];
         uint32_t code[4][NP][RP / 4];  // terms of p f for the four groups, four rows to a word
@@ -599,16 +687,28 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float* pr = x[k * TPR / 4] + r0;
-            float2 a = make_float2(pr[0] * f[k], pr[1] * f[k]), b = make_float2(pr[2] * f[k], pr[3] * f[k]);
+            const float2* pr = reinterpret_cast<const float2*>(&x[k * TPR / 4][r0]);
+            const float2 f2 = make_float2(f[k], f[k]);
+            float2 a = mul2(pr[0], f2), b = mul2(pr[1], f2);
+            uint32_t lo = pack_e4m3(a.x, a.y), hi = pack_e4m3(b.x, b.y);
+            code[k][0][r0 / 4] = lo | (hi << 16);
+            if constexpr (NP == 2) {
+              // (what the first term leaves, in fp16: 16 p f to 2^-11 less 16 times the term)
+              const float2 g2 = make_float2(16.f * f[k], 16.f * f[k]);
+              a = mul2(pr[0], g2);
+              b = mul2(pr[1], g2);
+              lo = rest_e4m3(pack2<false>(a.x, a.y), lo);
+              hi = rest_e4m3(pack2<false>(b.x, b.y), hi);
+              code[k][1][r0 / 4] = lo | (hi << 16);
+            } else {
 #pragma unroll
-            for (int t2 = 0; t2 < NP; ++t2) {
-              const uint32_t lo = pack_e4m3(a.x, a.y), hi = pack_e4m3(b.x, b.y);
-              code[k][t2][r0 / 4] = lo | (hi << 16);
-              if (t2 + 1 < NP) {
-                const float2 d0 = unpack_e4m3(lo), d1 = unpack_e4m3(hi);
-                a = make_float2((a.x - d0.x) * 16.f, (a.y - d0.y) * 16.f);
-                b = make_float2((b.x - d1.x) * 16.f, (b.y - d1.y) * 16.f);
+              for (int t2 = 1; t2 < NP; ++t2) {
+                const float2 d0 = unpack_e4m3(lo), d1 = unpack_e4m3(hi), mul16 = make_float2(16.f, 16.f);
+                a = mul2(sub2(a, d0), mul16);
+                b = mul2(sub2(b, d1), mul16);
+                lo = pack_e4m3(a.x, a.y);
+                hi = pack_e4m3(b.x, b.y);
+                code[k][t2][r0 / 4] = lo | (hi << 16);
               }
             }
           }
@@ -733,8 +833,8 @@ cudaError_t launch_kv4_append(Kv4AppendArgs a, int sms, cudaStream_t stream) {
 int kv4_rows(int R, bool bf16) { return R <= 4 ? 4 : (R <= 8 || !bf16 ? 8 : 16); }
 
 // All CTAs resident at once, no more than there can be tiles.
-int kv4_grid(int sms, long long max_units) {
-  long long g = 2ll * sms;
+int kv4_grid(int rp, bool bf16, int sms, long long max_units) {
+  long long g = (rp == 4 && bf16 ? 3ll : 2ll) * sms;
   if (g > kKvMaxCtas) g = kKvMaxCtas;
   if (g > max_units) g = max_units;
   return (int)(g < 1 ? 1 : g);

@@ -265,7 +265,7 @@ void kv_rows(Args* a, long long tok) {
 }
 cudaError_t launch_kv4_append(Kv4AppendArgs a, int sms, cudaStream_t stream);
 int kv4_rows(int R, bool bf16);
-int kv4_grid(int sms, long long max_units);
+int kv4_grid(int rp, bool bf16, int sms, long long max_units);
 cudaError_t launch_kv4_split(const KvDecArgs& a, cudaStream_t stream);
 
 // Cached keys and values as packed 16-bit rows (attn_kvread.cu).

@@ -163,6 +163,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
       : "memory");
 }
 
+// 16 bytes global -> shared, the first `n` of them read, the others zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// Arrives once on `bar` (counted in its init) when this thread's cp_async16 copies so far are there.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Barrier over `count` threads (a multiple of 32, whole warps) on hardware
 // barrier `id` that also ANDs a flag across them: every participant gets the
 // same answer, so code after it can branch uniformly (for example on whether
