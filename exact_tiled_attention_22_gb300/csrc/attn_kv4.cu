@@ -134,18 +134,21 @@ struct Kv4Layout {
   static constexpr int kSc = kV + kStages * kCode;
   static constexpr int kNorm = kSc + kStages * 2 * kScl;  // [stages][4] 2^-e, [4] 2^e: powers above the groups' largest V scale
   static constexpr int kXm = kNorm + kStages * 32;    // [2][4][RP] fp32 row maxima of the warps
-  static constexpr int kXl = kXm + 2 * 4 * RP * 4;    // [4][RP] fp32 row sums
+  static constexpr int kXl = kXm + 2 * 4 * RP * 4;    // [RP][4] fp32 row sums of the warps
   static constexpr int kQs = kXl + 4 * RP * 4;        // [RP] fp32 row factors
-  static constexpr int kQi = kQs + RP * 4;            // [RP] int query index of the row
-  static constexpr int kBar = kQi + RP * 4;
+  // what the MMA warp tells the softmax warps of a segment, for two of them in turn: int4 (length, tiles
+  // t0 .. t1 - 1 of nt); of a row int2 (place in o, in lse; -1: no row) and the index of its query, a byte
+  static constexpr int kInfo = kQs + RP * 4;
+  static constexpr int kRow = kInfo + 2 * 16;
+  static constexpr int kQi = kRow + 2 * RP * 8;
+  static constexpr int kBar = kQi + 2 * RP;
   static constexpr int kBarKFull = 0;
   static constexpr int kBarKEmpty = kBarKFull + kStages;
   static constexpr int kBarVFull = kBarKEmpty + kStages;
   static constexpr int kBarVEmpty = kBarVFull + kStages;
   static constexpr int kBarCFull = kBarVEmpty + kStages;   // scales
   static constexpr int kBarCEmpty = kBarCFull + kStages;
-  static constexpr int kBarNFull = kBarCEmpty + kStages;
-  static constexpr int kBarSFull = kBarNFull + kStages;  // [2]
+  static constexpr int kBarSFull = kBarCEmpty + kStages;   // [2] S^T and the scales' maxima
   static constexpr int kBarPFull = kBarSFull + 2;
   static constexpr int kBarOFull = kBarPFull + 1;
   static constexpr int kBarQFull = kBarOFull + 1;
@@ -225,13 +228,12 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
       mbar_init(bar(L::kBarVEmpty + s), 1);
       mbar_init(bar(L::kBarCFull + s), 32);
       mbar_init(bar(L::kBarCEmpty + s), 1);
-      mbar_init(bar(L::kBarNFull + s), 1);
     }
-    mbar_init(bar(L::kBarSFull), 1);
-    mbar_init(bar(L::kBarSFull + 1), 1);
-    mbar_init(bar(L::kBarPFull), 128);
+    mbar_init(bar(L::kBarSFull), 2);
+    mbar_init(bar(L::kBarSFull + 1), 2);
+    mbar_init(bar(L::kBarPFull), 4);
     mbar_init(bar(L::kBarOFull), 1);
-    mbar_init(bar(L::kBarQFull), 32);
+    mbar_init(bar(L::kBarQFull), 1);
     mbar_init(bar(L::kBarDrain), 1);
     fence_mbar_init();
     tma_prefetch(&p.tm_k);
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
         n[4 + lane] = pow2f(e);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kBarNFull + s));
+      if (lane == 0) mbar_arrive(bar(L::kBarSFull + (g & 1)));
       return true;
     };
     // The q terms of a segment's row block, eight lanes to a row: loaded (early), then
@@ -403,8 +405,11 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
         }
       }
     };
-    auto put_q = [&](const Seg& sg) {
-      const int rb = sg.hr % p.n_rb, c = lane & 7;
+    auto put_info = [&](int seg, int len, int t0, int t1, int nt) {
+      if (lane == 0) *reinterpret_cast<int4*>(sbase + L::kInfo + (seg & 1) * 16) = make_int4(len, t0, t1, nt);
+    };
+    auto put_q = [&](const Seg& sg, int seg) {
+      const int h = sg.hr / p.n_rb, rb = sg.hr % p.n_rb, c = lane & 7;
 #pragma unroll
       for (int ps = 0; ps < kPass; ++ps) {
         const int r = ps * 4 + (lane >> 3);
@@ -458,25 +463,29 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
         }
         if (c == 0) {
           reinterpret_cast<float*>(sbase + L::kQs)[r] = bad ? __uint_as_float(0x7fc00000u) : pow2f(e) * p.scale * kLog2e;
-          reinterpret_cast<int*>(sbase + L::kQi)[r] = (rb * RP + r) / p.G;
+          const int idx = rb * RP + r, i = idx / p.G, hq = h * p.G + idx % p.G;
+          reinterpret_cast<int2*>(sbase + L::kRow)[(seg & 1) * RP + r] =
+              idx < p.Nq * p.G ? make_int2((sg.b * p.Nq + i) * p.Hq + hq, (sg.b * p.Hq + hq) * p.Nq + i) : make_int2(-1, -1);
+          sbase[L::kQi + (seg & 1) * RP + r] = (uint8_t)min(i, 127);
         }
       }
+      put_info(seg, sg.len, sg.t0, sg.t1, sg.nt);
       fence_proxy_async_smem();
-      mbar_arrive(bar(L::kBarQFull));
       __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kBarQFull));
     };
     if constexpr (L::kPair) {  // (the zeros of the sets by twos stay)
       for (int i = lane; i < L::NS * 128 / 16; i += 32) reinterpret_cast<uint4*>(sbase + L::kQ)[i] = make_uint4(0, 0, 0, 0);
       __syncwarp();
     }
     bool ok = true;
-    int g = 0;
+    int g = 0, seg = 0;
     Walk w = w0;
     Seg sg;
     bool more = next_seg<TS>(p, Hr, w, sg);
     if (more) load_q(sg);
     while (more) {
-      put_q(sg);
+      put_q(sg, seg++);
       ok = wt(L::kBarKFull + g % L::kStages, (g / L::kStages) & 1);
       if (!ok) break;
       tc_fence_after();
@@ -507,6 +516,11 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
       }
       if (!ok) break;
     }
+    if (ok) {  // no more segments
+      put_info(seg, 0, 0, 0, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kBarQFull));
+    }
     tc_commit(bar(L::kBarDrain));
     mbar_wait_drain(bar(L::kBarDrain), 0, wc.limit_ns);
   } else {
@@ -517,17 +531,17 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
     float* xm = reinterpret_cast<float*>(sbase + L::kXm);
     float* xl = reinterpret_cast<float*>(sbase + L::kXl);
     float* qs_s = reinterpret_cast<float*>(sbase + L::kQs);
-    int* qi_s = reinterpret_cast<int*>(sbase + L::kQi);
-    const int R = p.Nq * p.G;
     uint8_t* prow = sbase + L::kP;
     bool ok = true;
-    int g = 0, seg = 0;
-    Walk w = w0;
-    Seg sg;
-    while (ok && next_seg<TS>(p, Hr, w, sg)) {
-      const int len = sg.len;
-      const int h = sg.hr / p.n_rb, rb = sg.hr % p.n_rb;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQFull), seg & 1, wc));  // (row factors and indices)
+    int g = 0;
+    for (int seg = 0;; ++seg) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQFull), seg & 1, wc));
+      if (!named_bar_and(kWgBar, 128, ok)) break;
+      const int4 info = *reinterpret_cast<const int4*>(sbase + L::kInfo + (seg & 1) * 16);
+      const int len = info.x, t0 = info.y, t1 = info.z;
+      if (t0 == t1) break;
+      const int2* rows = reinterpret_cast<const int2*>(sbase + L::kRow) + (seg & 1) * RP;
+      const uint8_t* qi = sbase + L::kQi + (seg & 1) * RP;
       float m[RP], l[RP], acc[RP];
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
@@ -555,12 +569,11 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
           acc[r] = fmaf(o, be[r], acc[r]);
         }
       };
-      for (int t = sg.t0; t < sg.t1; ++t, ++g) {
+      for (int t = t0; t < t1; ++t, ++g) {
         const int st = g % L::kStages, kv0 = (t << TS) + kl * TPR;  // first token of this row
-        const bool later = t > sg.t0;  // the tile before is of this segment, its O^T outstanding
-        const uint32_t ph = (g / L::kStages) & 1;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarSFull + (g & 1)), (g >> 1) & 1, wc) &&
-                                         mbar_wait(bar(L::kBarCFull + st), ph, wc) && mbar_wait(bar(L::kBarNFull + st), ph, wc));
+        const bool later = t > t0;  // the tile before is of this segment, its O^T outstanding
+        // S^T, and with the scales' maxima the scales: the MMA warp has waited for them
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarSFull + (g & 1)), (g >> 1) & 1, wc));
         __align__(8) float x[TPR][RP];  // scores in log2 units
         float f[4], lv[TPR], mul = 0.f;
         if (ok) {
@@ -630,7 +643,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
           if ((t << TS) + (1 << TS) - 1 > lim0) {
 #pragma unroll
             for (int r = 0; r < RP; ++r) {
-              const int lim = p.causal ? min(len - 1, len - p.Nq + qi_s[r]) : len - 1;
+              const int lim = p.causal ? min(len - 1, len - p.Nq + (int)qi[r]) : len - 1;
 #pragma unroll
               for (int j = 0; j < TPR; ++j)
                 if (kv0 + j > lim) x[j][r] = -INFINITY;
@@ -720,7 +733,8 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
           *reinterpret_cast<uint4*>(prow + p_off<L::PW>(kl, c)) = make_uint4(cw[4 * c], cw[4 * c + 1], cw[4 * c + 2], cw[4 * c + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(bar(L::kBarPFull));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarPFull));
         if (NB == 2 && later) add_o(g - 1);
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
@@ -730,12 +744,23 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
       }
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarOFull), (g - 1) & 1, wc));
       if (ok) add_o(g - 1);
-      // ---- end of the segment: row sums over the tile's rows, then O
+      // ---- end of the segment: row sums over the tile's rows, then O.  A lane keeps half of its rows and
+      // sends the others, until it has one, whose sum over the lanes that hold it goes on.
+      {
+        int row = 0;
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
+        for (int n = RP / 2, o = 16; n > 0; n >>= 1, o >>= 1) {
+          const bool up = lane & o;
+          row = row * 2 + (up ? 1 : 0);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-        if (lane == 0) xl[warp * RP + r] = l[r];
+          for (int r = 0; r < n; ++r) {
+            const float keep = up ? l[n + r] : l[r], send = up ? l[r] : l[n + r];
+            l[r] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+        }
+#pragma unroll
+        for (int o = 16 / RP; o > 0; o >>= 1) l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+        if (lane % (32 / RP) == 0) xl[row * 4 + warp] = l[0];
       }
       // (d = 64: lanes 64 to 127 hold the second token's part; P's rows are free)
       float* half = reinterpret_cast<float*>(prow);
@@ -745,22 +770,18 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
       }
       ok = named_bar_and(kWgBar, 128, ok);
       if (!ok) break;
-      const bool whole = sg.t1 - sg.t0 == sg.nt;
+      const bool whole = t1 - t0 == info.w;
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
-        const int idx = rb * RP + r;
-        if (idx >= R) break;
-        const float lt = (xl[r] + xl[RP + r]) + (xl[2 * RP + r] + xl[3 * RP + r]);
+        const int2 at = rows[r];
+        const float4 l4 = *reinterpret_cast<const float4*>(xl + r * 4);
+        const float lt = (l4.x + l4.y) + (l4.z + l4.w);
         const float sum = TPR == 2 && kl < 64 ? acc[r] + half[r * 64 + kl] : acc[r];
+        if (at.x < 0) continue;
         if (whole) {
-          const int i = idx / p.G, hq = h * p.G + idx % p.G;
-          const float v = lt != 0.f ? sum / lt : 0.f;
-          if (kl < D) {
-            const uint32_t c = pack2<BF16>(v, 0.f);
-            reinterpret_cast<uint16_t*>(p.o)[(((size_t)sg.b * p.Nq + i) * p.Hq + hq) * D + kl] = (uint16_t)c;
-          }
-          if (kl == 0)
-            p.lse[((size_t)sg.b * p.Hq + hq) * p.Nq + i] = lt != 0.f ? (m[r] + __log2f(lt)) * kLn2 : -INFINITY;
+          const float v = lt != 0.f ? __fdividef(sum, lt) : 0.f;
+          if (kl < D) reinterpret_cast<uint16_t*>(p.o)[(size_t)at.x * D + kl] = (uint16_t)pack2<BF16>(v, 0.f);
+          if (kl == 0) p.lse[at.y] = lt != 0.f ? (m[r] + __log2f(lt)) * kLn2 : -INFINITY;
         } else {
           const size_t part = ((size_t)blockIdx.x * 2 + (seg > 0 ? 1 : 0)) * RP + r;
           if (kl < D) p.ws_o[part * D + kl] = sum;
@@ -771,7 +792,6 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
         }
       }
       // (the next segment's P and row sums are written behind the barrier of its first tile)
-      ++seg;
     }
   }
   if (threadIdx.x == 0) griddep_launch_dependents();
