@@ -102,28 +102,29 @@ __global__ void __launch_bounds__(kAppThreads) attn_kv4_append_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ decode
-constexpr int kDecThreads = 192;  // warps 0-3 softmax, 4 producer, 5 MMA, query terms and scales
-constexpr int kWarpProd = 4, kWarpMma = 5;
-constexpr uint32_t kWgBar = 1;    // named barrier of the softmax warps
-
 __host__ __device__ constexpr int up1024(int x) { return (x + 1023) / 1024 * 1024; }
 
-// A row is 128 channels: a token (d = 128) or two (d = 64).  A tile is 128 rows.
-template <int D, int RP, int NP>
+// A row is 128 channels: a token (d = 128) or two (d = 64).  A tile is 128 rows.  WG
+// warpgroups of softmax take four query rows each.
+template <int D, int WG, int NP>
 struct Kv4Layout {
   static constexpr int TPR = 128 / D;                 // tokens to a row
   static constexpr int kTileShift = D == 128 ? 7 : 8; // tokens to a tile
-  static constexpr int NG = RP * NP;                  // operand rows: query rows times terms
+  static constexpr int RP = 4 * WG;                   // query rows
+  // warps: softmax, producer, MMA (with query terms and scale maxima)
+  static constexpr int kWarpProd = 4 * WG, kWarpMma = 4 * WG + 1, kWarps = 4 * WG + 2, kThreads = kWarps * 32;
+  static constexpr int N4 = 4 * NP;                   // operand rows of a warpgroup: its rows times terms
+  static constexpr int NG = RP * NP;                  // of all
   // S^T has a set of NG columns for each group of 32 channels.  M = 128 takes columns by 16: eight are
   // written by twos, a set with the next one (the other's rows of the query operand are zeros there).
   static constexpr bool kPair = NG == 8;
   static constexpr int NS = kPair ? 16 : (NG + 15) / 16 * 16;  // MMA columns
   static constexpr int kSet = kPair ? 8 : NS;         // columns from one set to the next
-  static constexpr int NO = 4 * NG;                   // O^T: likewise a set for each group
+  static constexpr int NO = 4 * NG;                   // O^T: a set for each warpgroup and group of channels
   static constexpr int PW = NO <= 32 ? 32 : (NO <= 64 ? 64 : 128);  // bytes of a P row, and its swizzle
-  // CTAs to an SM, by what shared memory, TMEM and registers leave
-  static constexpr int kCtas = PW == 32 ? 3 : 2;
-  static constexpr int kStages = PW == 64 ? 3 : 2;
+  // CTAs to an SM and stages, by what shared memory, TMEM and registers leave
+  static constexpr int kCtas = WG == 4 ? 1 : (PW == 32 ? 3 : 2);
+  static constexpr int kStages = WG == 4 ? 5 : (PW == 64 ? 3 : 2);
   static constexpr int kCode = 128 * 128;             // bytes of a tile's codes: 16 to 16 bytes, 8 of them filled
   static constexpr int kScl = 128 * 8;                // bytes of its scales: four bf16 a row
   static constexpr int kQ = 0;
@@ -133,9 +134,9 @@ struct Kv4Layout {
   static constexpr int kV = kK + kStages * kCode;
   static constexpr int kSc = kV + kStages * kCode;
   static constexpr int kNorm = kSc + kStages * 2 * kScl;  // [stages][4] 2^-e, [4] 2^e: powers above the groups' largest V scale
-  static constexpr int kXm = kNorm + kStages * 32;    // [2][4][RP] fp32 row maxima of the warps
-  static constexpr int kXl = kXm + 2 * 4 * RP * 4;    // [RP][4] fp32 row sums of the warps
-  static constexpr int kQs = kXl + 4 * RP * 4;        // [RP] fp32 row factors
+  static constexpr int kXm = kNorm + kStages * 32;    // [2][WG][4 warps][4 rows] fp32 row maxima
+  static constexpr int kXl = kXm + 2 * WG * 64;       // [RP][4 warps] fp32 row sums
+  static constexpr int kQs = kXl + RP * 16;           // [RP] fp32 row factors
   // what the MMA warp tells the softmax warps of a segment, for two of them in turn: int4 (length, tiles
   // t0 .. t1 - 1 of nt); of a row int2 (place in o, in lse; -1: no row) and the index of its query, a byte
   static constexpr int kInfo = kQs + RP * 4;
@@ -155,18 +156,18 @@ struct Kv4Layout {
   static constexpr int kBarDrain = kBarQFull + 1;
   static constexpr int kNumBars = kBarDrain + 1;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
-  static constexpr int kStart = kTmemSlot + 16;       // start of the CTA's range: long long u0, u1; int b, hr, t
-  static constexpr int kScan = kStart + 32;           // [6] warp sums
-  static constexpr int kSmem = kScan + 6 * 8;
+  static constexpr int kStart = kTmemSlot + 8;        // start of the CTA's range: long long u0, u1; int b, hr, t
+  static constexpr int kScan = kXm;                   // [kWarps] warp sums of the prologue
+  static constexpr int kSmem = kStart + 32;
   // TMEM: two buffers of S^T and of O^T where the columns are there, else one
-  static constexpr int kMaxCols = kCtas == 3 ? 128 : 256;
+  static constexpr int kMaxCols = kCtas == 3 ? 128 : (kCtas == 2 ? 256 : 512);
   static constexpr int kBufs = 2 * (4 * kSet + NO) <= kMaxCols ? 2 : 1;
-  static constexpr int kCols = kBufs * (4 * kSet + NO) <= 128 ? 128 : 256;
+  static constexpr int kCols = kBufs * (4 * kSet + NO) <= 128 ? 128 : (kBufs * (4 * kSet + NO) <= 256 ? 256 : 512);
   static constexpr int kColS = 0, kColO = kBufs * 4 * kSet;
   static_assert(kBufs * (4 * kSet + NO) <= kCols && kCols * kCtas <= 512, "TMEM budget");
   static_assert((kSmem + 1024) * kCtas <= 228 * 1024, "shared memory budget");
-  static_assert(NO % 16 == 0 && NO <= PW, "P rows");
-  static_assert(kBar % 8 == 0 && kNorm % 16 == 0 && kXm % 16 == 0 && kStart % 8 == 0 && kScan % 8 == 0, "alignment");
+  static_assert(NO % 16 == 0 && NO <= PW && kWarps * 8 <= 2 * WG * 64, "P rows, scan");
+  static_assert(kBar % 8 == 0 && kNorm % 16 == 0 && kXm % 16 == 0 && kInfo % 16 == 0 && kStart % 8 == 0, "alignment");
 };
 
 // Descriptor of the MN-major P operand: rows (keys) of PW bytes, PW-byte swizzle, 8-key
@@ -189,21 +190,40 @@ __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// e4m3 of (h16 - 16 t) for a pair: h16 fp16, t the e4m3 pair in the low 16 bits of w.
-__device__ __forceinline__ uint32_t rest_e4m3(uint32_t h16, uint32_t w) {
-  uint16_t r;
-  asm("{\n\t.reg .b32 t, m;\n\t"
-      "cvt.rn.f16x2.e4m3x2 t, %2;\n\t"
+// Four fp32 values to e4m3, from the lowest byte up.
+__device__ __forceinline__ uint32_t pack4_e4m3(float2 a, float2 b) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// e4m3 of (h - 16 t) for four values: h fp16 (two pairs), t the e4m3 values of w.
+__device__ __forceinline__ uint32_t rest4_e4m3(uint32_t h_lo, uint32_t h_hi, uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 a, b, m;\n\t"
+      "mov.b32 {lo, hi}, %3;\n\t"
+      "cvt.rn.f16x2.e4m3x2 a, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 b, hi;\n\t"
       "mov.b32 m, 0xcc00cc00;\n\t"  // -16
-      "fma.rn.f16x2 t, t, m, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 %0, t;\n\t}"
-      : "=h"(r) : "r"(h16), "h"((uint16_t)w));
+      "fma.rn.f16x2 a, a, m, %1;\n\t"
+      "fma.rn.f16x2 b, b, m, %2;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 lo, a;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 hi, b;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r) : "r"(h_lo), "r"(h_hi), "r"(w));
   return r;
 }
 
-template <int D, int RP, int NP>
-__global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn_kv4_split_kernel(const __grid_constant__ KvDecArgs p) {
-  using L = Kv4Layout<D, RP, NP>;
+constexpr float kNone = -1e30f;  // the maximum of scores that are all masked
+
+template <int D, int WG, int NP>
+__global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, WG, NP>::kCtas)
+    attn_kv4_split_kernel(const __grid_constant__ KvDecArgs p) {
+  using L = Kv4Layout<D, WG, NP>;
+  constexpr int RP = L::RP, kWarpProd = L::kWarpProd, kWarpMma = L::kWarpMma;
   constexpr bool BF16 = NP == 2;
   constexpr int TPR = L::TPR, TS = L::kTileShift, NB = L::kBufs;
   // (dynamic shared memory begins behind the 1024 bytes the system keeps: aligned as declared.
@@ -227,11 +247,11 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
       mbar_init(bar(L::kBarVFull + s), 1);
       mbar_init(bar(L::kBarVEmpty + s), 1);
       mbar_init(bar(L::kBarCFull + s), 32);
-      mbar_init(bar(L::kBarCEmpty + s), 1);
+      mbar_init(bar(L::kBarCEmpty + s), WG);
     }
     mbar_init(bar(L::kBarSFull), 2);
     mbar_init(bar(L::kBarSFull + 1), 2);
-    mbar_init(bar(L::kBarPFull), 4);
+    mbar_init(bar(L::kBarPFull), 4 * WG);
     mbar_init(bar(L::kBarOFull), 1);
     mbar_init(bar(L::kBarQFull), 1);
     mbar_init(bar(L::kBarDrain), 1);
@@ -244,7 +264,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
     tmem_relinquish();
   }
   griddep_wait();
-  deal_range<TS, kDecThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
+  deal_range<TS, L::kThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
                               reinterpret_cast<long long*>(sbase + L::kStart));
   tc_fence_before();
   __syncthreads();
@@ -389,12 +409,12 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
     };
     // The q terms of a segment's row block, eight lanes to a row: loaded (early), then
     // written where the last segment's products are done.
-    constexpr int E = D / 8, kPass = RP / 4;  // elements per lane; four rows a pass
-    uint4 qv[kPass][E / 8];
+    constexpr int E = D / 8;  // elements per lane; four rows, those of a warpgroup, at a time
+    uint4 qv[WG][E / 8];
     auto load_q = [&](const Seg& sg) {
       const int h = sg.hr / p.n_rb, rb = sg.hr % p.n_rb;
 #pragma unroll
-      for (int ps = 0; ps < kPass; ++ps) {
+      for (int ps = 0; ps < WG; ++ps) {
         const int idx = rb * RP + ps * 4 + (lane >> 3), i = idx / p.G, hq = h * p.G + idx % p.G;
 #pragma unroll
         for (int j = 0; j < E / 8; ++j) {
@@ -411,7 +431,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
     auto put_q = [&](const Seg& sg, int seg) {
       const int h = sg.hr / p.n_rb, rb = sg.hr % p.n_rb, c = lane & 7;
 #pragma unroll
-      for (int ps = 0; ps < kPass; ++ps) {
+      for (int ps = 0; ps < WG; ++ps) {
         const int r = ps * 4 + (lane >> 3);
         float f[E];
 #pragma unroll
@@ -452,7 +472,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
           for (int half = 0; half < TPR; ++half) {  // (d = 64: against both tokens of a row)
             const uint32_t byte = half * 64 + c * E;
             // (sets by twos: rows 0-7 hold the even groups, 8-15 the odd ones)
-            const uint32_t row = t * RP + r + (L::kPair ? ((byte >> 5) & 1) * 8 : 0);
+            const uint32_t row = ps * L::N4 + t * 4 + (lane >> 3) + (L::kPair ? ((byte >> 5) & 1) * 8 : 0);
             uint32_t off = row * 128 + byte;
             off ^= ((off >> 7) & 7u) << 4;
             if constexpr (E == 16)
@@ -525,27 +545,29 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
     mbar_wait_drain(bar(L::kBarDrain), 0, wc.limit_ns);
   } else {
     // ------------------------------------------------------------ softmax
-    const int kl = threadIdx.x;  // row of the tile = TMEM lane of S^T; channel of the row = lane of O^T
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    const uint32_t tS = tmem + lane_off + L::kColS, tO = tmem + lane_off + L::kColO + warp * L::NG;
-    float* xm = reinterpret_cast<float*>(sbase + L::kXm);
-    float* xl = reinterpret_cast<float*>(sbase + L::kXl);
-    float* qs_s = reinterpret_cast<float*>(sbase + L::kQs);
+    // All of a segment's barriers are passed by all warps, however a wait ends: the one over
+    // all warpgroups at its start and at its end, and within the tiles those of a warpgroup.
+    const int wg = warp >> 2, qw = warp & 3;
+    const int kl = threadIdx.x & 127;  // row of the tile = TMEM lane of S^T; channel of the row = lane of O^T
+    const uint32_t lane_off = (uint32_t)(qw * 32) << 16;
+    const uint32_t tS = tmem + lane_off + L::kColS + wg * L::N4;
+    const uint32_t tO = tmem + lane_off + L::kColO + (wg * 4 + qw) * L::N4;
+    float* xl = reinterpret_cast<float*>(sbase + L::kXl) + wg * 16;
+    const float4* qs = reinterpret_cast<const float4*>(sbase + L::kQs) + wg;
     uint8_t* prow = sbase + L::kP;
-    bool ok = true;
-    int g = 0;
+    const uint32_t all_bar = 1, wg_bar = WG == 1 ? 1 : 2 + wg;  // hardware barriers
+    int g = 0, st = 0;
     for (int seg = 0;; ++seg) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQFull), seg & 1, wc));
-      if (!named_bar_and(kWgBar, 128, ok)) break;
+      bool ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQFull), seg & 1, wc));
+      if (!named_bar_and(all_bar, 128 * WG, ok)) break;
       const int4 info = *reinterpret_cast<const int4*>(sbase + L::kInfo + (seg & 1) * 16);
       const int len = info.x, t0 = info.y, t1 = info.z;
       if (t0 == t1) break;
-      const int2* rows = reinterpret_cast<const int2*>(sbase + L::kRow) + (seg & 1) * RP;
-      const uint8_t* qi = sbase + L::kQi + (seg & 1) * RP;
-      float m[RP], l[RP], acc[RP];
+      const uint8_t* qi = sbase + L::kQi + (seg & 1) * RP + wg * 4;
+      float m[4], l[4], acc[4];  // sums of 2^(x - m), m the running maximum less 8: what P carries
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        m[r] = -INFINITY;
+      for (int r = 0; r < 4; ++r) {
+        m[r] = kNone;
         l[r] = 0.f;
         acc[r] = 0.f;
       }
@@ -553,43 +575,56 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
       // O^T of a tile is added a tile later, while the tensor core works on the
       // next one: be is the factor of the tile whose O^T is outstanding (acc is
       // already on that tile's scale), the power of two of its V scales in it.
-      float be[RP];
+      float be[4];
       auto add_o = [&](int go) {
         tc_fence_after();
-        uint32_t r_[L::NG];
-        tmem_ld_n<L::NG>(tO + (go % NB) * L::NO, r_);
+        uint32_t r_[L::N4];
+        tmem_ld_n<L::N4>(tO + (go % NB) * L::NO, r_);
         tmem_ld_wait();
-        reg_fence<L::NG>(r_);
+        reg_fence<L::N4>(r_);
         tc_fence_before();
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          float o = __uint_as_float(r_[r]), c = __uint_as_float(r_[RP + r]);
-          if constexpr (NP == 3) c = fmaf(__uint_as_float(r_[2 * RP + r]), 0.0625f, c);
+        for (int r = 0; r < 4; ++r) {
+          float o = __uint_as_float(r_[r]), c = __uint_as_float(r_[4 + r]);
+          if constexpr (NP == 3) c = fmaf(__uint_as_float(r_[8 + r]), 0.0625f, c);
           o = fmaf(c, 0.0625f, o);
           acc[r] = fmaf(o, be[r], acc[r]);
         }
       };
-      for (int t = t0; t < t1; ++t, ++g) {
-        const int st = g % L::kStages, kv0 = (t << TS) + kl * TPR;  // first token of this row
+      for (int t = t0; t < t1; ++t, ++g, st = st + 1 == L::kStages ? 0 : st + 1) {
+        const int kv0 = (t << TS) + kl * TPR;  // first token of this row
         const bool later = t > t0;  // the tile before is of this segment, its O^T outstanding
         // S^T, and with the scales' maxima the scales: the MMA warp has waited for them
         ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarSFull + (g & 1)), (g >> 1) & 1, wc));
-        __align__(8) float x[TPR][RP];  // scores in log2 units
+        float2 x[TPR][2];  // scores in log2 units
         float f[4], lv[TPR], mul = 0.f;
+        float4* xm = reinterpret_cast<float4*>(sbase + L::kXm) + ((g & 1) * WG + wg) * 4;
         if (ok) {
           tc_fence_after();
+          uint32_t r_[4 * L::N4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (L::kPair) {
+              if (k == 0) tmem_ld_n<4 * L::N4>(tS + (g % NB) * 4 * L::kSet, r_);
+            } else {
+              tmem_ld_n<L::N4>(tS + (g % NB) * 4 * L::kSet + k * L::kSet, r_ + k * L::N4);
+            }
+          }
           const uint2 kw = *reinterpret_cast<const uint2*>(sbase + L::kSc + st * 2 * L::kScl + kl * 8);
           const uint2 vw = *reinterpret_cast<const uint2*>(sbase + L::kSc + st * 2 * L::kScl + L::kScl + kl * 8);
           const float4 inv = *reinterpret_cast<const float4*>(sbase + L::kNorm + st * 32);
-          mul = *reinterpret_cast<const float*>(sbase + L::kNorm + st * 32 + 16 + warp * 4);
+          const float4 q4 = *qs;
+          mul = *reinterpret_cast<const float*>(sbase + L::kNorm + st * 32 + 16 + qw * 4);
           const float ks[4] = {bf16_lo(kw.x), bf16_hi(kw.x), bf16_lo(kw.y), bf16_hi(kw.y)};
           f[0] = bf16_lo(vw.x) * inv.x;
           f[1] = bf16_hi(vw.x) * inv.y;
           f[2] = bf16_lo(vw.y) * inv.z;
           f[3] = bf16_hi(vw.y) * inv.w;
+          if ((t + 1) << TS > len) {  // (a token behind the end has no weight, whatever its scales hold)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // (a token behind the end has no weight, whatever its scales hold)
-            if (kv0 + k * TPR / 4 >= len) f[k] = 0.f;
+            for (int k = 0; k < 4; ++k)
+              if (kv0 + k * TPR / 4 >= len) f[k] = 0.f;
+          }
           // the largest weight of each token's value, at most 1
           if constexpr (TPR == 1) {
             lv[0] = __log2f(fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), 0x1p-30f));
@@ -597,147 +632,114 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
             lv[0] = __log2f(fmaxf(fmaxf(f[0], f[1]), 0x1p-30f));
             lv[1] = __log2f(fmaxf(fmaxf(f[2], f[3]), 0x1p-30f));
           }
-          constexpr int kAt = L::NG <= 12 ? 4 : (L::NG <= 16 ? 2 : 1);  // groups loaded at a time
+          tmem_ld_wait();
+          reg_fence<4 * L::N4>(r_);
+          tc_fence_before();
+          constexpr int per = 4 / TPR;
 #pragma unroll
-          for (int k0 = 0; k0 < 4; k0 += kAt) {
-            uint32_t r_[kAt * L::NG];
-            const uint32_t from = tS + (g % NB) * 4 * L::kSet + k0 * L::kSet;
-            if constexpr (L::kSet == L::NG) {
-              tmem_ld_n<kAt * L::NG>(from, r_);
-            } else {
+          for (int k = 0; k < 4; ++k) {
+            const float2 k2 = make_float2(ks[k], ks[k]), sixteenth = make_float2(0.0625f, 0.0625f);
 #pragma unroll
-              for (int k = 0; k < kAt; ++k) tmem_ld_n<L::NG>(from + k * L::kSet, r_ + k * L::NG);
-            }
-            tmem_ld_wait();
-            reg_fence<kAt * L::NG>(r_);
-            constexpr int per = 4 / TPR;
-#pragma unroll
-            for (int k = 0; k < kAt; ++k) {
-              const int j = (k0 + k) / per;
-              const float2 k2 = make_float2(ks[k0 + k], ks[k0 + k]);
-#pragma unroll
-              for (int r = 0; r < RP; r += 2) {
-                auto term = [&](int t2) {
-                  const uint32_t* z = r_ + k * L::NG + t2 * RP + r;
-                  return make_float2(__uint_as_float(z[0]), __uint_as_float(z[1]));
-                };
-                const float2 sixteenth = make_float2(0.0625f, 0.0625f);
-                float2 c = term(1);
-                if constexpr (NP == 3) c = fma2(term(2), sixteenth, c);
-                const float2 s2 = fma2(c, sixteenth, term(0));
-                float2* to = reinterpret_cast<float2*>(&x[j][r]);
-                *to = (k0 + k) % per == 0 ? mul2(s2, k2) : fma2(s2, k2, *to);
-              }
+            for (int r = 0; r < 2; ++r) {
+              auto term = [&](int t2) {
+                const uint32_t* z = r_ + k * L::N4 + t2 * 4 + r * 2;
+                return make_float2(__uint_as_float(z[0]), __uint_as_float(z[1]));
+              };
+              float2 c = term(1);
+              if constexpr (NP == 3) c = fma2(term(2), sixteenth, c);
+              const float2 s2 = fma2(c, sixteenth, term(0));
+              float2& to = x[k / per][r];
+              to = k % per == 0 ? mul2(s2, k2) : fma2(s2, k2, to);
             }
           }
-          tc_fence_before();
 #pragma unroll
-          for (int r = 0; r < RP; r += 2) {
-            const float2 q2 = *reinterpret_cast<const float2*>(qs_s + r);
-#pragma unroll
-            for (int j = 0; j < TPR; ++j) {
-              float2* to = reinterpret_cast<float2*>(&x[j][r]);
-              *to = mul2(*to, q2);
-            }
+          for (int j = 0; j < TPR; ++j) {
+            x[j][0] = mul2(x[j][0], make_float2(q4.x, q4.y));
+            x[j][1] = mul2(x[j][1], make_float2(q4.z, q4.w));
           }
           if ((t << TS) + (1 << TS) - 1 > lim0) {
+            const uint32_t q8 = *reinterpret_cast<const uint32_t*>(qi);
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
-              const int lim = p.causal ? min(len - 1, len - p.Nq + (int)qi[r]) : len - 1;
+            for (int r = 0; r < 4; ++r) {
+              const int lim = p.causal ? min(len - 1, len - p.Nq + (int)((q8 >> (8 * r)) & 255)) : len - 1;
 #pragma unroll
               for (int j = 0; j < TPR; ++j)
-                if (kv0 + j > lim) x[j][r] = -INFINITY;
+                if (kv0 + j > lim) (r & 1 ? x[j][r / 2].y : x[j][r / 2].x) = -INFINITY;
             }
           }
-          float* mine = xm + ((g & 1) * 4 + warp) * RP;
+          float2 y[2];
 #pragma unroll
-          for (int r0 = 0; r0 < RP; r0 += 4) {
-            float v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float y = x[0][r0 + j] + lv[0];
-              if constexpr (TPR == 2) y = fmaxf(y, x[1][r0 + j] + lv[1]);
-              v[j] = warp_max(y);
+          for (int r = 0; r < 2; ++r) {
+            y[r] = add2(x[0][r], make_float2(lv[0], lv[0]));
+            if constexpr (TPR == 2) {
+              const float2 z = add2(x[1][r], make_float2(lv[1], lv[1]));
+              y[r] = make_float2(fmaxf(y[r].x, z.x), fmaxf(y[r].y, z.y));
             }
-            if (lane == 0) *reinterpret_cast<float4*>(mine + r0) = make_float4(v[0], v[1], v[2], v[3]);
           }
+          const float4 top = make_float4(warp_max(y[0].x), warp_max(y[0].y), warp_max(y[1].x), warp_max(y[1].y));
+          if (lane == 0) xm[qw] = top;
         }
         // (the O^T outstanding is complete: its MMA has read P, which is written again below)
         if (ok && later) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarOFull), (g - 1) & 1, wc));
-        ok = named_bar_and(kWgBar, 128, ok);
+        ok = named_bar_and(wg_bar, 128, ok);
         if (!ok) break;
-        if (threadIdx.x == 0) mbar_arrive(bar(L::kBarCEmpty + st));  // (every warp has its scales)
+        if (kl == 0) mbar_arrive(bar(L::kBarCEmpty + st));  // (every warp of the group has its scales)
         if (NB == 1 && later) add_o(g - 1);  // (before P lets the next O^T overwrite it)
-        float al_t[RP], be_t[RP];
-        uint32_t code[4][NP][RP / 4];  // terms of p f for the four groups, four rows to a word
+        const float4 v0 = xm[0], v1 = xm[1], v2 = xm[2], v3 = xm[3];
+        const float mt4[4] = {max3(max3(v0.x, v1.x, v2.x), v3.x, kNone) - 8.f, max3(max3(v0.y, v1.y, v2.y), v3.y, kNone) - 8.f,
+                              max3(max3(v0.z, v1.z, v2.z), v3.z, kNone) - 8.f, max3(max3(v0.w, v1.w, v2.w), v3.w, kNone) - 8.f};
+        float al_t[4], be_t[4];
 #pragma unroll
-        for (int r0 = 0; r0 < RP; r0 += 4) {
-          float4 v[4];
+        for (int r = 0; r < 4; ++r) {
+          // running maximum: one of the factors of the old and the new part is 1
+          const float d = mt4[r] - m[r], e = ex2(-fabsf(d));
+          al_t[r] = d > 0.f ? e : 1.f;
+          const float be_r = d < 0.f ? e : 1.f;
+          m[r] = fmaxf(m[r], mt4[r]);
+          float sum = 0.f;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const float4*>(xm + ((g & 1) * 4 + q) * RP + r0);
-          const float mt4[4] = {fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x)),
-                                fmaxf(fmaxf(v[0].y, v[1].y), fmaxf(v[2].y, v[3].y)),
-                                fmaxf(fmaxf(v[0].z, v[1].z), fmaxf(v[2].z, v[3].z)),
-                                fmaxf(fmaxf(v[0].w, v[1].w), fmaxf(v[2].w, v[3].w))};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = r0 + j;
-            const float mt = mt4[j];
-            // running maximum: one of the factors of the old and the new part is 1
-            const float e = ex2(mt > m[r] ? m[r] - mt : mt - m[r]);
-            al_t[r] = mt > m[r] ? e : 1.f;
-            be_t[r] = (mt < m[r] ? e : 1.f) * 0.00390625f;  // p below carries 2^8
-            m[r] = fmaxf(m[r], mt);
-            const float ref = mt == -INFINITY ? 0.f : mt - 8.f;
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < TPR; ++k) {
-              x[k][r] = ex2(x[k][r] - ref);  // p 2^8
-              sum += x[k][r];
-            }
-            l[r] = fmaf(sum, be_t[r], l[r] * al_t[r]);
-            be_t[r] *= mul;
+          for (int j = 0; j < TPR; ++j) {
+            float& y = r & 1 ? x[j][r / 2].y : x[j][r / 2].x;
+            y = ex2(y - mt4[r]);  // p 2^8
+            sum += y;
           }
+          l[r] = fmaf(sum, be_r, l[r] * al_t[r]);
+          be_t[r] = be_r * mul;
+        }
+        uint32_t code[4][NP];  // terms of p f for the four groups of channels, four rows to a word
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2* pr = reinterpret_cast<const float2*>(&x[k * TPR / 4][r0]);
-            const float2 f2 = make_float2(f[k], f[k]);
-            float2 a = mul2(pr[0], f2), b = mul2(pr[1], f2);
-            uint32_t lo = pack_e4m3(a.x, a.y), hi = pack_e4m3(b.x, b.y);
-            code[k][0][r0 / 4] = lo | (hi << 16);
-            if constexpr (NP == 2) {
-              // (what the first term leaves, in fp16: 16 p f to 2^-11 less 16 times the term)
-              const float2 g2 = make_float2(16.f * f[k], 16.f * f[k]);
-              a = mul2(pr[0], g2);
-              b = mul2(pr[1], g2);
-              lo = rest_e4m3(pack2<false>(a.x, a.y), lo);
-              hi = rest_e4m3(pack2<false>(b.x, b.y), hi);
-              code[k][1][r0 / 4] = lo | (hi << 16);
-            } else {
+        for (int k = 0; k < 4; ++k) {
+          const float2* pr = x[k * TPR / 4];
+          const float2 f2 = make_float2(f[k], f[k]);
+          float2 a = mul2(pr[0], f2), b = mul2(pr[1], f2);
+          const float2 mul16 = make_float2(16.f, 16.f);
+          code[k][0] = pack4_e4m3(a, b);
+          if constexpr (NP == 2) {  // what the first term leaves, in fp16: 16 p f to 2^-11 less 16 times the term
+            a = mul2(a, mul16);
+            b = mul2(b, mul16);
+            code[k][1] = rest4_e4m3(pack2<false>(a.x, a.y), pack2<false>(b.x, b.y), code[k][0]);
+          } else {
 #pragma unroll
-              for (int t2 = 1; t2 < NP; ++t2) {
-                const float2 d0 = unpack_e4m3(lo), d1 = unpack_e4m3(hi), mul16 = make_float2(16.f, 16.f);
-                a = mul2(sub2(a, d0), mul16);
-                b = mul2(sub2(b, d1), mul16);
-                lo = pack_e4m3(a.x, a.y);
-                hi = pack_e4m3(b.x, b.y);
-                code[k][t2][r0 / 4] = lo | (hi << 16);
-              }
+            for (int t2 = 1; t2 < NP; ++t2) {
+              a = mul2(sub2(a, unpack_e4m3(code[k][t2 - 1] & 0xffffu)), mul16);
+              b = mul2(sub2(b, unpack_e4m3(code[k][t2 - 1] >> 16)), mul16);
+              code[k][t2] = pack4_e4m3(a, b);
             }
           }
         }
-        // row kl of P: column (group, term, row) one byte each
-        const uint32_t* cw = &code[0][0][0];
+        // row kl of P: column (warpgroup, group, term, row) one byte each
+        const uint32_t* cw = &code[0][0];
 #pragma unroll
-        for (int c = 0; c < L::NO / 16; ++c)
-          *reinterpret_cast<uint4*>(prow + p_off<L::PW>(kl, c)) = make_uint4(cw[4 * c], cw[4 * c + 1], cw[4 * c + 2], cw[4 * c + 3]);
+        for (int c = 0; c < NP; ++c)
+          *reinterpret_cast<uint4*>(prow + p_off<L::PW>(kl, wg * NP + c)) =
+              make_uint4(cw[4 * c], cw[4 * c + 1], cw[4 * c + 2], cw[4 * c + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kBarPFull));
         if (NB == 2 && later) add_o(g - 1);
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
+        for (int r = 0; r < 4; ++r) {
           acc[r] *= al_t[r];
           be[r] = be_t[r];
         }
@@ -747,32 +749,25 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
       // ---- end of the segment: row sums over the tile's rows, then O.  A lane keeps half of its rows and
       // sends the others, until it has one, whose sum over the lanes that hold it goes on.
       {
-        int row = 0;
+        const bool up = lane & 16, up2 = lane & 8;
+        const float s0 = (up ? l[2] : l[0]) + __shfl_xor_sync(0xffffffffu, up ? l[0] : l[2], 16);
+        const float s1 = (up ? l[3] : l[1]) + __shfl_xor_sync(0xffffffffu, up ? l[1] : l[3], 16);
+        float s = (up2 ? s1 : s0) + __shfl_xor_sync(0xffffffffu, up2 ? s0 : s1, 8);
 #pragma unroll
-        for (int n = RP / 2, o = 16; n > 0; n >>= 1, o >>= 1) {
-          const bool up = lane & o;
-          row = row * 2 + (up ? 1 : 0);
-#pragma unroll
-          for (int r = 0; r < n; ++r) {
-            const float keep = up ? l[n + r] : l[r], send = up ? l[r] : l[n + r];
-            l[r] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-          }
-        }
-#pragma unroll
-        for (int o = 16 / RP; o > 0; o >>= 1) l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
-        if (lane % (32 / RP) == 0) xl[row * 4 + warp] = l[0];
+        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane % 8 == 0) xl[((up ? 2 : 0) + (up2 ? 1 : 0)) * 4 + qw] = s;
       }
       // (d = 64: lanes 64 to 127 hold the second token's part; P's rows are free)
-      float* half = reinterpret_cast<float*>(prow);
+      float* half = reinterpret_cast<float*>(prow) + wg * 256;
       if (TPR == 2 && kl >= 64) {
 #pragma unroll
-        for (int r = 0; r < RP; ++r) half[r * 64 + kl - 64] = acc[r];
+        for (int r = 0; r < 4; ++r) half[r * 64 + kl - 64] = acc[r];
       }
-      ok = named_bar_and(kWgBar, 128, ok);
-      if (!ok) break;
+      if (!named_bar_and(all_bar, 128 * WG, ok)) break;
       const bool whole = t1 - t0 == info.w;
+      const int2* rows = reinterpret_cast<const int2*>(sbase + L::kRow) + (seg & 1) * RP + wg * 4;
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
+      for (int r = 0; r < 4; ++r) {
         const int2 at = rows[r];
         const float4 l4 = *reinterpret_cast<const float4*>(xl + r * 4);
         const float lt = (l4.x + l4.y) + (l4.z + l4.w);
@@ -783,7 +778,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
           if (kl < D) reinterpret_cast<uint16_t*>(p.o)[(size_t)at.x * D + kl] = (uint16_t)pack2<BF16>(v, 0.f);
           if (kl == 0) p.lse[at.y] = lt != 0.f ? (m[r] + __log2f(lt)) * kLn2 : -INFINITY;
         } else {
-          const size_t part = ((size_t)blockIdx.x * 2 + (seg > 0 ? 1 : 0)) * RP + r;
+          const size_t part = ((size_t)blockIdx.x * 2 + (seg > 0 ? 1 : 0)) * RP + wg * 4 + r;
           if (kl < D) p.ws_o[part * D + kl] = sum;
           if (kl == 0) {
             p.ws_ml[part * 2] = m[r];
@@ -791,7 +786,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
           }
         }
       }
-      // (the next segment's P and row sums are written behind the barrier of its first tile)
+      // (the next segment's P and row sums are written behind the barrier at its start)
     }
   }
   if (threadIdx.x == 0) griddep_launch_dependents();
@@ -803,21 +798,21 @@ __global__ void __launch_bounds__(kDecThreads, Kv4Layout<D, RP, NP>::kCtas) attn
   }
 }
 
-template <int D, int RP, int NP>
+template <int D, int WG, int NP>
 cudaError_t launch_split_t(const KvDecArgs& a, cudaStream_t stream) {
-  using L = Kv4Layout<D, RP, NP>;
-  auto* k = attn_kv4_split_kernel<D, RP, NP>;
+  using L = Kv4Layout<D, WG, NP>;
+  auto* k = attn_kv4_split_kernel<D, WG, NP>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, (unsigned)a.grid, kDecThreads, L::kSmem, stream, a);
+  return launch_pdl(k, (unsigned)a.grid, L::kThreads, L::kSmem, stream, a);
 }
 
 template <int D>
 cudaError_t launch_split_d(const KvDecArgs& a, cudaStream_t stream) {
   if (a.bf16)
-    return a.rp == 4 ? launch_split_t<D, 4, 2>(a, stream)
-                     : (a.rp == 8 ? launch_split_t<D, 8, 2>(a, stream) : launch_split_t<D, 16, 2>(a, stream));
-  return a.rp == 4 ? launch_split_t<D, 4, 3>(a, stream) : launch_split_t<D, 8, 3>(a, stream);
+    return a.rp == 4 ? launch_split_t<D, 1, 2>(a, stream)
+                     : (a.rp == 8 ? launch_split_t<D, 2, 2>(a, stream) : launch_split_t<D, 4, 2>(a, stream));
+  return a.rp == 4 ? launch_split_t<D, 1, 3>(a, stream) : launch_split_t<D, 2, 3>(a, stream);
 }
 
 }  // namespace
@@ -854,7 +849,7 @@ int kv4_rows(int R, bool bf16) { return R <= 4 ? 4 : (R <= 8 || !bf16 ? 8 : 16);
 
 // All CTAs resident at once, no more than there can be tiles.
 int kv4_grid(int rp, bool bf16, int sms, long long max_units) {
-  long long g = (rp == 4 && bf16 ? 3ll : 2ll) * sms;
+  long long g = (rp == 16 ? 1ll : (rp == 4 && bf16 ? 3ll : 2ll)) * sms;
   if (g > kKvMaxCtas) g = kKvMaxCtas;
   if (g > max_units) g = max_units;
   return (int)(g < 1 ? 1 : g);
