@@ -915,10 +915,9 @@ int attn_kv4_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   a.bf16 = dtype == ATTN_BF16;
   a.rp = attn::kv4_rows(R, a.bf16);
   a.n_rb = (R + a.rp - 1) / a.rp;
-  a.tile_shift = d == 128 ? 7 : 8;
   a.causal = causal ? 1 : 0;
   a.scale = scale;
-  const long long tile = 1ll << a.tile_shift, tiles = ((long long)width * page + tile - 1) / tile;
+  const long long tile = 128 * (128 / d), tiles = ((long long)width * page + tile - 1) / tile;
   a.grid = attn::kv4_grid(a.rp, a.bf16, dev->sms, tiles * B * H * a.n_rb);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.ws_o = reinterpret_cast<float*>(ws);
@@ -1062,7 +1061,6 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   a.width = width; a.page_shift = shift; a.P = P;
   const int R = Nq * a.G;
   a.rp = attn::kv8_rows(R);
-  a.tile_shift = 7;
   a.n_rb = (R + a.rp - 1) / a.rp;
   a.causal = causal ? 1 : 0;
   a.bf16 = dtype == ATTN_BF16;

@@ -264,7 +264,9 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
     tmem_relinquish();
   }
   griddep_wait();
-  deal_range<TS, L::kThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
+  // (the merge kernel's blocks may come as CTAs end: they look at the lengths meanwhile)
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  deal_range<TS, kKv4SegCost, L::kThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
                               reinterpret_cast<long long*>(sbase + L::kStart));
   tc_fence_before();
   __syncthreads();
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
       };
       Walk w = w0;
       Seg sg;
-      while (ok && next_seg<TS>(p, Hr, w, sg)) {
+      while (ok && next_seg<TS, kKv4SegCost>(p, Hr, w, sg)) {
         const int h = sg.hr / p.n_rb;
         const int pages = (sg.len + (1 << p.page_shift) - 1) >> p.page_shift;
         const int* row = p.table + (size_t)sg.b * p.width;
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
     int g = 0, seg = 0;
     Walk w = w0;
     Seg sg;
-    bool more = next_seg<TS>(p, Hr, w, sg);
+    bool more = next_seg<TS, kKv4SegCost>(p, Hr, w, sg);
     if (more) load_q(sg);
     while (more) {
       put_q(sg, seg++);
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
       ok = norms(g, sg, sg.t0);
       if (!ok) break;
       const Seg now = sg;
-      more = next_seg<TS>(p, Hr, w, sg);
+      more = next_seg<TS, kKv4SegCost>(p, Hr, w, sg);
       if (more) load_q(sg);
       for (int t = now.t0; t < now.t1; ++t, ++g) {
         auto next_s = [&] {
@@ -789,7 +791,6 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
       // (the next segment's P and row sums are written behind the barrier at its start)
     }
   }
-  if (threadIdx.x == 0) griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) {

@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
     tmem_relinquish();
   }
   griddep_wait();
-  deal_range<7, kDecThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
+  deal_range<7, kKv8SegCost, kDecThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
                              reinterpret_cast<long long*>(sbase + L::kStart));
   tc_fence_before();
   __syncthreads();
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
       bool ok = true;
       Walk w = w0;
       Seg sg;
-      while (ok && next_seg<7>(p, Hr, w, sg)) {
+      while (ok && next_seg<7, kKv8SegCost>(p, Hr, w, sg)) {
         const int len = sg.len;
         const int h = sg.hr / p.n_rb;
         const int pages = (len + page_rows - 1) >> p.page_shift;
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
     int g = 0, seg = 0;
     Walk w = w0;
     Seg sg;
-    while (ok && next_seg<7>(p, Hr, w, sg)) {
+    while (ok && next_seg<7, kKv8SegCost>(p, Hr, w, sg)) {
       const int cnt = sg.t1 - sg.t0;
       ok = wt(L::kBarQFull, seg & 1) && wt(L::kBarKFull + g % L::kStages, (g / L::kStages) & 1);
       if (!ok) break;
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
     int g = 0, seg = 0;
     Walk w = w0;
     Seg sg;
-    while (ok && next_seg<7>(p, Hr, w, sg)) {
+    while (ok && next_seg<7, kKv8SegCost>(p, Hr, w, sg)) {
       const int len = sg.len;
       const int h = sg.hr / p.n_rb, rb = sg.hr % p.n_rb;
       // ---- the q terms of the row block: eight lanes to a row
@@ -696,12 +696,12 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
 // warp per row, four rows of a segment at a time, p.merge_run times (many rows: most
 // segments are one CTA's, and their blocks only find that out).  Always in the same
 // order.
-template <int D, bool BF16, int WPR, int TS>
+template <int D, bool BF16, int WPR, int TS, int SC>
 __global__ void __launch_bounds__(128) attn_kv_merge_kernel(const __grid_constant__ KvDecArgs p) {
   __shared__ long long sums[4][2];
   __shared__ float xo[4][D];
   __shared__ float xml[4][2];
-  griddep_wait();
+  // (Before the wait only what the split kernel reads as well, which waited for the kernels before it.)
   constexpr int kPer = D / 32, kU = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int Hr = p.H * p.n_rb, R = p.Nq * p.G;
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(128) attn_kv_merge_kernel(const __grid_constan
   int b = (int)(first / n_in / (unsigned)Hr);
   long long before = 0, total = 0;
   for (int i = threadIdx.x; i < p.B; i += 128) {
-    const int n = seg_units(kv_tiles<TS>(kv_len(p, i)));
+    const int n = seg_units<SC>(kv_tiles<TS>(kv_len(p, i)));
     total += n;
     if (i < b) before += n;
   }
@@ -730,45 +730,42 @@ __global__ void __launch_bounds__(128) attn_kv_merge_kernel(const __grid_constan
   total = sums[0][1] + sums[1][1] + sums[2][1] + sums[3][1];
   const long long units = total * Hr, n_cta = min((long long)p.grid, units);
   int nt = kv_tiles<TS>(kv_len(p, b));
+  bool waited = false;
   for (unsigned unit = first; unit < min(first + run, units_all); ++unit) {
     const unsigned blk = unit / n_in;  // (b, head, row block)
     if ((int)(blk / (unsigned)Hr) != b) {
-      before += seg_units(nt);
+      before += seg_units<SC>(nt);
       nt = kv_tiles<TS>(kv_len(p, ++b));
     }
     const int hr = (int)(blk - (unsigned)b * Hr);
     const int h = hr / p.n_rb, rb = hr - h * p.n_rb;
     const int r = (int)((unit - blk * n_in) * per) + (WPR == 4 ? 0 : warp), idx = rb * p.rp + r;
-    const long long u0 = before * Hr + (long long)hr * seg_units(nt);
-    const int c0 = nt ? (int)range_owner(u0 + kSegCost, units, n_cta) : 0;
-    const int c1 = nt ? (int)range_owner(u0 + kSegCost + nt - 1, units, n_cta) : 0;
+    const long long u0 = before * Hr + (long long)hr * seg_units<SC>(nt);
+    const int c0 = nt ? (int)range_owner(u0 + SC, units, n_cta) : 0;
+    const int c1 = nt ? (int)range_owner(u0 + SC + nt - 1, units, n_cta) : 0;
     if ((nt == 0 || c0 != c1) && (WPR == 1 || idx < R)) {
       // the first CTA's part is in its second slot if its range began earlier
       const int s0 = nt && range_start(c0, units, n_cta) < u0 ? 1 : 0;
       auto part = [&](int c) -> size_t { return ((size_t)c * 2 + (c == c0 ? s0 : 0)) * p.rp + r; };
       const bool live = idx < R;  // (WPR = 1: a warp may have no row)
+      if (!waited) griddep_wait();
+      waited = true;
       float acc[kPer];
 #pragma unroll
       for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
       float M = -INFINITY, Ls = 0.f;
       if (nt && live) {
-        for (int c = c0 + (WPR == 4 ? (int)threadIdx.x : lane); c <= c1; c += 32 * WPR) M = fmaxf(M, p.ws_ml[part(c) * 2]);
-        M = warp_max(M);
-        if constexpr (WPR == 4) {
-          if (lane == 0) xml[warp][0] = M;
-          __syncthreads();
-          M = fmaxf(fmaxf(xml[0][0], xml[1][0]), fmaxf(xml[2][0], xml[3][0]));
-        }
-        for (int cb = c0 + (WPR == 4 ? warp * kU : 0); cb <= c1; cb += WPR * kU) {
-          float wgt = 0.f;
+        // eight parts from cb on: maximum and sum of one a lane, columns of all
+        float mc, lc;
+        float4 v[kU];
+        auto fetch = [&](int cb) {
+          mc = -INFINITY;
+          lc = 0.f;
           if (lane < kU && cb + lane <= c1) {
-            const size_t at = part(cb + lane) * 2;
-            const float mc = p.ws_ml[at], lc = p.ws_ml[at + 1];
-            wgt = mc == -INFINITY ? 0.f : ex2(mc - M);
-            // (a part whose every score is NaN has m = -inf and a NaN sum)
-            Ls += lc != lc ? lc : wgt * lc;
+            const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + part(cb + lane) * 2);
+            mc = ml.x;
+            lc = ml.y;
           }
-          float4 v[kU];
 #pragma unroll
           for (int k = 0; k < kU; ++k) {
             v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -782,6 +779,24 @@ __global__ void __launch_bounds__(128) attn_kv_merge_kernel(const __grid_constan
                 v[k].y = v2.y;
               }
             }
+          }
+        };
+        const int cb0 = c0 + (WPR == 4 ? warp * kU : 0);
+        fetch(cb0);  // (on its way while the maximum is looked for)
+        for (int c = c0 + (WPR == 4 ? (int)threadIdx.x : lane); c <= c1; c += 32 * WPR) M = fmaxf(M, p.ws_ml[part(c) * 2]);
+        M = warp_max(M);
+        if constexpr (WPR == 4) {
+          if (lane == 0) xml[warp][0] = M;
+          __syncthreads();
+          M = fmaxf(fmaxf(xml[0][0], xml[1][0]), fmaxf(xml[2][0], xml[3][0]));
+        }
+        for (int cb = cb0; cb <= c1; cb += WPR * kU) {
+          if (cb != cb0) fetch(cb);
+          float wgt = 0.f;
+          if (lane < kU && cb + lane <= c1) {
+            wgt = mc == -INFINITY ? 0.f : ex2(mc - M);
+            // (a part whose every score is NaN has m = -inf and a NaN sum)
+            Ls += lc != lc ? lc : wgt * lc;
           }
 #pragma unroll
           for (int k = 0; k < kU; ++k) {
@@ -822,6 +837,7 @@ __global__ void __launch_bounds__(128) attn_kv_merge_kernel(const __grid_constan
       }
     }
   }
+  if (!waited) griddep_wait();  // (so that whoever waits for this kernel has waited for the split)
   griddep_launch_dependents();
 }
 
@@ -862,25 +878,30 @@ cudaError_t launch_kv8_split(const KvDecArgs& a, cudaStream_t stream) {
 
 constexpr long long kMergeBlocks = 2 * 8 * kSms;  // two waves of eight blocks to an SM
 
-template <int D, bool BF16, int TS>
+template <int D, bool BF16, int TS, int SC>
 static cudaError_t launch_merge_t(KvDecArgs a, cudaStream_t stream) {
   const long long segs = (long long)a.B * a.H * a.n_rb;
   // parts of a segment: about a.grid / segs + 1 (64 requests of 8 heads: 51 us with a
   // warp per row, 52 with a block; 17 requests of 2 heads and 3 row blocks: 20 and 19)
   if (a.grid >= 2 * segs)
-    return launch_pdl(attn_kv_merge_kernel<D, BF16, 4, TS>, (unsigned)(segs * a.rp), 128, 0, stream, a);
+    return launch_pdl(attn_kv_merge_kernel<D, BF16, 4, TS, SC>, (unsigned)(segs * a.rp), 128, 0, stream, a);
   // Every block sums all the lengths, so with many rows a block takes several, two
   // waves of blocks in all (4096 requests of 30 to 60 tokens, 8 heads: the merge 43 us, 127
   // with a block for every four rows).
   const long long rows4 = segs * ((a.rp + 3) / 4);
   a.merge_run = (int)((rows4 + kMergeBlocks - 1) / kMergeBlocks);
-  return launch_pdl(attn_kv_merge_kernel<D, BF16, 1, TS>, (unsigned)((rows4 + a.merge_run - 1) / a.merge_run), 128, 0, stream, a);
+  return launch_pdl(attn_kv_merge_kernel<D, BF16, 1, TS, SC>, (unsigned)((rows4 + a.merge_run - 1) / a.merge_run), 128, 0, stream, a);
+}
+
+template <bool BF16>
+static cudaError_t launch_merge_b(const KvDecArgs& a, cudaStream_t stream) {
+  if (a.k_scale16)  // the cache in 4 bits
+    return a.d == 128 ? launch_merge_t<128, BF16, 7, kKv4SegCost>(a, stream) : launch_merge_t<64, BF16, 8, kKv4SegCost>(a, stream);
+  return a.d == 128 ? launch_merge_t<128, BF16, 7, kKv8SegCost>(a, stream) : launch_merge_t<64, BF16, 7, kKv8SegCost>(a, stream);
 }
 
 cudaError_t launch_kv_merge(const KvDecArgs& a, cudaStream_t stream) {
-  if (a.d == 128) return a.bf16 ? launch_merge_t<128, true, 7>(a, stream) : launch_merge_t<128, false, 7>(a, stream);
-  if (a.tile_shift == 8) return a.bf16 ? launch_merge_t<64, true, 8>(a, stream) : launch_merge_t<64, false, 8>(a, stream);
-  return a.bf16 ? launch_merge_t<64, true, 7>(a, stream) : launch_merge_t<64, false, 7>(a, stream);
+  return a.bf16 ? launch_merge_b<true>(a, stream) : launch_merge_b<false>(a, stream);
 }
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int sms, cudaStream_t stream) {

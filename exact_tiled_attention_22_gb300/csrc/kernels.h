@@ -212,6 +212,9 @@ struct Kv8AppendArgs {
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int sms, cudaStream_t stream);
 
 constexpr int kKvMaxCtas = 640;  // workspace bound of the decode grids
+// What a segment (one request's tiles of one head group) costs a CTA besides its tiles, in tiles.
+constexpr int kKv8SegCost = 2;   // (64 ragged requests: 65, 53, 52, 53 us with a cost of 0 to 3)
+constexpr int kKv4SegCost = 1;
 // Decoding from a paged cache, in 8 bits or in 4.
 struct KvDecArgs {
   CUtensorMap tm_k, tm_v;    // one page of one head a box: (d, page, P * H), in 4 bits (128, page * d / 128, P * H)
@@ -228,7 +231,6 @@ struct KvDecArgs {
   float* ws_ml;              // [CTA][2][rows][2]
   int B, Nq, Hq, H, G, d, width, page_shift, P;
   int rp, n_rb;              // rows of a row block, row blocks
-  int tile_shift;            // a tile is 2^tile_shift tokens
   int grid;
   int merge_run;             // groups of four rows to a block of the merge: the launcher's choice
   int causal, bf16;

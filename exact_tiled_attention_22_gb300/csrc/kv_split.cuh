@@ -13,21 +13,25 @@
 namespace attn {
 namespace {
 
-// What a segment (a request's tiles of one head group) costs besides its tiles,
+// What a segment (a request's tiles of one head group) costs besides its tiles, SC
 // in tiles: its query terms, the first S and the last O^T, during which nothing
 // else of the CTA runs.  Units are counted with it, tile t of a segment being
-// unit kSegCost + t, so that a CTA with many short requests gets fewer tiles (64
-// ragged requests: 65, 53, 52, 53 us with a cost of 0 to 3).
-constexpr int kSegCost = 2;
-
-__device__ __forceinline__ int seg_units(int nt) { return nt > 0 ? nt + kSegCost : 0; }
+// unit SC + t, so that a CTA with many short requests gets fewer tiles.  Both
+// caches' figures stand at kKv8SegCost and kKv4SegCost.
+template <int SC>
+__device__ __forceinline__ int seg_units(int nt) { return nt > 0 ? nt + SC : 0; }
 
 // The units are dealt to min(grid, units) CTAs, so that none of those has an
-// empty range (the merge kernel reads a part from each CTA of a segment).
-__host__ __device__ inline long long range_start(long long c, long long units, long long grid) { return c * units / grid; }
+// empty range (the merge kernel reads a part from each CTA of a segment).  (Divisions in 32
+// bits where the products fit: 64-bit ones took 0.3 us of a short decoding step.)
+__device__ __forceinline__ bool fits32(long long units, long long grid) { return units <= 0xffffffffll / grid; }
+__device__ __forceinline__ long long range_start(long long c, long long units, long long grid) {
+  return fits32(units, grid) ? (long long)((uint32_t)c * (uint32_t)units / (uint32_t)grid) : c * units / grid;
+}
 // The CTA whose range holds unit u.
 __device__ __forceinline__ long long range_owner(long long u, long long units, long long grid) {
-  return ((u + 1) * grid - 1) / units;
+  return fits32(units, grid) ? (long long)((((uint32_t)u + 1) * (uint32_t)grid - 1) / (uint32_t)units)
+                             : ((u + 1) * grid - 1) / units;
 }
 
 __device__ __forceinline__ int kv_len(const KvDecArgs& p, int b) {
@@ -49,12 +53,12 @@ struct Walk {
 struct Seg {
   int b, hr, len, nt, t0, t1;
 };
-template <int TS>
+template <int TS, int SC>
 __device__ __forceinline__ bool next_seg(const KvDecArgs& p, int Hr, Walk& w, Seg& s) {
   while (w.left > 0) {
     s.len = kv_len(p, w.b);
     s.nt = kv_tiles<TS>(s.len);
-    const int n = seg_units(s.nt);
+    const int n = seg_units<SC>(s.nt);
     if (n == 0) {  // (a request without tokens has no units)
       ++w.b;
       w.hr = 0;
@@ -64,8 +68,8 @@ __device__ __forceinline__ bool next_seg(const KvDecArgs& p, int Hr, Walk& w, Se
     const int end = (int)min((long long)n, w.v + w.left);
     s.b = w.b;
     s.hr = w.hr;
-    s.t0 = max(0, w.v - kSegCost);
-    s.t1 = max(0, end - kSegCost);
+    s.t0 = max(0, w.v - SC);
+    s.t1 = max(0, end - SC);
     w.left -= end - w.v;
     w.v = 0;
     if (++w.hr == Hr) {
@@ -80,13 +84,13 @@ __device__ __forceinline__ bool next_seg(const KvDecArgs& p, int Hr, Walk& w, Se
 // The CTA's range of units [u0, u1) and where it starts: every thread sums the units
 // of a run of requests, a scan finds the thread whose run holds u0.  wsum: [THREADS / 32]
 // and st: [4] in shared memory; st is valid behind the caller's next barrier.
-template <int TS, int THREADS>
+template <int TS, int SC, int THREADS>
 __device__ __forceinline__ void deal_range(const KvDecArgs& p, int Hr, long long* wsum, long long* st) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (p.B + THREADS - 1) / THREADS;
   const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seg_units(kv_tiles<TS>(kv_len(p, b)));
+  for (int b = b0; b < b1; ++b) mine += seg_units<SC>(kv_tiles<TS>(kv_len(p, b)));
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -112,13 +116,13 @@ __device__ __forceinline__ void deal_range(const KvDecArgs& p, int Hr, long long
   if (u0 < u1 && before * Hr <= u0 && u0 < (before + mine) * Hr) {
     long long at = before;
     for (int b = b0; b < b1; ++b) {
-      const int n = seg_units(kv_tiles<TS>(kv_len(p, b)));
+      const int n = seg_units<SC>(kv_tiles<TS>(kv_len(p, b)));
       if (u0 < (at + n) * Hr) {
-        const long long in = u0 - at * Hr;
+        const long long in = u0 - at * Hr;  // (below n Hr)
         int* w = reinterpret_cast<int*>(st + 2);
         w[0] = b;
-        w[1] = (int)(in / n);
-        w[2] = (int)(in % n);
+        w[1] = in <= 0xffffffffll ? (int)((uint32_t)in / (uint32_t)n) : (int)(in / n);
+        w[2] = (int)(in - (long long)w[1] * n);
         break;
       }
       at += n;
