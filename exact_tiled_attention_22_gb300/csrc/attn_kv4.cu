@@ -266,13 +266,28 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
   griddep_wait();
   // (the merge kernel's blocks may come as CTAs end: they look at the lengths meanwhile)
   if (threadIdx.x == 0) griddep_launch_dependents();
-  deal_range<TS, kKv4SegCost, L::kThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
-                              reinterpret_cast<long long*>(sbase + L::kStart));
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sbase + L::kTmemSlot);
-  const Walk w0 = first_walk(reinterpret_cast<const long long*>(sbase + L::kStart));
+  Walk w0;
+  if (p.B <= kWarpDealB) {
+    w0 = deal_warp<TS, kKv4SegCost>(p, Hr);
+  } else {
+    deal_range<TS, kKv4SegCost, L::kThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
+                                             reinterpret_cast<long long*>(sbase + L::kStart));
+    __syncthreads();
+    w0 = first_walk(reinterpret_cast<const long long*>(sbase + L::kStart));
+    __syncthreads();  // (the scan lies where the row maxima will)
+  }
+  // Barriers and TMEM are there for the warps that wait here; the producer, which made the
+  // barriers, goes on.
+  uint32_t tmem = 0;
+  if (warp == kWarpProd) {
+    __syncwarp();
+    named_bar_arrive(2 + WG, L::kThreads);
+  } else {
+    tc_fence_before();
+    named_bar_sync(2 + WG, L::kThreads);
+    tc_fence_after();
+    tmem = *reinterpret_cast<volatile uint32_t*>(sbase + L::kTmemSlot);
+  }
 
   if (warp == kWarpProd) {
     // ------------------------------------------------------------ producer

@@ -129,6 +129,49 @@ __device__ __forceinline__ void deal_range(const KvDecArgs& p, int Hr, long long
     }
   }
 }
+// The same by a warp alone, for at most kWarpDealB requests: no barrier, so that a warp that
+// copies can begin (17 drafts of 5 tokens: 14.8 -> 14.4 us, 38 x 4096 tokens 39.3 -> 38.9).
+constexpr int kWarpDealB = 128;
+template <int TS, int SC>
+__device__ __forceinline__ Walk deal_warp(const KvDecArgs& p, int Hr) {
+  const int lane = threadIdx.x & 31, per = (p.B + 31) / 32, b0 = lane * per;
+  uint32_t n[kWarpDealB / 32], mine = 0;  // (units of 128 requests fit 31 bits)
+#pragma unroll
+  for (int i = 0; i < kWarpDealB / 32; ++i) {
+    n[i] = i < per && b0 + i < p.B ? seg_units<SC>(kv_tiles<TS>(kv_len(p, b0 + i))) : 0;
+    mine += n[i];
+  }
+  uint32_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t a = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += a;
+  }
+  const long long units = (long long)__shfl_sync(0xffffffffu, inc, 31) * Hr, n_cta = min((long long)p.grid, units);
+  Walk w = {0, 0, 0, 0};
+  if (blockIdx.x >= n_cta) return w;
+  const long long u0 = range_start(blockIdx.x, units, n_cta);
+  long long at = (long long)(inc - mine) * Hr;
+  const bool here = at <= u0 && u0 < (long long)inc * Hr;
+  if (here) {
+#pragma unroll
+    for (int i = 0; i < kWarpDealB / 32; ++i) {
+      const long long in = u0 - at, all = (long long)n[i] * Hr;
+      if (in >= 0 && in < all) {
+        w.b = b0 + i;
+        w.hr = in <= 0xffffffffll ? (int)((uint32_t)in / n[i]) : (int)(in / n[i]);
+        w.v = (int)(in - (long long)w.hr * n[i]);
+      }
+      at += all;
+    }
+  }
+  const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  w.b = __shfl_sync(0xffffffffu, w.b, src);
+  w.hr = __shfl_sync(0xffffffffu, w.hr, src);
+  w.v = __shfl_sync(0xffffffffu, w.v, src);
+  w.left = range_start(blockIdx.x + 1ll, units, n_cta) - u0;
+  return w;
+}
 __device__ __forceinline__ Walk first_walk(const long long* st) {
   const int* w = reinterpret_cast<const int*>(st + 2);
   Walk w0;
