@@ -941,7 +941,8 @@ int attn_kv_read(const uint8_t* k_cache, const uint8_t* v_cache, const void* k_s
   if (B < 1 || width < 1) return fail(ATTN_ERR_INVALID, "B >= 1, width >= 1 needed (got %d, %d)", B, width);
   if (T < 0 || T >= (1ll << 31) || T * H >= (1ll << 33)) return fail(ATTN_ERR_INVALID, "T must be in [0, 2^31), T * H below 2^33");
   if ((long long)width * page >= (1ll << 31)) return fail(ATTN_ERR_INVALID, "width * page must be < 2^31");
-  if (!aligned16(k) || !aligned16(v)) return fail(ATTN_ERR_ALIGN, "k and v must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u)
+    return fail(ATTN_ERR_ALIGN, "k and v must be 32-byte aligned");
   if (!aligned4(block_table) || !aligned4(lens) || !aligned4(cu))
     return fail(ATTN_ERR_ALIGN, "block_table, lens and cu must be 4-byte aligned");
   if (T == 0) return ATTN_OK;

@@ -30,72 +30,84 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// A thread rounds 8 channels (16 bytes in, 4 out), four neighbours share a scale.
-// A block takes p.tok tokens of K or of V (blockIdx.y), all their heads, U items of a
-// thread at a time.
-template <int D, bool BF16, int U>
+// A thread rounds 16 channels (32 bytes in, 8 out), two neighbours share a scale.  A block
+// takes p.tok tokens of K or of V (blockIdx.y), all their heads.  W32: tokens begin on
+// 32-byte borders, and a thread's channels are read at once.  AHEAD: the next item is read
+// before this one is rounded.
+template <int D, bool BF16, bool W32, bool AHEAD>
 __global__ void __launch_bounds__(kAppThreads) attn_kv4_append_kernel(const __grid_constant__ Kv4AppendArgs p) {
   griddep_wait();
-  constexpr int kParts = D / 8;  // threads to a token and head
+  constexpr int kParts = D / 16;  // threads to a token and head
   const int kv = blockIdx.y;
   const long long t0 = (long long)blockIdx.x * p.tok;
   const int n_tok = (int)min((long long)p.tok, p.T - t0);
   const int items = n_tok * p.H * kParts;
   const uint8_t* x = static_cast<const uint8_t*>(p.x[kv]);
   const int ps = 1 << p.page_shift;
-  for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < items; i0 += kAppThreads * U) {
-    uint4 v[U];
-    long long at[U];  // (page, head, place) of the item, -1: none
+  auto fetch = [&](int i, uint32_t* w, long long& at) {
+    const int row = i / kParts, part = i % kParts;
+    const int tl = (int)__umulhi((uint32_t)row * 2, p.h_magic), h = row - tl * p.H;
+    at = -1;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kAppThreads;
-      const int row = i / kParts, part = i % kParts;
-      const int tl = (int)__umulhi((uint32_t)row * 2, p.h_magic), h = row - tl * p.H;
-      at[u] = -1;
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (i < items) {
-        const long long t = t0 + tl, slot = p.slots[t];
-        v[u] = *reinterpret_cast<const uint4*>(x + (t * p.x_stride[kv] + (long long)h * D + part * 8) * 2);
-        if (slot >= 0 && slot < p.n_slots)
-          at[u] = ((((slot >> p.page_shift) * p.H + h) << p.page_shift) + (slot & (ps - 1))) * kParts + part;
+    for (int j = 0; j < 8; ++j) w[j] = 0;
+    if (i < items) {
+      const long long t = t0 + tl, slot = p.slots[t];
+      const uint8_t* src = x + (t * p.x_stride[kv] + (long long)h * D + part * 16) * 2;
+      if constexpr (W32) {
+        ld_global_32(src, w);
+      } else {
+        *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(src);
+        *reinterpret_cast<uint4*>(w + 4) = *reinterpret_cast<const uint4*>(src + 16);
       }
+      if (slot >= 0 && slot < p.n_slots)
+        at = ((((slot >> p.page_shift) * p.H + h) << p.page_shift) + (slot & (ps - 1))) * kParts + part;
     }
+  };
+  uint32_t next[8];
+  long long next_at = -1;  // (page, head, place) of an item, -1: none
+  if constexpr (AHEAD) fetch(threadIdx.x, next, next_at);
+  for (int i = threadIdx.x; i - (int)threadIdx.x < items; i += kAppThreads) {
+    uint32_t w[8];
+    long long at = next_at;
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t* w = &v[u].x;
-      // largest magnitude as the 16 bits of it: ordered as numbers, infinity and NaN above all
-      uint32_t top = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                               max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-      top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      top = max(top & 0xffffu, top >> 16);
-      const float amax = unpack2<BF16>(top).x;
-      // s = amax / 6 rounded to bf16.  (The quotient of 11 bits by 6 is exact in 32 bits where
-      // it lies half-way between two bf16 values, so rounding it twice is rounding it once.)
-      // fminf and fmaxf pass a NaN over, so a NaN is put back.
-      const float f = fminf(fmaxf(__fdiv_rn(amax, 6.f), 0x1p-64f), 0x1p60f);
-      const uint32_t sb = amax != amax ? 0x7fc0u : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f));
-      const float s = __uint_as_float(sb << 16), inv = 1.f / s;
-      uint32_t code = 0;
+      for (int j = 0; j < 8; ++j) w[j] = next[j];
+      if (i - (int)threadIdx.x + kAppThreads < items) fetch(i + kAppThreads, next, next_at);
+    } else {
+      fetch(i, w, at);
+    }
+    // largest magnitude as the 16 bits of it: ordered as numbers, infinity and NaN above all
+    uint32_t top = w[0] & 0x7fff7fffu;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float2 n = unpack2<BF16>(w[j] ^ 0x80008000u);  // -x
-        if (amax > 0x1p63f) {  // (beyond the largest scale: saturated below; an infinity has no residual)
-          n.x = fminf(fmaxf(n.x, -0x1p63f), 0x1p63f);
-          n.y = fminf(fmaxf(n.y, -0x1p63f), 0x1p63f);
-        }
-        // x / s to 32 bits: the product with 1 / s, corrected by its residual.  A quotient of 11 by 8
-        // bits that is no border between two codes is at least 2^-12 of its value away from it; one
-        // that is comes out exactly.  (From -x, so that a zero keeps its sign.)
-        float2 y = mul2(n, make_float2(-inv, -inv));
-        const float2 r = fma2(y, make_float2(s, s), n);
-        y = fma2(r, make_float2(-inv, -inv), y);
-        code |= pack_e2m1(y.x, y.y) << (8 * j);
+    for (int j = 1; j < 8; ++j) top = max_u16x2(top, w[j] & 0x7fff7fffu);
+    top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top & 0xffffu, top >> 16);
+    const float amax = unpack2<BF16>(top).x;
+    // s = amax / 6 rounded to bf16.  (The quotient of 11 bits by 6 is exact in 32 bits where
+    // it lies half-way between two bf16 values, so rounding it twice is rounding it once.)
+    // fminf and fmaxf pass a NaN over, so a NaN is put back.
+    const float f = fminf(fmaxf(__fdiv_rn(amax, 6.f), 0x1p-64f), 0x1p60f);
+    const uint32_t sb = amax != amax ? 0x7fc0u : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f));
+    const float s = __uint_as_float(sb << 16), inv = 1.f / s;
+    float2 y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float2 n = unpack2<BF16>(w[j] ^ 0x80008000u);  // -x
+      if (amax > 0x1p63f) {  // (beyond the largest scale: saturated below; an infinity has no residual)
+        n.x = fminf(fmaxf(n.x, -0x1p63f), 0x1p63f);
+        n.y = fminf(fmaxf(n.y, -0x1p63f), 0x1p63f);
       }
-      if (at[u] >= 0) {
-        *reinterpret_cast<uint32_t*>(p.cache[kv] + at[u] * 4) = code;
-        if ((i0 & 3) == 0) p.scale[kv][at[u] >> 2] = (uint16_t)sb;
-      }
+      // x / s to 32 bits: the product with 1 / s, corrected by its residual.  A quotient of 11 by 8
+      // bits that is no border between two codes is at least 2^-12 of its value away from it; one
+      // that is comes out exactly.  (From -x, so that a zero keeps its sign.)
+      y[j] = mul2(n, make_float2(-inv, -inv));
+      const float2 r = fma2(y[j], make_float2(s, s), n);
+      y[j] = fma2(r, make_float2(-inv, -inv), y[j]);
+    }
+    if (at >= 0) {
+      *reinterpret_cast<uint2*>(p.cache[kv] + at * 8) =
+          make_uint2(pack8_e2m1(y[0], y[1], y[2], y[3]), pack8_e2m1(y[4], y[5], y[6], y[7]));
+      if ((i & 1) == 0) p.scale[kv][at >> 1] = (uint16_t)sb;
     }
   }
   if (threadIdx.x == 0) griddep_launch_dependents();
@@ -833,8 +845,8 @@ cudaError_t launch_split_d(const KvDecArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-template <int U>
-static cudaError_t launch_append_u(const Kv4AppendArgs& a, cudaStream_t stream) {
+template <int D, bool BF16>
+static cudaError_t launch_append_t(const Kv4AppendArgs& a, bool w32, bool ahead, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((a.T + a.tok - 1) / a.tok), 2);
   cfg.blockDim = dim3(kAppThreads);
@@ -844,19 +856,25 @@ static cudaError_t launch_append_u(const Kv4AppendArgs& a, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (a.d == 128)
-    return a.bf16 ? cudaLaunchKernelEx(&cfg, attn_kv4_append_kernel<128, true, U>, a)
-                  : cudaLaunchKernelEx(&cfg, attn_kv4_append_kernel<128, false, U>, a);
-  return a.bf16 ? cudaLaunchKernelEx(&cfg, attn_kv4_append_kernel<64, true, U>, a)
-                : cudaLaunchKernelEx(&cfg, attn_kv4_append_kernel<64, false, U>, a);
+  if (ahead)
+    return w32 ? cudaLaunchKernelEx(&cfg, attn_kv4_append_kernel<D, BF16, true, true>, a)
+               : cudaLaunchKernelEx(&cfg, attn_kv4_append_kernel<D, BF16, false, true>, a);
+  return w32 ? cudaLaunchKernelEx(&cfg, attn_kv4_append_kernel<D, BF16, true, false>, a)
+             : cudaLaunchKernelEx(&cfg, attn_kv4_append_kernel<D, BF16, false, false>, a);
 }
 
 cudaError_t launch_kv4_append(Kv4AppendArgs a, int sms, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
-  const long long per_tok = (long long)a.H * (a.d / 8);
-  const int u = a.T * per_tok * 2 > 4ll * sms * 2048 ? 4 : 1;
-  kv_rows(&a, (long long)kAppThreads * u / per_tok);
-  return u == 4 ? launch_append_u<4>(a, stream) : launch_append_u<1>(a, stream);
+  // An item a thread, or all of a token's; where there are many blocks four, the next one read ahead
+  // (256k tokens of 8 heads, d = 128: 264 us, 293 with one; 31749 of 4 heads, d = 64: 7.1, 7.5 with four;
+  // a step of 256: 1.7 and 3.4).
+  const long long per_tok = (long long)a.H * (a.d / 16);
+  const bool ahead = a.T * per_tok * 2 / kAppThreads > 64ll * sms;
+  kv_rows(&a, (ahead ? 4 : 1) * (long long)kAppThreads / per_tok);
+  const bool w32 = !((reinterpret_cast<uintptr_t>(a.x[0]) | reinterpret_cast<uintptr_t>(a.x[1])) & 31u) &&
+                   a.x_stride[0] % 16 == 0 && a.x_stride[1] % 16 == 0;
+  if (a.d == 128) return a.bf16 ? launch_append_t<128, true>(a, w32, ahead, stream) : launch_append_t<128, false>(a, w32, ahead, stream);
+  return a.bf16 ? launch_append_t<64, true>(a, w32, ahead, stream) : launch_append_t<64, false>(a, w32, ahead, stream);
 }
 
 // Row blocks of 4, 8 or, in bf16, 16 rows: the work per tile grows with the rows.  (16 rows of

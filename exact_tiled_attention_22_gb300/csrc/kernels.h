@@ -283,7 +283,7 @@ struct KvReadArgs {
   int tok;                  // tokens of a block
   uint32_t h_magic;         // as above
 };
-cudaError_t launch_kv_read(KvReadArgs a, int sms, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvReadArgs& a, int sms, cudaStream_t stream);
 
 // Id of the calling thread's current CUDA context (unique for the life of
 // the process, unlike the CUcontext handle, which a new context may reuse).

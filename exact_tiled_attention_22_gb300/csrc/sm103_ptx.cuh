@@ -173,6 +173,19 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// 32 bytes from global memory (32-byte aligned) at once.
+__device__ __forceinline__ void ld_global_32(const void* src, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(src));
+}
+// 32 bytes to global memory (32-byte aligned) at once.
+__device__ __forceinline__ void st_global_32(void* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // Barrier over `count` threads (a multiple of 32, whole warps) on hardware
 // barrier `id` that also ANDs a flag across them: every participant gets the
 // same answer, so code after it can branch uniformly (for example on whether
@@ -516,15 +529,16 @@ __device__ __forceinline__ float2 unpack_e4m3(uint32_t w) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-// Two fp32 values to e2m1 (RNE, saturating at +-6): `lo` in bits 0-3, `hi` in
-// bits 4-7.
-__device__ __forceinline__ uint32_t pack_e2m1(float lo, float hi) {
+// Eight fp32 values to e2m1 (RNE, saturating at +-6), four bits each from bit 0 up.
+__device__ __forceinline__ uint32_t pack8_e2m1(float2 a, float2 b, float2 c, float2 d) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b, z;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-      "mov.b32 {z, _, _, _}, 0;\n\t"
-      "mov.b32 %0, {b, z, z, z};\n\t}"
-      : "=r"(r) : "f"(hi), "f"(lo));
+  asm("{\n\t.reg .b8 p, q, s, t;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 s, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t, %8, %7;\n\t"
+      "mov.b32 %0, {p, q, s, t};\n\t}"
+      : "=r"(r) : ATTN_F2_IN(a), ATTN_F2_IN(b), ATTN_F2_IN(c), ATTN_F2_IN(d));
   return r;
 }
 // Eight e2m1 values, four bits each from bit 0 up, as fp16 pairs (exact).

@@ -504,7 +504,7 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
  * after a cached prefix (attn_varlen_fwd takes the rows).
  *   bits : 8 or 4, which cache it is (its layout and scales as above)
  *   cu   : device int32 [B + 1], ascending: request b has rows cu[b] .. cu[b + 1] - 1
- *   k, v : [T, H, d] of dtype; row cu[b] + i becomes token i of request b, for i < lens[b] and
+ *   k, v : [T, H, d] of dtype, 32-byte aligned; row cu[b] + i becomes token i of request b, for i < lens[b] and
  *          within the request's rows and the T.  All other rows are left as they are, those
  *          behind the cached tokens of a request among them (its new tokens go there)
  * Values are scale * code, rounded to nearest even, at most the type's largest (NaN stays

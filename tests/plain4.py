@@ -37,11 +37,11 @@ def append(x, slots, codes, scales):
     """(codes, scales) after the tokens x [T, H, d] (float64) have gone to `slots`."""
     codes, scales = codes.clone(), scales.clone()
     P, H, page, _ = codes.shape
-    c, s = quantise(x)
-    for t, slot in enumerate(slots):
-        if 0 <= slot < P * page:
-            codes[slot // page, :, slot % page] = c[t]
-            scales[slot // page, :, slot % page] = s[t].to(scales.dtype)
+    at = torch.tensor(slots)
+    used = (at >= 0) & (at < P * page)
+    c, s = quantise(x[used])
+    codes[at[used] // page, :, at[used] % page] = c
+    scales[at[used] // page, :, at[used] % page] = s.to(scales.dtype)
     return codes, scales
 
 

@@ -72,10 +72,11 @@ def test_append_is_its_definition(page, H, d, dtype):
 
 
 @pytest.mark.parametrize("T,H,d,page", [(1, 1, 64, 16), (1, 1, 128, 128), (7, 300, 64, 16), (5000, 3, 128, 64),
-                                        (20000, 1, 64, 32), (1201, 7, 64, 16), (2, 4100, 128, 16), (700, 40, 128, 32)])
+                                        (20000, 1, 64, 32), (1201, 7, 64, 16), (2, 4100, 128, 16), (700, 40, 128, 32),
+                                        (21001, 8, 128, 16), (4003, 83, 64, 64)])
 def test_append_launch_shapes(T, H, d, page):
-    """From one token of one head to blocks of many tokens and tokens of many blocks, k and v slices of one
-    projection."""
+    """From one token of one head to blocks of many tokens, tokens of many blocks and blocks that read ahead, k and v
+    slices of one projection."""
     g = torch.Generator().manual_seed(T)
     P = T // page + 2
     x = torch.randn((T, 1 + 2 * H, d), generator=g).half()
@@ -83,6 +84,19 @@ def test_append_launch_shapes(T, H, d, page):
     kc, ks = plain4.cache(P, H, page, d, g)
     xg = x.cuda()
     check_append(x[:, 1:1 + H], x[:, 1 + H:], slots, kc, kc.flip(0), ks, ks.flip(0), xg[:, 1:1 + H], xg[:, 1 + H:])
+
+
+@pytest.mark.parametrize("T,H,d", [(5, 2, 64), (21001, 8, 128)])
+def test_append_tokens_on_16_byte_borders(T, H, d):
+    """Token strides that are multiples of 8 only, and a first token between two 32-byte borders."""
+    g = torch.Generator().manual_seed(T)
+    flat = torch.randn(8 + T * (H * d + 8), generator=g).bfloat16()
+    fg = flat.cuda()
+    view = lambda f: f.as_strided((T, H, d), (H * d + 8, d, 1), 8)  # noqa: E731
+    P = T // 16 + 1
+    slots = torch.randperm(P * 16, generator=g)[:T].tolist()
+    kc, ks = plain4.cache(P, H, 16, d, g)
+    check_append(view(flat), view(flat), slots, kc, kc, ks, ks, view(fg), view(fg))
 
 
 @pytest.mark.parametrize("s", [1.0, 75 / 64, 129 / 128, 85 / 32, 2.0 ** -14 * 1.5])
