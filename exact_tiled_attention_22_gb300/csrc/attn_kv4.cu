@@ -135,6 +135,7 @@ struct Kv4Layout {
   static constexpr int NO = 4 * NG;                   // O^T: a set for each warpgroup and group of channels
   static constexpr int PW = NO <= 32 ? 32 : (NO <= 64 ? 64 : 128);  // bytes of a P row, and its swizzle
   // CTAs to an SM and stages, by what shared memory, TMEM and registers leave
+  static constexpr int kSegCost = kv4_seg_cost(RP, NP == 2);
   static constexpr int kCtas = WG == 4 ? 1 : (PW == 32 ? 3 : 2);
   static constexpr int kStages = WG == 4 ? 5 : (PW == 64 ? 3 : 2);
   static constexpr int kCode = 128 * 128;             // bytes of a tile's codes: 16 to 16 bytes, 8 of them filled
@@ -280,9 +281,9 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
   if (threadIdx.x == 0) griddep_launch_dependents();
   Walk w0;
   if (p.B <= kWarpDealB) {
-    w0 = deal_warp<TS, kKv4SegCost>(p, Hr);
+    w0 = deal_warp<TS, L::kSegCost>(p, Hr);
   } else {
-    deal_range<TS, kKv4SegCost, L::kThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
+    deal_range<TS, L::kSegCost, L::kThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
                                              reinterpret_cast<long long*>(sbase + L::kStart));
     __syncthreads();
     w0 = first_walk(reinterpret_cast<const long long*>(sbase + L::kStart));
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
       };
       Walk w = w0;
       Seg sg;
-      while (ok && next_seg<TS, kKv4SegCost>(p, Hr, w, sg)) {
+      while (ok && next_seg<TS, L::kSegCost>(p, Hr, w, sg)) {
         const int h = sg.hr / p.n_rb;
         const int pages = (sg.len + (1 << p.page_shift) - 1) >> p.page_shift;
         const int* row = p.table + (size_t)sg.b * p.width;
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
     int g = 0, seg = 0;
     Walk w = w0;
     Seg sg;
-    bool more = next_seg<TS, kKv4SegCost>(p, Hr, w, sg);
+    bool more = next_seg<TS, L::kSegCost>(p, Hr, w, sg);
     if (more) load_q(sg);
     while (more) {
       put_q(sg, seg++);
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
       ok = norms(g, sg, sg.t0);
       if (!ok) break;
       const Seg now = sg;
-      more = next_seg<TS, kKv4SegCost>(p, Hr, w, sg);
+      more = next_seg<TS, L::kSegCost>(p, Hr, w, sg);
       if (more) load_q(sg);
       for (int t = now.t0; t < now.t1; ++t, ++g) {
         auto next_s = [&] {

@@ -895,8 +895,13 @@ static cudaError_t launch_merge_t(KvDecArgs a, cudaStream_t stream) {
 
 template <bool BF16>
 static cudaError_t launch_merge_b(const KvDecArgs& a, cudaStream_t stream) {
-  if (a.k_scale16)  // the cache in 4 bits
-    return a.d == 128 ? launch_merge_t<128, BF16, 7, kKv4SegCost>(a, stream) : launch_merge_t<64, BF16, 8, kKv4SegCost>(a, stream);
+  if (a.k_scale16) {  // the cache in 4 bits
+    if (a.rp == 4)
+      return a.d == 128 ? launch_merge_t<128, BF16, 7, kv4_seg_cost(4, BF16)>(a, stream)
+                        : launch_merge_t<64, BF16, 8, kv4_seg_cost(4, BF16)>(a, stream);
+    return a.d == 128 ? launch_merge_t<128, BF16, 7, kv4_seg_cost(8, BF16)>(a, stream)
+                      : launch_merge_t<64, BF16, 8, kv4_seg_cost(8, BF16)>(a, stream);
+  }
   return a.d == 128 ? launch_merge_t<128, BF16, 7, kKv8SegCost>(a, stream) : launch_merge_t<64, BF16, 7, kKv8SegCost>(a, stream);
 }
 

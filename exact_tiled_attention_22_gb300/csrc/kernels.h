@@ -214,7 +214,9 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int sms, cudaStream_t stre
 constexpr int kKvMaxCtas = 640;  // workspace bound of the decode grids
 // What a segment (one request's tiles of one head group) costs a CTA besides its tiles, in tiles.
 constexpr int kKv8SegCost = 2;   // (64 ragged requests: 65, 53, 52, 53 us with a cost of 0 to 3)
-constexpr int kKv4SegCost = 1;
+// (64 ragged requests in 4 bits, 0 to 2: three CTAs to an SM 43.3, 32.9, 33.4 us; two, in fp16, 47.7, 37.1, 35.7;
+// 16 query rows, one CTA: 61.1, 57.2, 55.3.)
+constexpr int kv4_seg_cost(int rp, bool bf16) { return rp == 4 && bf16 ? 1 : 2; }
 // Decoding from a paged cache, in 8 bits or in 4.
 struct KvDecArgs {
   CUtensorMap tm_k, tm_v;    // one page of one head a box: (d, page, P * H), in 4 bits (128, page * d / 128, P * H)

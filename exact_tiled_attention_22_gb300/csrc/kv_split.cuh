@@ -17,7 +17,7 @@ namespace {
 // in tiles: its query terms, the first S and the last O^T, during which nothing
 // else of the CTA runs.  Units are counted with it, tile t of a segment being
 // unit SC + t, so that a CTA with many short requests gets fewer tiles.  Both
-// caches' figures stand at kKv8SegCost and kKv4SegCost.
+// caches' figures stand at kKv8SegCost and kv4_seg_cost.
 template <int SC>
 __device__ __forceinline__ int seg_units(int nt) { return nt > 0 ? nt + SC : 0; }
 
