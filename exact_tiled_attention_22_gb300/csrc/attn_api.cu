@@ -918,7 +918,9 @@ int attn_kv4_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   a.causal = causal ? 1 : 0;
   a.scale = scale;
   const long long tile = 128 * (128 / d), tiles = ((long long)width * page + tile - 1) / tile;
-  a.grid = attn::kv4_grid(a.rp, a.bf16, dev->sms, tiles * B * H * a.n_rb);
+  const long long segs = (long long)B * H * a.n_rb;
+  a.cluster = attn::kv4_cluster(a.rp, a.bf16, dev->sms, B, segs, tiles);
+  a.grid = a.cluster ? (int)(segs * a.cluster) : attn::kv4_grid(a.rp, a.bf16, dev->sms, tiles * segs);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.ws_o = reinterpret_cast<float*>(ws);
   a.ws_ml = reinterpret_cast<float*>(ws + ((size_t)attn::kKvMaxCtas * 2 * a.rp * d * 4 + 255) / 256 * 256);
@@ -926,6 +928,7 @@ int attn_kv4_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = timed(attn::kKKv4Split, s, [&] { return attn::launch_kv4_split(a, s); });
   if (e != cudaSuccess) return cuda_fail(e, "attn_kv4_decode launch");
+  if (a.cluster) return ATTN_OK;
   e = timed(attn::kKKv4Merge, s, [&] { return attn::launch_kv_merge(a, s); });
   return e != cudaSuccess ? cuda_fail(e, "attn_kv4_decode merge launch") : ATTN_OK;
 }

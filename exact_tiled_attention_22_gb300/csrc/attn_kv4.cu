@@ -230,9 +230,12 @@ __device__ __forceinline__ uint32_t rest4_e4m3(uint32_t h_lo, uint32_t h_hi, uin
   return r;
 }
 
+constexpr int kMaxCluster = 16;
 constexpr float kNone = -1e30f;  // the maximum of scores that are all masked
 
-template <int D, int WG, int NP>
+// CL: a cluster of p.cluster CTAs takes one segment, whose tiles are dealt to them evenly, and joins
+// their parts through shared memory: no merge kernel, and no sums over the lengths to begin with.
+template <int D, int WG, int NP, bool CL>
 __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, WG, NP>::kCtas)
     attn_kv4_split_kernel(const __grid_constant__ KvDecArgs p) {
   using L = Kv4Layout<D, WG, NP>;
@@ -280,7 +283,19 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
   // (the merge kernel's blocks may come as CTAs end: they look at the lengths meanwhile)
   if (threadIdx.x == 0) griddep_launch_dependents();
   Walk w0;
-  if (p.B <= kWarpDealB) {
+  Seg mine;  // CL: the segment
+  const int rank = CL ? (int)(blockIdx.x % (unsigned)p.cluster) : 0;
+  if constexpr (CL) {
+    const unsigned seg = blockIdx.x / (unsigned)p.cluster;
+    mine.b = (int)(seg / (unsigned)Hr);
+    mine.hr = (int)(seg - (unsigned)mine.b * Hr);
+    mine.len = kv_len(p, mine.b);
+    mine.nt = kv_tiles<TS>(mine.len);
+    const int per = (mine.nt + p.cluster - 1) / p.cluster;
+    mine.t0 = min(mine.nt, rank * per);
+    mine.t1 = min(mine.nt, mine.t0 + per);
+    w0.left = mine.t1 - mine.t0;
+  } else if (p.B <= kWarpDealB) {
     w0 = deal_warp<TS, L::kSegCost>(p, Hr);
   } else {
     deal_range<TS, L::kSegCost, L::kThreads>(p, Hr, reinterpret_cast<long long*>(sbase + L::kScan),
@@ -289,6 +304,16 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
     w0 = first_walk(reinterpret_cast<const long long*>(sbase + L::kStart));
     __syncthreads();  // (the scan lies where the row maxima will)
   }
+  auto next_segment = [&](Walk& w, Seg& sg) {
+    if constexpr (CL) {
+      const bool first = w.left > 0;
+      w.left = 0;
+      sg = mine;
+      return first;
+    } else {
+      return next_seg<TS, L::kSegCost>(p, Hr, w, sg);
+    }
+  };
   // Barriers and TMEM are there for the warps that wait here; the producer, which made the
   // barriers, goes on.
   uint32_t tmem = 0;
@@ -354,7 +379,7 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
       };
       Walk w = w0;
       Seg sg;
-      while (ok && next_seg<TS, L::kSegCost>(p, Hr, w, sg)) {
+      while (ok && next_segment(w, sg)) {
         const int h = sg.hr / p.n_rb;
         const int pages = (sg.len + (1 << p.page_shift) - 1) >> p.page_shift;
         const int* row = p.table + (size_t)sg.b * p.width;
@@ -532,7 +557,7 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
     int g = 0, seg = 0;
     Walk w = w0;
     Seg sg;
-    bool more = next_seg<TS, L::kSegCost>(p, Hr, w, sg);
+    bool more = next_segment(w, sg);
     if (more) load_q(sg);
     while (more) {
       put_q(sg, seg++);
@@ -543,7 +568,7 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
       ok = norms(g, sg, sg.t0);
       if (!ok) break;
       const Seg now = sg;
-      more = next_seg<TS, L::kSegCost>(p, Hr, w, sg);
+      more = next_segment(w, sg);
       if (more) load_q(sg);
       for (int t = now.t0; t < now.t1; ++t, ++g) {
         auto next_s = [&] {
@@ -585,6 +610,9 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
     float* xl = reinterpret_cast<float*>(sbase + L::kXl) + wg * 16;
     const float4* qs = reinterpret_cast<const float4*>(sbase + L::kQs) + wg;
     uint8_t* prow = sbase + L::kP;
+    // CL: the CTA's part, where K was (all of its copies have been waited for)
+    float* part_o = reinterpret_cast<float*>(sbase + L::kK);
+    float2* part_ml = reinterpret_cast<float2*>(sbase + L::kK + RP * 512);
     const uint32_t all_bar = 1, wg_bar = WG == 1 ? 1 : 2 + wg;  // hardware barriers
     int g = 0, st = 0;
     for (int seg = 0;; ++seg) {
@@ -803,6 +831,11 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
         const float lt = (l4.x + l4.y) + (l4.z + l4.w);
         const float sum = TPR == 2 && kl < 64 ? acc[r] + half[r * 64 + kl] : acc[r];
         if (at.x < 0) continue;
+        if constexpr (CL) {  // joined below
+          part_o[(wg * 4 + r) * 128 + kl] = sum;
+          if (kl == 0) part_ml[wg * 4 + r] = make_float2(m[r], lt);
+          continue;
+        }
         if (whole) {
           const float v = lt != 0.f ? __fdividef(sum, lt) : 0.f;
           if (kl < D) reinterpret_cast<uint16_t*>(p.o)[(size_t)at.x * D + kl] = (uint16_t)pack2<BF16>(v, 0.f);
@@ -819,6 +852,56 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
       // (the next segment's P and row sums are written behind the barrier at its start)
     }
   }
+  if constexpr (CL) {
+    if (mine.nt == 0) {  // a request without tokens
+      if (rank == 0 && warp < 4 * WG) {
+        const int h = mine.hr / p.n_rb, rb = mine.hr % p.n_rb;
+        for (int r = warp; r < RP; r += 4 * WG) {
+          const int idx = rb * RP + r, i = idx / p.G, hq = h * p.G + idx % p.G;
+          if (idx >= p.Nq * p.G) break;
+          const size_t at = ((size_t)mine.b * p.Nq + i) * p.Hq + hq;
+          for (int c = lane; c < D; c += 32) reinterpret_cast<uint16_t*>(p.o)[at * D + c] = 0;
+          if (lane == 0) p.lse[((size_t)mine.b * p.Hq + hq) * p.Nq + i] = -INFINITY;
+        }
+      }
+    } else {
+      // The parts of the CTAs that had tiles; those deal the rows among them, in the order of rows.
+      cluster_sync();
+      const int per = (mine.nt + p.cluster - 1) / p.cluster, n = (mine.nt + per - 1) / per;
+      if (rank < n && warp < 4 * WG) {
+        const int c = threadIdx.x & 127;
+        const int2* rows = reinterpret_cast<const int2*>(sbase + L::kRow);
+        for (int r = rank + n * (warp >> 2); r < RP; r += n * WG) {
+          const int2 at = rows[r];
+          if (at.x < 0) break;
+          float mr[kMaxCluster], lr[kMaxCluster], o[kMaxCluster], M = kNone;
+#pragma unroll
+          for (int k = 0; k < kMaxCluster; ++k) {
+            mr[k] = kNone;
+            lr[k] = o[k] = 0.f;
+            if (k < n) {
+              const float2 ml = ld_cluster_f2(base + L::kK + RP * 512 + r * 8, k);
+              mr[k] = ml.x;
+              lr[k] = ml.y;
+              o[k] = ld_cluster_f(base + L::kK + (r * 128 + c) * 4, k);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, mr[k]);
+          float l = 0.f, sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < kMaxCluster; ++k) {
+            const float w = ex2(mr[k] - M);
+            l = fmaf(w, lr[k], l);
+            sum = fmaf(w, o[k], sum);
+          }
+          if (c < D) reinterpret_cast<uint16_t*>(p.o)[(size_t)at.x * D + c] = (uint16_t)pack2<BF16>(l != 0.f ? __fdividef(sum, l) : 0.f, 0.f);
+          if (c == 0) p.lse[at.y] = l != 0.f ? (M + __log2f(l)) * kLn2 : -INFINITY;
+        }
+      }
+      cluster_sync();  // (before any of them leaves)
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) {
@@ -830,10 +913,24 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
 template <int D, int WG, int NP>
 cudaError_t launch_split_t(const KvDecArgs& a, cudaStream_t stream) {
   using L = Kv4Layout<D, WG, NP>;
-  auto* k = attn_kv4_split_kernel<D, WG, NP>;
+  auto* k = a.cluster ? attn_kv4_split_kernel<D, WG, NP, true> : attn_kv4_split_kernel<D, WG, NP, false>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (e == cudaSuccess && a.cluster > 8) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, (unsigned)a.grid, L::kThreads, L::kSmem, stream, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.grid);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k, a);
 }
 
 template <int D>
@@ -882,9 +979,26 @@ cudaError_t launch_kv4_append(Kv4AppendArgs a, int sms, cudaStream_t stream) {
 // fp16 in three terms would take 384 columns of TMEM.)
 int kv4_rows(int R, bool bf16) { return R <= 4 ? 4 : (R <= 8 || !bf16 ? 8 : 16); }
 
+static long long resident(int rp, bool bf16, int sms) { return (rp == 16 ? 1ll : (rp == 4 && bf16 ? 3ll : 2ll)) * sms; }
+
+// CTAs of the cluster that takes a segment, of `tiles` tiles at most, or 0: the tiles of all
+// requests are dealt to all CTAs, and a second kernel joins the parts.  A cluster saves that
+// kernel and the sums over the lengths, but a long request among short ones is its few CTAs'
+// alone: four tiles to a CTA, eight where there is one request.  Up to 8 CTAs; 16 where that is one to an
+// SM (more such clusters do not fit at once: 24 segments of 4096 tokens 14 us, 9 with 8) and a
+// CTA would have more than two tiles.
+// Requests of equal length, us by clusters and dealt (bf16, 8 heads, groups of 4, d = 128): one of 1000 tokens
+// 5.5 and 8.0, of 8192 8.9 and 11.9, of 16384 13.5 and 13.3; 12 of 2048 10.1 and 13.5; 24 of 1024 10.7 and
+// 13.9.  Of 1 to 2048 tokens, 12: 9.2 and 10.0; of 1 to 4096, eight tiles to a CTA: 12.6 and 11.2.
+int kv4_cluster(int rp, bool bf16, int sms, int B, long long segs, long long tiles) {
+  int c = segs * 16 <= sms && tiles > 16 ? kMaxCluster : 8;
+  while (c > 1 && (segs * c > resident(rp, bf16, sms) || c / 2 >= tiles)) c /= 2;
+  return c > 1 && tiles <= (B == 1 ? 8 : 4) * c ? c : 0;
+}
+
 // All CTAs resident at once, no more than there can be tiles.
 int kv4_grid(int rp, bool bf16, int sms, long long max_units) {
-  long long g = (rp == 16 ? 1ll : (rp == 4 && bf16 ? 3ll : 2ll)) * sms;
+  long long g = resident(rp, bf16, sms);
   if (g > kKvMaxCtas) g = kKvMaxCtas;
   if (g > max_units) g = max_units;
   return (int)(g < 1 ? 1 : g);

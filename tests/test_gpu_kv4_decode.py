@@ -58,13 +58,22 @@ def reference(args, lens, scale, causal, dtype):
     return plain4.decoded(q.double(), plain4.values(kc, ks), plain4.values(vc, ones), vs, table, lens, scale, causal, dtype)
 
 
+def wide(table):
+    """The same block table with room for 70000 tokens a request: the tiles of all requests are dealt to all
+    blocks then, where a narrow table lets a cluster of blocks take a request's."""
+    room = torch.full((table.shape[0], 70000 // 16), 2 ** 30, dtype=torch.int32, device=table.device)
+    return torch.cat([table, room], 1)
+
+
 def decode_and_check(args, lens, scale, causal, dtype):
+    """Through clusters, if the table is narrow enough, and through dealt tiles."""
     from exact_tiled_attention_22_gb300 import attn
-    o, lse = attn.kv4_decode(*(x.cuda() for x in args), i32(lens), scale, causal)
-    attn.check(attn.attn_status())
     (ro, bo), (rl, bl) = reference(args, lens, scale, causal, dtype)
-    plain64.check(lse, rl, bl, "lse")
-    plain64.check(o, ro, bo, "o")
+    for table in (wide(args[-1]), args[-1]):
+        o, lse = attn.kv4_decode(*(x.cuda() for x in (*args[:-1], table)), i32(lens), scale, causal)
+        attn.check(attn.attn_status())
+        plain64.check(lse, rl, bl, "lse")
+        plain64.check(o, ro, bo, "o")
     return o, lse
 
 
@@ -93,6 +102,14 @@ DECODE = [
     ([33] * 400, 1, 2, 1, 64, 16, "fp16", True),         # more requests than threads
     ([20000, 1, 64], 1, 8, 1, 128, 64, "bf16", True),    # split over many blocks
     ([20001, 1, 64], 1, 4, 1, 64, 64, "fp16", True),
+    ([0, 900, 0, 1, 257], 1, 8, 2, 128, 16, "bf16", True),    # empty requests among others' clusters
+    ([2000], 1, 4, 1, 128, 16, "bf16", True),                 # a cluster of 16, one tile each
+    ([10000], 1, 32, 8, 128, 64, "bf16", True),               # ... five each
+    ([16001], 1, 8, 2, 64, 64, "fp16", True),
+    ([3000, 2999, 5], 2, 32, 8, 128, 128, "bf16", True),
+    ([1300] * 12, 1, 32, 8, 128, 64, "bf16", True),           # clusters of four, three tiles each
+    ([400] * 20, 1, 64, 8, 64, 32, "bf16", True),
+    ([511, 77] * 8, 1, 16, 1, 128, 16, "bf16", True),
 ]
 
 
@@ -153,18 +170,20 @@ def test_decode_not_numbers_stay_where_they_are():
     from exact_tiled_attention_22_gb300 import attn
     lens = [200, 200]
     q, kc, vc, ks, vs, table = problem(lens, 2, 4, 2, 64, 16, "fp16", seed=12)
-    clean, _ = attn.kv4_decode(*(x.cuda() for x in (q, kc, vc, ks, vs, table)), i32(lens))
+    tables = (table, wide(table))
+    clean = [attn.kv4_decode(*(x.cuda() for x in (q, kc, vc, ks, vs, t)), i32(lens))[0] for t in tables]
     q[0, 1, 3] = math.inf
     ks[table[1, 0], 1, 3, 1] = math.nan     # key head 1 of request 1
     vs[table[1, 12], 0, 7, 0] = math.nan    # its last token's value, head 0, channels 0 to 31
-    o, _ = attn.kv4_decode(*(x.cuda() for x in (q, kc, vc, ks, vs, table)), i32(lens))
-    nan = torch.isnan(o)
-    want = torch.zeros_like(nan)
-    want[0, 1, 3] = True
-    want[1, :, 2:] = True
-    want[1, :, :2, :32] = True              # (a hidden NaN times a zero is one, too)
-    assert torch.equal(nan, want)
-    assert torch.equal(o[~want], clean[~want])
+    for t, c in zip(tables, clean):
+        o, _ = attn.kv4_decode(*(x.cuda() for x in (q, kc, vc, ks, vs, t)), i32(lens))
+        nan = torch.isnan(o)
+        want = torch.zeros_like(nan)
+        want[0, 1, 3] = True
+        want[1, :, 2:] = True
+        want[1, :, :2, :32] = True          # (a hidden NaN times a zero is one, too)
+        assert torch.equal(nan, want)
+        assert torch.equal(o[~want], c[~want])
 
 
 def test_far_into_a_large_cache():
@@ -200,10 +219,11 @@ def test_far_into_a_large_cache():
         assert torch.equal(x.cpu().view(torch.int16), want.view(torch.int16))
 
 
-def test_two_calls_at_once_and_repeats():
+@pytest.mark.parametrize("narrow", [False, True])
+def test_two_calls_at_once_and_repeats(narrow):
     """Two streams with their own workspaces; equal results every time."""
     from exact_tiled_attention_22_gb300 import attn
-    lens = [5000, 17, 900]
+    lens = [900, 17, 700] if narrow else [5000, 17, 900]
     args = [x.cuda() for x in problem(lens, 1, 16, 4, 128, 64, "bf16", seed=4)]
     ln = i32(lens)
     want = attn.kv4_decode(*args, ln)
@@ -242,9 +262,10 @@ def test_pages_that_are_not_there_read_as_zeros():
         ks[0], vs[0] = math.nan, math.nan
         for j, i in zip(gone, (-1, kc.shape[0], 2 ** 31 - 1)):
             bad[0, j] = i
-        o, lse = attn.kv4_decode(q.cuda(), kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda(), bad.cuda(), i32(lens), 0.125)
-        plain64.check(lse, rl, bl, "lse")
-        plain64.check(o, ro, bo, "o")
+        for t in (bad, wide(bad)):
+            o, lse = attn.kv4_decode(q.cuda(), kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda(), t.cuda(), i32(lens), 0.125)
+            plain64.check(lse, rl, bl, "lse")
+            plain64.check(o, ro, bo, "o")
 
 
 def test_errors_of_decode():
@@ -276,6 +297,7 @@ def test_what_the_workspace_held_does_not_matter(lens):
     """A workspace full of NaN: only parts that this call wrote are read, also when there are fewer tiles than blocks."""
     from exact_tiled_attention_22_gb300 import attn
     args = [x.cuda() for x in problem(lens, 1, 8, 2, 128, 16, "bf16", seed=4)]
+    args[-1] = wide(args[-1])
     ln = i32(lens)
     n = attn.attn_kv4_decode_workspace_size(1, 8, 2, 128)
     clean = torch.zeros(n, dtype=torch.uint8, device="cuda")
@@ -284,14 +306,16 @@ def test_what_the_workspace_held_does_not_matter(lens):
     assert torch.isfinite(a[0]).all() and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_lengths_beyond_the_table_and_negative_ones():
+@pytest.mark.parametrize("n", [64, 1600, 40000])
+def test_lengths_beyond_the_table_and_negative_ones(n):
     from exact_tiled_attention_22_gb300 import attn
-    lens = [64, 64, 64]
+    lens = [n, n, n]
     q, kc, vc, ks, vs, table = problem(lens, 1, 4, 2, 64, 16, "bf16", seed=5)
-    short = table[:, :4].contiguous()
+    short = table[:, :n // 16].contiguous()
+    table = torch.cat([short, short[:, :1]], 1)
     args = [x.cuda() for x in (q, kc, vc, ks, vs)]
-    want = attn.kv4_decode(*args, table.cuda(), i32([64, 0, 64]), 0.1)
-    got = attn.kv4_decode(*args, short.cuda(), i32([2 ** 31 - 1, -5, 64]), 0.1)
+    want = attn.kv4_decode(*args, table.cuda(), i32([n, 0, n]), 0.1)
+    got = attn.kv4_decode(*args, short.cuda(), i32([2 ** 31 - 1, -5, n]), 0.1)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert (got[0][1] == 0).all() and (got[1][1] == -math.inf).all()
 
@@ -331,10 +355,13 @@ def test_tensors_freed_after_a_call_on_another_stream():
     del others
 
 
-def test_wait_limit_reports_a_timeout():
+@pytest.mark.parametrize("narrow", [False, True])
+@pytest.mark.parametrize("Hq", [2, 8, 16])
+def test_wait_limit_reports_a_timeout(narrow, Hq):
     from exact_tiled_attention_22_gb300 import attn
-    lens = [300]
-    args = [x.cuda() for x in problem(lens, 1, 2, 1, 64, 16, "fp16", seed=6)]
+    lens = [300, 0, 700]
+    args = [x.cuda() for x in problem(lens, 1, Hq, 1, 64, 16, "bf16", seed=6)]
+    args[-1] = args[-1] if narrow else wide(args[-1])
     ln = i32(lens)
     want = attn.kv4_decode(*args, ln)
     try:
