@@ -231,7 +231,7 @@ __device__ __forceinline__ uint32_t rest4_e4m3(uint32_t h_lo, uint32_t h_hi, uin
 }
 
 constexpr int kMaxCluster = 16;
-constexpr float kNone = -1e30f;  // the maximum of scores that are all masked
+constexpr float kNone = -3e38f;  // the maximum of scores that are all masked
 
 // CL: a cluster of p.cluster CTAs takes one segment, whose tiles are dealt to them evenly, and joins
 // their parts through shared memory: no merge kernel, and no sums over the lengths to begin with.

@@ -317,3 +317,35 @@ def test_streams_of_append_and_read():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all(torch.equal(a, b) for a, b in zip((kc, vc, ks, vs), state))
+
+
+# ------------------------------------------------------------------ the C ABI's mirrors
+def test_raw_calls():
+    """attn_kv4_append, attn_kv4_decode and attn_kv_read on the caller's buffers and stream: the bits of the
+    conveniences."""
+    from exact_tiled_attention_22_gb300 import attn
+    g = torch.Generator().manual_seed(11)
+    lens, H, Hq, d, page = [40, 900], 2, 8, 128, 32
+    kc, vc, ks, vs, table = (x.cuda() for x in read_problem(4, lens, H, d, page, g))
+    P, width = kc.shape[0], table.shape[1]
+    new = torch.randn((2, 2, H, d), generator=g).bfloat16().cuda()
+    q = torch.randn((2, 1, Hq, d), generator=g).bfloat16().cuda()
+    slots = torch.stack([table[0, 1].long() * page + 7, table[1, 28].long() * page + 3])
+    ln, cu = i32(lens), i32([0, 40, 940])
+    mine = [x.clone() for x in (kc, vc, ks, vs)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    attn.check(attn.attn_kv4_append(new[:, 0], new[:, 1], 2 * H * d, 2 * H * d, slots, 2, H, d, *mine, P, page, "bf16", side))
+    o, lse = torch.empty_like(q), torch.empty((2, Hq, 1), device="cuda")
+    n = attn.attn_kv4_decode_workspace_size(1, Hq, H, d)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    attn.check(attn.attn_kv4_decode(q, *mine, table, ln, o, lse, 2, 1, Hq, H, d, P, page, width, 0.1, True, "bf16", ws, n, side))
+    k, v = (torch.empty((940, H, d), dtype=torch.float16, device="cuda") for _ in range(2))
+    attn.check(attn.attn_kv_read(*mine, table, ln, cu, k, v, 2, 940, H, d, P, page, width, 4, "fp16", side))
+    side.synchronize()
+    attn.kv4_append(new[:, 0], new[:, 1], slots, kc, vc, ks, vs)
+    want = (kc, vc, ks, vs, *attn.kv4_decode(q, kc, vc, ks, vs, table, ln, 0.1),
+            *attn.kv4_read(kc, vc, ks, vs, table, ln, cu, 940, torch.float16))
+    for a, b in zip((*mine, o, lse, k, v), want):
+        assert torch.equal(a, b)
+    assert torch.isfinite(lse).all()

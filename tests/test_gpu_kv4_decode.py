@@ -151,6 +151,28 @@ def test_decode_sharp_scores_and_wide_queries():
     decode_and_check(args, lens, 0.01, True, "bf16")
 
 
+@pytest.mark.parametrize("size", [1e25, 1e-25])
+def test_decode_scores_of_any_size(size):
+    """Scores of 1e32 and more, of either sign (one key takes all, even where all are far below zero), and next to
+    none (a mean)."""
+    lens = [300, 1]
+    args = list(problem(lens, 1, 4, 1, 64, 16, "bf16", seed=20, spread=1))
+    args[0] = (args[0].float() * size).bfloat16()
+    args[3] = args[3] * 1e7
+    from exact_tiled_attention_22_gb300 import attn
+    for q in (args[0], -args[0]):
+        (ro, bo), (rl, bl) = reference([q, *args[1:]], lens, 1.0, True, "bf16")
+        for t in (args[-1], wide(args[-1])):
+            o, lse = attn.kv4_decode(*(x.cuda() for x in (q, *args[1:-1], t)), i32(lens), 1.0)
+            if size > 1:  # (the score's own rounding decides between keys whose scores are close: the others' are not)
+                far = (o.double().cpu() - ro).abs() <= 2.0 ** -8 * ro.abs() + 1e-3
+                assert torch.isfinite(o).all() and far.all()
+                assert ((lse.double().cpu() - rl).abs() <= 2.0 ** -16 * rl.abs()).all()
+            else:
+                plain64.check(lse, rl, bl, "lse")
+                plain64.check(o, ro, bo, "o")
+
+
 def test_decode_a_heavy_token_of_small_value():
     """A first token that takes nearly all the weight and whose value is next to nothing: the others' part stays exact."""
     lens = [200]
@@ -375,13 +397,14 @@ def test_wait_limit_reports_a_timeout(narrow, Hq):
 
 
 # ------------------------------------------------------------------ together
-def test_a_serving_run():
+@pytest.mark.parametrize("width", [12, 70])
+def test_a_serving_run(width):
     """Prompts are attended to as a packed batch and written to the cache; one goes on with a second turn, whose
     queries attend to the cached prefix read back in front of the new keys; then all are decoded token by token from a
     captured step; requests leave and their pages are used again.  Every step against 64 bits over the cache as the
-    definition fills it."""
+    definition fills it.  (Tables of 70 pages: five tiles a request, clusters.)"""
     from exact_tiled_attention_22_gb300 import attn
-    B, Hq, H, d, page, width = 4, 8, 2, 64, 16, 12
+    B, Hq, H, d, page = 4, 8, 2, 64, 16
     g = torch.Generator().manual_seed(42)
     P = 40
     kc = torch.full((P, H, page, d // 2), 0xFF, dtype=torch.uint8, device="cuda")  # nothing written yet
