@@ -921,6 +921,7 @@ int attn_kv4_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   const long long segs = (long long)B * H * a.n_rb;
   a.cluster = attn::kv4_cluster(a.rp, a.bf16, dev->sms, B, segs, tiles);
   a.grid = a.cluster ? (int)(segs * a.cluster) : attn::kv4_grid(a.rp, a.bf16, dev->sms, tiles * segs);
+  a.full = attn::kv4_full(a.rp, a.bf16, dev->sms, a.grid);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.ws_o = reinterpret_cast<float*>(ws);
   a.ws_ml = reinterpret_cast<float*>(ws + ((size_t)attn::kKvMaxCtas * 2 * a.rp * d * 4 + 255) / 256 * 256);

@@ -7,7 +7,36 @@
 //
 // attn_kv4_append_kernel   rounds new keys and values into their slots.
 // attn_kv4_split_kernel    O = softmax(s q K^T) V over the cache, split (joined by
-//                          attn_kv_merge_kernel).
+//                          attn_kv_merge_kernel or within clusters).
+//
+// Decoding streams the codes and scales once, 1.125 d bytes a key and head.  As in the
+// cache in 8 bits no thread converts a cached value: TMA copies the packed codes and
+// spreads them over shared memory as the tensor core takes e2m1 (16 codes in 8 bytes,
+// 8 bytes unused), and the *other* operand of each product is a short sum of e4m3
+// terms (see attn_kv8.cu).  What is new is that the scales change along d and from token
+// to token.  With groups g of 32 channels, which is one k-step of the MMA,
+//   s_j      = sum_g ks[j][g] (K_g q_g^T)_j           the four k-steps of S^T go to columns of their own
+//                                                     and are added by the thread that owns the key
+//   O[c in g] = sum_j code[j][c] (p_j vs[j][g])       P has a set of columns for each group, with the
+//                                                     scale multiplied in; a warp of the accumulator's
+//                                                     lanes, 32 channels, reads its own group's set
+// A row of an operand is 128 channels: a token at d = 128, two at d = 64 (the query then stands twice in
+// its row, and P's sets belong to the first and the second token), so both sizes are one kernel.
+//
+// P's numbers fill e4m3's range whatever the scales are: group g is measured by a power of two above the
+// largest vs[.][g] of the tile, found by the MMA warp while it waits, and the row's reference is
+// the maximum of s_j + log2 u_j, u_j the token's largest measured scale.  l sums 2^(s - m) without the scales.
+//
+// Work: deal and merge as attn_kv8.cu, or, for few or short requests, a cluster of CTAs to a segment
+// (kv4_cluster), which joins its parts through shared memory.  Three rings of stages, for K, V and scales:
+// K is let go when S is there, a softmax earlier than V, which keeps twice as much in flight (with one ring
+// for all, four long requests took 107 us, 86 with one CTA less and a stage more, 80 with three rings).
+//
+// Measured (graph replay, bf16, d = 128): four requests of 50001 to 131072 tokens, 32 query and 8 key heads, 450 MB:
+// 75.8 us or 5.9 TB/s, 88 % of the measured copy bandwidth (from tile to tile 97 %; the rest is the start, the
+// uneven ends and the merge); 64 requests of 100 to 8192 tokens, 130 MB: 31.7 us; one of 1000 tokens: 5.6 us.
+// The tensor pipe is 9 % busy, the warp schedulers 47 %.  With 8 and 16 query rows the conversions and
+// the softmax bound it: 0.6 and 1.2 us a tile and SM, 0.43 with 4 rows, which is the memory's rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,6 +59,8 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Bound by memory for long prompts (256k tokens of 8 heads, d = 128, 1.35 GB: 264 us or 5.1 TB/s) and half by its
+// own instructions (issue slots 45 %), by its launch for a decoding step (256 tokens 1.7 us in a graph).
 // A thread rounds 16 channels (32 bytes in, 8 out), two neighbours share a scale.  A block
 // takes p.tok tokens of K or of V (blockIdx.y), all their heads.  W32: tokens begin on
 // 32-byte borders, and a thread's channels are read at once.  AHEAD: the next item is read
@@ -975,8 +1006,9 @@ cudaError_t launch_kv4_append(Kv4AppendArgs a, int sms, cudaStream_t stream) {
   return a.bf16 ? launch_append_t<64, true>(a, w32, ahead, stream) : launch_append_t<64, false>(a, w32, ahead, stream);
 }
 
-// Row blocks of 4, 8 or, in bf16, 16 rows: the work per tile grows with the rows.  (16 rows of
-// fp16 in three terms would take 384 columns of TMEM.)
+// Row blocks of 4, 8 or, in bf16, 16 rows, a warpgroup for every four: what a thread does for a tile does not
+// grow, and a block of 16 rows is one CTA's (32 requests of 1000 to 16384 tokens, 64 query and 4 key heads: 55 us;
+// one warpgroup for all 16 rows 67).  (16 rows of fp16 in three terms would take P rows of 192 bytes.)
 int kv4_rows(int R, bool bf16) { return R <= 4 ? 4 : (R <= 8 || !bf16 ? 8 : 16); }
 
 static long long resident(int rp, bool bf16, int sms) { return (rp == 16 ? 1ll : (rp == 4 && bf16 ? 3ll : 2ll)) * sms; }
@@ -1003,6 +1035,12 @@ int kv4_grid(int rp, bool bf16, int sms, long long max_units) {
   if (g > max_units) g = max_units;
   return (int)(g < 1 ? 1 : g);
 }
+
+// Of three CTAs to an SM the last one starts a microsecond after the others and goes 5 % slower:
+// four long requests, equal shares: the first two thirds of the CTAs end at 68 us, the others at 73.  Shares
+// of 8 and 7: 75.8 us in all, 78.6 with equal ones, 76.7 with 9 and 8, 75.9 with 7 and 6 (64 ragged
+// requests 31.7, 32.9, 31.8, 31.5).
+int kv4_full(int rp, bool bf16, int sms, int grid) { return resident(rp, bf16, sms) == 3ll * sms && grid == 3 * sms ? 2 * sms : 0; }
 
 cudaError_t launch_kv4_split(const KvDecArgs& a, cudaStream_t stream) {
   return a.d == 128 ? launch_split_d<128>(a, stream) : launch_split_d<64>(a, stream);

@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(128) attn_kv_merge_kernel(const __grid_constan
   __syncthreads();
   before = sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0];
   total = sums[0][1] + sums[1][1] + sums[2][1] + sums[3][1];
-  const long long units = total * Hr, n_cta = min((long long)p.grid, units);
+  const Deal deal(p, total * Hr);
   int nt = kv_tiles<TS>(kv_len(p, b));
   bool waited = false;
   for (unsigned unit = first; unit < min(first + run, units_all); ++unit) {
@@ -741,11 +741,11 @@ __global__ void __launch_bounds__(128) attn_kv_merge_kernel(const __grid_constan
     const int h = hr / p.n_rb, rb = hr - h * p.n_rb;
     const int r = (int)((unit - blk * n_in) * per) + (WPR == 4 ? 0 : warp), idx = rb * p.rp + r;
     const long long u0 = before * Hr + (long long)hr * seg_units<SC>(nt);
-    const int c0 = nt ? (int)range_owner(u0 + SC, units, n_cta) : 0;
-    const int c1 = nt ? (int)range_owner(u0 + SC + nt - 1, units, n_cta) : 0;
+    const int c0 = nt ? (int)deal.owner(u0 + SC) : 0;
+    const int c1 = nt ? (int)deal.owner(u0 + SC + nt - 1) : 0;
     if ((nt == 0 || c0 != c1) && (WPR == 1 || idx < R)) {
       // the first CTA's part is in its second slot if its range began earlier
-      const int s0 = nt && range_start(c0, units, n_cta) < u0 ? 1 : 0;
+      const int s0 = nt && deal.start(c0) < u0 ? 1 : 0;
       auto part = [&](int c) -> size_t { return ((size_t)c * 2 + (c == c0 ? s0 : 0)) * p.rp + r; };
       const bool live = idx < R;  // (WPR = 1: a warp may have no row)
       if (!waited) griddep_wait();

@@ -234,6 +234,7 @@ struct KvDecArgs {
   int B, Nq, Hq, H, G, d, width, page_shift, P;
   int rp, n_rb;              // rows of a row block, row blocks
   int grid;
+  int full;                  // CTAs with a full share, those after them have a little less; 0: equal shares
   int cluster;               // 4 bits: CTAs of a cluster that takes a segment, or 0
   int merge_run;             // groups of four rows to a block of the merge: the launcher's choice
   int causal, bf16;
@@ -272,6 +273,7 @@ cudaError_t launch_kv4_append(Kv4AppendArgs a, int sms, cudaStream_t stream);
 int kv4_rows(int R, bool bf16);
 int kv4_cluster(int rp, bool bf16, int sms, int B, long long segs, long long tiles);
 int kv4_grid(int rp, bool bf16, int sms, long long max_units);
+int kv4_full(int rp, bool bf16, int sms, int grid);
 cudaError_t launch_kv4_split(const KvDecArgs& a, cudaStream_t stream);
 
 // Cached keys and values as packed 16-bit rows (attn_kvread.cu).

@@ -21,18 +21,32 @@ namespace {
 template <int SC>
 __device__ __forceinline__ int seg_units(int nt) { return nt > 0 ? nt + SC : 0; }
 
-// The units are dealt to min(grid, units) CTAs, so that none of those has an
-// empty range (the merge kernel reads a part from each CTA of a segment).  (Divisions in 32
-// bits where the products fit: 64-bit ones took 0.3 us of a short decoding step.)
-__device__ __forceinline__ bool fits32(long long units, long long grid) { return units <= 0xffffffffll / grid; }
-__device__ __forceinline__ long long range_start(long long c, long long units, long long grid) {
-  return fits32(units, grid) ? (long long)((uint32_t)c * (uint32_t)units / (uint32_t)grid) : c * units / grid;
-}
-// The CTA whose range holds unit u.
-__device__ __forceinline__ long long range_owner(long long u, long long units, long long grid) {
-  return fits32(units, grid) ? (long long)((((uint32_t)u + 1) * (uint32_t)grid - 1) / (uint32_t)units)
-                             : ((u + 1) * grid - 1) / units;
-}
+// The units are dealt to n = min(grid, units) CTAs, so that none of those has an empty range (the merge
+// kernel reads a part from each CTA of a segment): in equal shares, or, where `full` says so and there
+// are units enough, with shares of kFull to the first `full` CTAs and of kLate to the others.
+// (Divisions in 32 bits where the products fit: 64-bit ones took 0.3 us of a short decoding step.)
+constexpr int kFull = 8, kLate = 7;
+struct Deal {
+  long long units, n, all;  // all: the sum of the shares
+  long long full;           // 0: equal shares of 1
+  bool small;
+  __device__ __forceinline__ Deal(const KvDecArgs& p, long long units_) : units(units_), n(min((long long)p.grid, units_)) {
+    full = p.full && units >= 4ll * p.grid ? p.full : 0;
+    all = full ? full * kFull + (n - full) * kLate : n;
+    small = units <= 0xffffffffll / max(all, 1ll);
+  }
+  // The first unit of CTA c's range.
+  __device__ __forceinline__ long long start(long long c) const {
+    const long long x = !full ? c : (c < full ? c * kFull : full * kFull + (c - full) * kLate);
+    return small ? (long long)((uint32_t)x * (uint32_t)units / (uint32_t)all) : x * units / all;
+  }
+  // The CTA whose range holds unit u: the last one that starts at u or before.
+  __device__ __forceinline__ long long owner(long long u) const {
+    const long long y = small ? (long long)((((uint32_t)u + 1) * (uint32_t)all - 1) / (uint32_t)units) : ((u + 1) * all - 1) / units;
+    if (!full) return y;
+    return y < full * kFull ? (uint32_t)y / kFull : full + (uint32_t)(y - full * kFull) / kLate;
+  }
+};
 
 __device__ __forceinline__ int kv_len(const KvDecArgs& p, int b) {
   const long long cap = (long long)p.width << p.page_shift;
@@ -105,10 +119,10 @@ __device__ __forceinline__ void deal_range(const KvDecArgs& p, int Hr, long long
     total += wsum[w];
   }
   const long long units = total * Hr;
-  const long long n_cta = min((long long)p.grid, units);
-  const bool has = blockIdx.x < n_cta;
-  const long long u0 = has ? range_start(blockIdx.x, units, n_cta) : 0;
-  const long long u1 = has ? range_start(blockIdx.x + 1ll, units, n_cta) : 0;
+  const Deal deal(p, units);
+  const bool has = blockIdx.x < deal.n;
+  const long long u0 = has ? deal.start(blockIdx.x) : 0;
+  const long long u1 = has ? deal.start(blockIdx.x + 1ll) : 0;
   if (threadIdx.x == 0) {
     st[0] = u0;
     st[1] = u1;
@@ -147,10 +161,10 @@ __device__ __forceinline__ Walk deal_warp(const KvDecArgs& p, int Hr) {
     const uint32_t a = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += a;
   }
-  const long long units = (long long)__shfl_sync(0xffffffffu, inc, 31) * Hr, n_cta = min((long long)p.grid, units);
+  const Deal deal(p, (long long)__shfl_sync(0xffffffffu, inc, 31) * Hr);
   Walk w = {0, 0, 0, 0};
-  if (blockIdx.x >= n_cta) return w;
-  const long long u0 = range_start(blockIdx.x, units, n_cta);
+  if (blockIdx.x >= deal.n) return w;
+  const long long u0 = deal.start(blockIdx.x);
   long long at = (long long)(inc - mine) * Hr;
   const bool here = at <= u0 && u0 < (long long)inc * Hr;
   if (here) {
@@ -169,7 +183,7 @@ __device__ __forceinline__ Walk deal_warp(const KvDecArgs& p, int Hr) {
   w.b = __shfl_sync(0xffffffffu, w.b, src);
   w.hr = __shfl_sync(0xffffffffu, w.hr, src);
   w.v = __shfl_sync(0xffffffffu, w.v, src);
-  w.left = range_start(blockIdx.x + 1ll, units, n_cta) - u0;
+  w.left = deal.start(blockIdx.x + 1ll) - u0;
   return w;
 }
 __device__ __forceinline__ Walk first_walk(const long long* st) {
