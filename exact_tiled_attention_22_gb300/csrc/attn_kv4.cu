@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kAppThreads) attn_kv4_append_kernel(const __gr
   const int items = n_tok * p.H * kParts;
   const uint8_t* x = static_cast<const uint8_t*>(p.x[kv]);
   const int ps = 1 << p.page_shift;
-  auto fetch = [&](int i, uint32_t* w, long long& at) {
+  auto fetch = [&](int i, uint32_t* w, long long& at) {  // (w on a 16-byte border)
     const int row = i / kParts, part = i % kParts;
     const int tl = (int)__umulhi((uint32_t)row * 2, p.h_magic), h = row - tl * p.H;
     at = -1;
@@ -94,11 +94,11 @@ __global__ void __launch_bounds__(kAppThreads) attn_kv4_append_kernel(const __gr
         at = ((((slot >> p.page_shift) * p.H + h) << p.page_shift) + (slot & (ps - 1))) * kParts + part;
     }
   };
-  uint32_t next[8];
+  __align__(16) uint32_t next[8];
   long long next_at = -1;  // (page, head, place) of an item, -1: none
   if constexpr (AHEAD) fetch(threadIdx.x, next, next_at);
   for (int i = threadIdx.x; i - (int)threadIdx.x < items; i += kAppThreads) {
-    uint32_t w[8];
+    __align__(16) uint32_t w[8];
     long long at = next_at;
     if constexpr (AHEAD) {
 #pragma unroll
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
     tmem_relinquish();
   }
   griddep_wait();
-  // (the merge kernel's blocks may come as CTAs end: they look at the lengths meanwhile)
+  // (What comes next may be scheduled as CTAs end: the merge kernel looks at the lengths meanwhile.)
   if (threadIdx.x == 0) griddep_launch_dependents();
   Walk w0;
   Seg mine;  // CL: the segment
@@ -1007,8 +1007,9 @@ cudaError_t launch_kv4_append(Kv4AppendArgs a, int sms, cudaStream_t stream) {
 }
 
 // Row blocks of 4, 8 or, in bf16, 16 rows, a warpgroup for every four: what a thread does for a tile does not
-// grow, and a block of 16 rows is one CTA's (32 requests of 1000 to 16384 tokens, 64 query and 4 key heads: 55 us;
-// one warpgroup for all 16 rows 67).  (16 rows of fp16 in three terms would take P rows of 192 bytes.)
+// grow, and a block of 16 rows is one CTA's (32 requests of 1000 to 16384 tokens, 64 query and 4 key heads: 55 us,
+// with 8 rows, 64 and 8 heads, 55; one warpgroup for all of a block's rows 57 and 53, but 19.8 us against 18.1 for 912
+// heads of 128 tokens in groups of 8).  (16 rows of fp16 in three terms would take P rows of 192 bytes.)
 int kv4_rows(int R, bool bf16) { return R <= 4 ? 4 : (R <= 8 || !bf16 ? 8 : 16); }
 
 static long long resident(int rp, bool bf16, int sms) { return (rp == 16 ? 1ll : (rp == 4 && bf16 ? 3ll : 2ll)) * sms; }

@@ -495,7 +495,7 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
  * page id outside [0, P) reads as zeros.  Scales must be finite and >= 0; a NaN among a
  * request's cached values may reach all its queries.  Query and key products carry
  * queries exactly up to 2^-21 of a row's largest element; a probability times its value's scale
- * is rounded to 2^-14 (fp16) or 2^-9 (bf16) of itself, and by no more than 2^-25 or 2^-21 of
+ * is rounded to 2^-14 (fp16) or 1.25 * 2^-9 (bf16) of itself, and by no more than 2^-25 or 2^-21 of
  * the largest such product in its tile of 128 (d = 128) or 256 tokens, every group of 32
  * channels measured by its own largest scale there.
  * width * page at most 2^31 - 256, Hq / H at most 2^23.
