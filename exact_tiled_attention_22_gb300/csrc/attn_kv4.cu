@@ -24,7 +24,8 @@
 // its row, and P's sets belong to the first and the second token), so both sizes are one kernel.
 //
 // P's numbers fill e4m3's range whatever the scales are: group g is measured by a power of two above the
-// largest vs[.][g] of the tile, found by the MMA warp while it waits, and the row's reference is
+// largest vs[.][g] of the tile (at d = 64 of both tokens of its rows: measured apart, the other one's P could
+// fall among e4m3's subnormals), found by the MMA warp while it waits, and the row's reference is
 // the maximum of s_j + log2 u_j, u_j the token's largest measured scale.  l sums 2^(s - m) without the scales.
 //
 // Work: deal and merge as attn_kv8.cu, or, for few or short requests, a cluster of CTAs to a segment
@@ -56,6 +57,12 @@ constexpr float kLog2e = 1.44269504088896340736f;
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -469,21 +476,25 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
       if (!wt(L::kBarCFull + s, (g / L::kStages) & 1)) return false;
       const uint4* sc = reinterpret_cast<const uint4*>(sbase + L::kSc + s * 2 * L::kScl + L::kScl);
       const int live = sg.len - (t << TS);  // tokens of the tile that there are, or more
-      uint32_t a = 0, b = 0;                // largest magnitudes of groups 0 and 1, 2 and 3, as bits
+      // Magnitudes as bits + 0x7f, so that a NaN, negative as 16 signed bits, does not count: its own scale makes
+      // its group a NaN, and the others are measured without it.
+      uint32_t a = 0x007f007fu, b = a;  // the largest of groups 0 and 1, 2 and 3
+      auto with = [](uint32_t top, uint32_t v) { return max_s16x2(top, (v & 0x7fff7fffu) + 0x007f007fu); };
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint4 v = sc[i * 32 + lane];  // rows 2 (32 i + lane) and the next
         const int tok = 2 * (i * 32 + lane) * TPR;
-        if (tok < live) a = max_u16x2(a, v.x & 0x7fff7fffu);
-        if (tok + TPR - 1 < live) b = max_u16x2(b, v.y & 0x7fff7fffu);
-        if (tok + TPR < live) a = max_u16x2(a, v.z & 0x7fff7fffu);
-        if (tok + 2 * TPR - 1 < live) b = max_u16x2(b, v.w & 0x7fff7fffu);
+        if (tok < live) a = with(a, v.x);
+        if (tok + TPR - 1 < live) b = with(b, v.y);
+        if (tok + TPR < live) a = with(a, v.z);
+        if (tok + 2 * TPR - 1 < live) b = with(b, v.w);
       }
-      const uint32_t top[4] = {__reduce_max_sync(0xffffffffu, a & 0xffffu), __reduce_max_sync(0xffffffffu, a >> 16),
-                               __reduce_max_sync(0xffffffffu, b & 0xffffu), __reduce_max_sync(0xffffffffu, b >> 16)};
+      if (TPR == 2) a = max_s16x2(a, b);  // one measure for the first and the second tokens of the rows
+      uint32_t top[4] = {__reduce_max_sync(0xffffffffu, a & 0xffffu), __reduce_max_sync(0xffffffffu, a >> 16)};
+      top[2] = TPR == 2 ? top[0] : __reduce_max_sync(0xffffffffu, b & 0xffffu);
+      top[3] = TPR == 2 ? top[1] : __reduce_max_sync(0xffffffffu, b >> 16);
       if (lane < 4) {
-        const uint32_t m = lane == 0 ? top[0] : (lane == 1 ? top[1] : (lane == 2 ? top[2] : top[3]));
-        // (a NaN among them says nothing of the others: its own scale makes its group a NaN)
+        const uint32_t m = (lane == 0 ? top[0] : (lane == 1 ? top[1] : (lane == 2 ? top[2] : top[3]))) - 0x7f;
         const int e = min(max((int)(m >> 7) - 126, -100), 100);
         float* n = reinterpret_cast<float*>(sbase + L::kNorm + s * 32);
         n[lane] = pow2f(-e);

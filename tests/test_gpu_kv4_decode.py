@@ -187,6 +187,30 @@ def test_decode_a_heavy_token_of_small_value():
         decode_and_check(args, lens, 128.0 / d * 0.08, True, "bf16")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heavy,large", [(0, 7), (1, 6), (0, 6), (1, 7)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_decode_small_values_between_a_heavy_token_and_a_large_value(d, heavy, large, dtype):
+    """A token with nearly all the weight whose value is zero in half of the channels, one without weight but with a
+    scale 700 times the others', on even and odd places: the other tokens' values keep their precision in those
+    channels."""
+    lens = [8]
+    q, kc, vc, ks, vs, table = problem(lens, 1, 4, 1, d, 16, dtype, seed=21)
+    page = table[0, 0].item()
+    q.fill_(0.25)
+    kc[page, 0, :8] = 0x22                                       # ones
+    ks[page, 0, :8] = 0.01
+    ks[page, 0, heavy] = 0.01 + 6.0 * 4 / d
+    ks[page, 0, large] = -9.0 * 4 / d
+    vc[page, 0, :8] = 0x55                                       # threes
+    vs[page, 0, :8] = 2.0 ** -11
+    vs[page, 0, heavy] = 2.0 ** -8
+    vs[page, 0, large] = 0.35
+    vc[page, 0, heavy, d // 4:] = 0
+    vc[page, 0, large, d // 4:] = 0
+    decode_and_check((q, kc, vc, ks, vs, table), lens, 1.0, True, dtype)
+
+
 def test_decode_not_numbers_stay_where_they_are():
     """A NaN in a query or in a cached token reaches the heads that see it, no other."""
     from exact_tiled_attention_22_gb300 import attn
