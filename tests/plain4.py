@@ -12,7 +12,7 @@ GRID = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float6
 def quantise(x):
     """x [.., d] in float64 -> codes uint8 [.., d / 2], scales float64 [.., d / 32] (NaN where
     the group holds one)."""
-    g = x.reshape(*x.shape[:-1], -1, 32)
+    g = x.unflatten(-1, (-1, 32))
     m, e = torch.frexp(g.abs().amax(-1) / 6)
     s = torch.where(torch.isinf(m), 2.0 ** 60, torch.round(m * 256) * torch.exp2((e - 8).double()))
     s = s.clamp(2.0 ** -64, 2.0 ** 60)
@@ -22,7 +22,7 @@ def quantise(x):
     for i in range(1, 8):
         border = (GRID[i - 1] + GRID[i]) / 2
         code += (y > border) | ((y == border) & (i % 2 == 0))
-    code = (code + 8 * torch.signbit(g)).reshape(*x.shape[:-1], -1, 2)
+    code = (code + 8 * torch.signbit(g)).flatten(-2).unflatten(-1, (-1, 2))
     return (code[..., 0] + 16 * code[..., 1]).to(torch.uint8), s
 
 
