@@ -318,8 +318,9 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
     tmem_relinquish();
   }
   griddep_wait();
-  // (What comes next may be scheduled as CTAs end: the merge kernel looks at the lengths meanwhile.)
-  if (threadIdx.x == 0) griddep_launch_dependents();
+  // What comes next may be scheduled as CTAs end: the merge kernel looks at the lengths meanwhile.  The warp that
+  // says so has its tensor memory: a kernel that took it first would wait for this one, which could not begin.
+  if (threadIdx.x == kWarpMma * 32) griddep_launch_dependents();
   Walk w0;
   Seg mine;  // CL: the segment
   const int rank = CL ? (int)(blockIdx.x % (unsigned)p.cluster) : 0;
