@@ -26,7 +26,7 @@
 // P's numbers fill e4m3's range whatever the scales are: group g is measured by a power of two above the
 // largest vs[.][g] of the tile (at d = 64 of both tokens of its rows: measured apart, the other one's P could
 // fall among e4m3's subnormals), found by the MMA warp while it waits, and the row's reference is
-// the maximum of s_j + log2 u_j, u_j the token's largest measured scale.  l sums 2^(s - m) without the scales.
+// the maximum of s_j + log2 u_j, u_j the token's largest measured scale (or 2^-80).  l sums 2^(s - m) without the scales.
 //
 // Work: deal and merge as attn_kv8.cu, or, for few or short requests, a cluster of CTAs to a segment
 // (kv4_cluster), which joins its parts through shared memory.  Three rings of stages, for K, V and scales:
@@ -270,6 +270,11 @@ __device__ __forceinline__ uint32_t rest4_e4m3(uint32_t h_lo, uint32_t h_hi, uin
 
 constexpr int kMaxCluster = 16;
 constexpr float kNone = -3e38f;  // the maximum of scores that are all masked
+// A token's values count for the row's reference as this much of the tile's largest scale, if they are smaller: p is at
+// most 2^88 then, and its sum over 2^31 tokens below the 2^126 that __fdividef takes.  (A zero value whose token has
+// 2^gap times the others' weight lifts the reference by gap - 80: below that the others' P keeps its precision.  With
+// 2^-30 it was off by 1 % at a gap of 45 and gone at 55.)
+constexpr float kLeast = 0x1p-80f;
 
 // CL: a cluster of p.cluster CTAs takes one segment, whose tiles are dealt to them evenly, and joins
 // their parts through shared memory: no merge kernel, and no sums over the lengths to begin with.
@@ -728,10 +733,10 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
           }
           // the largest weight of each token's value, at most 1
           if constexpr (TPR == 1) {
-            lv[0] = __log2f(fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), 0x1p-30f));
+            lv[0] = __log2f(fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), kLeast));
           } else {
-            lv[0] = __log2f(fmaxf(fmaxf(f[0], f[1]), 0x1p-30f));
-            lv[1] = __log2f(fmaxf(fmaxf(f[2], f[3]), 0x1p-30f));
+            lv[0] = __log2f(fmaxf(fmaxf(f[0], f[1]), kLeast));
+            lv[1] = __log2f(fmaxf(fmaxf(f[2], f[3]), kLeast));
           }
           tmem_ld_wait();
           reg_fence<4 * L::N4>(r_);

@@ -497,7 +497,9 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
  * queries exactly up to 2^-21 of a row's largest element; a probability times its value's scale
  * is rounded to 2^-14 (fp16) or 1.25 * 2^-9 (bf16) of itself, and by no more than 2^-25 or 2^-21 of
  * the largest such product in its tile of 128 (d = 128) or 256 tokens, every group of 32
- * channels measured by its own largest scale there.
+ * channels measured by its own largest scale there.  (For that a token's value counts as no smaller than
+ * 2^-80 of the tile's scales: one that is zero, in a token with 2^90 times the weight of all others,
+ * is the largest product, with 2^10 times theirs.)
  * width * page at most 2^31 - 256, Hq / H at most 2^23.
  *
  * attn_kv_read -- cached keys and values as packed 16-bit rows, for a prompt that goes on
