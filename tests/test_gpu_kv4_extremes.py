@@ -1,4 +1,5 @@
-"""attn_kv4_decode where its powers of two end: values next to nothing under nearly all the weight."""
+"""attn_kv4_decode where its powers of two end: values next to nothing under nearly all the weight, queries
+near the type's largest number."""
 import math
 
 import pytest
@@ -6,7 +7,7 @@ import torch
 
 import plain64
 from plain64 import DT
-from test_gpu_kv4_decode import i32, problem, reference, wide
+from test_gpu_kv4_decode import decode_and_check, i32, problem, reference, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +67,16 @@ def test_decode_a_heavier_token_whose_value_is_zero(d, dtype):
     said = [x.clone() for x in args]
     said[4][args[5][0, 0].item(), 0, 5] = 2.0 ** 82 * 2.0 ** -80
     check_both_ways(args, said, dtype)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq", [4, 8, 16])
+def test_decode_queries_up_to_the_largest_number(d, Hq):
+    """Elements up to bf16's largest, 2^128 less a step: no more than 2^-21 of the row's largest is lost."""
+    g = torch.Generator().manual_seed(40)
+    args = problem([300, 17], 1, Hq, 1, d, 16, "bf16", seed=41)
+    top = torch.finfo(torch.bfloat16).max
+    args[0].copy_((torch.rand(args[0].shape, generator=g, dtype=torch.float64) * 2 - 1) * top)
+    args[0][:, :, ::2, 3] = top
+    args[3].copy_(args[3] * 2.0 ** -60)
+    decode_and_check(args, [300, 17], 2.0 ** -66, True, "bf16")
