@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kDecThreads, Kv8Layout<D, RP, NP>::kCtas) attn
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         // 2^-e brings the row's largest into [128, 256)
-        const int e = min(max((int)(top >> 23) - 127 - 7, -100), 119);
+        const int e = min(max((int)(top >> 23) - 127 - 7, -100), 120);
         const float mul = pow2f(-e);
         const bool bad = top >= 0x7f800000u;
 #pragma unroll
