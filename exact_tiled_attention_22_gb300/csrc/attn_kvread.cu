@@ -20,6 +20,14 @@ namespace {
 constexpr int kReadThreads = 256;
 constexpr int kReadMaxTok = 128;
 
+// A product in 32 bits, cut off towards zero, with its last bit set where that lost something: rounding it to 16 bits
+// rounds the product itself, ties included.  (Infinities and NaN leave no rest that is a number.)  48k tokens with scales
+// of 24 bits: 47.6 us, 46.3 with powers of two.
+__device__ __forceinline__ float mul_to_odd(float a, float b) {
+  const float r = __fmul_rz(a, b);
+  return fabsf(fmaf(a, b, -r)) > 0.f ? __uint_as_float(__float_as_uint(r) | 1u) : r;
+}
+
 // BITS = 8: e4m3 codes, a scale for each page and head.  BITS = 4: e2m1 codes, a scale
 // for 32 channels of a token and head.
 template <int D, int BITS, bool BF16, int U>
@@ -97,8 +105,14 @@ __global__ void __launch_bounds__(kReadThreads) attn_kv_read_kernel(const __grid
 #pragma unroll
           for (int k = 0; k < 4; ++k) f[k] = unpack2<false>(hw[k]);
         }
+        // (e2m1 times bf16 has 11 bits, e4m3 times a scale of 20 has 24: exact, as with append's powers of two)
+        if (BITS == 8 && (__float_as_uint(s[u]) & 15u)) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[j + k] = pack2_sat<BF16>(f[k].x * s[u], f[k].y * s[u]);
+          for (int k = 0; k < 4; ++k) w[j + k] = pack2_sat<BF16>(mul_to_odd(f[k].x, s[u]), mul_to_odd(f[k].y, s[u]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[j + k] = pack2_sat<BF16>(f[k].x * s[u], f[k].y * s[u]);
+        }
       }
       st_global_32(static_cast<uint8_t*>(p.out[kv]) + dst[u] * 32, w);
     }

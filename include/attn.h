@@ -509,8 +509,8 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
  *   k, v : [T, H, d] of dtype, 32-byte aligned; row cu[b] + i becomes token i of request b, for i < lens[b] and
  *          within the request's rows and the T.  All other rows are left as they are, those
  *          behind the cached tokens of a request among them (its new tokens go there)
- * Values are scale * code, rounded to nearest even, at most the type's largest (NaN stays
- * one).  A page id outside [0, P) reads as zeros; lengths are clamped to [0, width * page].
+ * Values are scale * code, rounded once, to nearest even (a product with an 8-bit cache's scale that is no power of
+ * two, below 2^-126, twice), at most the type's largest (NaN stays one).  A page id outside [0, P) reads as zeros; lengths are clamped to [0, width * page].
  * 0 <= T < 2^31, T * H < 2^33, width * page < 2^31.
  */
 int attn_kv4_append(const void* k, const void* v, long long k_stride, long long v_stride,
