@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdint>
@@ -48,6 +49,8 @@ struct DeviceInfo {
   int sms = 0;
   int* status = nullptr;            // device address of g_attn_status ...
   unsigned long long status_ctx = 0;  // ... in the context with this id
+  // In that context, of each form of the 4-bit decode two bits: whether a cluster of 16 was asked for, and fits.
+  std::atomic<unsigned> kv4_fit{0};
 };
 
 std::mutex g_mu;
@@ -113,6 +116,7 @@ int current_device(DeviceInfo** out) {
       return cuda_fail(e, "cudaGetSymbolAddress(status)");
     d.status = static_cast<int*>(ptr);
     d.status_ctx = ctx;
+    d.kv4_fit = 0;
   }
   *out = &d;
   return ATTN_OK;
@@ -873,6 +877,18 @@ static int encode_pages4(CUtensorMap* m, const void* ptr, long long PH, int page
   return ATTN_OK;
 }
 
+// Whether the GPU has the SMs together for a cluster of the call's: beyond 8 not every GPU, or part of one, does.  Asked
+// once for each form of the kernel (0.7 us).
+static bool kv4_fits(DeviceInfo* dev, const attn::KvDecArgs& a) {
+  const int bit = 2 * ((a.d == 128 ? 0 : 6) + (a.bf16 ? 0 : 3) + (a.rp == 4 ? 0 : (a.rp == 8 ? 1 : 2)));
+  unsigned got = dev->kv4_fit >> bit & 3u;
+  if (!got) {
+    got = attn::kv4_clusters_fit(a) ? 3u : 1u;
+    dev->kv4_fit |= got << bit;
+  }
+  return got == 3u;
+}
+
 int attn_kv4_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cache, const uint16_t* k_scale,
                     const uint16_t* v_scale, const int32_t* block_table, const int32_t* lens, void* o, float* lse, int B,
                     int Nq, int Hq, int H, int d, int P, int page, int width, float scale, int causal,
@@ -919,8 +935,12 @@ int attn_kv4_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
   a.scale = scale;
   const long long tile = 128 * (128 / d), tiles = ((long long)width * page + tile - 1) / tile;
   const long long segs = (long long)B * H * a.n_rb;
-  a.cluster = attn::kv4_cluster(a.rp, a.bf16, dev->sms, B, segs, tiles);
-  a.grid = a.cluster ? (int)(segs * a.cluster) : attn::kv4_grid(a.rp, a.bf16, dev->sms, tiles * segs);
+  auto deal = [&](int most) {
+    a.cluster = attn::kv4_cluster(a.rp, a.bf16, dev->sms, B, segs, tiles, most);
+    a.grid = a.cluster ? (int)(segs * a.cluster) : attn::kv4_grid(a.rp, a.bf16, dev->sms, tiles * segs);
+  };
+  deal(attn::kKv4MaxCluster);
+  if (a.cluster > 8 && !kv4_fits(dev, a)) deal(8);
   a.full = attn::kv4_full(a.rp, a.bf16, dev->sms, a.grid);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.ws_o = reinterpret_cast<float*>(ws);

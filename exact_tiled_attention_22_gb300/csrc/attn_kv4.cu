@@ -268,7 +268,6 @@ __device__ __forceinline__ uint32_t rest4_e4m3(uint32_t h_lo, uint32_t h_hi, uin
   return r;
 }
 
-constexpr int kMaxCluster = 16;
 constexpr float kNone = -3e38f;  // the maximum of scores that are all masked
 // A token's values count for the row's reference as this much of the tile's largest scale, if they are smaller: p is at
 // most 2^88 then, and its sum over 2^31 tokens below the 2^126 that __fdividef takes.  (A zero value whose token has
@@ -922,9 +921,9 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
         for (int r = rank + n * (warp >> 2); r < RP; r += n * WG) {
           const int2 at = rows[r];
           if (at.x < 0) break;
-          float mr[kMaxCluster], lr[kMaxCluster], o[kMaxCluster], M = kNone;
+          float mr[kKv4MaxCluster], lr[kKv4MaxCluster], o[kKv4MaxCluster], M = kNone;
 #pragma unroll
-          for (int k = 0; k < kMaxCluster; ++k) {
+          for (int k = 0; k < kKv4MaxCluster; ++k) {
             mr[k] = kNone;
             lr[k] = o[k] = 0.f;
             if (k < n) {
@@ -935,10 +934,10 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
             }
           }
 #pragma unroll
-          for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, mr[k]);
+          for (int k = 0; k < kKv4MaxCluster; ++k) M = fmaxf(M, mr[k]);
           float l = 0.f, sum = 0.f;
 #pragma unroll
-          for (int k = 0; k < kMaxCluster; ++k) {
+          for (int k = 0; k < kKv4MaxCluster; ++k) {
             const float w = ex2(mr[k] - M);
             l = fmaf(w, lr[k], l);
             sum = fmaf(w, o[k], sum);
@@ -958,8 +957,9 @@ __global__ void __launch_bounds__(Kv4Layout<D, WG, NP>::kThreads, Kv4Layout<D, W
   }
 }
 
+// Launches the kernel for `a`, or, with `fit`, asks how many of its clusters the GPU can hold at once.
 template <int D, int WG, int NP>
-cudaError_t launch_split_t(const KvDecArgs& a, cudaStream_t stream) {
+cudaError_t split_t(const KvDecArgs& a, cudaStream_t stream, int* fit) {
   using L = Kv4Layout<D, WG, NP>;
   auto* k = a.cluster ? attn_kv4_split_kernel<D, WG, NP, true> : attn_kv4_split_kernel<D, WG, NP, false>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
@@ -971,22 +971,25 @@ cudaError_t launch_split_t(const KvDecArgs& a, cudaStream_t stream) {
   cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)a.cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute& pdl = attr[a.cluster ? 1 : 0];
   cfg.attrs = attr;
-  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+  cfg.numAttrs = 1;
+  if (fit) return cudaOccupancyMaxActiveClusters(fit, k, &cfg);
+  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl.val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = a.cluster ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, a);
 }
 
 template <int D>
-cudaError_t launch_split_d(const KvDecArgs& a, cudaStream_t stream) {
+cudaError_t split_d(const KvDecArgs& a, cudaStream_t stream, int* fit) {
   if (a.bf16)
-    return a.rp == 4 ? launch_split_t<D, 1, 2>(a, stream)
-                     : (a.rp == 8 ? launch_split_t<D, 2, 2>(a, stream) : launch_split_t<D, 4, 2>(a, stream));
-  return a.rp == 4 ? launch_split_t<D, 1, 3>(a, stream) : launch_split_t<D, 2, 3>(a, stream);
+    return a.rp == 4 ? split_t<D, 1, 2>(a, stream, fit)
+                     : (a.rp == 8 ? split_t<D, 2, 2>(a, stream, fit) : split_t<D, 4, 2>(a, stream, fit));
+  return a.rp == 4 ? split_t<D, 1, 3>(a, stream, fit) : split_t<D, 2, 3>(a, stream, fit);
 }
 
 }  // namespace
@@ -1023,45 +1026,15 @@ cudaError_t launch_kv4_append(Kv4AppendArgs a, int sms, cudaStream_t stream) {
   return a.bf16 ? launch_append_t<64, true>(a, w32, ahead, stream) : launch_append_t<64, false>(a, w32, ahead, stream);
 }
 
-// Row blocks of 4, 8 or, in bf16, 16 rows, a warpgroup for every four: what a thread does for a tile does not
-// grow, and a block of 16 rows is one CTA's (32 requests of 1000 to 16384 tokens, 64 query and 4 key heads: 55 us,
-// with 8 rows, 64 and 8 heads, 55; one warpgroup for all of a block's rows 57 and 53, but 19.8 us against 18.1 for 912
-// heads of 128 tokens in groups of 8).  (16 rows of fp16 in three terms would take P rows of 192 bytes.)
-int kv4_rows(int R, bool bf16) { return R <= 4 ? 4 : (R <= 8 || !bf16 ? 8 : 16); }
-
-static long long resident(int rp, bool bf16, int sms) { return (rp == 16 ? 1ll : (rp == 4 && bf16 ? 3ll : 2ll)) * sms; }
-
-// CTAs of the cluster that takes a segment, of `tiles` tiles at most, or 0: the tiles of all
-// requests are dealt to all CTAs, and a second kernel joins the parts.  A cluster saves that
-// kernel and the sums over the lengths, but a long request among short ones is its few CTAs'
-// alone: four tiles to a CTA, eight where there is one request.  Up to 8 CTAs; 16 where that is one to an
-// SM (more such clusters do not fit at once: 24 segments of 4096 tokens 14 us, 9 with 8) and a
-// CTA would have more than two tiles.
-// Requests of equal length, us by clusters and dealt (bf16, 8 heads, groups of 4, d = 128): one of 1000 tokens
-// 5.5 and 8.0, of 8192 8.9 and 11.9, of 16384 13.5 and 13.3; 12 of 2048 10.1 and 13.5; 24 of 1024 10.7 and
-// 13.9.  Of 1 to 2048 tokens, 12: 9.2 and 10.0; of 1 to 4096, eight tiles to a CTA: 12.6 and 11.2.
-int kv4_cluster(int rp, bool bf16, int sms, int B, long long segs, long long tiles) {
-  int c = segs * 16 <= sms && tiles > 16 ? kMaxCluster : 8;
-  while (c > 1 && (segs * c > resident(rp, bf16, sms) || c / 2 >= tiles)) c /= 2;
-  return c > 1 && tiles <= (B == 1 ? 8 : 4) * c ? c : 0;
-}
-
-// All CTAs resident at once, no more than there can be tiles.
-int kv4_grid(int rp, bool bf16, int sms, long long max_units) {
-  long long g = resident(rp, bf16, sms);
-  if (g > kKvMaxCtas) g = kKvMaxCtas;
-  if (g > max_units) g = max_units;
-  return (int)(g < 1 ? 1 : g);
-}
-
-// Of three CTAs to an SM the last one starts a microsecond after the others and goes 5 % slower:
-// four long requests, equal shares: the first two thirds of the CTAs end at 68 us, the others at 73.  Shares
-// of 8 and 7: 75.8 us in all, 78.6 with equal ones, 76.7 with 9 and 8, 75.9 with 7 and 6 (64 ragged
-// requests 31.7, 32.9, 31.8, 31.5).
-int kv4_full(int rp, bool bf16, int sms, int grid) { return resident(rp, bf16, sms) == 3ll * sms && grid == 3 * sms ? 2 * sms : 0; }
-
 cudaError_t launch_kv4_split(const KvDecArgs& a, cudaStream_t stream) {
-  return a.d == 128 ? launch_split_d<128>(a, stream) : launch_split_d<64>(a, stream);
+  return a.d == 128 ? split_d<128>(a, stream, nullptr) : split_d<64>(a, stream, nullptr);
+}
+
+bool kv4_clusters_fit(const KvDecArgs& a) {
+  int n = 0;
+  if ((a.d == 128 ? split_d<128>(a, nullptr, &n) : split_d<64>(a, nullptr, &n)) == cudaSuccess) return n > 0;
+  cudaGetLastError();  // (an answer, not a fault of the call)
+  return false;
 }
 
 }  // namespace attn

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "kv4_rules.h"
 #include "var_split.h"
 
 namespace attn {
@@ -211,7 +212,6 @@ struct Kv8AppendArgs {
 };
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int sms, cudaStream_t stream);
 
-constexpr int kKvMaxCtas = 640;  // workspace bound of the decode grids
 // What a segment (one request's tiles of one head group) costs a CTA besides its tiles, in tiles.
 constexpr int kKv8SegCost = 2;   // (64 ragged requests: 65, 53, 52, 53 us with a cost of 0 to 3)
 // (64 ragged requests in 4 bits, 0 to 2: three CTAs to an SM 43.3, 32.9, 33.4 us; two, in fp16, 47.7, 37.1, 35.7;
@@ -270,11 +270,9 @@ void kv_rows(Args* a, long long tok) {
   a->h_magic = a->tok == 1 ? 0 : (uint32_t)(((1ull << 31) + a->H - 1) / a->H);
 }
 cudaError_t launch_kv4_append(Kv4AppendArgs a, int sms, cudaStream_t stream);
-int kv4_rows(int R, bool bf16);
-int kv4_cluster(int rp, bool bf16, int sms, int B, long long segs, long long tiles);
-int kv4_grid(int rp, bool bf16, int sms, long long max_units);
-int kv4_full(int rp, bool bf16, int sms, int grid);
 cudaError_t launch_kv4_split(const KvDecArgs& a, cudaStream_t stream);
+// Whether a cluster of the call's finds as many SMs together.
+bool kv4_clusters_fit(const KvDecArgs& a);
 
 // Cached keys and values as packed 16-bit rows (attn_kvread.cu).
 struct KvReadArgs {
