@@ -741,11 +741,10 @@ __global__ void __launch_bounds__(128) attn_kv_merge_kernel(const __grid_constan
     const int h = hr / p.n_rb, rb = hr - h * p.n_rb;
     const int r = (int)((unit - blk * n_in) * per) + (WPR == 4 ? 0 : warp), idx = rb * p.rp + r;
     const long long u0 = before * Hr + (long long)hr * seg_units<SC>(nt);
-    const int c0 = nt ? (int)deal.owner(u0 + SC) : 0;
-    const int c1 = nt ? (int)deal.owner(u0 + SC + nt - 1) : 0;
+    Parts at = {0, 0, 0};
+    if (nt) at = kv_parts<SC>(deal, u0, nt);
+    const int c0 = at.c0, c1 = at.c1, s0 = at.s0;
     if ((nt == 0 || c0 != c1) && (WPR == 1 || idx < R)) {
-      // the first CTA's part is in its second slot if its range began earlier
-      const int s0 = nt && deal.start(c0) < u0 ? 1 : 0;
       auto part = [&](int c) -> size_t { return ((size_t)c * 2 + (c == c0 ? s0 : 0)) * p.rp + r; };
       const bool live = idx < R;  // (WPR = 1: a warp may have no row)
       if (!waited) griddep_wait();
