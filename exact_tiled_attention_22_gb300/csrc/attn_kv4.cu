@@ -35,7 +35,8 @@
 //
 // Measured (graph replay, bf16, d = 128): four requests of 50001 to 131072 tokens, 32 query and 8 key heads, 450 MB:
 // 75.8 us or 5.9 TB/s, 88 % of the measured copy bandwidth (from tile to tile 97 %; the rest is the start, the
-// uneven ends and the merge); 64 requests of 100 to 8192 tokens, 130 MB: 31.7 us; one of 1000 tokens: 5.6 us.
+// uneven ends and the merge); 64 requests of 100 to 8192 tokens, 130 MB: 31.7 us; one of 1000 tokens: 5.3 us behind
+// a table of that length, 8.0 behind a wide one (kv4_cluster).
 // The tensor pipe is 9 % busy, the warp schedulers 47 %.  With 8 and 16 query rows the conversions and
 // the softmax bound it: 0.6 and 1.2 us a tile and SM, 0.43 with 4 rows, which is the memory's rate.
 #include <cuda_bf16.h>

@@ -18,7 +18,8 @@ inline long long kv4_resident(int rp, bool bf16, int sms) { return (rp == 16 ? 1
 // CTAs of the cluster that takes a segment, of `tiles` tiles at most, or 0: the tiles of all
 // requests are dealt to all CTAs, and a second kernel joins the parts.  A cluster saves that
 // kernel and the sums over the lengths, but a long request among short ones is its few CTAs'
-// alone: four tiles to a CTA, eight where there is one request.  Up to 8 CTAs; 16 where that is one to an
+// alone: four tiles to a CTA, eight where there is one request.  (The tiles are the block table's: the
+// lengths are on the device.  A table with room for long requests is dealt, however short they are.)  Up to 8 CTAs; 16 where that is one to an
 // SM (more such clusters do not fit at once: 24 segments of 4096 tokens 14 us, 9 with 8) and a
 // CTA would have more than two tiles.
 // Requests of equal length, us by clusters and dealt (bf16, 8 heads, groups of 4, d = 128): one of 1000 tokens

@@ -500,7 +500,9 @@ int attn_kv8_decode(const void* q, const uint8_t* k_cache, const uint8_t* v_cach
  * channels measured by its own largest scale there.  (For that a token's value counts as no smaller than
  * 2^-80 of the tile's scales: one that is zero, in a token with 2^90 times the weight of all others,
  * is the largest product, with 2^10 times theirs.)
- * width * page at most 2^31 - 256, Hq / H at most 2^23.
+ * width * page at most 2^31 - 256, Hq / H at most 2^23.  Behind a table of few tiles (width * page counts, not the
+ * lengths) clusters of blocks take the requests, which is faster for few or short ones and adds in another order.
+ * With some 100 query rows Nq * Hq / H and more to a key head (64 in fp16) attn_kv_read and attn_varlen_fwd take less time.
  *
  * attn_kv_read -- cached keys and values as packed 16-bit rows, for a prompt that goes on
  * after a cached prefix (attn_varlen_fwd takes the rows).

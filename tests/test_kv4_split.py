@@ -23,7 +23,7 @@ def test_dependents_may_start_when_tensor_memory_is_there():
     assert alloc.start() < trigger.start()
 
 
-def checker(tmp_path_factory, name):
+def host_program(tmp_path_factory, name):
     exe = str(tmp_path_factory.mktemp(name) / "check")
     subprocess.run(["g++", "-std=c++17", "-O2", "-Wall", "-Werror", os.path.join(ROOT, "tests", "c_client", name + ".cpp"),
                     "-I" + CSRC, "-o", exe], check=True)
@@ -40,12 +40,12 @@ def checker(tmp_path_factory, name):
 
 @pytest.fixture(scope="module")
 def rules(tmp_path_factory):
-    return checker(tmp_path_factory, "kv4_rules_check")
+    return host_program(tmp_path_factory, "kv4_rules_check")
 
 
 @pytest.fixture(scope="module")
 def walk(tmp_path_factory):
-    return checker(tmp_path_factory, "kv_split_check")
+    return host_program(tmp_path_factory, "kv_split_check")
 
 
 def test_clusters_of_eight_where_none_of_sixteen_fits(rules):
